@@ -28,6 +28,8 @@ CONV_LINEAR, CONV_SILU_SKIP = 0, 1
 OUT_DELTA = 1
 RETRIEVE_IN_PROJECTION = 2  # engram_forward: retrieval inside the projection launches
 WEIGHTS_PACKED = 4  # engram_forward / engram_gate_fuse: W_k and W_v as engram_pack_weight wrote them
+GRAD_ACCUMULATE = 8  # engram_embed_backward / engram_layer_norm_backward: add to the parameters' gradients
+QUANTIZE_TRANSPOSE = 16  # engram_quantize_fp8: quantise the transpose
 MAX_TABLES, MAX_BRANCHES = 32, 4
 NOALLOC_SCRATCH_BYTES = 64 << 20  # ENGRAM_NOALLOC_SCRATCH_BYTES
 KERNEL_NAMES = ("hash", "gather", "gemm", "fuse", "aux", "gemm_v", "gate", "seam", "bwd_gemm", "bwd_fuse",
@@ -120,6 +122,25 @@ def lib() -> C.CDLL:
         L.engram_backward.restype = C.c_int
         L.engram_backward.argtypes = [P, P, P, P, C.POINTER(WeightsC), P, i32, i32, u32, P, C.POINTER(GradsC),
                                       P, C.c_size_t, P]
+        f32 = C.c_float
+        L.engram_embed.restype = C.c_int
+        L.engram_embed.argtypes = [P, P, i64, P, f32, P, P, P]
+        L.engram_embed_backward_workspace_size.restype = C.c_size_t
+        L.engram_embed_backward_workspace_size.argtypes = [P, i64]
+        L.engram_embed_backward.restype = C.c_int
+        L.engram_embed_backward.argtypes = [P, P, i64, P, f32, u32, P, P, C.c_size_t, P]
+        L.engram_layer_norm.restype = C.c_int
+        L.engram_layer_norm.argtypes = [P, P, i64, P, P, f32, P, P, P, P]
+        L.engram_layer_norm_backward_workspace_size.restype = C.c_size_t
+        L.engram_layer_norm_backward_workspace_size.argtypes = [P, i64]
+        L.engram_layer_norm_backward.restype = C.c_int
+        L.engram_layer_norm_backward.argtypes = [P, P, P, i64, P, P, P, u32, P, P, P, P, C.c_size_t, P]
+        L.engram_quantize_fp8.restype = C.c_int
+        L.engram_quantize_fp8.argtypes = [P, P, i64, i64, i32, u32, P, P, P]
+        L.engram_matmul_fp8_workspace_size.restype = C.c_size_t
+        L.engram_matmul_fp8_workspace_size.argtypes = [P, i64, i64, i64]
+        L.engram_matmul_fp8.restype = C.c_int
+        L.engram_matmul_fp8.argtypes = [P, P, P, i32, P, P, i32, i64, i64, i64, P, C.c_int, P, C.c_size_t, P]
         L.engram_profile_begin.restype = C.c_int
         L.engram_profile_begin.argtypes = [P, i32, u32]
         L.engram_profile_end.restype = C.c_int
@@ -268,6 +289,39 @@ def _stream(stream) -> C.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
+
+
+def _shape(t: Optional[torch.Tensor], name: str, *shape: int):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+
+
+class _On:
+    """The device and stream of one call: every tensor on one device, which is
+    made the current one around the launch; `stream` must be that device's.
+    Without one, that device's current stream is used."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError("tensors on %s and %s in one call" % (dev, t.device))
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError("a stream of %s with tensors on %s" % (stream.device, dev))
+        self.stream = C.c_void_p(stream.cuda_stream)
+        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
 
 
 def _torch_dtype(dt: int):
@@ -461,6 +515,152 @@ class Plan:
         if n == 0:
             raise EngramError("engram_backward_workspace_size", E_UNSUPPORTED, "unsupported shape")
         return torch.empty(n, dtype=torch.uint8, device=device)
+
+    # ------------------------------------------------------------------ operators beside the layer
+    def engram_embed(self, tokens, table, out, scale: float = 1.0, bad_tokens=None, stream=None):
+        """out[m][t] = scale * table[tokens[t]] for every branch m; ids outside
+        [0, vocab) give zeros and are counted in bad_tokens.
+        tokens: int32, any shape of n_tok ids; table: [vocab][d]; out: [n_branches][n_tok][d]."""
+        pt, pb = _ptr(tokens, "tokens", torch.int32), _ptr(bad_tokens, "bad_tokens", (torch.int32, torch.uint32))
+        pe, po = _ptr(table, "table", self.torch_dtype), _ptr(out, "out", self.torch_dtype)
+        n_tok, d = tokens.numel(), self.cfg.d_model
+        _shape(table, "table", self.cfg.vocab, d)
+        _shape(out, "out", self.cfg.n_branches, n_tok, d)
+        if bad_tokens is not None and bad_tokens.numel() < 1:
+            raise ValueError("bad_tokens is empty")
+        with _On(stream, tokens, table, out, bad_tokens) as s:
+            _check("engram_embed", lib().engram_embed(self._h, pt, n_tok, pe, scale, po, pb, s))
+
+    def engram_embed_backward_workspace_size(self, n_tok: int) -> int:
+        return int(lib().engram_embed_backward_workspace_size(self._h, n_tok))
+
+    def embed_backward_workspace(self, n_tok: int, device="cuda") -> torch.Tensor:
+        return self._workspace("engram_embed_backward", self.engram_embed_backward_workspace_size(n_tok), device)
+
+    def engram_embed_backward(self, tokens, dout, dtable, workspace, scale: float = 1.0, flags: int = 0, stream=None):
+        """dtable[r] = scale * the sum of dout ([n_branches][n_tok][d]) over the
+        branches and the tokens with id r; dtable: [vocab][d] fp32, every row
+        written (flags=GRAD_ACCUMULATE: added to the rows that tokens name)."""
+        pt, pg = _ptr(tokens, "tokens", torch.int32), _ptr(dout, "dout", self.torch_dtype)
+        pd, pw = _ptr(dtable, "dtable", torch.float32), _ptr(workspace, "workspace")
+        n_tok, d = tokens.numel(), self.cfg.d_model
+        _shape(dout, "dout", self.cfg.n_branches, n_tok, d)
+        _shape(dtable, "dtable", self.cfg.vocab, d)
+        with _On(stream, tokens, dout, dtable, workspace) as s:
+            _check("engram_embed_backward", lib().engram_embed_backward(
+                self._h, pt, n_tok, pg, scale, flags, pd, pw, workspace.numel() * workspace.element_size(), s))
+
+    def engram_layer_norm(self, x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
+        """y = layer norm of x's rows ([..., d]; y may be x), beta may be None;
+        mean and rstd (fp32, one a row) are kept for the backward if given."""
+        px, py = _ptr(x, "x", self.torch_dtype), _ptr(y, "y", self.torch_dtype)
+        pg, pb = _ptr(gamma, "gamma", torch.float32), _ptr(beta, "beta", torch.float32)
+        pm, pr = _ptr(mean, "mean", torch.float32), _ptr(rstd, "rstd", torch.float32)
+        n_rows = self._rows(x, "x")
+        _shape(y, "y", *x.shape)
+        self._columns(gamma=gamma, beta=beta)
+        self._row_values(n_rows, mean=mean, rstd=rstd)
+        with _On(stream, x, y, gamma, beta, mean, rstd) as s:
+            _check("engram_layer_norm", lib().engram_layer_norm(self._h, px, n_rows, pg, pb, eps, py, pm, pr, s))
+
+    def engram_layer_norm_backward_workspace_size(self, n_rows: int) -> int:
+        return int(lib().engram_layer_norm_backward_workspace_size(self._h, n_rows))
+
+    def layer_norm_backward_workspace(self, n_rows: int, device="cuda") -> torch.Tensor:
+        return self._workspace("engram_layer_norm_backward", self.engram_layer_norm_backward_workspace_size(n_rows),
+                               device)
+
+    def engram_layer_norm_backward(self, x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, flags: int = 0,
+                                   stream=None):
+        """dx (which may be dy or x), dgamma and dbeta (None: not wanted) of
+        engram_layer_norm; flags=GRAD_ACCUMULATE adds to dgamma and dbeta."""
+        px, py = _ptr(x, "x", self.torch_dtype), _ptr(dy, "dy", self.torch_dtype)
+        pd = _ptr(dx, "dx", self.torch_dtype)
+        pg, pm, pr = (_ptr(t, n, torch.float32) for t, n in ((gamma, "gamma"), (mean, "mean"), (rstd, "rstd")))
+        pdg, pdb = _ptr(dgamma, "dgamma", torch.float32), _ptr(dbeta, "dbeta", torch.float32)
+        pw = _ptr(workspace, "workspace")
+        n_rows = self._rows(x, "x")
+        _shape(dy, "dy", *x.shape)
+        _shape(dx, "dx", *x.shape)
+        self._columns(gamma=gamma, dgamma=dgamma, dbeta=dbeta)
+        self._row_values(n_rows, mean=mean, rstd=rstd)
+        with _On(stream, x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace) as s:
+            _check("engram_layer_norm_backward", lib().engram_layer_norm_backward(
+                self._h, px, py, n_rows, pg, pm, pr, flags, pd, pdg, pdb, pw,
+                workspace.numel() * workspace.element_size(), s))
+
+    def engram_quantize_fp8(self, x, q, scales, block_rows: int = 1, transpose: bool = False, stream=None):
+        """q, scales = x ([rows][cols]) or its transpose in 8 bits, a scale for each
+        128 values of block_rows (1 or 128) rows.  q: float8_e4m3fn; scales:
+        float8_e8m0fnu (or uint8) of fp8_scale_shape(*q.shape, block_rows)."""
+        px = _ptr(x, "x", self.torch_dtype)
+        pq, ps = _ptr(q, "q", torch.float8_e4m3fn), _ptr(scales, "scales", (torch.float8_e8m0fnu, torch.uint8))
+        if x.dim() != 2:
+            raise ValueError("x must have two dimensions")
+        rows, cols = x.shape
+        _shape(q, "q", *((cols, rows) if transpose else (rows, cols)))
+        if block_rows in (1, 128):  # (the library refuses others)
+            _shape(scales, "scales", *self.fp8_scale_shape(*q.shape, block_rows))
+        with _On(stream, x, q, scales) as s:
+            _check("engram_quantize_fp8", lib().engram_quantize_fp8(
+                self._h, px, rows, cols, block_rows, QUANTIZE_TRANSPOSE if transpose else 0, pq, ps, s))
+
+    @staticmethod
+    def fp8_scale_shape(rows: int, cols: int, block_rows: int):
+        """Shape of the scales of a quantised [rows][cols] matrix."""
+        blocks = -(-cols // 128)
+        return (-(-rows // block_rows), -(-blocks // 4) * 4)
+
+    def engram_matmul_fp8_workspace_size(self, m: int, n: int, k: int) -> int:
+        return int(lib().engram_matmul_fp8_workspace_size(self._h, m, n, k))
+
+    def matmul_fp8_workspace(self, m: int, n: int, k: int, device="cuda") -> Optional[torch.Tensor]:
+        """A workspace for engram_matmul_fp8, or None where none is needed."""
+        size = self.engram_matmul_fp8_workspace_size(m, n, k)
+        return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+    def engram_matmul_fp8(self, a, a_scales, b, b_scales, out, workspace=None, a_block_rows: int = 1,
+                          b_block_rows: int = 128, stream=None):
+        """out[m][n] = a ([m][k]) times the rows of b ([n][k]), both quantised
+        with a scale for each 128 values of *_block_rows rows; out bf16 or fp32."""
+        e8 = (torch.float8_e8m0fnu, torch.uint8)
+        pa, psa = _ptr(a, "a", torch.float8_e4m3fn), _ptr(a_scales, "a_scales", e8)
+        pb, psb = _ptr(b, "b", torch.float8_e4m3fn), _ptr(b_scales, "b_scales", e8)
+        po, pw = _ptr(out, "out", (torch.float32, torch.bfloat16)), _ptr(workspace, "workspace")
+        if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+            raise ValueError("a and b must be [m][k] and [n][k], got %s and %s" % (tuple(a.shape), tuple(b.shape)))
+        (m, k), n = a.shape, b.shape[0]
+        _shape(out, "out", m, n)
+        if a_block_rows in (1, 128) and b_block_rows in (1, 128):  # (the library refuses others)
+            _shape(a_scales, "a_scales", *self.fp8_scale_shape(m, k, a_block_rows))
+            _shape(b_scales, "b_scales", *self.fp8_scale_shape(n, k, b_block_rows))
+        with _On(stream, a, a_scales, b, b_scales, out, workspace) as s:
+            _check("engram_matmul_fp8", lib().engram_matmul_fp8(
+                self._h, pa, psa, a_block_rows, pb, psb, b_block_rows, m, n, k, po,
+                F32 if out.dtype == torch.float32 else BF16, pw,
+                0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+
+    def _rows(self, x, name: str) -> int:
+        d = self.cfg.d_model
+        if x.dim() < 1 or x.shape[-1] != d:
+            raise ValueError("%s has shape %s, expected rows of %d" % (name, tuple(x.shape), d))
+        return x.numel() // d
+
+    def _columns(self, **ts):
+        for n, t in ts.items():
+            _shape(t, n, self.cfg.d_model)
+
+    @staticmethod
+    def _row_values(n_rows: int, **ts):
+        for n, t in ts.items():
+            if t is not None and t.numel() != n_rows:
+                raise ValueError("%s has %d values, expected one for each of %d rows" % (n, t.numel(), n_rows))
+
+    @staticmethod
+    def _workspace(fn: str, size: int, device) -> torch.Tensor:
+        if size == 0:
+            raise EngramError(fn + "_workspace_size", E_UNSUPPORTED, "unsupported shape")
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
     def engram_profile_begin(self, max_launches: int = 4096, kinds: Optional[Sequence[str]] = None):
         """Time launches of the named kinds (KERNEL_NAMES; None: all)."""

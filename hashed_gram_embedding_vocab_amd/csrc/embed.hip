@@ -1,0 +1,322 @@
+// embed.hip -- the dense token embedding beside the hashed tables: rows of a
+// [vocab][d] table scaled into the hidden state of every residual branch, and
+// the table's gradient by sorted tokens.
+//
+// Forward: h[m][t] = round(scale * table[id_t]), a row copy.
+//
+// Backward: dtable[r] = scale * sum over {t : id_t = r} (ascending) and
+// branches m of dh[m][t], in three launches whose results depend on the
+// tokens alone (no float atomics):
+//   embed_sort_kernel   stable counting sort of the token positions by id.
+//   embed_rows_kernel   sums of the runs inside each chunk of kRunChunk sorted
+//                       positions, and zeros for the rows no token names.
+//   embed_join_kernel   runs that cross chunks, from the chunks' parts.
+#include <algorithm>
+
+#include "engram_internal.h"
+#include "vec8.h"
+
+namespace engram {
+namespace {
+
+// One wave per (token, 512 channels): 8 channels a lane.
+template <typename T>
+__global__ __launch_bounds__(256) void embed_kernel(const int32_t *tokens, int64_t n_tok, int32_t vocab,
+                                                    const T *table, int32_t d, int32_t n_branches, float scale,
+                                                    T *h, uint32_t *bad) {
+    const int lane = threadIdx.x & 63;
+    const int32_t strips = (d + 511) / 512;
+    const int64_t waves = (int64_t)gridDim.x * 4, n_items = n_tok * strips;
+    for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < n_items; item += waves) {
+        const int64_t t = item / strips;
+        const int32_t strip = (int32_t)(item - t * strips);
+        const int32_t c = strip * 512 + lane * 8;
+        const int32_t id = tokens[t];
+        const bool ok = id >= 0 && id < vocab;
+        if (!ok && strip == 0 && lane == 0 && bad) atomicAdd(bad, 1u);
+        if (c >= d) continue;
+        F8 x = {};
+        if (ok) {
+            x = load8(table + (int64_t)id * d + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.v[i] *= scale;
+        }
+        for (int m = 0; m < n_branches; ++m) store8(h + ((int64_t)m * n_tok + t) * d + c, x);
+    }
+}
+
+// Stable counting sort by id in one launch: workgroup b owns the ids
+// [b * kBucket, (b + 1) * kBucket) and reads every token twice (they stay in
+// L2).  First pass: how many tokens have a lower id (where the bucket's
+// output starts; no workgroup waits for another), and a count per id and
+// wave.  Second pass: wave w places the tokens of its contiguous share in
+// order, 64 at a time, equal ids ranked by ballot.  The cost is n_tok * (vocab
+// / kBucket) id reads.
+constexpr int kSortWaves = 16;
+constexpr int kBucket = 512;
+
+__global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32_t *tokens, int64_t n_tok,
+                                                                     int32_t vocab, uint32_t *order, int32_t *sid,
+                                                                     uint32_t *start) {
+    __shared__ uint32_t cnt[kSortWaves][kBucket];
+    __shared__ uint32_t below_s[kSortWaves], wtot[kBucket / 64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t lo64 = (int64_t)blockIdx.x * kBucket;
+    const int32_t lo = (int32_t)lo64;
+    const int32_t n_ids = (int32_t)min((int64_t)kBucket, (int64_t)vocab - lo64);
+    for (int i = threadIdx.x; i < kSortWaves * kBucket; i += 64 * kSortWaves) (&cnt[0][0])[i] = 0u;
+    __syncthreads();
+    const int64_t share = (n_tok + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
+    const int64_t first = min(w * share, n_tok), last = min(first + share, n_tok);
+    uint32_t below = 0u;
+    for (int64_t g = first; g < last; g += 64 * 8) {
+        int32_t id[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t t = g + 64 * u + lane;
+            id[u] = t < last ? tokens[t] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            below += (id[u] >= 0 && id[u] < lo) ? 1u : 0u;
+            if (id[u] >= lo && id[u] - lo < n_ids) atomicAdd(&cnt[w][id[u] - lo], 1u);
+        }
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off);
+    if (lane == 0) below_s[w] = below;
+    __syncthreads();
+    // exclusive prefix over the ids (thread r: id lo + r), then over the waves of each id
+    const int r = threadIdx.x;
+    uint32_t base = 0u, tot = 0u, incl = 0u;
+    for (int i = 0; i < kSortWaves; ++i) base += below_s[i];
+    if (r < kBucket) {
+        for (int i = 0; i < kSortWaves; ++i) tot += cnt[i][r];
+        incl = tot;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t y = __shfl_up(incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 63) wtot[w] = incl;
+    }
+    __syncthreads();
+    if (r < kBucket) {
+        uint32_t at = base + incl - tot;
+        for (int i = 0; i < w; ++i) at += wtot[i];
+        if (r < n_ids) start[lo + r] = at;
+        if (lo64 + r == (int64_t)vocab - 1) start[vocab] = at + tot;
+        for (int i = 0; i < kSortWaves; ++i) {
+            const uint32_t c = cnt[i][r];
+            cnt[i][r] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t g = first; g < last; g += 64 * 8) {
+        int32_t id[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t t = g + 64 * u + lane;
+            id[u] = t < last ? tokens[t] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool mine = id[u] >= lo && id[u] - lo < n_ids;
+            uint64_t left = __ballot(mine);
+            while (left) {
+                const int32_t x = __builtin_amdgcn_readlane(id[u], __builtin_ctzll(left));
+                const bool peer = mine && id[u] == x;
+                const uint64_t peers = __ballot(peer);
+                const uint32_t at = cnt[w][x - lo];
+                // (a wave's LDS accesses complete in order: every lane has read the slot)
+                asm volatile("" ::: "memory");
+                if (peer) {
+                    const uint32_t pos = at + (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
+                    order[pos] = (uint32_t)(g + 64 * u + lane);
+                    sid[pos] = x;
+                    if ((peers >> lane) == 1ull) cnt[w][x - lo] = pos + 1u;
+                }
+                asm volatile("" ::: "memory");
+                left &= ~peers;
+            }
+        }
+    }
+}
+
+constexpr int kRunChunk = 32;  // sorted positions per wave
+constexpr int kZeroRows = 8;   // table rows per wave of the zero part
+
+__device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, bool accumulate) {
+    F8 x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.v[i] = acc.v[i] * scale;
+    if (accumulate) {
+        const F8 old = load8(dst);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.v[i] += old.v[i];
+    }
+    store8(dst, x);
+}
+
+// Blocks [0, sum_blocks): one wave per (chunk of sorted positions, 512
+// channels) adds the chunk's rows in order.  A run that lies inside the chunk
+// goes to its table row; the part of one that began earlier goes to lead[c],
+// the part of one that began here and goes on to tail[c].  The other blocks
+// write zeros to the table rows without tokens.
+template <typename T, int BR>
+__global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, const int32_t *sid,
+                                                         const uint32_t *start, int64_t n_tok, int32_t vocab,
+                                                         int32_t d, const T *dh, float scale, bool accumulate,
+                                                         float *dtable, float *lead, float *tail,
+                                                         uint32_t sum_blocks) {
+    constexpr int U = BR <= 2 ? 8 : 4;  // tokens whose rows are in flight
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (blockIdx.x >= sum_blocks) {
+        const int64_t r0 = (wave - (int64_t)sum_blocks * 4) * kZeroRows;
+        for (int64_t r = r0; r < min(r0 + kZeroRows, (int64_t)vocab); ++r) {
+            if (start[r] != start[r + 1]) continue;
+            for (int32_t c = lane * 4; c < d; c += 256)
+                *reinterpret_cast<f32x4_t *>(dtable + r * d + c) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        return;
+    }
+    const int32_t strips = (d + 511) / 512;
+    const int64_t c = wave / strips;
+    const int32_t col = (int32_t)(wave - c * strips) * 512 + lane * 8;
+    const bool in = col < d;
+    const int64_t n = start[vocab], base = c * kRunChunk;
+    if (base >= n) return;
+    const int cnt = (int)min((int64_t)kRunChunk, n - base);
+    uint32_t my_tok = 0u;
+    int32_t my_id = -1;
+    if (lane < cnt) {
+        my_tok = order[base + lane];
+        my_id = sid[base + lane];
+    }
+    const int32_t before = base > 0 ? sid[base - 1] : -1;
+    const int32_t after = base + cnt < n ? sid[base + cnt] : -1;
+    bool started = __builtin_amdgcn_readlane(my_id, 0) != before;
+    F8 acc = {};
+    for (int k0 = 0; k0 < cnt; k0 += U) {
+        F8 x[U][BR];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t t = (uint32_t)__builtin_amdgcn_readlane((int)my_tok, min(k0 + u, cnt - 1));
+#pragma unroll
+            for (int m = 0; m < BR; ++m) {
+                x[u][m] = F8{};
+                if (in) x[u][m] = load8(dh + ((int64_t)m * n_tok + t) * d + col);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u;
+            if (k >= cnt) break;
+#pragma unroll
+            for (int m = 0; m < BR; ++m)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc.v[i] += x[u][m].v[i];
+            const int32_t id = __builtin_amdgcn_readlane(my_id, k);
+            const int32_t next = k == cnt - 1 ? after : __builtin_amdgcn_readlane(my_id, min(k + 1, kRunChunk));
+            const bool ends = next != id;
+            if (!ends && k < cnt - 1) continue;
+            if (in) {
+                if (!started)
+                    store8(lead + c * d + col, acc);
+                else if (ends)
+                    put_row(dtable + (int64_t)id * d + col, acc, scale, accumulate);
+                else
+                    store8(tail + c * d + col, acc);
+            }
+            acc = F8{};
+            started = true;
+        }
+    }
+}
+
+// One workgroup per chunk and 1024 channels: where a run starts in the chunk
+// and goes on, its tail part plus the lead parts of the chunks behind it, in order.
+__global__ __launch_bounds__(256) void embed_join_kernel(const int32_t *sid, const uint32_t *start, int32_t vocab,
+                                                         int32_t d, const float *lead, const float *tail,
+                                                         float scale, bool accumulate, float *dtable) {
+    const int64_t c = blockIdx.x, base = c * kRunChunk, n = start[vocab];
+    if (base + kRunChunk >= n) return;
+    const int32_t id = sid[base + kRunChunk - 1];
+    const int64_t first = start[id], end = (int64_t)start[id + 1];
+    if (first < base || end <= base + kRunChunk) return;
+    const int32_t col = (int32_t)blockIdx.y * 1024 + threadIdx.x * 4;
+    if (col >= d) return;
+    const int64_t last = (end - 1) / kRunChunk;
+    f32x4_t acc = *reinterpret_cast<const f32x4_t *>(tail + c * d + col);
+    int64_t k = c + 1;
+    for (; k + 7 <= last; k += 8) {
+        f32x4_t x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const f32x4_t *>(lead + (k + u) * d + col);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc += x[u];
+    }
+    for (; k <= last; ++k) acc += *reinterpret_cast<const f32x4_t *>(lead + k * d + col);
+    f32x4_t *dst = reinterpret_cast<f32x4_t *>(dtable + (int64_t)id * d + col);
+    acc *= scale;
+    if (accumulate) acc += *dst;
+    *dst = acc;
+}
+
+template <typename T>
+void embed_rows(const EmbedBwdArgs &a, hipStream_t s) {
+    const int64_t chunks = embed_chunks(a.n_tok), strips = (a.d + 511) / 512;
+    const uint32_t sum_blocks = (uint32_t)((chunks * strips + 3) / 4);
+    const uint32_t zero_blocks = a.accumulate ? 0u : (uint32_t)((a.vocab + 4 * kZeroRows - 1) / (4 * kZeroRows));
+    const dim3 grid(sum_blocks + zero_blocks);
+#define ENGRAM_EMBED_ROWS(BR)                                                                                   \
+    launch_kernel((embed_rows_kernel<T, BR>), grid, dim3(256), s, a.order, a.sid, a.start, a.n_tok, a.vocab,    \
+                  a.d, static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, a.lead, a.tail, sum_blocks)
+    switch (a.n_branches) {
+        case 1: ENGRAM_EMBED_ROWS(1); break;
+        case 2: ENGRAM_EMBED_ROWS(2); break;
+        case 3: ENGRAM_EMBED_ROWS(3); break;
+        default: ENGRAM_EMBED_ROWS(4); break;
+    }
+#undef ENGRAM_EMBED_ROWS
+}
+
+}  // namespace
+
+void launch_embed(engram_dtype dt, const int32_t *tokens, int64_t n_tok, int32_t vocab, const void *table, int32_t d,
+                  int32_t n_branches, float scale, void *h, uint32_t *bad, hipStream_t s) {
+    const int64_t items = n_tok * ((d + 511) / 512);
+    const dim3 grid((unsigned)std::min<int64_t>((items + 3) / 4, (int64_t)1 << 22));
+    if (dt == ENGRAM_BF16)
+        launch_kernel(embed_kernel<uint16_t>, grid, dim3(256), s, tokens, n_tok, vocab,
+                      static_cast<const uint16_t *>(table), d, n_branches, scale, static_cast<uint16_t *>(h), bad);
+    else
+        launch_kernel(embed_kernel<float>, grid, dim3(256), s, tokens, n_tok, vocab,
+                      static_cast<const float *>(table), d, n_branches, scale, static_cast<float *>(h), bad);
+}
+
+int64_t embed_chunks(int64_t n_tok) { return (n_tok + kRunChunk - 1) / kRunChunk; }
+
+bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d) {
+    // a launch holds fewer than 2^32 threads along x, and 65535 blocks along y
+    const int64_t strips = (d + 511) / 512;
+    const int64_t blocks = (embed_chunks(n_tok) * strips + 3) / 4 + ((int64_t)vocab + 31) / 32;
+    return blocks < ((int64_t)1 << 24) && embed_chunks(n_tok) < ((int64_t)1 << 24) && (d + 1023) / 1024 <= 65535;
+}
+
+void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s) {
+    launch_kernel(embed_sort_kernel, dim3((unsigned)(((int64_t)a.vocab + kBucket - 1) / kBucket)),
+                  dim3(64 * kSortWaves), s, a.tokens, a.n_tok, a.vocab, a.order, a.sid, a.start);
+    if (dt == ENGRAM_BF16)
+        embed_rows<uint16_t>(a, s);
+    else
+        embed_rows<float>(a, s);
+    const int64_t chunks = embed_chunks(a.n_tok);
+    if (chunks > 1)
+        launch_kernel(embed_join_kernel, dim3((unsigned)chunks, (unsigned)((a.d + 1023) / 1024)), dim3(256), s, a.sid,
+                      a.start, a.vocab, a.d, a.lead, a.tail, a.scale, a.accumulate, a.dtable);
+}
+
+}  // namespace engram

@@ -363,6 +363,71 @@ int64_t bwd_row_chunks(int64_t n_items);
 size_t bwd_table_temp_bytes(int64_t n_items);
 hipError_t launch_bwd_table_grad(const BwdTableArgs &t, hipStream_t s);
 
+// ---------------------------------------------------------------- embedding
+// h[m][t] = round(scale * table[tokens[t]]) (zeros for ids outside [0, vocab),
+// counted in *bad if given), d % 8 == 0
+void launch_embed(engram_dtype dt, const int32_t *tokens, int64_t n_tok, int32_t vocab, const void *table, int32_t d,
+                  int32_t n_branches, float scale, void *h, uint32_t *bad, hipStream_t s);
+
+struct EmbedBwdArgs {
+    const int32_t *tokens;                  // [n_tok]
+    const void *dh;                         // [B_r][n_tok][d] plan dtype
+    float *dtable;                          // [vocab][d]
+    uint32_t *order;                        // [n_tok] token positions sorted by id (those in [0, vocab))
+    int32_t *sid;                           // [n_tok] their ids
+    uint32_t *start;                        // [vocab + 1] first sorted position of each id; start[vocab]: how many
+    float *lead, *tail;                     // [embed_chunks(n_tok)][d] parts of runs that cross chunks
+    int64_t n_tok;
+    int32_t vocab, d, n_branches;
+    float scale;
+    bool accumulate;
+};
+int64_t embed_chunks(int64_t n_tok);
+bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d);
+void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- layer norm
+struct NormArgs {
+    const void *x, *dy;                     // [n_rows][d] plan dtype (dy: backward)
+    void *y, *dx;                           // [n_rows][d] plan dtype
+    const float *gamma, *beta;              // [d]; beta may be null
+    float *mean, *rstd;                     // [n_rows]: written by the forward (if given), read by the backward
+    float *part;                            // [2][norm_bwd_blocks][d] partial sums of dgamma and dbeta
+    float *dgamma, *dbeta;                  // [d]; dbeta may be null
+    int64_t n_rows;
+    int32_t d;
+    float eps;
+    bool accumulate;
+};
+bool norm_fits(int32_t d);
+int32_t norm_bwd_blocks(int64_t n_rows, int32_t d);
+void launch_norm(engram_dtype dt, const NormArgs &a, hipStream_t s);
+void launch_norm_bwd(engram_dtype dt, const NormArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- 8-bit product
+struct QuantArgs {
+    const void *x;                          // [rows][cols] plan dtype
+    void *q;                                // [rows][cols] e4m3, or [cols][rows] (transpose)
+    uint8_t *scales;                        // e8m0, [ceil(R / block_rows)][blocks of C filled up to 4s] of q [R][C]
+    int64_t rows, cols;
+    int32_t block_rows;                     // 1 or 128
+    bool transpose;
+};
+void launch_quantize(engram_dtype dt, const QuantArgs &a, hipStream_t s);
+
+struct ProductArgs {
+    const uint8_t *a, *b;                   // [M][K] and [N][K] e4m3, K % 16 == 0
+    const uint8_t *a_scales, *b_scales;     // as QuantArgs writes them
+    void *c;                                // [M][N] fp32 or bf16
+    void *ws;                               // product_workspace bytes
+    int64_t M, N, K;
+    int32_t a_block_rows, b_block_rows;     // 1 or 128
+    bool out_bf16;
+};
+size_t product_workspace(int64_t M, int64_t N, int64_t K);
+bool product_fits(int64_t M, int64_t N, int64_t K);
+void launch_product(const ProductArgs &a, hipStream_t s);
+
 // ---------------------------------------------------------------- synthetic tables
 // ---------------------------------------------------------------- copies
 void launch_copy_f32(const float *src, float *dst, int64_t n, hipStream_t s);  // n % 4 == 0

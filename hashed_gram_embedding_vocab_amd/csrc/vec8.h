@@ -1,0 +1,39 @@
+// vec8.h -- eight consecutive bf16 or fp32 elements moved as fp32 values: the
+// unit in which the row kernels (embed.hip, norm.hip, fp8.hip) read and write.
+// Rounding to bf16 is to nearest even and keeps NaN and infinity.
+#pragma once
+
+#include "engram_internal.h"
+
+namespace engram {
+
+// 8 consecutive elements as fp32, from 16 bytes of bf16 or 32 of fp32
+struct F8 {
+    float v[8];
+};
+
+__device__ __forceinline__ F8 load8(const uint16_t *p) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(p);
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.v[2 * i] = __uint_as_float(w[i] << 16);
+        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    return r;
+}
+__device__ __forceinline__ F8 load8(const float *p) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p);
+    const f32x4_t b = *reinterpret_cast<const f32x4_t *>(p + 4);
+    return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+__device__ __forceinline__ void store8(uint16_t *p, const F8 &x) {
+    *reinterpret_cast<u32x4_t *>(p) = u32x4_t{pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]),
+                                              pack_bf16x2(x.v[4], x.v[5]), pack_bf16x2(x.v[6], x.v[7])};
+}
+__device__ __forceinline__ void store8(float *p, const F8 &x) {
+    *reinterpret_cast<f32x4_t *>(p) = f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]};
+    *reinterpret_cast<f32x4_t *>(p + 4) = f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]};
+}
+
+}  // namespace engram

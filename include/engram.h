@@ -82,6 +82,12 @@ enum { ENGRAM_RETRIEVE_IN_PROJECTION = 1u << 1 };
  * (bf16 plans only; engram_backward takes the [d][D_e] matrices and rejects
  * the flag).  Same results bit for bit. */
 enum { ENGRAM_WEIGHTS_PACKED = 1u << 2 };
+/* engram_embed_backward / engram_layer_norm_backward flag: the parameters'
+ * gradients are added to what their buffers hold instead of overwriting it
+ * (micro-batches of one optimizer step). */
+enum { ENGRAM_GRAD_ACCUMULATE = 1u << 3 };
+/* engram_quantize_fp8 flag: quantise the transpose of x. */
+enum { ENGRAM_QUANTIZE_TRANSPOSE = 1u << 4 };
 
 #define ENGRAM_MAX_TABLES 32
 #define ENGRAM_MAX_BRANCHES 4
@@ -126,19 +132,23 @@ typedef struct {
 /* Per-kernel timing gathered while profiling is on (see engram_profile_*). */
 enum {
     ENGRAM_K_HASH = 0,    /* engram_hash                                                     */
-    ENGRAM_K_GATHER = 1,  /* engram_gather, or the fused hash + gather of engram_forward      */
+    ENGRAM_K_GATHER = 1,  /* engram_gather, or the fused hash + gather of engram_forward;
+                             engram_embed                                                    */
     ENGRAM_K_GEMM = 2,    /* projections W_k e of every branch with the gate partials fused
-                             (and W_v e on the fusion-kernel path)                           */
+                             (and W_v e on the fusion-kernel path); engram_matmul_fp8        */
     ENGRAM_K_FUSE = 3,    /* fusion-kernel path (short chunks, fp32): gated value, conv,
                              residual, state                                                 */
-    ENGRAM_K_AUX = 4,     /* context / state bookkeeping                                      */
+    ENGRAM_K_AUX = 4,     /* context / state bookkeeping, packing; engram_layer_norm,
+                             engram_quantize_fp8                                             */
     ENGRAM_K_GEMM_V = 5,  /* W_v e with gated value, conv, residual, state fused (prefill)     */
     ENGRAM_K_GATE = 6,    /* gate per token and branch from the partial sums                  */
     ENGRAM_K_SEAM = 7,    /* rows at 256-token tile seams left by ENGRAM_K_GEMM_V             */
     ENGRAM_K_BWD_GEMM = 8,  /* engram_backward: the MFMA contractions (k and v again, dE, dW)  */
     ENGRAM_K_BWD_FUSE = 9,  /* engram_backward: gate statistics, conv / gate / RMSNorm backward,
-                               transposes and the reductions of the small gradients           */
-    ENGRAM_K_BWD_TABLE = 10,/* engram_backward: sort, scan and per-row sums of the table gradient */
+                               transposes and the reductions of the small gradients;
+                               engram_layer_norm_backward                                    */
+    ENGRAM_K_BWD_TABLE = 10,/* engram_backward: sort, scan and per-row sums of the table gradient;
+                               engram_embed_backward                                         */
     ENGRAM_K_COUNT = 11
 };
 
@@ -458,6 +468,131 @@ ENGRAM_API engram_status engram_backward(engram_plan p, const uint32_t *d_idx, c
                               int32_t batch, int32_t seqlen, uint32_t flags, void *d_dh,
                               const engram_grads *g, void *d_workspace, size_t workspace_bytes,
                               hipStream_t stream);
+
+/*
+ * Operators beside the layer: what a model puts around it.  They take the
+ * plan for its dtype, d_model, vocab and n_branches, follow the conventions
+ * above, and none of them allocates or synchronises.  Buffers written by a
+ * call must not overlap its other buffers (ENGRAM_E_INVALID_ARG) except where
+ * it is said that they may.  Calls that overlap in time on one device need
+ * workspaces of their own; so do two captured graphs that may replay at once.
+ * Every result depends on the inputs alone (no float atomics): repeated calls
+ * give the same bits.
+ */
+
+/*
+ * The dense token embedding: h_t = scale * table[token t], rounded once, into
+ * every residual branch (the hidden state engram_forward takes as d_h).
+ *   d_tokens     [n_tok] int32 raw ids (batch and sequence flattened)
+ *   d_table      [vocab][d_model] plan dtype
+ *   scale        finite factor of the rows, e.g. sqrt(d_model); 1 copies them
+ *   d_h          [n_branches][n_tok][d_model] plan dtype
+ *   d_bad_tokens optional uint32 counter, incremented once per id outside
+ *                [0, vocab); such ids (padding) give rows of zeros.
+ * n_tok above 2^31 - 1: ENGRAM_E_UNSUPPORTED.
+ */
+ENGRAM_API engram_status engram_embed(engram_plan p, const int32_t *d_tokens, int64_t n_tok, const void *d_table,
+                                      float scale, void *d_h, uint32_t *d_bad_tokens, hipStream_t stream);
+
+/* Bytes of device workspace engram_embed_backward needs (0 on invalid or
+ * unsupported sizes): 8 bytes a token, 4 an id and n_tok * d_model / 4. */
+ENGRAM_API size_t engram_embed_backward_workspace_size(engram_plan p, int64_t n_tok);
+
+/*
+ * The gradient of engram_embed by sorted tokens:
+ *   dtable[r] = scale * sum over t with token t = r, and branches m, of dh[m][t]
+ * in fp32, tokens ascending (branches inside a token) within fixed pieces of
+ * the sorted order that are then added in order.
+ *   d_dh         [n_branches][n_tok][d_model] plan dtype, as engram_backward writes it
+ *   flags        ENGRAM_GRAD_ACCUMULATE: add to d_dtable (rows no token names
+ *                are not touched); without it every row is written, zeros
+ *                where no token names it
+ *   d_dtable     [vocab][d_model] fp32
+ *   d_workspace  >= engram_embed_backward_workspace_size(p, n_tok) bytes, 256-byte aligned
+ * Ids outside [0, vocab) contribute nothing.
+ */
+ENGRAM_API engram_status engram_embed_backward(engram_plan p, const int32_t *d_tokens, int64_t n_tok,
+                                               const void *d_dh, float scale, uint32_t flags, float *d_dtable,
+                                               void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Layer norm of n_rows rows of d_model channels:
+ *   y = (x - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * statistics in fp32 (the variance from centred values), y rounded once.
+ *   d_x, d_y      [n_rows][d_model] plan dtype; d_y may be d_x
+ *   d_gamma       [d_model] fp32;  d_beta the same, or NULL for none
+ *   d_mean, d_rstd  [n_rows] fp32 statistics for the backward, or NULL
+ * d_model above 32768: ENGRAM_E_UNSUPPORTED.
+ */
+ENGRAM_API engram_status engram_layer_norm(engram_plan p, const void *d_x, int64_t n_rows, const float *d_gamma,
+                                           const float *d_beta, float eps, void *d_y, float *d_mean, float *d_rstd,
+                                           hipStream_t stream);
+
+/* Bytes of device workspace engram_layer_norm_backward needs (0 on invalid
+ * or unsupported sizes). */
+ENGRAM_API size_t engram_layer_norm_backward_workspace_size(engram_plan p, int64_t n_rows);
+
+/*
+ * The gradients of engram_layer_norm: with g = dy * gamma and xh = (x - mean) * rstd,
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)),  dgamma = sum dy * xh,  dbeta = sum dy.
+ *   d_x, d_gamma, d_mean, d_rstd   as the forward had and wrote them
+ *   d_dy, d_dx    [n_rows][d_model] plan dtype; d_dx may be d_dy or d_x
+ *   flags         ENGRAM_GRAD_ACCUMULATE: add to d_dgamma and d_dbeta
+ *   d_dgamma      [d_model] fp32;  d_dbeta the same, or NULL
+ *   d_workspace   >= engram_layer_norm_backward_workspace_size bytes, 256-byte aligned
+ */
+ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d_x, const void *d_dy, int64_t n_rows,
+                                                    const float *d_gamma, const float *d_mean, const float *d_rstd,
+                                                    uint32_t flags, void *d_dx, float *d_dgamma, float *d_dbeta,
+                                                    void *d_workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The layer's products in 8-bit floating point, a scale for each block of 128.
+ *
+ * A quantised matrix [R][C] is its e4m3 values (4 exponent bits, bias 7, no
+ * infinities, largest 448), rows of C bytes, and its scales: blocks of 128
+ * values along a row, of block_rows = 1 row or 128 rows, each scale a power of
+ * two kept as its biased exponent (e8m0: byte e stands for 2^(e - 127)), as
+ * bytes [ceil(R / block_rows)][ceil(C / 128) rounded up to a multiple of 4].
+ *
+ * engram_quantize_fp8 makes one from x [rows][cols] in the plan dtype, or from
+ * its transpose (ENGRAM_QUANTIZE_TRANSPOSE: R = cols, C = rows).  Per block
+ *   scale = the smallest power of two >= 2^-126 with amax / scale <= 448
+ *   q     = x / scale rounded to nearest-even e4m3
+ * amax over the block's finite values; NaN and infinities become e4m3's NaN.
+ * Scale bytes behind a row's last block are set to 127 (one).
+ *
+ * engram_matmul_fp8 multiplies two of them:
+ *   C[m][n] = sum over blocks kb of  sa[m][kb] sb[n][kb]  sum_{k in kb} a[m][k] b[n][k]
+ * rounded once to c_dtype.  An fp32 result is summed in fp32 throughout, over
+ * the values q * scale held as bf16 (exact while they lie in bf16's normal
+ * range).  A bf16 result takes the 8-bit matrix instructions at twice the rate:
+ * sums across blocks are fp32, but inside a block a product counts only to
+ * 2^-13 of the largest one there (about 1.5e-5 of the result's norm, against
+ * 1.7e-3 for its rounding).
+ *   d_a, d_b     [M][K] and [N][K] e4m3, rows contiguous; K % 16 == 0 (else
+ *                ENGRAM_E_UNSUPPORTED) and K < 2^22; the last block may be short
+ *   a_block_rows, b_block_rows   1 or 128, as the scales were made
+ *   d_c          [M][N] fp32 or bf16 (c_dtype)
+ *   d_workspace  >= engram_matmul_fp8_workspace_size(p, M, N, K) bytes,
+ *                256-byte aligned; may be NULL where that is 0
+ * A scale byte of 255 stands for NaN.
+ *
+ * One projection of the layer and its gradients, E [n_tok][D_e] and W [d][D_e]:
+ *   v  = E W^T       E by token (block_rows 1), W by 128 x 128
+ *   dE = dv W        dv by token, W transposed by 128 x 128
+ *   dW = dv^T E      both transposed, block_rows 1 (blocks of 128 tokens)
+ */
+ENGRAM_API engram_status engram_quantize_fp8(engram_plan p, const void *d_x, int64_t rows, int64_t cols,
+                                             int32_t block_rows, uint32_t flags, void *d_q, uint8_t *d_scales,
+                                             hipStream_t stream);
+/* 0 also on invalid or unsupported sizes (engram_matmul_fp8 then refuses the call). */
+ENGRAM_API size_t engram_matmul_fp8_workspace_size(engram_plan p, int64_t M, int64_t N, int64_t K);
+ENGRAM_API engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const uint8_t *d_a_scales,
+                                           int32_t a_block_rows, const void *d_b, const uint8_t *d_b_scales,
+                                           int32_t b_block_rows, int64_t M, int64_t N, int64_t K, void *d_c,
+                                           engram_dtype c_dtype, void *d_workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
 
 /*
  * Profiling: while on, each launch of a kind selected by kind_mask (bit k

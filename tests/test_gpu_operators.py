@@ -1,0 +1,766 @@
+"""The operators beside the layer on the GPU (embedding, layer norm, 8-bit
+product) against plain 64-bit implementations.
+
+Tolerances count roundings: u = 2^-24 is fp32's half step, a sum of n terms in
+any order of rounded additions is off by at most about n u times the sum of
+magnitudes, and an output rounded to bf16 by 2^-8 of its value (fp32: u).
+"""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DTYPES = ("bf16", "f32")
+
+
+def tdt(dtype):
+    return torch.bfloat16 if dtype == "bf16" else torch.float32
+
+
+def half_step(dtype):
+    return torch.finfo(tdt(dtype)).eps / 2
+
+
+def make_plan(dtype="bf16", d=256, vocab=1000, n_branches=1, **kw):
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    return B.Plan(vocab=vocab, vocab_comp=min(vocab, 770), heads=4, head_dim=32, table_rows=[10007] * 8, hash_seed=1,
+                  d_model=d, n_branches=n_branches, dtype=B.BF16 if dtype == "bf16" else B.F32, **kw)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(shape, dtype, seed, sd=1.0):
+    return (torch.randn(shape, generator=gen(seed)) * sd).to(tdt(dtype))
+
+
+def zipf_ids(n, vocab, seed, bad=True):
+    w = torch.arange(1, vocab + 1, dtype=torch.float64).pow(-1.05).cumsum(0)
+    r = torch.searchsorted(w, torch.rand(n, dtype=torch.float64, generator=gen(seed)) * w[-1]).clamp_(max=vocab - 1)
+    ids = torch.randperm(vocab, generator=gen(seed + 1))[r].to(torch.int32)
+    if bad and n > 4:
+        ids[1], ids[n // 2], ids[-1] = -1, vocab, 2 ** 31 - 1
+    return ids
+
+
+def close(got, ref, bound, what=""):
+    d = (got.double().cpu() - ref).abs()
+    over = d > bound
+    assert not over.any() and not torch.isnan(d).any(), "%s: %d of %d off, worst %.3g over a bound of %.3g" % (
+        what, int(over.sum()), d.numel(), float(d.flatten()[(d - bound).flatten().argmax()]),
+        float(torch.broadcast_to(bound, d.shape).flatten()[(d - bound).flatten().argmax()]))
+
+
+# ---------------------------------------------------------------- embedding
+
+
+def embed_ref(ids, table, scale, n_branches):
+    """scale * row in fp32 (one IEEE product), rounded once: the kernel's bits."""
+    ok = (ids >= 0) & (ids < table.shape[0])
+    rows = table[ids.long().clamp(0, table.shape[0] - 1)].float() * torch.tensor(scale, dtype=torch.float32)
+    rows[~ok] = 0.0
+    return rows.to(table.dtype).expand(n_branches, -1, -1), int((~ok).sum())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d,branches,scale", [
+    (1, 1, 8, 1, 1.0), (1, 50, 256, 4, 16.0), (77, 1000, 264, 2, 0.3), (513, 700, 1032, 3, 1.0), (4099, 3001, 64, 1, -2.5)])
+def test_embed(gpu, dtype, n_tok, vocab, d, branches, scale):
+    p = make_plan(dtype, d, vocab, branches)
+    ids, table = zipf_ids(n_tok, vocab, 3), randn((vocab, d), dtype, 4)
+    out = torch.full((branches, n_tok, d), 7.0, dtype=tdt(dtype), device=gpu)
+    bad = torch.zeros(4, dtype=torch.int32, device=gpu)
+    p.engram_embed(ids.to(gpu), table.to(gpu), out, scale=scale, bad_tokens=bad)
+    ref, n_bad = embed_ref(ids, table, scale, branches)
+    assert torch.equal(out.cpu(), ref)
+    assert bad.tolist() == [n_bad, 0, 0, 0]
+    p.engram_embed(ids.to(gpu), table.to(gpu), out, scale=scale)  # the counter is optional
+    assert torch.equal(out.cpu(), ref)
+
+
+def test_embed_keeps_nan_and_infinity(gpu):
+    p = make_plan("bf16", 64, 10)
+    table = randn((10, 64), "bf16", 1)
+    table[3, 5], table[3, 6], table[4, 7] = math.nan, math.inf, -math.inf
+    ids = torch.tensor([3, 4, 5, -7], dtype=torch.int32)
+    out = torch.empty((1, 4, 64), dtype=torch.bfloat16, device=gpu)
+    p.engram_embed(ids.to(gpu), table.to(gpu), out, scale=2.0)
+    ref, _ = embed_ref(ids, table, 2.0, 1)
+    assert torch.equal(out.cpu().isnan(), ref.isnan())
+    assert torch.equal(out.cpu().nan_to_num(9.0), ref.nan_to_num(9.0))
+
+
+def embed_grad_ref(ids, dh, vocab, scale):
+    """(gradient, sum of magnitudes, terms) of each row in 64 bits."""
+    ok = (ids >= 0) & (ids < vocab)
+    at = ids[ok].long()
+    g = dh.double().sum(0)[ok]
+    m = dh.double().abs().sum(0)[ok]
+    d = dh.shape[-1]
+    ref = torch.zeros((vocab, d), dtype=torch.float64).index_add_(0, at, g) * scale
+    mag = torch.zeros((vocab, d), dtype=torch.float64).index_add_(0, at, m) * abs(scale)
+    cnt = torch.zeros(vocab, dtype=torch.float64).index_add_(0, at, torch.ones(len(at), dtype=torch.float64))
+    return ref, mag, cnt * dh.shape[0]
+
+
+IDS = {
+    "zipf": lambda n, v: zipf_ids(n, v, 5),
+    "one": lambda n, v: torch.full((n,), v - 1, dtype=torch.int32),          # one run over every chunk
+    "none": lambda n, v: torch.full((n,), -1, dtype=torch.int32),            # nothing to add anywhere
+    "two": lambda n, v: torch.tensor([0, v - 1], dtype=torch.int32).repeat(n)[:n].contiguous(),
+    "rising": lambda n, v: (torch.arange(n) % v).to(torch.int32),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("ids_of,n_tok,vocab,d,branches,scale", [
+    ("zipf", 1, 1, 8, 1, 1.0), ("zipf", 333, 1000, 256, 1, 16.0), ("zipf", 4099, 1537, 264, 2, 0.3),
+    ("zipf", 2048, 511, 1032, 3, 1.0), ("zipf", 1000, 513, 520, 4, -2.0), ("one", 32, 512, 64, 1, 1.0),
+    ("one", 33, 513, 64, 2, 1.0), ("one", 1500, 2000, 72, 1, 1.0), ("none", 65, 600, 64, 1, 1.0),
+    ("two", 4097, 1025, 128, 1, 1.0), ("rising", 3000, 1000, 64, 4, 1.0)])
+def test_embed_backward(gpu, dtype, ids_of, n_tok, vocab, d, branches, scale):
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    p = make_plan(dtype, d, vocab, branches)
+    ids, dh = IDS[ids_of](n_tok, vocab), randn((branches, n_tok, d), dtype, 8)
+    ws = p.embed_backward_workspace(n_tok)
+    ws.fill_(255)  # whatever the workspace held
+    got = torch.full((vocab, d), 7.0, device=gpu)
+    p.engram_embed_backward(ids.to(gpu), dh.to(gpu), got, ws, scale=scale)
+    ref, mag, terms = embed_grad_ref(ids, dh, vocab, scale)
+    # terms - 1 additions and the scale; scale itself rounded to fp32
+    bound = (terms[:, None] + 2) * U * mag
+    close(got, ref, bound, "dtable")
+    again = torch.full_like(got, -1.0)
+    p.engram_embed_backward(ids.to(gpu), dh.to(gpu), again, ws, scale=scale)
+    assert torch.equal(got, again)
+    # accumulated: rows without tokens keep their bits
+    old = randn((vocab, d), "f32", 9)
+    acc = old.to(gpu)
+    p.engram_embed_backward(ids.to(gpu), dh.to(gpu), acc, ws, scale=scale, flags=B.GRAD_ACCUMULATE)
+    close(acc, ref + old.double(), bound + U * (ref + old.double()).abs() + U * bound, "accumulated")
+    assert torch.equal(acc.cpu()[terms == 0], old[terms == 0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_embed_far_rows(gpu, dtype):
+    """A table and a gradient whose element offsets pass 2^31 (and bytes 2^32)."""
+    vocab, d = 300001, 8192
+    p = make_plan(dtype, d, vocab)
+    ids = torch.tensor([vocab - 1, 0, 262144, vocab - 1, 131073, 299999], dtype=torch.int32)
+    table = torch.zeros((vocab, d), dtype=tdt(dtype), device=gpu)
+    rows = randn((6, d), dtype, 2)
+    for i in (0, 1, 2, 4, 5):
+        table[int(ids[i])] = rows[i].to(gpu)
+    out = torch.empty((1, 6, d), dtype=tdt(dtype), device=gpu)
+    p.engram_embed(ids.to(gpu), table, out)
+    want = rows.clone()
+    want[3] = rows[0]
+    assert torch.equal(out[0].cpu(), want)
+    del table
+    got = torch.full((vocab, d), 1.0, device=gpu)
+    p.engram_embed_backward(ids.to(gpu), out, got, p.embed_backward_workspace(6))
+    for i in (1, 2, 4, 5):
+        assert torch.equal(got[int(ids[i])].cpu(), want[i].float())
+    assert torch.equal(got[vocab - 1].cpu(), want[0].float() * 2)  # x + x is exact
+    got[ids.long().to(gpu)] = 0.0
+    assert int(torch.count_nonzero(got)) == 0
+
+
+def test_embed_backward_is_the_difference_of_embed(gpu):
+    """dL/dtable along a random direction against L at table +- step: L = <w, h> is
+    linear in the table, so only roundings remain: each of n outputs is off by
+    u |h| on either side, so L's difference by about 2 u sum |w h| / step."""
+    p = make_plan("f32", 128, 97, 2)
+    ids, table, dirn = zipf_ids(301, 97, 1), randn((97, 128), "f32", 2), randn((97, 128), "f32", 3)
+    w = randn((2, 301, 128), "f32", 4)
+    step, scale = 0.5, 1.5
+    out, L, mag = torch.empty((2, 301, 128), device=gpu), [], 0.0
+    for sgn in (1.0, -1.0):
+        p.engram_embed(ids.to(gpu), (table + sgn * step * dirn).to(gpu), out, scale=scale)
+        L.append(float((out.double().cpu() * w.double()).sum()))
+        mag += float((out.double().cpu() * w.double()).abs().sum())
+    got = torch.empty((97, 128), device=gpu)
+    p.engram_embed_backward(ids.to(gpu), w.to(gpu), got, p.embed_backward_workspace(301), scale=scale)
+    _, gmag, terms = embed_grad_ref(ids, w, 97, scale)
+    along = float((got.double().cpu() * dirn.double()).sum())
+    # table +- step dirn is rounded too (one more u of each value)
+    bound = 3 * U * mag / (2 * step) + float(((terms[:, None] + 2) * U * gmag * dirn.double().abs()).sum())
+    assert abs((L[0] - L[1]) / (2 * step) - along) <= bound
+
+
+# ---------------------------------------------------------------- layer norm
+
+DEPTH = 66  # additions on the longest path of a row's sum: 8 values a step and at most 5 steps, 6 across lanes, 16 waves
+
+
+def norm_ref(x, gamma, beta, eps):
+    x = x.double()
+    mean = x.mean(-1)
+    xc = x - mean[..., None]
+    var = xc.square().mean(-1)
+    rstd = (var + eps).rsqrt()
+    y = xc * rstd[..., None] * gamma.double()
+    if beta is not None:
+        y = y + beta.double()
+    return y, mean, rstd
+
+
+def norm_bounds(x, gamma, beta, eps, dtype):
+    """Bounds of y, mean and rstd: the mean is off by e_mu = (DEPTH + 1) u max|x|; a
+    centred value by e_mu + u |xc|; the variance, relative to var + eps, by
+    2 e_mu rstd + (e_mu rstd)^2 + (DEPTH + 4) u; rstd by half of that and 3 u."""
+    y, mean, rstd = norm_ref(x, gamma, beta, eps)
+    x = x.double()
+    xc = (x - mean[..., None]).abs()
+    e_mu = (DEPTH + 1) * U * x.abs().amax(-1)
+    rv = 2 * e_mu * rstd + (e_mu * rstd) ** 2 + (DEPTH + 4) * U
+    r = rv / 2 + rv * rv + 3 * U
+    g = gamma.double().abs()
+    e_y = g * rstd[..., None] * (e_mu[..., None] + U * xc) + g * xc * rstd[..., None] * (r[..., None] + 3 * U)
+    e_y = e_y * 1.01 + 2 * U * (y.abs() + (0 if beta is None else beta.double().abs()))
+    return e_y + half_step(dtype) * (y.abs() + e_y), e_mu + U * mean.abs(), r * rstd * 1.01
+
+
+NORM_SHAPES = [(1, 8), (1, 2560), (3, 256), (5, 512), (77, 1024), (130, 1032), (33, 1544), (9, 2568), (6, 4096), (5, 4104),
+               (4, 8192), (3, 12296), (2, 16384), (3, 20488), (2, 32768)]
+
+
+def norm_inputs(rows, d, dtype, seed):
+    x = randn((rows, d), dtype, seed) * 1.0 + randn((1, d), dtype, seed + 1, 0.3)
+    x = x.to(tdt(dtype))
+    if rows > 1:
+        x[1] = 3.0                 # no variance
+    if rows > 2:
+        x[2] = x[2] + 100.0        # a mean far above the spread
+    gamma = 1.0 + randn((d,), "f32", seed + 2, 0.1)
+    beta = randn((d,), "f32", seed + 3, 0.1)
+    return x, gamma, beta
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("with_beta", (True, False))
+@pytest.mark.parametrize("rows,d", NORM_SHAPES)
+def test_layer_norm(gpu, dtype, with_beta, rows, d):
+    p = make_plan(dtype, d)
+    x, gamma, beta = norm_inputs(rows, d, dtype, 11)
+    beta = beta if with_beta else None
+    f = lambda t: None if t is None else t.to(gpu)  # noqa: E731
+    y = torch.full((rows, d), 7.0, dtype=tdt(dtype), device=gpu)
+    mean, rstd = torch.empty(rows, device=gpu), torch.empty(rows, device=gpu)
+    p.engram_layer_norm(f(x), f(gamma), f(beta), y, mean=mean, rstd=rstd, eps=1e-5)
+    ry, rm, rr = norm_ref(x, gamma, beta, 1e-5)
+    by, bm, br = norm_bounds(x, gamma, beta, 1e-5, dtype)
+    close(mean, rm, bm, "mean")
+    close(rstd, rr, br, "rstd")
+    close(y, ry, by, "y")
+    z = f(x)
+    p.engram_layer_norm(z, f(gamma), f(beta), z, eps=1e-5)  # in place, without statistics
+    assert torch.equal(z, y)
+
+
+def test_layer_norm_rows_are_apart(gpu):
+    """A row with a NaN or an infinity spoils itself alone."""
+    p = make_plan("bf16", 1024)
+    x, gamma, beta = norm_inputs(9, 1024, "bf16", 5)
+    y0, y1 = (torch.empty((9, 1024), dtype=torch.bfloat16, device=gpu) for _ in range(2))
+    p.engram_layer_norm(x.to(gpu), gamma.to(gpu), beta.to(gpu), y0)
+    x[4, 100], x[6, 0] = math.nan, math.inf
+    p.engram_layer_norm(x.to(gpu), gamma.to(gpu), beta.to(gpu), y1)
+    keep = [r for r in range(9) if r not in (4, 6)]
+    assert torch.equal(y0[keep], y1[keep])
+    assert bool(y1[4].isnan().all()) and bool(y1[6].isnan().all())
+
+
+def norm_grad_ref(x, dy, gamma, mean, rstd):
+    x, dy, gamma = x.double(), dy.double(), gamma.double()
+    rs = rstd.double()[:, None]
+    xh = (x - mean.double()[:, None]) * rs
+    g = dy * gamma
+    dx = rs * (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True))
+    # dx: every term carries a few u, the two means DEPTH u of their magnitudes
+    e = (DEPTH + 14) * U * rs * (g.abs() + g.abs().mean(1, keepdim=True) + xh.abs() * (g * xh).abs().mean(1, keepdim=True))
+    n = len(x)
+    return (dx, e), ((dy * xh).sum(0), (n + 6) * U * (dy * xh).abs().sum(0)), (dy.sum(0), (n + 6) * U * dy.abs().sum(0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,d", NORM_SHAPES + [(2051, 256), (4100, 64), (517, 1024), (600, 6152)])
+def test_layer_norm_backward(gpu, dtype, rows, d):
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    p = make_plan(dtype, d)
+    x, gamma, _ = norm_inputs(rows, d, dtype, 21)
+    dy = randn((rows, d), dtype, 25, 0.1)
+    _, mean, rstd = norm_ref(x, gamma, None, 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    (rdx, bdx), (rdg, bdg), (rdb, bdb) = norm_grad_ref(x, dy, gamma, mean, rstd)
+    bdx = bdx + half_step(dtype) * (rdx.abs() + bdx)
+    f = lambda t: t.to(gpu)  # noqa: E731
+    dx = torch.full((rows, d), 7.0, dtype=tdt(dtype), device=gpu)
+    dg, db = torch.full((d,), 7.0, device=gpu), torch.full((d,), 7.0, device=gpu)
+    ws = p.layer_norm_backward_workspace(rows)
+    ws.fill_(255)
+    args = (f(x), f(dy), f(gamma), f(mean), f(rstd))
+    p.engram_layer_norm_backward(*args, dx, dg, db, ws)
+    close(dx, rdx, bdx, "dx")
+    close(dg, rdg, bdg, "dgamma")
+    close(db, rdb, bdb, "dbeta")
+    # in place of dy, without dbeta, accumulated
+    old = randn((d,), "f32", 26)
+    dg2, dyx = old.to(gpu), f(dy)
+    p.engram_layer_norm_backward(f(x), dyx, f(gamma), f(mean), f(rstd), dyx, dg2, None, ws, flags=B.GRAD_ACCUMULATE)
+    assert torch.equal(dyx, dx)
+    assert torch.equal(dg2, old.to(gpu) + dg)
+    # in place of x
+    xx = f(x)
+    p.engram_layer_norm_backward(xx, f(dy), f(gamma), f(mean), f(rstd), xx, dg2, db, ws)
+    assert torch.equal(xx, dx) and torch.equal(dg2, dg)
+
+
+def test_layer_norm_backward_is_the_difference_of_the_forward(gpu):
+    """Along a direction v: (L(x + hv) - L(x - hv)) / 2h against <dx, v>.  L = <w, y>.
+    The difference misses by h^2/6 of L's third derivative, taken in 64 bits
+    from the same difference of the formula, and by the forward's bounds."""
+    rows, d, h = 7, 512, 2.0 ** -6
+    p = make_plan("f32", d)
+    x, v, w = randn((rows, d), "f32", 1), randn((rows, d), "f32", 2), randn((rows, d), "f32", 3)
+    gamma = 1.0 + randn((d,), "f32", 4, 0.1)
+    L, ref, bound = [], [], 0.0
+    for sgn in (1.0, -1.0):
+        xs = x + sgn * h * v
+        y = torch.empty((rows, d), device=gpu)
+        p.engram_layer_norm(xs.to(gpu), gamma.to(gpu), None, y)
+        L.append(float((y.double().cpu() * w.double()).sum()))
+        ref.append(float((norm_ref(xs, gamma, None, 1e-5)[0] * w.double()).sum()))
+        bound += float((norm_bounds(xs, gamma, None, 1e-5, "f32")[0] * w.double().abs()).sum())
+    mean, rstd = torch.empty(rows, device=gpu), torch.empty(rows, device=gpu)
+    y = torch.empty((rows, d), device=gpu)
+    p.engram_layer_norm(x.to(gpu), gamma.to(gpu), None, y, mean=mean, rstd=rstd)
+    dx, dg = torch.empty((rows, d), device=gpu), torch.empty(d, device=gpu)
+    p.engram_layer_norm_backward(x.to(gpu), w.to(gpu), gamma.to(gpu), mean, rstd, dx, dg, None,
+                                 p.layer_norm_backward_workspace(rows))
+    along = float((dx.double().cpu() * v.double()).sum())
+    rm, rr = norm_ref(x, gamma, None, 1e-5)[1:]
+    (rdx, bdx), _, _ = norm_grad_ref(x, w, gamma, rm, rr)
+    truncation = abs((ref[0] - ref[1]) / (2 * h) - float((rdx * v.double()).sum()))
+    # the saved statistics carry the forward's bounds: u-sized, covered by twice dx's own
+    assert truncation < 1e-2 * float((rdx * v.double()).abs().sum())
+    assert abs((L[0] - L[1]) / (2 * h) - along) <= truncation + bound / (2 * h) + 4 * float((bdx * v.double().abs()).sum())
+
+
+# ---------------------------------------------------------------- 8-bit product
+
+
+def pow2_scale_bytes(amax):
+    """Biased exponents of the smallest powers of two >= 2^-126 with amax / s <= 448."""
+    m, e = torch.frexp(amax.double())              # amax = m 2^e, m in [0.5, 1); 448 = 0.875 * 2^9
+    k = torch.where(m > 0.875, e - 8, e - 9)
+    k = torch.where(amax == 0, torch.full_like(k, -126), k).clamp(min=-126)
+    return (k + 127).to(torch.uint8)
+
+
+def e4m3_values(v):
+    """v (|v| <= 448) rounded to nearest-even e4m3, in 64 bits."""
+    e = torch.frexp(v.abs())[1].clamp(min=-5) - 1   # exponent of the leading bit, at least -6
+    step = torch.ldexp(torch.ones_like(v), (e - 3).to(v.dtype))
+    return torch.round(v / step) * step
+
+
+def quantize_ref(x, block_rows, transpose):
+    x = x.double()
+    if transpose:
+        x = x.t().contiguous()
+    r, c = x.shape
+    full = torch.nn.functional.pad(x, (0, -c % 128, 0, -r % block_rows))
+    tiles = full.reshape(full.shape[0] // block_rows, block_rows, -1, 128)
+    fin = torch.where(torch.isfinite(tiles), tiles.abs(), torch.zeros_like(tiles))
+    byte = pow2_scale_bytes(fin.amax((1, 3)))
+    s = torch.ldexp(torch.ones(byte.shape, dtype=torch.float64), byte.double() - 127)
+    v = tiles / s[:, None, :, None]
+    v = torch.where(torch.isfinite(v), v, torch.full_like(v, math.nan))
+    q = e4m3_values(v).reshape(full.shape)[:r, :c]
+    return q, torch.nn.functional.pad(byte, (0, -byte.shape[1] % 4), value=127)
+
+
+def quantize_gpu(p, x, block_rows, transpose, gpu, scale_dtype=torch.float8_e8m0fnu):
+    r, c = (x.shape[1], x.shape[0]) if transpose else x.shape
+    q = torch.full((r, c), 3.0, device=gpu).to(torch.float8_e4m3fn)
+    s = torch.full(p.fp8_scale_shape(r, c, block_rows), 99, dtype=torch.uint8, device=gpu).view(scale_dtype)
+    p.engram_quantize_fp8(x.to(gpu), q, s, block_rows=block_rows, transpose=transpose)
+    return q, s
+
+
+def spread_bytes(byte, rows, cols, block_rows):
+    s = torch.ldexp(torch.ones(byte.shape, dtype=torch.float64), byte.double() - 127)
+    return s.repeat_interleave(block_rows, 0)[:rows].repeat_interleave(128, 1)[:, :cols]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("block_rows,transpose", [(1, False), (128, False), (1, True), (128, True)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 16), (128, 128), (130, 257), (77, 640), (256, 513), (37, 1288),
+                                       (600, 136), (129, 2056)])
+def test_quantize(gpu, dtype, block_rows, transpose, rows, cols):
+    p = make_plan(dtype)
+    x = randn((rows, cols), dtype, 31, 0.02)
+    # magnitudes over many binades, so that blocks differ and e4m3's small steps are met
+    x = (x.float() * torch.exp2(torch.randint(-12, 13, (rows, cols), generator=gen(32)).float())).to(tdt(dtype))
+    if rows > 2:
+        x[2] = 0.0
+    q, s = quantize_gpu(p, x, block_rows, transpose, gpu)
+    rq, rs = quantize_ref(x, block_rows, transpose)
+    assert torch.equal(s.view(torch.uint8).cpu(), rs)
+    assert torch.equal(q.cpu().double(), rq)
+
+
+@pytest.mark.parametrize("block_rows,transpose", [(1, False), (128, False), (1, True), (128, True)])
+def test_quantize_extremes(gpu, block_rows, transpose):
+    """Zeros, the smallest and the largest values, amax on either side of
+    448 * 2^k, values between two e4m3 steps, NaN and infinities."""
+    p = make_plan("f32")
+    x = torch.zeros((256, 256))
+    big, tiny = torch.finfo(torch.float32).max, 2.0 ** -149
+    x[0, :4] = torch.tensor([big, -big, big / 3, 1.0])
+    x[1, :4] = torch.tensor([tiny, -tiny, 0.0, 2.0 ** -126])
+    x[2, 0] = 448.0 * 2.0 ** -5
+    x[3, 0] = math.nextafter(448.0, math.inf) * 2.0 ** -5  # rounds to 448 * 2^-5 in fp32
+    x[4, 0] = torch.nextafter(torch.tensor(448.0), torch.tensor(1e9)).item()
+    x[130, 128:160] = torch.arange(32) * 14.5 - 448 + 16  # halves of e4m3's steps
+    x[131, 128:131] = torch.tensor([math.nan, math.inf, -math.inf])
+    x[131, 131] = 5.0
+    q, s = quantize_gpu(p, x, block_rows, transpose, gpu, torch.uint8)
+    rq, rs = quantize_ref(x, block_rows, transpose)
+    assert torch.equal(s.cpu(), rs)
+    got = q.cpu().double()
+    assert torch.equal(got.isnan(), rq.isnan())
+    assert torch.equal(got.nan_to_num(1e9), rq.nan_to_num(1e9))
+
+
+def random_quantized(rows, cols, block_rows, seed):
+    """e4m3 values and scale bytes of every kind (not only those a quantiser makes)."""
+    q = (torch.randn((rows, cols), generator=gen(seed)) * 30).to(torch.float8_e4m3fn)
+    blocks = -(-cols // 128)
+    s = torch.randint(117, 134, (-(-rows // block_rows), -(-blocks // 4) * 4), generator=gen(seed + 1)).to(torch.uint8)
+    return q, s
+
+
+def product_ref(a, sa, abr, b, sb, bbr):
+    av = a.double() * spread_bytes(sa, *a.shape, abr)
+    bv = b.double() * spread_bytes(sb, *b.shape, bbr)
+    return av @ bv.t(), av.abs() @ bv.abs().t()
+
+
+def lost_in_blocks(a, sa, abr, b, sb, bbr):
+    av = (a.double() * spread_bytes(sa, *a.shape, abr)).abs()
+    bv = (b.double() * spread_bytes(sb, *b.shape, bbr)).abs()
+    lost = torch.zeros((len(av), len(bv)), dtype=torch.float64)
+    for k in range(0, av.shape[1], 128):
+        x, y = av[:, k:k + 128], bv[:, k:k + 128]
+        for m in range(0, len(av), 64):
+            lost[m:m + 64] += (x[m:m + 64, None] * y[None]).amax(-1) * (x.shape[1] * 2.0 ** -13)
+    return lost
+
+
+PRODUCT_SHAPES = [(1, 1, 16), (1, 16, 128), (1, 2560, 1280), (2, 333, 144), (5, 128, 2048), (16, 130, 4112), (17, 257, 640),
+                  (64, 64, 64), (77, 1000, 528), (128, 128, 128), (129, 255, 1264), (256, 256, 512), (300, 520, 400),
+                  (513, 129, 272), (128, 64, 16384), (1000, 24, 1024), (31, 2049, 96)]
+
+
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("abr,bbr", [(1, 128), (1, 1), (128, 1), (128, 128)])
+@pytest.mark.parametrize("m,n,k", PRODUCT_SHAPES)
+def test_matmul(gpu, out, abr, bbr, m, n, k):
+    """The product's K additions may each lose up to a step (2 u) of the running
+    sum of magnitudes inside the matrix unit; then one rounding to the output.
+    For a bf16 result the 8-bit matrix instructions keep a block's products to
+    2^-13 of the largest of them (beside a product of 1 one of 2^-13 counts, one
+    of 2^-14 is lost): each of a block's up to 128 products is off by less than
+    2^-13 of the block's largest, which adds 128 * 2^-13 of it for every block."""
+    p = make_plan()
+    a, sa = random_quantized(m, k, abr, 41)
+    b, sb = random_quantized(n, k, bbr, 43)
+    got = torch.full((m, n), 7.0, dtype=tdt(out), device=gpu)
+    ws = p.matmul_fp8_workspace(m, n, k)
+    if ws is not None:
+        ws.fill_(255)
+    e8 = torch.float8_e8m0fnu
+    p.engram_matmul_fp8(a.to(gpu), sa.to(gpu).view(e8), b.to(gpu), sb.to(gpu), got, ws, a_block_rows=abr, b_block_rows=bbr)
+    ref, mag = product_ref(a, sa, abr, b, sb, bbr)
+    bound = 2 * U * (k + 2) * mag
+    if out == "bf16":
+        bound = bound + lost_in_blocks(a, sa, abr, b, sb, bbr)
+    close(got, ref, bound + half_step(out) * (ref.abs() + bound), "product")
+    again = torch.empty_like(got)
+    p.engram_matmul_fp8(a.to(gpu), sa.to(gpu), b.to(gpu), sb.to(gpu), again, ws, a_block_rows=abr, b_block_rows=bbr)
+    assert torch.equal(got, again)
+
+
+def test_matmul_of_whole_numbers_is_exact(gpu):
+    """Small whole numbers and scales of one: every partial sum is a whole number below 2^24."""
+    p = make_plan()
+    for m, n, k in [(3, 5, 48), (200, 300, 1024), (1, 700, 1280), (140, 260, 8192)]:
+        a = torch.randint(-8, 9, (m, k), generator=gen(m)).float()
+        b = torch.randint(-8, 9, (n, k), generator=gen(n)).float()
+        sa = torch.full(p.fp8_scale_shape(m, k, 1), 127, dtype=torch.uint8)
+        sb = torch.full(p.fp8_scale_shape(n, k, 128), 127, dtype=torch.uint8)
+        got = torch.empty((m, n), device=gpu)
+        f8 = torch.float8_e4m3fn
+        p.engram_matmul_fp8(a.to(f8).to(gpu), sa.to(gpu), b.to(f8).to(gpu), sb.to(gpu), got, p.matmul_fp8_workspace(m, n, k))
+        assert torch.equal(got.cpu().double(), a.double() @ b.double().t())
+
+
+def test_matmul_nan_stays_in_its_row_and_column(gpu):
+    p = make_plan("f32")
+    for m, n, k in [(150, 140, 272), (3, 300, 640)]:
+        x, w = randn((m, k), "f32", 1), randn((n, k), "f32", 2)
+        x[2, 100], w[139, 5] = math.inf, math.nan
+        a, sa = quantize_gpu(p, x, 1, False, gpu)
+        b, sb = quantize_gpu(p, w, 128, False, gpu)
+        got = torch.empty((m, n), device=gpu)
+        p.engram_matmul_fp8(a, sa, b, sb, got, p.matmul_fp8_workspace(m, n, k))
+        want = torch.zeros((m, n), dtype=torch.bool)
+        want[2, :] = True
+        want[:, 139] = True
+        assert torch.equal(got.isnan().cpu(), want)
+        # a scale byte of 255 is NaN
+        sb.view(torch.uint8)[0, 0] = 255
+        p.engram_matmul_fp8(a, sa, b, sb, got, p.matmul_fp8_workspace(m, n, k))
+        assert bool(got[:, :128].isnan().all())
+        want[:, :128] = True
+        assert torch.equal(got.isnan().cpu(), want)
+
+
+def test_matmul_scales_of_every_size(gpu):
+    """Scale bytes at the ends of their range: products of 2^-127 .. 2^127 scales
+    that meet in the middle, and far from it (0 or infinity, never NaN from a zero)."""
+    p = make_plan()
+    k = 256
+    one = torch.ones((1, k)).to(torch.float8_e4m3fn)
+    ea = torch.tensor([1, 40, 127, 200, 240], dtype=torch.uint8)
+    eb = torch.tensor([240, 200, 127, 60, 2], dtype=torch.uint8)
+    sa = torch.zeros((5, 4), dtype=torch.uint8)
+    sb = torch.zeros((5, 4), dtype=torch.uint8)
+    sa[:, :2], sb[:, :2] = ea[:, None], eb[:, None]
+    a, b = one.repeat(5, 1), one.repeat(5, 1)
+    e = (ea[:, None].double() + eb[None, :].double() - 254)
+    want = torch.ldexp(torch.full((5, 5), 256.0, dtype=torch.float64), e).float()  # inf above, 0 below
+    normal = (want == 0) | want.isinf() | (want >= 2.0 ** -126)
+    for dt in (torch.float32, torch.bfloat16):
+        got = torch.empty((5, 5), dtype=dt, device=gpu)
+        p.engram_matmul_fp8(a.to(gpu), sa.to(gpu), b.to(gpu), sb.to(gpu), got, p.matmul_fp8_workspace(5, 5, k),
+                            b_block_rows=1)
+        assert torch.equal(got.float().cpu()[normal], want.to(dt).float()[normal]), dt
+        zero = torch.zeros_like(got)
+        z = torch.zeros((5, k)).to(torch.float8_e4m3fn)
+        p.engram_matmul_fp8(z.to(gpu), sa.to(gpu), b.to(gpu), sb.to(gpu), got, p.matmul_fp8_workspace(5, 5, k),
+                            b_block_rows=1)
+        assert torch.equal(got, zero), dt
+
+
+def test_projection_and_its_gradients(gpu):
+    """v = E W^T and, from dv, dE = dv W and dW = dv^T E, each through the
+    quantiser and the product, against the formula on the values the 8 bits stand
+    for (product's bound), and against the unquantised product: a value is off by
+    at most 2^-4 of itself, or 2^-10 of its block's scale, 2^-10 / 224 of its amax."""
+    p = make_plan("bf16")
+    n_tok, d, de = 272, 256, 384
+    e, w, dv = randn((n_tok, de), "bf16", 1, 0.02), randn((d, de), "bf16", 2, 0.05), randn((n_tok, d), "bf16", 3)
+
+    def rel_bound(x, block_rows, transpose):
+        """elementwise |q s - x| in 64 bits"""
+        xt = x.double().t() if transpose else x.double()
+        r, c = xt.shape
+        t = torch.nn.functional.pad(xt, (0, -c % 128, 0, -r % block_rows))
+        t = t.reshape(t.shape[0] // block_rows, block_rows, -1, 128)
+        am = t.abs().amax((1, 3), keepdim=True).expand_as(t).reshape(t.shape[0] * block_rows, -1)[:r, :c]
+        return xt, torch.maximum(xt.abs() * 2.0 ** -4, am * 2.0 ** -10 / 224)
+
+    for x, xbr, xt, y, ybr, yt in [(e, 1, False, w, 128, False), (dv, 1, False, w, 128, True), (dv, 1, True, e, 1, True)]:
+        a, sa = quantize_gpu(p, x, xbr, xt, gpu)
+        b, sb = quantize_gpu(p, y, ybr, yt, gpu)
+        m, n, k = a.shape[0], b.shape[0], a.shape[1]
+        assert b.shape[1] == k
+        got = torch.empty((m, n), device=gpu)
+        p.engram_matmul_fp8(a, sa, b, sb, got, p.matmul_fp8_workspace(m, n, k), a_block_rows=xbr, b_block_rows=ybr)
+        ref, mag = product_ref(a.cpu(), sa.view(torch.uint8).cpu(), xbr, b.cpu(), sb.view(torch.uint8).cpu(), ybr)
+        bound = 2 * U * (k + 2) * mag + U * ref.abs()
+        close(got, ref, bound, "product")
+        xv, xe = rel_bound(x, xbr, xt)
+        yv, ye = rel_bound(y, ybr, yt)
+        slack = xe @ yv.abs().t() + xv.abs() @ ye.t() + xe @ ye.t()
+        close(got, xv @ yv.t(), slack + bound * 1.2, "unquantised")
+
+
+# ---------------------------------------------------------------- together, streams, graphs
+
+
+def test_a_training_step_through_all_of_them(gpu):
+    """tokens -> embedding -> layer norm -> the layer, its values also through the
+    8-bit product, and back: layer backward -> layer norm backward -> embedding
+    gradient.  Every stage against 64 bits on what the stage before gave."""
+    import numpy as np
+
+    from hashed_gram_embedding_vocab_amd import binding as B
+    from synthetic import workloads as W
+    from synthetic.device import make_device_layer, to_device
+
+    wl = W.workload("tiny").with_shape(2, 96)
+    import dataclasses
+    wl = dataclasses.replace(wl, dtype="bf16", n_branches=2)
+    dl = make_device_layer(wl, device=gpu)
+    p, d, n_tok, br = dl.plan, wl.d_model, wl.n_tokens, wl.n_branches
+    toks = to_device(W.make_tokens(wl), torch.int32, gpu)
+    table = randn((wl.vocab, d), "bf16", 51)
+    gamma, beta = 1.0 + randn((d,), "f32", 52, 0.1), randn((d,), "f32", 53, 0.1)
+    f = lambda t: t.to(gpu)  # noqa: E731
+    h0 = torch.empty((br, n_tok, d), dtype=torch.bfloat16, device=gpu)
+    h1, out, dh1, dh0 = (torch.empty_like(h0) for _ in range(4))
+    mean, rstd = torch.empty(br * n_tok, device=gpu), torch.empty(br * n_tok, device=gpu)
+    p.engram_embed(toks, f(table), h0, scale=16.0)
+    p.engram_layer_norm(h0, f(gamma), f(beta), h1, mean=mean, rstd=rstd)
+    ws = p.workspace(wl.batch, wl.seqlen)
+    p.engram_forward(toks, dl.comp_map, dl.tables, h1, dl.weights, out, ws)
+    # the layer's v by the 8-bit product of the same rows and weights
+    emb = torch.empty((n_tok, wl.emb_dim), dtype=torch.bfloat16, device=gpu)
+    p.engram_retrieve(toks, dl.comp_map, dl.tables, emb)
+    a, sa = quantize_gpu(p, emb.cpu(), 1, False, gpu)
+    b, sb = quantize_gpu(p, dl.weights.w_v.cpu(), 128, False, gpu)
+    v8 = torch.empty((n_tok, d), device=gpu)
+    p.engram_matmul_fp8(a, sa, b, sb, v8, p.matmul_fp8_workspace(n_tok, d, wl.emb_dim))
+    # loss = <w, out>
+    dout = randn((br, n_tok, d), "bf16", 54, 0.1).to(gpu)
+    idx = torch.empty((n_tok, wl.n_tables), dtype=torch.int32, device=gpu)
+    p.engram_hash(toks, dl.comp_map, idx)
+    grads = B.Grads(br, d, wl.emb_dim, wl.conv_kernel, wl.n_tables, n_tok, wl.head_dim)
+    p.engram_backward(idx, dl.tables, h1, dl.weights, dout, dh1, grads, p.backward_workspace(wl.batch, wl.seqlen),
+                      wl.batch, wl.seqlen)
+    dg, db = torch.empty(d, device=gpu), torch.empty(d, device=gpu)
+    p.engram_layer_norm_backward(h0, dh1, f(gamma), mean, rstd, dh0, dg, db, p.layer_norm_backward_workspace(br * n_tok))
+    dtable = torch.empty((wl.vocab, d), device=gpu)
+    p.engram_embed_backward(toks, dh0, dtable, p.embed_backward_workspace(n_tok), scale=16.0)
+
+    ids = toks.flatten().cpu()
+    ref, _ = embed_ref(ids, table, 16.0, br)
+    assert torch.equal(h0.cpu(), ref)
+    rows = lambda t: t.cpu().reshape(br * n_tok, d)  # noqa: E731
+    ry, rm, rr = norm_ref(rows(h0), gamma, beta, 1e-5)
+    by, bm, brs = norm_bounds(rows(h0), gamma, beta, 1e-5, "bf16")
+    close(rows(h1), ry, by, "h1")
+    close(mean, rm, bm, "mean")
+    close(rstd, rr, brs, "rstd")
+    (rdx, bdx), (rdg, bdg), (rdb, bdb) = norm_grad_ref(rows(h0), rows(dh1), gamma, mean.cpu(), rstd.cpu())
+    close(rows(dh0), rdx, bdx + half_step("bf16") * (rdx.abs() + bdx), "dh0")
+    close(dg, rdg, bdg, "dgamma")
+    close(db, rdb, bdb, "dbeta")
+    rt, mag, terms = embed_grad_ref(ids, dh0.cpu(), wl.vocab, 16.0)
+    close(dtable, rt, (terms[:, None] + 2) * U * mag, "dtable")
+    vref, vmag = product_ref(a.cpu(), sa.view(torch.uint8).cpu(), 1, b.cpu(), sb.view(torch.uint8).cpu(), 128)
+    close(v8, vref, 2 * U * (wl.emb_dim + 2) * vmag + U * vref.abs(), "v8")
+    v = emb.cpu().double() @ dl.weights.w_v.cpu().double().t()
+    assert float((v8.cpu().double() - v).norm() / v.norm()) <= 2 * 2.0 ** -4  # both operands within 2^-4 of themselves
+    assert np.isfinite(out.float().cpu().numpy()).all()
+
+
+def _operators(gpu, seed):
+    """Every entry point once over its own buffers: (call(stream), outputs)."""
+    n_tok, d, vocab, br = 300, 512, 700, 2
+    p = make_plan("bf16", d, vocab, br)
+    f = lambda t: t.to(gpu)  # noqa: E731
+    ids, table = f(zipf_ids(n_tok, vocab, seed)), f(randn((vocab, d), "bf16", seed + 1))
+    gamma, w = f(1.0 + randn((d,), "f32", seed + 2, 0.1)), f(randn((640, d), "bf16", seed + 3))
+    bf = dict(dtype=torch.bfloat16, device=gpu)
+    h, y, dx = (torch.zeros((br, n_tok, d), **bf) for _ in range(3))
+    mean, rstd, dg, db = (torch.zeros(k, device=gpu) for k in (br * n_tok, br * n_tok, d, d))
+    dt = torch.zeros((vocab, d), device=gpu)
+    q, s = torch.zeros((n_tok, d), device=gpu).to(torch.float8_e4m3fn), torch.zeros(p.fp8_scale_shape(n_tok, d, 1), dtype=torch.uint8, device=gpu)
+    qw, sw = torch.zeros((640, d), device=gpu).to(torch.float8_e4m3fn), torch.zeros(p.fp8_scale_shape(640, d, 128), dtype=torch.uint8, device=gpu)
+    c = torch.zeros((n_tok, 640), device=gpu)
+    ws = [p.layer_norm_backward_workspace(br * n_tok), p.embed_backward_workspace(n_tok), p.matmul_fp8_workspace(n_tok, 640, d)]
+
+    def call(stream=None):
+        p.engram_embed(ids, table, h, scale=3.0, stream=stream)
+        p.engram_layer_norm(h, gamma, None, y, mean=mean, rstd=rstd, stream=stream)
+        p.engram_layer_norm_backward(h, y, gamma, mean, rstd, dx, dg, db, ws[0], stream=stream)
+        p.engram_embed_backward(ids, dx, dt, ws[1], stream=stream)
+        p.engram_quantize_fp8(y[0], q, s, stream=stream)
+        p.engram_quantize_fp8(w, qw, sw, block_rows=128, stream=stream)
+        p.engram_matmul_fp8(q, s, qw, sw, c, ws[2], stream=stream)
+    return call, [h, y, mean, rstd, dx, dg, db, dt, q.view(torch.uint8), s, qw.view(torch.uint8), sw, c], ids
+
+
+def test_captured_graphs_replay_the_eager_results(gpu):
+    """Two graphs with workspaces of their own, replayed several times and at once
+    on two streams, with eager work in between and inputs changed."""
+    sets = [_operators(gpu, s) for s in (60, 70)]
+    eager = []
+    for call, outs, _ in sets:
+        call()
+        torch.cuda.synchronize()
+        eager.append([o.clone() for o in outs])
+    graphs = []
+    for call, outs, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for turn in range(4):
+        for _, outs, _ in sets:
+            for o in outs:
+                o.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, outs, _), want in zip(sets, eager):
+            for o, e in zip(outs, want):
+                assert torch.equal(o, e), turn
+        sets[0][0]()  # eager work between the replays
+    # new ids in the same buffer: the replay and an eager call agree
+    sets[0][2].copy_(zipf_ids(300, 700, 99).to(gpu))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    replayed = [o.clone() for o in sets[0][1]]
+    sets[0][0]()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(replayed, sets[0][1]))
+    assert not torch.equal(replayed[0], eager[0][0])
+
+
+def test_side_stream(gpu):
+    """On a stream of the caller's, behind work of that stream, without touching the current one."""
+    call, outs, ids = _operators(gpu, 80)
+    call()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    keep = ids.clone()
+    ids.fill_(0)
+    for o in outs:
+        o.zero_()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        big = torch.zeros(1 << 28, device=gpu)  # work the calls have to wait behind
+        big += 1
+        ids.copy_(keep)
+    call(st)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_profiling_counts_the_operators(gpu):
+    call, _, _ = _operators(gpu, 90)
+    p = make_plan("bf16", 512, 700, 2)
+    x = torch.zeros((4, 512), dtype=torch.bfloat16, device=gpu)
+    g = torch.ones(512, device=gpu)
+    p.engram_profile_begin(16, ["aux"])
+    p.engram_layer_norm(x, g, None, x)
+    r = p.engram_profile_end()
+    assert r["aux"]["launches"] == 1 and r["aux"]["total_ms"] > 0
