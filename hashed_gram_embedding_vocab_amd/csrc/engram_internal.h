@@ -423,6 +423,10 @@ struct ProductArgs {
     int64_t M, N, K;
     int32_t a_block_rows, b_block_rows;     // 1 or 128
     bool out_bf16;
+    // set by launch_product: launch z of `splits` takes blocks
+    // [z split_blocks, (z + 1) split_blocks) and stores at ws + z split_elems
+    int32_t splits, split_blocks;
+    int64_t split_elems;
 };
 size_t product_workspace(int64_t M, int64_t N, int64_t K);
 bool product_fits(int64_t M, int64_t N, int64_t K);

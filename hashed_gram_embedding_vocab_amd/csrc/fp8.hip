@@ -21,6 +21,7 @@
 // takes the bf16 matrix instructions, whose sums are fp32 throughout (1e-8
 // measured), at half the matrix rate.
 #include <algorithm>
+#include <type_traits>
 
 #include "engram_internal.h"
 #include "vec8.h"
@@ -261,18 +262,20 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // K-contiguous: lane l holds row l % 16 and 32 of the block's 128 bytes, and
 // result lane l holds C[m = l % 16][n = 4 (l / 16) .. + 3].  Which 32 bytes a
 // lane group takes does not matter as long as both sides agree (the sum runs
-// over the whole block): pieces (l / 16) and (l / 16) + 4 of 16 bytes.
+// over the whole block): pieces (l / 16) and (l / 16) + 4 of 16 bytes, i.e.
+// one piece of each half of 64 bytes.
+//
+// A workgroup makes BN x BM outputs with WN x WM waves, each FN x FM fragments
+// of 16 x 16.  Both operands go from global memory straight into LDS, one
+// block of 128 along K a stage, two stages: while one is multiplied the other
+// fills.  A stage is [half][row block of 16][1 KB]; inside the 1 KB the four
+// pieces of a row are XOR-swizzled so that fragment reads take distinct banks.
+// Rows past the matrix and pieces past K read as zeros (the buffer's bounds).
+typedef __attribute__((address_space(3))) void lds_void_t;
+
 struct Frag {
     u32x4_t half[2];
 };
-
-__device__ __forceinline__ Frag load_frag(const uint8_t *row, int64_t k, int64_t K, int lane) {
-    Frag f = {};
-    const int64_t p = k + 16 * (lane >> 4);
-    if (p < K) f.half[0] = *reinterpret_cast<const u32x4_t *>(row + p);
-    if (p + 64 < K) f.half[1] = *reinterpret_cast<const u32x4_t *>(row + p + 64);
-    return f;
-}
 
 __device__ __forceinline__ i32x8_t e4m3x32(const Frag &f) {
     const u32x4_t &a = f.half[0], &b = f.half[1];
@@ -289,72 +292,310 @@ __device__ __forceinline__ bf16x8_t to_bf16x8(uint32_t w0, uint32_t w1, uint32_t
     return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// 128 x 128 outputs per workgroup, 64 x 64 per wave, operands from global memory.
-template <bool F32>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs g) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * 128 + 64 * (w & 1), m0 = (int64_t)blockIdx.y * 128 + 64 * (w >> 1);
-    const int64_t kb = (g.K + 127) / 128, pitch = (kb + 3) / 4 * 4;
-    const uint8_t *ar[4], *br[4], *as[4], *bs[4];
+__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0,
+                                             (int)min(bytes, (int64_t)0x7FFFFFFF), 0x00020000);
+}
+
+// This wave's loads have landed and its LDS reads are done, then the
+// workgroup's barrier: every wave's are.
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x7 << 4);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+constexpr int kXcds = 8;
+constexpr uint32_t kPast = 0x80000000u;  // an offset behind every buffer
+
+template <bool F32, int BN, int BM, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g) {
+// (The host pass only needs the launch stub, and drops it where it cannot
+// check a device builtin's template-dependent arguments.)
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int W = WN * WM, FN = BN / 16 / WN, FM = BM / 16 / WM;
+    constexpr int kBlocks = (BN + BM) / 16, kHalfBytes = kBlocks * 1024;
+    constexpr int kBPerWave = BN / 16 / W, kAPerWave = (BM / 16 + W - 1) / W;
+    static_assert(BN / 16 % W == 0, "every wave loads as many row blocks of b");
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kHalfBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kHalfBytes];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // consecutive workgroups go to the XCDs in turn: give each XCD a
+    // contiguous range of tiles, all n tiles of kGroup m tiles before the next
+    const int64_t tiles_n = (g.N + BN - 1) / BN, tiles_m = (g.M + BM - 1) / BM;
+    const uint32_t tiles = (uint32_t)(tiles_n * tiles_m);
+    const uint32_t xq = tiles / kXcds, xr = tiles % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const uint32_t logical = x < xr ? x * (xq + 1) + slot : xr * (xq + 1) + (x - xr) * xq + slot;
+    constexpr uint32_t kGroup = 4;
+    const uint32_t grp = logical / (kGroup * (uint32_t)tiles_n), in = logical - grp * (kGroup * (uint32_t)tiles_n);
+    const uint32_t gm = min(kGroup, (uint32_t)tiles_m - grp * kGroup);
+    const int64_t n0 = (int64_t)(in / gm) * BN, m0 = (int64_t)(grp * kGroup + in % gm) * BM;
+
+    const int64_t K = g.K;
+    const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
+    const int kb_first = (int)blockIdx.y * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
+
+    const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)BN, g.N - n0) * K);
+    const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)BM, g.M - m0) * K);
+    const int lr = lane >> 2, lchunk = (lane & 3) ^ swz(lr);
+    uint32_t boff[kBPerWave], aoff[kAPerWave];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = min(m0 + 16 * i + (lane & 15), g.M - 1), n = min(n0 + 16 * i + (lane & 15), g.N - 1);
-        ar[i] = g.a + m * g.K;
-        br[i] = g.b + n * g.K;
-        as[i] = g.a_scales + m / g.a_block_rows * pitch;
-        bs[i] = g.b_scales + n / g.b_block_rows * pitch;
-    }
-    f32x4_t acc[4][4] = {};
-    for (int64_t k = 0; k < kb; ++k) {
-        Frag fa[4], fb[4];
-        uint32_t sa[4], sb[4];
+    for (int i = 0; i < kBPerWave; ++i) boff[i] = (uint32_t)((wave + W * i) * 16 + lr) * (uint32_t)K + lchunk * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fa[i] = load_frag(ar[i], 128 * k, g.K, lane);
-            fb[i] = load_frag(br[i], 128 * k, g.K, lane);
-            sa[i] = as[i][k];
-            sb[i] = bs[i][k];
+    for (int i = 0; i < kAPerWave; ++i) aoff[i] = (uint32_t)((wave + W * i) * 16 + lr) * (uint32_t)K + lchunk * 16;
+
+    auto issue = [&](uint8_t *st, int kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = kb * 128 + h * 64;
+            const bool in_k = k + lchunk * 16 < (int)K;
+#pragma unroll
+            for (int i = 0; i < kBPerWave; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void_t *)(st + h * kHalfBytes + (wave + W * i) * 1024),
+                                                         16, in_k ? boff[i] : kPast, k, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kAPerWave; ++i)
+                if (BM / 16 % W == 0 || wave + W * i < BM / 16)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        ares, (lds_void_t *)(st + h * kHalfBytes + (BN / 16 + wave + W * i) * 1024), 16,
+                        in_k ? aoff[i] : kPast, k, 0, 0);
         }
+    };
+
+    // scale bytes of two blocks (kb even) for this lane's rows
+    const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
+    const int64_t brows = (g.N + g.b_block_rows - 1) / g.b_block_rows, arows = (g.M + g.a_block_rows - 1) / g.a_block_rows;
+    const int64_t bs0 = n0 / g.b_block_rows, as0 = m0 / g.a_block_rows;
+    const __amdgpu_buffer_rsrc_t bsres = make_rsrc(g.b_scales + bs0 * pitch, (brows - bs0) * pitch);
+    const __amdgpu_buffer_rsrc_t asres = make_rsrc(g.a_scales + as0 * pitch, (arows - as0) * pitch);
+    uint32_t bsoff[FN], asoff[FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const int r = (wn + i) * 16 + (lane & 15);
+        bsoff[i] = (uint32_t)((g.b_block_rows == 1 ? r : r / 128) * pitch);
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int r = (wm + j) * 16 + (lane & 15);
+        asoff[j] = (uint32_t)((g.a_block_rows == 1 ? r : r / 128) * pitch);
+    }
+    uint32_t sb[FN], sa[FM];
+    auto load_scales = [&](int kb, uint32_t (&b2)[FN], uint32_t (&a2)[FM]) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) b2[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bsres, bsoff[i], kb, 0);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) a2[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(asres, asoff[j], kb, 0);
+    };
+
+    f32x4_t acc[FN][FM] = {};
+    const int fr = lane & 15;
+    const int fpos = fr * 64 + ((lane >> 4) ^ swz(fr)) * 16;
+    auto read_frag = [&](const uint8_t *st, int blk) {
+        Frag f;
+        f.half[0] = *reinterpret_cast<const u32x4_t *>(st + blk * 1024 + fpos);
+        f.half[1] = *reinterpret_cast<const u32x4_t *>(st + kHalfBytes + blk * 1024 + fpos);
+        return f;
+    };
+    auto compute = [&](const uint8_t *st, auto opc) {
+        constexpr int OP = decltype(opc)::value;  // which byte of sb and sa
         if constexpr (F32) {
+            // half a block at a time: its expanded a side is 8 FM registers
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8_t ha[4], hb[4];
+            for (int h = 0; h < 2; ++h) {
+                bf16x8_t ha[FM][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = q >> 1, o = 2 * (q & 1);
-                    ha[i] = to_bf16x8(fa[i].half[h][o], fa[i].half[h][o + 1], sa[i]);
-                    hb[i] = to_bf16x8(fb[i].half[h][o], fb[i].half[h][o + 1], sb[i]);
+                for (int j = 0; j < FM; ++j) {
+                    const u32x4_t w =
+                        *reinterpret_cast<const u32x4_t *>(st + h * kHalfBytes + (BN / 16 + wm + j) * 1024 + fpos);
+                    const uint32_t s = (sa[j] >> (8 * OP)) & 0xFFu;
+                    ha[j][0] = to_bf16x8(w[0], w[1], s);
+                    ha[j][1] = to_bf16x8(w[2], w[3], s);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < FN; ++i) {
+                    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(st + h * kHalfBytes + (wn + i) * 1024 + fpos);
+                    const uint32_t s = (sb[i] >> (8 * OP)) & 0xFFu;
+                    const bf16x8_t hb[2] = {to_bf16x8(w[0], w[1], s), to_bf16x8(w[2], w[3], s)};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hb[i], ha[j], acc[i][j], 0, 0, 0);
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int j = 0; j < FM; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hb[q], ha[j][q], acc[i][j], 0, 0, 0);
+                }
             }
         } else {
+            Frag fa[FM];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < FM; ++j) fa[j] = read_frag(st, BN / 16 + wm + j);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+            for (int i = 0; i < FN; ++i) {
+                const Frag fb = read_frag(st, wn + i);
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        e4m3x32(fb[i]), e4m3x32(fa[j]), acc[i][j], 0, 0, 0, (int)sb[i], 0, (int)sa[j]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + 16 * j + (lane & 15);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t n = n0 + 16 * i + 4 * (lane >> 4) + r;
-                if (m >= g.M || n >= g.N) continue;
-                if constexpr (F32)
-                    static_cast<float *>(g.c)[m * g.N + n] = acc[i][j][r];
-                else
-                    static_cast<__bf16 *>(g.c)[m * g.N + n] = (__bf16)acc[i][j][r];
+                        e4m3x32(fb), e4m3x32(fa[j]), acc[i][j], 0, 0, OP, (int)sb[i], OP, (int)sa[j]);
             }
         }
+    };
+
+    // Block kb sits in stage kb % 2 (kb_first is even).  Each step: its loads
+    // have landed everywhere and the other stage is free, fill that one with
+    // the next block, multiply.  (The last fills may lie past K: zeros.)
+    load_scales(kb_first, sb, sa);
+    issue(st0, kb_first);
+    int kb = kb_first;
+    for (; kb + 2 <= kb_last; kb += 2) {
+        uint32_t sb_next[FN], sa_next[FM];
+        stage_barrier();
+        issue(st1, kb + 1);
+        compute(st0, std::integral_constant<int, 0>{});
+        stage_barrier();
+        load_scales(kb + 2, sb_next, sa_next);
+        issue(st0, kb + 2);
+        compute(st1, std::integral_constant<int, 1>{});
+#pragma unroll
+        for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) sa[j] = sa_next[j];
+    }
+    stage_barrier();
+    if (kb < kb_last) {
+        compute(st0, std::integral_constant<int, 0>{});
+        stage_barrier();
+    }
+
+    if (g.splits > 1 || F32) {
+        // fp32: a lane's four n of one m, 16 bytes
+        float *c = g.splits > 1 ? static_cast<float *>(g.ws) + (int64_t)blockIdx.y * g.split_elems : static_cast<float *>(g.c);
+        const bool vec = g.N % 4 == 0;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int64_t m = m0 + (wm + j) * 16 + (lane & 15);
+            if (m >= g.M) continue;
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int64_t n = n0 + (wn + i) * 16 + 4 * (lane >> 4);
+                float *dst = c + m * g.N + n;
+                if (vec) {
+                    if (n < g.N) *reinterpret_cast<f32x4_t *>(dst) = acc[i][j];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (n + r < g.N) dst[r] = acc[i][j][r];
+                }
+            }
+        }
+        return;
+    }
+    // bf16: the wave's FM x 16 rows of FN x 16 values pass through LDS (the
+    // stages are free), so that a store instruction writes whole rows of
+    // 32 FN bytes instead of 32-byte pieces of 16 rows; the pieces of a row
+    // are XOR-swizzled by the row
+    constexpr int kRow = FN * 32, kPieces = FN * 2;
+    static_assert(W / 2 * FM * 16 * kRow <= 2 * kHalfBytes, "half of the waves' tiles in each stage");
+    uint8_t *img = (wave < W / 2 ? st0 : st1) + (wave % (W / 2)) * FM * 16 * kRow;
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int piece = 2 * i + (lane >> 5);
+            *reinterpret_cast<u32x2_t *>(img + (j * 16 + fr) * kRow + ((piece ^ fr) & (kPieces - 1)) * 16 +
+                                         ((lane >> 4) & 1) * 8) =
+                u32x2_t{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        }
+    asm volatile("" ::: "memory");  // (a wave reads what it wrote itself; LDS keeps a wave's order)
+    uint16_t *c = static_cast<uint16_t *>(g.c);
+    const bool vec = g.N % 8 == 0;
+    constexpr int kRowsPer = 64 / kPieces;  // rows of one store instruction
+#pragma unroll 4
+    for (int r0 = 0; r0 < FM * 16; r0 += kRowsPer) {
+        const int r = r0 + lane / kPieces, piece = lane % kPieces;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(img + r * kRow + ((piece ^ r) & (kPieces - 1)) * 16);
+        const int64_t m = m0 + wm * 16 + r, n = n0 + wn * 16 + piece * 8;
+        if (m >= g.M) continue;
+        uint16_t *dst = c + m * g.N + n;
+        if (vec) {
+            if (n < g.N) *reinterpret_cast<u32x4_t *>(dst) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < g.N) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+#endif
+}
+
+// C = the splits' sums in order, rounded to the result's type.
+__global__ __launch_bounds__(256) void product_join_kernel(const float *parts, int32_t splits, int64_t split_elems,
+                                                           int64_t n, void *c, bool out_bf16) {
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+        f32x4_t s = *reinterpret_cast<const f32x4_t *>(parts + i);
+        for (int32_t z = 1; z < splits; ++z) s += *reinterpret_cast<const f32x4_t *>(parts + z * split_elems + i);
+        if (i + 4 <= n) {
+            if (out_bf16)
+                *reinterpret_cast<u32x2_t *>(static_cast<uint16_t *>(c) + i) =
+                    u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+            else
+                *reinterpret_cast<f32x4_t *>(static_cast<float *>(c) + i) = s;
+        } else {
+            for (int r = 0; i + r < n; ++r) {
+                if (out_bf16)
+                    static_cast<__bf16 *>(c)[i + r] = (__bf16)s[r];
+                else
+                    static_cast<float *>(c)[i + r] = s[r];
+            }
+        }
+    }
+}
+
+// How a product is cut: 256 x 256 tiles where they fill the chip, else 128 x
+// 128 (64 or 16 rows of a where it has no more), and the blocks of K in
+// `splits` parts, each of at least four blocks, until there are about two
+// workgroups a CU.
+struct ProductCut {
+    bool wide;
+    int bm;
+    int32_t splits, split_blocks;
+};
+
+ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
+    ProductCut c{};
+    auto tiles = [&](int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
+    c.wide = tiles(256, 256) >= 256;
+    c.bm = c.wide ? 256 : M > 64 ? 128 : M > 16 ? 64 : 16;
+    const int64_t t = tiles(c.wide ? 256 : 128, c.bm), kb = (K + 127) / 128;
+    int64_t s = c.wide ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(t, 1), kb / 4));
+    int64_t per = (kb + s - 1) / s;
+    per += per & 1;  // scales are read two blocks at a time
+    c.splits = (int32_t)((kb + per - 1) / per);
+    c.split_blocks = (int32_t)per;
+    return c;
+}
+
+int64_t split_elems_of(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
+
+template <bool F32, int BN, int BM, int WN, int WM>
+void product(const ProductArgs &g, hipStream_t s) {
+    const int64_t tiles = ((g.N + BN - 1) / BN) * ((g.M + BM - 1) / BM);
+    launch_kernel((product_kernel<F32, BN, BM, WN, WM>), dim3((unsigned)tiles, (unsigned)g.splits), dim3(64 * WN * WM), s,
+                  g);
+}
+
+template <bool F32>
+void product_of(const ProductCut &c, const ProductArgs &g, hipStream_t s) {
+    if (c.wide)
+        product<F32, 256, 256, 2, 4>(g, s);
+    else if (c.bm == 128)
+        product<F32, 128, 128, 2, 2>(g, s);
+    else if (c.bm == 64)
+        product<F32, 128, 64, 4, 1>(g, s);
+    else
+        product<F32, 128, 16, 4, 1>(g, s);
 }
 
 }  // namespace
@@ -375,18 +616,31 @@ void launch_quantize(engram_dtype dt, const QuantArgs &a, hipStream_t s) {
     }
 }
 
-size_t product_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t product_workspace(int64_t M, int64_t N, int64_t K) {
+    const ProductCut c = cut_of(M, N, K);
+    return c.splits > 1 ? (size_t)c.splits * (size_t)split_elems_of(M, N) * 4 : 0;
+}
 
 bool product_fits(int64_t M, int64_t N, int64_t) {
-    return (M + 127) / 128 <= 65535 && (N + 127) / 128 < ((int64_t)1 << 24);
+    // one launch: fewer than 2^32 threads
+    return ((N + 127) / 128) * ((M + 15) / 16) < ((int64_t)1 << 24);
 }
 
 void launch_product(const ProductArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)((a.M + 127) / 128));
+    const ProductCut c = cut_of(a.M, a.N, a.K);
+    ProductArgs g = a;
+    g.splits = c.splits;
+    g.split_blocks = c.split_blocks;
+    g.split_elems = split_elems_of(a.M, a.N);
     if (a.out_bf16)
-        launch_kernel(product_kernel<false>, grid, dim3(256), s, a);
+        product_of<false>(c, g, s);
     else
-        launch_kernel(product_kernel<true>, grid, dim3(256), s, a);
+        product_of<true>(c, g, s);
+    if (c.splits > 1) {
+        const int64_t n = a.M * a.N;
+        launch_kernel(product_join_kernel, dim3((unsigned)std::min<int64_t>((n + 1023) / 1024, (int64_t)1 << 22)), dim3(256),
+                      s, static_cast<const float *>(a.ws), c.splits, g.split_elems, n, a.c, a.out_bf16);
+    }
 }
 
 }  // namespace engram
