@@ -262,14 +262,15 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // K-contiguous: lane l holds row l % 16 and 32 of the block's 128 bytes, and
 // result lane l holds C[m = l % 16][n = 4 (l / 16) .. + 3].  Which 32 bytes a
 // lane group takes does not matter as long as both sides agree (the sum runs
-// over the whole block): pieces (l / 16) and (l / 16) + 4 of 16 bytes, i.e.
-// one piece of each half of 64 bytes.
+// over the whole block): pieces (l / 16) and (l / 16) + 4 of 16 bytes.
 //
 // A workgroup makes BN x BM outputs with WN x WM waves, each FN x FM fragments
 // of 16 x 16.  Both operands go from global memory straight into LDS, one
 // block of 128 along K a stage, two stages: while one is multiplied the other
-// fills.  A stage is [half][row block of 16][1 KB]; inside the 1 KB the four
-// pieces of a row are XOR-swizzled so that fragment reads take distinct banks.
+// fills.  A load instruction takes 8 rows x 128 bytes, whole cache lines (16 rows
+// x 64 bytes took 1.63 us a stage of 256 + 256 rows without the products, whole
+// lines 1.32).  A stage is its rows, b's first, 128 bytes each, the eight pieces
+// of a row XOR-swizzled by the row so that fragment reads take distinct banks.
 // Rows past the matrix and pieces past K read as zeros (the buffer's bounds).
 typedef __attribute__((address_space(3))) void lds_void_t;
 
@@ -292,8 +293,6 @@ __device__ __forceinline__ bf16x8_t to_bf16x8(uint32_t w0, uint32_t w1, uint32_t
     return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ int swz(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
-
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0,
                                              (int)min(bytes, (int64_t)0x7FFFFFFF), 0x00020000);
@@ -311,30 +310,77 @@ __device__ __forceinline__ void stage_barrier() {
 constexpr int kXcds = 8;
 constexpr uint32_t kPast = 0x80000000u;  // an offset behind every buffer
 
+// First row of b and of a of this workgroup's tile.  Consecutive workgroups go
+// to the XCDs in turn: each XCD gets a contiguous range of tiles, all n tiles
+// of kGroup m tiles before the next.
+template <int BN, int BM>
+__device__ __forceinline__ void tile_origin(const ProductArgs &g, int64_t &n0, int64_t &m0) {
+    constexpr uint32_t kGroup = 4;
+    const uint32_t tiles_n = (uint32_t)((g.N + BN - 1) / BN), tiles_m = (uint32_t)((g.M + BM - 1) / BM);
+    const uint32_t tiles = tiles_n * tiles_m;
+    const uint32_t xq = tiles / kXcds, xr = tiles % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const uint32_t logical = x < xr ? x * (xq + 1) + slot : xr * (xq + 1) + (x - xr) * xq + slot;
+    const uint32_t grp = logical / (kGroup * tiles_n), in = logical - grp * (kGroup * tiles_n);
+    const uint32_t gm = min(kGroup, tiles_m - grp * kGroup);
+    n0 = (int64_t)(in / gm) * BN;
+    m0 = (int64_t)(grp * kGroup + in % gm) * BM;
+}
+
+// A wave's FM x 16 rows (from m0) of FN x 16 values (from n0) as bf16.  They
+// pass through LDS (`img`, FM * 16 * FN * 32 bytes of the wave's own), so that a
+// store instruction writes whole rows of 32 FN bytes instead of 32-byte pieces
+// of 16 rows; the pieces of a row are XOR-swizzled by the row.
+template <int FN, int FM>
+__device__ __forceinline__ void store_bf16(const ProductArgs &g, const f32x4_t (&acc)[FN][FM], uint8_t *img, int64_t m0,
+                                           int64_t n0, int lane) {
+    constexpr int kRow = FN * 32, kPieces = FN * 2;
+    const int fr = lane & 15;
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int piece = 2 * i + (lane >> 5);
+            *reinterpret_cast<u32x2_t *>(img + (j * 16 + fr) * kRow + ((piece ^ fr) & (kPieces - 1)) * 16 +
+                                         ((lane >> 4) & 1) * 8) =
+                u32x2_t{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        }
+    asm volatile("" ::: "memory");  // (a wave reads what it wrote itself; LDS keeps a wave's order)
+    uint16_t *c = static_cast<uint16_t *>(g.c);
+    const bool vec = g.N % 8 == 0;
+    constexpr int kRowsPer = 64 / kPieces;  // rows of one store instruction
+#pragma unroll 4
+    for (int r0 = 0; r0 < FM * 16; r0 += kRowsPer) {
+        const int r = r0 + lane / kPieces, piece = lane % kPieces;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(img + r * kRow + ((piece ^ r) & (kPieces - 1)) * 16);
+        const int64_t m = m0 + r, n = n0 + piece * 8;
+        if (m >= g.M) continue;
+        uint16_t *dst = c + m * g.N + n;
+        if (vec) {
+            if (n < g.N) *reinterpret_cast<u32x4_t *>(dst) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < g.N) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
 template <bool F32, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g) {
 // (The host pass only needs the launch stub, and drops it where it cannot
 // check a device builtin's template-dependent arguments.)
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int W = WN * WM, FN = BN / 16 / WN, FM = BM / 16 / WM;
-    constexpr int kBlocks = (BN + BM) / 16, kHalfBytes = kBlocks * 1024;
-    constexpr int kBPerWave = BN / 16 / W, kAPerWave = (BM / 16 + W - 1) / W;
-    static_assert(BN / 16 % W == 0, "every wave loads as many row blocks of b");
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kHalfBytes];
-    __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kHalfBytes];
+    constexpr int kStage = (BN + BM) * 128;
+    constexpr int kBPerWave = BN / 8 / W, kAPerWave = (BM / 8 + W - 1) / W;
+    static_assert(BN / 8 % W == 0, "every wave loads as many row blocks of b");
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // consecutive workgroups go to the XCDs in turn: give each XCD a
-    // contiguous range of tiles, all n tiles of kGroup m tiles before the next
-    const int64_t tiles_n = (g.N + BN - 1) / BN, tiles_m = (g.M + BM - 1) / BM;
-    const uint32_t tiles = (uint32_t)(tiles_n * tiles_m);
-    const uint32_t xq = tiles / kXcds, xr = tiles % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    const uint32_t logical = x < xr ? x * (xq + 1) + slot : xr * (xq + 1) + (x - xr) * xq + slot;
-    constexpr uint32_t kGroup = 4;
-    const uint32_t grp = logical / (kGroup * (uint32_t)tiles_n), in = logical - grp * (kGroup * (uint32_t)tiles_n);
-    const uint32_t gm = min(kGroup, (uint32_t)tiles_m - grp * kGroup);
-    const int64_t n0 = (int64_t)(in / gm) * BN, m0 = (int64_t)(grp * kGroup + in % gm) * BM;
+    int64_t n0, m0;
+    tile_origin<BN, BM>(g, n0, m0);
 
     const int64_t K = g.K;
     const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
@@ -342,29 +388,31 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
 
     const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)BN, g.N - n0) * K);
     const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)BM, g.M - m0) * K);
-    const int lr = lane >> 2, lchunk = (lane & 3) ^ swz(lr);
+    // lane l of a load fills row l / 8 of its 8-row block, place l % 8; piece c
+    // of row r sits at place c ^ (r / 2 % 8): 16 consecutive rows of 128 bytes
+    // take the 64 banks once (a wave's blocks are all even or all odd)
+    static_assert(W % 2 == 0, "one swizzle for all blocks of a wave");
+    const int lr = lane >> 3, lpiece = (lane & 7) ^ (((wave & 1) * 8 + lr) >> 1);
     uint32_t boff[kBPerWave], aoff[kAPerWave];
 #pragma unroll
-    for (int i = 0; i < kBPerWave; ++i) boff[i] = (uint32_t)((wave + W * i) * 16 + lr) * (uint32_t)K + lchunk * 16;
+    for (int i = 0; i < kBPerWave; ++i) boff[i] = (uint32_t)((wave + W * i) * 8 + lr) * (uint32_t)K + lpiece * 16;
 #pragma unroll
-    for (int i = 0; i < kAPerWave; ++i) aoff[i] = (uint32_t)((wave + W * i) * 16 + lr) * (uint32_t)K + lchunk * 16;
+    for (int i = 0; i < kAPerWave; ++i) aoff[i] = (uint32_t)((wave + W * i) * 8 + lr) * (uint32_t)K + lpiece * 16;
 
     auto issue = [&](uint8_t *st, int kb) {
+        const int k = kb * 128;
+        const bool in_k = k + lpiece * 16 < (int)K;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = kb * 128 + h * 64;
-            const bool in_k = k + lchunk * 16 < (int)K;
+        for (int i = 0; i < kBPerWave; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
+                                                     in_k ? boff[i] : kPast, k, 0, 0);
 #pragma unroll
-            for (int i = 0; i < kBPerWave; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void_t *)(st + h * kHalfBytes + (wave + W * i) * 1024),
-                                                         16, in_k ? boff[i] : kPast, k, 0, 0);
-#pragma unroll
-            for (int i = 0; i < kAPerWave; ++i)
-                if (BM / 16 % W == 0 || wave + W * i < BM / 16)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        ares, (lds_void_t *)(st + h * kHalfBytes + (BN / 16 + wave + W * i) * 1024), 16,
-                        in_k ? aoff[i] : kPast, k, 0, 0);
-        }
+        for (int i = 0; i < kAPerWave; ++i)
+            if (BM / 8 % W == 0 || wave + W * i < BM / 8)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t *)(st + (BN / 8 + wave + W * i) * 1024), 16,
+                                                         in_k ? aoff[i] : kPast, k, 0, 0);
+        // (the scheduler would put the fills off until they are waited for)
+        __builtin_amdgcn_sched_barrier(0);
     };
 
     // scale bytes of two blocks (kb even) for this lane's rows
@@ -373,32 +421,32 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
     const int64_t bs0 = n0 / g.b_block_rows, as0 = m0 / g.a_block_rows;
     const __amdgpu_buffer_rsrc_t bsres = make_rsrc(g.b_scales + bs0 * pitch, (brows - bs0) * pitch);
     const __amdgpu_buffer_rsrc_t asres = make_rsrc(g.a_scales + as0 * pitch, (arows - as0) * pitch);
-    uint32_t bsoff[FN], asoff[FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-        const int r = (wn + i) * 16 + (lane & 15);
-        bsoff[i] = (uint32_t)((g.b_block_rows == 1 ? r : r / 128) * pitch);
-    }
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-        const int r = (wm + j) * 16 + (lane & 15);
-        asoff[j] = (uint32_t)((g.a_block_rows == 1 ? r : r / 128) * pitch);
-    }
+    // (a wave's rows of one side lie in one block of 128, so they share a scale row there)
+    const uint32_t bsoff = (uint32_t)((g.b_block_rows == 1 ? wn * 16 + (lane & 15) : wn / 8) * pitch);
+    const uint32_t asoff = (uint32_t)((g.a_block_rows == 1 ? wm * 16 + (lane & 15) : wm / 8) * pitch);
+    const int bstep = g.b_block_rows == 1 ? 16 * pitch : 0, astep = g.a_block_rows == 1 ? 16 * pitch : 0;
+    static_assert(FN <= 8 && 8 % FN == 0 && FM <= 8 && 8 % FM == 0, "a wave's rows inside one block of 128");
     uint32_t sb[FN], sa[FM];
     auto load_scales = [&](int kb, uint32_t (&b2)[FN], uint32_t (&a2)[FM]) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) b2[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bsres, bsoff[i], kb, 0);
+        for (int i = 0; i < FN; ++i)
+            b2[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bsres, bsoff, i * bstep + kb, 0);
 #pragma unroll
-        for (int j = 0; j < FM; ++j) a2[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(asres, asoff[j], kb, 0);
+        for (int j = 0; j < FM; ++j)
+            a2[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(asres, asoff, j * astep + kb, 0);
     };
 
     f32x4_t acc[FN][FM] = {};
     const int fr = lane & 15;
-    const int fpos = fr * 64 + ((lane >> 4) ^ swz(fr)) * 16;
+    // this lane's two pieces of a fragment: rows blk * 16 + fr
+    const int fp0 = fr * 128 + ((lane >> 4) ^ (fr >> 1)) * 16, fp1 = fr * 128 + (((lane >> 4) + 4) ^ (fr >> 1)) * 16;
+    auto read_half = [&](const uint8_t *st, int blk, int h) {
+        return *reinterpret_cast<const u32x4_t *>(st + blk * 2048 + (h == 0 ? fp0 : fp1));
+    };
     auto read_frag = [&](const uint8_t *st, int blk) {
         Frag f;
-        f.half[0] = *reinterpret_cast<const u32x4_t *>(st + blk * 1024 + fpos);
-        f.half[1] = *reinterpret_cast<const u32x4_t *>(st + kHalfBytes + blk * 1024 + fpos);
+        f.half[0] = read_half(st, blk, 0);
+        f.half[1] = read_half(st, blk, 1);
         return f;
     };
     auto compute = [&](const uint8_t *st, auto opc) {
@@ -410,15 +458,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
                 bf16x8_t ha[FM][2];
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    const u32x4_t w =
-                        *reinterpret_cast<const u32x4_t *>(st + h * kHalfBytes + (BN / 16 + wm + j) * 1024 + fpos);
+                    const u32x4_t w = read_half(st, BN / 16 + wm + j, h);
                     const uint32_t s = (sa[j] >> (8 * OP)) & 0xFFu;
                     ha[j][0] = to_bf16x8(w[0], w[1], s);
                     ha[j][1] = to_bf16x8(w[2], w[3], s);
                 }
 #pragma unroll
                 for (int i = 0; i < FN; ++i) {
-                    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(st + h * kHalfBytes + (wn + i) * 1024 + fpos);
+                    const u32x4_t w = read_half(st, wn + i, h);
                     const uint32_t s = (sb[i] >> (8 * OP)) & 0xFFu;
                     const bf16x8_t hb[2] = {to_bf16x8(w[0], w[1], s), to_bf16x8(w[2], w[3], s)};
 #pragma unroll
@@ -449,25 +496,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
     load_scales(kb_first, sb, sa);
     issue(st0, kb_first);
     int kb = kb_first;
-    for (; kb + 2 <= kb_last; kb += 2) {
-        uint32_t sb_next[FN], sa_next[FM];
+    for (;;) {
         stage_barrier();
         issue(st1, kb + 1);
         compute(st0, std::integral_constant<int, 0>{});
+        if (++kb == kb_last) break;
+        uint32_t sb_next[FN], sa_next[FM];
         stage_barrier();
-        load_scales(kb + 2, sb_next, sa_next);
-        issue(st0, kb + 2);
+        load_scales(kb + 1, sb_next, sa_next);
+        issue(st0, kb + 1);
         compute(st1, std::integral_constant<int, 1>{});
+        if (++kb == kb_last) break;
 #pragma unroll
         for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
 #pragma unroll
         for (int j = 0; j < FM; ++j) sa[j] = sa_next[j];
     }
-    stage_barrier();
-    if (kb < kb_last) {
-        compute(st0, std::integral_constant<int, 0>{});
-        stage_barrier();
-    }
+    stage_barrier();  // the last fills have landed and every read is done: the stages are free
 
     if (g.splits > 1 || F32) {
         // fp32: a lane's four n of one m, 16 bytes
@@ -492,41 +537,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         }
         return;
     }
-    // bf16: the wave's FM x 16 rows of FN x 16 values pass through LDS (the
-    // stages are free), so that a store instruction writes whole rows of
-    // 32 FN bytes instead of 32-byte pieces of 16 rows; the pieces of a row
-    // are XOR-swizzled by the row
-    constexpr int kRow = FN * 32, kPieces = FN * 2;
-    static_assert(W / 2 * FM * 16 * kRow <= 2 * kHalfBytes, "half of the waves' tiles in each stage");
-    uint8_t *img = (wave < W / 2 ? st0 : st1) + (wave % (W / 2)) * FM * 16 * kRow;
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const int piece = 2 * i + (lane >> 5);
-            *reinterpret_cast<u32x2_t *>(img + (j * 16 + fr) * kRow + ((piece ^ fr) & (kPieces - 1)) * 16 +
-                                         ((lane >> 4) & 1) * 8) =
-                u32x2_t{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-        }
-    asm volatile("" ::: "memory");  // (a wave reads what it wrote itself; LDS keeps a wave's order)
-    uint16_t *c = static_cast<uint16_t *>(g.c);
-    const bool vec = g.N % 8 == 0;
-    constexpr int kRowsPer = 64 / kPieces;  // rows of one store instruction
-#pragma unroll 4
-    for (int r0 = 0; r0 < FM * 16; r0 += kRowsPer) {
-        const int r = r0 + lane / kPieces, piece = lane % kPieces;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(img + r * kRow + ((piece ^ r) & (kPieces - 1)) * 16);
-        const int64_t m = m0 + wm * 16 + r, n = n0 + wn * 16 + piece * 8;
-        if (m >= g.M) continue;
-        uint16_t *dst = c + m * g.N + n;
-        if (vec) {
-            if (n < g.N) *reinterpret_cast<u32x4_t *>(dst) = v;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < g.N) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-        }
-    }
+    static_assert(W / 2 * FM * 16 * FN * 32 <= kStage, "half of the waves' tiles in each stage");
+    store_bf16<FN, FM>(g, acc, (wave < W / 2 ? st0 : st1) + (wave % (W / 2)) * FM * 16 * FN * 32, m0 + wm * 16,
+                       n0 + wn * 16, lane);
 #endif
 }
 
