@@ -298,11 +298,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, in
                                              (int)min(bytes, (int64_t)0x7FFFFFFF), 0x00020000);
 }
 
-// This wave's loads have landed and its LDS reads are done, then the
-// workgroup's barrier: every wave's are.
+// All but this wave's last N loads have landed and its LDS reads are done, then
+// the workgroup's barrier: every wave's are.
+template <int N>
 __device__ __forceinline__ void stage_barrier() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x7 << 4);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));  // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -310,17 +312,20 @@ __device__ __forceinline__ void stage_barrier() {
 constexpr int kXcds = 8;
 constexpr uint32_t kPast = 0x80000000u;  // an offset behind every buffer
 
-// First row of b and of a of this workgroup's tile.  Consecutive workgroups go
-// to the XCDs in turn: each XCD gets a contiguous range of tiles, all n tiles
-// of kGroup m tiles before the next.
+// First row of b and of a of this workgroup's tile, and its part of K.
+// Consecutive workgroups go to the XCDs in turn: each XCD gets a contiguous
+// range of (part, tile), all n tiles of kGroup m tiles before the next, so
+// that the workgroups of an L2 share operand rows of the same part.
 template <int BN, int BM>
-__device__ __forceinline__ void tile_origin(const ProductArgs &g, int64_t &n0, int64_t &m0) {
+__device__ __forceinline__ void tile_origin(const ProductArgs &g, int64_t &n0, int64_t &m0, int &split) {
     constexpr uint32_t kGroup = 4;
     const uint32_t tiles_n = (uint32_t)((g.N + BN - 1) / BN), tiles_m = (uint32_t)((g.M + BM - 1) / BM);
-    const uint32_t tiles = tiles_n * tiles_m;
-    const uint32_t xq = tiles / kXcds, xr = tiles % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const uint32_t tiles = tiles_n * tiles_m, all = gridDim.x;
+    const uint32_t xq = all / kXcds, xr = all % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
     const uint32_t logical = x < xr ? x * (xq + 1) + slot : xr * (xq + 1) + (x - xr) * xq + slot;
-    const uint32_t grp = logical / (kGroup * tiles_n), in = logical - grp * (kGroup * tiles_n);
+    split = (int)(logical / tiles);
+    const uint32_t tile = logical - (uint32_t)split * tiles;
+    const uint32_t grp = tile / (kGroup * tiles_n), in = tile - grp * (kGroup * tiles_n);
     const uint32_t gm = min(kGroup, tiles_m - grp * kGroup);
     n0 = (int64_t)(in / gm) * BN;
     m0 = (int64_t)(grp * kGroup + in % gm) * BM;
@@ -365,7 +370,7 @@ __device__ __forceinline__ void store_bf16(const ProductArgs &g, const f32x4_t (
     }
 }
 
-template <bool F32, int BN, int BM, int WN, int WM>
+template <bool F32, int BN, int BM, int WN, int WM, int NBUF>
 __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g) {
 // (The host pass only needs the launch stub, and drops it where it cannot
 // check a device builtin's template-dependent arguments.)
@@ -374,17 +379,21 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
     constexpr int kStage = (BN + BM) * 128;
     constexpr int kBPerWave = BN / 8 / W, kAPerWave = (BM / 8 + W - 1) / W;
     static_assert(BN / 8 % W == 0, "every wave loads as many row blocks of b");
+    static_assert(NBUF == 2 || NBUF == 4, "the scales' byte goes with the stage");
     __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st2[NBUF == 4 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t st3[NBUF == 4 ? kStage : 16];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t n0, m0;
-    tile_origin<BN, BM>(g, n0, m0);
+    int split;
+    tile_origin<BN, BM>(g, n0, m0, split);
 
     const int64_t K = g.K;
     const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
-    const int kb_first = (int)blockIdx.y * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
+    const int kb_first = split * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
 
     const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)BN, g.N - n0) * K);
     const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)BM, g.M - m0) * K);
@@ -490,33 +499,50 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         }
     };
 
-    // Block kb sits in stage kb % 2 (kb_first is even).  Each step: its loads
-    // have landed everywhere and the other stage is free, fill that one with
-    // the next block, multiply.  (The last fills may lie past K: zeros.)
+    // Block kb sits in stage (kb - kb_first) % NBUF (kb_first is even).  Each
+    // step: its loads have landed everywhere (those of the NBUF - 2 blocks
+    // behind it may be in flight) and the stage of the block before is free,
+    // fill that one, multiply.  (The last fills lie past K, or past this
+    // split: never multiplied.)  A pair's scales are loaded a pair ahead.
+    uint32_t sb_next[FN], sa_next[FM];
     load_scales(kb_first, sb, sa);
     issue(st0, kb_first);
-    int kb = kb_first;
-    for (;;) {
-        stage_barrier();
-        issue(st1, kb + 1);
-        compute(st0, std::integral_constant<int, 0>{});
-        if (++kb == kb_last) break;
-        uint32_t sb_next[FN], sa_next[FM];
-        stage_barrier();
-        load_scales(kb + 1, sb_next, sa_next);
-        issue(st0, kb + 1);
-        compute(st1, std::integral_constant<int, 1>{});
-        if (++kb == kb_last) break;
-#pragma unroll
-        for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
-#pragma unroll
-        for (int j = 0; j < FM; ++j) sa[j] = sa_next[j];
+    if constexpr (NBUF == 4) {
+        issue(st1, kb_first + 1);
+        issue(st2, kb_first + 2);
     }
-    stage_barrier();  // the last fills have landed and every read is done: the stages are free
+    int kb = kb_first;
+    auto step = [&](const uint8_t *cur, uint8_t *fill, auto opc) {
+        stage_barrier<(NBUF - 2) * kBPerWave>();
+        if constexpr (decltype(opc)::value == 0) load_scales(kb + 2, sb_next, sa_next);
+        issue(fill, kb + NBUF - 1);
+        compute(cur, opc);
+        if constexpr (decltype(opc)::value == 1) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
+#pragma unroll
+            for (int j = 0; j < FM; ++j) sa[j] = sa_next[j];
+        }
+        return ++kb == kb_last;
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    for (;;) {
+        if constexpr (NBUF == 2) {
+            if (step(st0, st1, even)) break;
+            if (step(st1, st0, odd)) break;
+        } else {
+            if (step(st0, st3, even)) break;
+            if (step(st1, st0, odd)) break;
+            if (step(st2, st1, even)) break;
+            if (step(st3, st2, odd)) break;
+        }
+    }
+    stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
 
     if (g.splits > 1 || F32) {
         // fp32: a lane's four n of one m, 16 bytes
-        float *c = g.splits > 1 ? static_cast<float *>(g.ws) + (int64_t)blockIdx.y * g.split_elems : static_cast<float *>(g.c);
+        float *c = g.splits > 1 ? static_cast<float *>(g.ws) + (int64_t)split * g.split_elems : static_cast<float *>(g.c);
         const bool vec = g.N % 4 == 0;
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
@@ -566,10 +592,10 @@ __global__ __launch_bounds__(256) void product_join_kernel(const float *parts, i
     }
 }
 
-// How a product is cut: 256 x 256 tiles where they fill the chip, else 128 x
-// 128 (64 or 16 rows of a where it has no more), and the blocks of K in
-// `splits` parts, each of at least four blocks, until there are about two
-// workgroups a CU.
+// How a product is cut: 256 x 256 tiles where they (or they and parts of K of
+// at least eight blocks) come to about one workgroup a CU, else 128 x 128 (64
+// or 16 rows of a where it has no more), the blocks of K in parts of at least
+// four where the tiles leave CUs idle.
 struct ProductCut {
     bool wide;
     int bm;
@@ -579,10 +605,12 @@ struct ProductCut {
 ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
     ProductCut c{};
     auto tiles = [&](int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
-    c.wide = tiles(256, 256) >= 256;
+    const int64_t kb = (K + 127) / 128;
+    const int64_t wt = tiles(256, 256), ws = std::max<int64_t>(1, std::min<int64_t>(256 / wt, kb / 8));
+    c.wide = wt * ws >= 192;
     c.bm = c.wide ? 256 : M > 64 ? 128 : M > 16 ? 64 : 16;
-    const int64_t t = tiles(c.wide ? 256 : 128, c.bm), kb = (K + 127) / 128;
-    int64_t s = c.wide ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(t, 1), kb / 4));
+    const int64_t t = c.wide ? wt : tiles(128, c.bm);
+    int64_t s = c.wide ? ws : std::max<int64_t>(1, std::min<int64_t>(256 / t, kb / 4));
     int64_t per = (kb + s - 1) / s;
     per += per & 1;  // scales are read two blocks at a time
     c.splits = (int32_t)((kb + per - 1) / per);
@@ -592,23 +620,23 @@ ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
 
 int64_t split_elems_of(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
 
-template <bool F32, int BN, int BM, int WN, int WM>
+template <bool F32, int BN, int BM, int WN, int WM, int NBUF>
 void product(const ProductArgs &g, hipStream_t s) {
     const int64_t tiles = ((g.N + BN - 1) / BN) * ((g.M + BM - 1) / BM);
-    launch_kernel((product_kernel<F32, BN, BM, WN, WM>), dim3((unsigned)tiles, (unsigned)g.splits), dim3(64 * WN * WM), s,
+    launch_kernel((product_kernel<F32, BN, BM, WN, WM, NBUF>), dim3((unsigned)(tiles * g.splits)), dim3(64 * WN * WM), s,
                   g);
 }
 
 template <bool F32>
 void product_of(const ProductCut &c, const ProductArgs &g, hipStream_t s) {
     if (c.wide)
-        product<F32, 256, 256, 2, 4>(g, s);
+        product<F32, 256, 256, 2, 4, 2>(g, s);
     else if (c.bm == 128)
-        product<F32, 128, 128, 2, 2>(g, s);
+        product<F32, 128, 128, 2, 2, 4>(g, s);
     else if (c.bm == 64)
-        product<F32, 128, 64, 4, 1>(g, s);
+        product<F32, 128, 64, 4, 1, 4>(g, s);
     else
-        product<F32, 128, 16, 4, 1>(g, s);
+        product<F32, 128, 16, 4, 1, 4>(g, s);
 }
 
 }  // namespace
