@@ -292,36 +292,59 @@ def _stream(stream) -> C.c_void_p:
 
 
 def _shape(t: Optional[torch.Tensor], name: str, *shape: int):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
 
 
-class _On:
-    """The device and stream of one call: every tensor on one device, which is
-    made the current one around the launch; `stream` must be that device's.
-    Without one, that device's current stream is used."""
+def _count(t: Optional[torch.Tensor], name: str, n: int):
+    if t is not None and t.numel() != n:
+        raise ValueError("%s has %d values, expected %d" % (name, t.numel(), n))
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError("tensors on %s and %s in one call" % (dev, t.device))
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError("a stream of %s with tensors on %s" % (stream.device, dev))
-        self.stream = C.c_void_p(stream.cuda_stream)
-        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
+_E8M0 = (torch.float8_e8m0fnu, torch.uint8)  # e8m0 scales, or their bytes
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+
+def _addr(t: Optional[torch.Tensor], name: str, *dtypes) -> Optional[int]:
+    """_ptr as a plain address (ctypes takes it as it is), for the calls whose
+    kernels take no longer than their host side."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA (HIP) tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if dtypes and t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+    return t.data_ptr()
+
+
+# the current stream of a device as an address; torch.cuda.current_stream builds a Stream object around it (2 us)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn: str, stream, tensors, *args):
+    """One library call on one device: every tensor must be on it, it is made the
+    current device around the launch, and `stream` must be one of its streams
+    (None: its current one).  The stream is the call's last argument."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s: tensors on devices %d and %d in one call" % (fn, dev, t.get_device()))
+    if stream is None:
+        s = _current_raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("%s: a stream of %s with tensors on device %d" % (fn, stream.device, dev))
+    else:
+        s = stream.cuda_stream
+    f = getattr(lib(), fn)
+    if dev == torch.cuda.current_device():
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != OK:
+        _check(fn, status)
 
 
 def _torch_dtype(dt: int):
@@ -391,6 +414,7 @@ class Plan:
         self.emb_dim = self.n_tables * head_dim
         self.dtype = dtype
         self.torch_dtype = _torch_dtype(dtype)
+        self._vocab, self._d, self._branches = vocab, d_model, n_branches
         h = C.c_void_p()
         _check("engram_plan_create", lib().engram_plan_create(C.byref(cfg), C.byref(h)))
         self._h = h
@@ -521,15 +545,14 @@ class Plan:
         """out[m][t] = scale * table[tokens[t]] for every branch m; ids outside
         [0, vocab) give zeros and are counted in bad_tokens.
         tokens: int32, any shape of n_tok ids; table: [vocab][d]; out: [n_branches][n_tok][d]."""
-        pt, pb = _ptr(tokens, "tokens", torch.int32), _ptr(bad_tokens, "bad_tokens", (torch.int32, torch.uint32))
-        pe, po = _ptr(table, "table", self.torch_dtype), _ptr(out, "out", self.torch_dtype)
-        n_tok, d = tokens.numel(), self.cfg.d_model
-        _shape(table, "table", self.cfg.vocab, d)
-        _shape(out, "out", self.cfg.n_branches, n_tok, d)
+        dt, d = self.torch_dtype, self._d
+        args = (_addr(tokens, "tokens", torch.int32), tokens.numel(), _addr(table, "table", dt), scale,
+                _addr(out, "out", dt), _addr(bad_tokens, "bad_tokens", torch.int32, torch.uint32))
+        _shape(table, "table", self._vocab, d)
+        _shape(out, "out", self._branches, args[1], d)
         if bad_tokens is not None and bad_tokens.numel() < 1:
             raise ValueError("bad_tokens is empty")
-        with _On(stream, tokens, table, out, bad_tokens) as s:
-            _check("engram_embed", lib().engram_embed(self._h, pt, n_tok, pe, scale, po, pb, s))
+        _call("engram_embed", stream, (tokens, table, out, bad_tokens), self._h, *args)
 
     def engram_embed_backward_workspace_size(self, n_tok: int) -> int:
         return int(lib().engram_embed_backward_workspace_size(self._h, n_tok))
@@ -541,27 +564,26 @@ class Plan:
         """dtable[r] = scale * the sum of dout ([n_branches][n_tok][d]) over the
         branches and the tokens with id r; dtable: [vocab][d] fp32, every row
         written (flags=GRAD_ACCUMULATE: added to the rows that tokens name)."""
-        pt, pg = _ptr(tokens, "tokens", torch.int32), _ptr(dout, "dout", self.torch_dtype)
-        pd, pw = _ptr(dtable, "dtable", torch.float32), _ptr(workspace, "workspace")
-        n_tok, d = tokens.numel(), self.cfg.d_model
-        _shape(dout, "dout", self.cfg.n_branches, n_tok, d)
-        _shape(dtable, "dtable", self.cfg.vocab, d)
-        with _On(stream, tokens, dout, dtable, workspace) as s:
-            _check("engram_embed_backward", lib().engram_embed_backward(
-                self._h, pt, n_tok, pg, scale, flags, pd, pw, workspace.numel() * workspace.element_size(), s))
+        n_tok, d = tokens.numel(), self._d
+        args = (_addr(tokens, "tokens", torch.int32), n_tok, _addr(dout, "dout", self.torch_dtype), scale, flags,
+                _addr(dtable, "dtable", torch.float32), _addr(workspace, "workspace"), workspace.nbytes)
+        _shape(dout, "dout", self._branches, n_tok, d)
+        _shape(dtable, "dtable", self._vocab, d)
+        _call("engram_embed_backward", stream, (tokens, dout, dtable, workspace), self._h, *args)
 
     def engram_layer_norm(self, x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, stream=None):
         """y = layer norm of x's rows ([..., d]; y may be x), beta may be None;
         mean and rstd (fp32, one a row) are kept for the backward if given."""
-        px, py = _ptr(x, "x", self.torch_dtype), _ptr(y, "y", self.torch_dtype)
-        pg, pb = _ptr(gamma, "gamma", torch.float32), _ptr(beta, "beta", torch.float32)
-        pm, pr = _ptr(mean, "mean", torch.float32), _ptr(rstd, "rstd", torch.float32)
+        dt, f32 = self.torch_dtype, torch.float32
         n_rows = self._rows(x, "x")
+        args = (_addr(x, "x", dt), n_rows, _addr(gamma, "gamma", f32), _addr(beta, "beta", f32), eps,
+                _addr(y, "y", dt), _addr(mean, "mean", f32), _addr(rstd, "rstd", f32))
         _shape(y, "y", *x.shape)
-        self._columns(gamma=gamma, beta=beta)
-        self._row_values(n_rows, mean=mean, rstd=rstd)
-        with _On(stream, x, y, gamma, beta, mean, rstd) as s:
-            _check("engram_layer_norm", lib().engram_layer_norm(self._h, px, n_rows, pg, pb, eps, py, pm, pr, s))
+        _shape(gamma, "gamma", self._d)
+        _shape(beta, "beta", self._d)
+        _count(mean, "mean", n_rows)
+        _count(rstd, "rstd", n_rows)
+        _call("engram_layer_norm", stream, (x, y, gamma, beta, mean, rstd), self._h, *args)
 
     def engram_layer_norm_backward_workspace_size(self, n_rows: int) -> int:
         return int(lib().engram_layer_norm_backward_workspace_size(self._h, n_rows))
@@ -574,42 +596,40 @@ class Plan:
                                    stream=None):
         """dx (which may be dy or x), dgamma and dbeta (None: not wanted) of
         engram_layer_norm; flags=GRAD_ACCUMULATE adds to dgamma and dbeta."""
-        px, py = _ptr(x, "x", self.torch_dtype), _ptr(dy, "dy", self.torch_dtype)
-        pd = _ptr(dx, "dx", self.torch_dtype)
-        pg, pm, pr = (_ptr(t, n, torch.float32) for t, n in ((gamma, "gamma"), (mean, "mean"), (rstd, "rstd")))
-        pdg, pdb = _ptr(dgamma, "dgamma", torch.float32), _ptr(dbeta, "dbeta", torch.float32)
-        pw = _ptr(workspace, "workspace")
+        dt, f32, d = self.torch_dtype, torch.float32, self._d
         n_rows = self._rows(x, "x")
+        args = (_addr(x, "x", dt), _addr(dy, "dy", dt), n_rows, _addr(gamma, "gamma", f32), _addr(mean, "mean", f32),
+                _addr(rstd, "rstd", f32), flags, _addr(dx, "dx", dt), _addr(dgamma, "dgamma", f32),
+                _addr(dbeta, "dbeta", f32), _addr(workspace, "workspace"), workspace.nbytes)
         _shape(dy, "dy", *x.shape)
         _shape(dx, "dx", *x.shape)
-        self._columns(gamma=gamma, dgamma=dgamma, dbeta=dbeta)
-        self._row_values(n_rows, mean=mean, rstd=rstd)
-        with _On(stream, x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace) as s:
-            _check("engram_layer_norm_backward", lib().engram_layer_norm_backward(
-                self._h, px, py, n_rows, pg, pm, pr, flags, pd, pdg, pdb, pw,
-                workspace.numel() * workspace.element_size(), s))
+        _shape(gamma, "gamma", d)
+        _shape(dgamma, "dgamma", d)
+        _shape(dbeta, "dbeta", d)
+        _count(mean, "mean", n_rows)
+        _count(rstd, "rstd", n_rows)
+        _call("engram_layer_norm_backward", stream, (x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace), self._h,
+              *args)
 
     def engram_quantize_fp8(self, x, q, scales, block_rows: int = 1, transpose: bool = False, stream=None):
         """q, scales = x ([rows][cols]) or its transpose in 8 bits, a scale for each
         128 values of block_rows (1 or 128) rows.  q: float8_e4m3fn; scales:
         float8_e8m0fnu (or uint8) of fp8_scale_shape(*q.shape, block_rows)."""
-        px = _ptr(x, "x", self.torch_dtype)
-        pq, ps = _ptr(q, "q", torch.float8_e4m3fn), _ptr(scales, "scales", (torch.float8_e8m0fnu, torch.uint8))
         if x.dim() != 2:
             raise ValueError("x must have two dimensions")
         rows, cols = x.shape
-        _shape(q, "q", *((cols, rows) if transpose else (rows, cols)))
+        args = (_addr(x, "x", self.torch_dtype), rows, cols, block_rows, QUANTIZE_TRANSPOSE if transpose else 0,
+                _addr(q, "q", torch.float8_e4m3fn), _addr(scales, "scales", *_E8M0))
+        r, c = (cols, rows) if transpose else (rows, cols)
+        _shape(q, "q", r, c)
         if block_rows in (1, 128):  # (the library refuses others)
-            _shape(scales, "scales", *self.fp8_scale_shape(*q.shape, block_rows))
-        with _On(stream, x, q, scales) as s:
-            _check("engram_quantize_fp8", lib().engram_quantize_fp8(
-                self._h, px, rows, cols, block_rows, QUANTIZE_TRANSPOSE if transpose else 0, pq, ps, s))
+            _shape(scales, "scales", *self.fp8_scale_shape(r, c, block_rows))
+        _call("engram_quantize_fp8", stream, (x, q, scales), self._h, *args)
 
     @staticmethod
     def fp8_scale_shape(rows: int, cols: int, block_rows: int):
         """Shape of the scales of a quantised [rows][cols] matrix."""
-        blocks = -(-cols // 128)
-        return (-(-rows // block_rows), -(-blocks // 4) * 4)
+        return (-(-rows // block_rows), -(-cols // 512) * 4)
 
     def engram_matmul_fp8_workspace_size(self, m: int, n: int, k: int) -> int:
         return int(lib().engram_matmul_fp8_workspace_size(self._h, m, n, k))
@@ -623,38 +643,25 @@ class Plan:
                           b_block_rows: int = 128, stream=None):
         """out[m][n] = a ([m][k]) times the rows of b ([n][k]), both quantised
         with a scale for each 128 values of *_block_rows rows; out bf16 or fp32."""
-        e8 = (torch.float8_e8m0fnu, torch.uint8)
-        pa, psa = _ptr(a, "a", torch.float8_e4m3fn), _ptr(a_scales, "a_scales", e8)
-        pb, psb = _ptr(b, "b", torch.float8_e4m3fn), _ptr(b_scales, "b_scales", e8)
-        po, pw = _ptr(out, "out", (torch.float32, torch.bfloat16)), _ptr(workspace, "workspace")
         if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
             raise ValueError("a and b must be [m][k] and [n][k], got %s and %s" % (tuple(a.shape), tuple(b.shape)))
         (m, k), n = a.shape, b.shape[0]
+        e4 = torch.float8_e4m3fn
+        args = (_addr(a, "a", e4), _addr(a_scales, "a_scales", *_E8M0), a_block_rows, _addr(b, "b", e4),
+                _addr(b_scales, "b_scales", *_E8M0), b_block_rows, m, n, k,
+                _addr(out, "out", torch.bfloat16, torch.float32), F32 if out.dtype == torch.float32 else BF16,
+                _addr(workspace, "workspace"), 0 if workspace is None else workspace.nbytes)
         _shape(out, "out", m, n)
         if a_block_rows in (1, 128) and b_block_rows in (1, 128):  # (the library refuses others)
             _shape(a_scales, "a_scales", *self.fp8_scale_shape(m, k, a_block_rows))
             _shape(b_scales, "b_scales", *self.fp8_scale_shape(n, k, b_block_rows))
-        with _On(stream, a, a_scales, b, b_scales, out, workspace) as s:
-            _check("engram_matmul_fp8", lib().engram_matmul_fp8(
-                self._h, pa, psa, a_block_rows, pb, psb, b_block_rows, m, n, k, po,
-                F32 if out.dtype == torch.float32 else BF16, pw,
-                0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+        _call("engram_matmul_fp8", stream, (a, a_scales, b, b_scales, out, workspace), self._h, *args)
 
     def _rows(self, x, name: str) -> int:
-        d = self.cfg.d_model
+        d = self._d
         if x.dim() < 1 or x.shape[-1] != d:
             raise ValueError("%s has shape %s, expected rows of %d" % (name, tuple(x.shape), d))
         return x.numel() // d
-
-    def _columns(self, **ts):
-        for n, t in ts.items():
-            _shape(t, n, self.cfg.d_model)
-
-    @staticmethod
-    def _row_values(n_rows: int, **ts):
-        for n, t in ts.items():
-            if t is not None and t.numel() != n_rows:
-                raise ValueError("%s has %d values, expected one for each of %d rows" % (n, t.numel(), n_rows))
 
     @staticmethod
     def _workspace(fn: str, size: int, device) -> torch.Tensor:

@@ -155,23 +155,21 @@ def test_the_binding_refuses_tensors_of_another_kind(B):
 def test_the_binding_refuses_shapes(B, monkeypatch):
     """Shapes, types and contiguity are checked before the library is called (the
     tensors stand on the CPU here, with the device check taken out of the way)."""
-    real = B._ptr
-
-    def ptr(t, name, dtype=None):
+    def addr(t, name, *dtypes):
         if t is None:
             return None
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        if dtypes and t.dtype not in dtypes:
             raise TypeError(name)
-        return C.c_void_p(t.data_ptr())
+        return t.data_ptr()
 
-    monkeypatch.setattr(B, "_ptr", ptr)
+    monkeypatch.setattr(B, "_addr", addr)
 
     def never(*a):
         raise AssertionError("reached the launch")
 
-    monkeypatch.setattr(B, "_On", never)
+    monkeypatch.setattr(B, "_call", never)
     p = plan(B)
     i32 = torch.zeros(4, dtype=torch.int32)
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
@@ -216,42 +214,64 @@ def test_the_binding_refuses_shapes(B, monkeypatch):
                  lambda: p.engram_matmul_fp8(f8(4, 256), u8(4, 4), f8(5, 256), u8(1, 4), torch.zeros(4, 5).half())):
         with pytest.raises(TypeError):
             call()
-    assert real is not ptr
 
 
 def test_one_device_and_its_stream(B, monkeypatch):
-    """Tensors on two devices, or a stream of another device, are refused."""
+    """Tensors on two devices, or a stream of another device, are refused; the
+    tensors' device is the current one during the call, on its current stream."""
     class T:
         def __init__(self, d):
-            self.device = torch.device("cuda", d)
+            self.d = d
+
+        def get_device(self):
+            return self.d
 
     class S:
+        cuda_stream = 5
+
         def __init__(self, d):
             self.device = torch.device("cuda", d)
-            self.cuda_stream = 5
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    entered = []
+    seen = []
 
     class Guard:
         def __init__(self, d):
-            entered.append(d.index)
+            seen.append("device %d" % d)
 
         def __enter__(self):
             return self
 
         def __exit__(self, *a):
-            entered.append("left")
+            seen.append("left")
 
+    class Lib:
+        @staticmethod
+        def engram_thing(*a):
+            seen.append(a)
+            return B.E_UNSUPPORTED if a[0] == "bad" else B.OK
+
+        engram_status_string = staticmethod(lambda s: b"said so")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", Guard)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: S(d.index))
+    monkeypatch.setattr(B, "_current_raw_stream", lambda d: 70 + d)
+    monkeypatch.setattr(B, "lib", lambda: Lib)
     with pytest.raises(ValueError):
-        B._On(None, T(0), None, T(1))
+        B._call("engram_thing", None, (T(0), None, T(1)), 1)
     with pytest.raises(ValueError):
-        B._On(S(1), T(0))
-    with B._On(S(0), T(0), None) as s:
-        assert s.value == 5
-    assert entered == []
-    with B._On(None, T(1), T(1)) as s:  # the tensors' device is made the current one around the launch
-        assert s.value == 5 and entered == [1]
-    assert entered == [1, "left"]
+        B._call("engram_thing", S(1), (T(0),), 1)
+    assert seen == []
+    B._call("engram_thing", S(0), (T(0), None), 1, 2)
+    B._call("engram_thing", None, (T(0), T(0)), 3)
+    assert seen == [(1, 2, 5), (3, 70)]
+    B._call("engram_thing", None, (T(1), T(1)), 4)
+    B._call("engram_thing", S(1), (T(1),), 5)
+    assert seen[2:] == ["device 1", (4, 71), "left", "device 1", (5, 5), "left"]
+    with pytest.raises(B.EngramError):
+        B._call("engram_thing", None, (T(0),), "bad")
+
+
+def test_scale_shape(B):
+    for cols, pitch in ((1, 4), (128, 4), (129, 4), (512, 4), (513, 8), (1280, 12), (16384, 128)):
+        assert B.Plan.fp8_scale_shape(300, cols, 1) == (300, pitch)
+        assert B.Plan.fp8_scale_shape(300, cols, 128) == (3, pitch)
