@@ -12,20 +12,36 @@ struct F8 {
     float v[8];
 };
 
-__device__ __forceinline__ F8 load8(const uint16_t *p) {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(p);
-    F8 r;
+// The same unit as loaded: half the registers for bf16 while a load is in flight.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    u32x4_t w;
+    __device__ __forceinline__ F8 get() const {
+        F8 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.v[2 * i] = __uint_as_float(w[i] << 16);
-        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            r.v[2 * i] = __uint_as_float(w[i] << 16);
+            r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        return r;
     }
-    return r;
+};
+template <>
+struct Raw8<float> {
+    f32x4_t a, b;
+    __device__ __forceinline__ F8 get() const { return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}}; }
+};
+__device__ __forceinline__ Raw8<uint16_t> load_raw8(const uint16_t *p) {
+    return Raw8<uint16_t>{*reinterpret_cast<const u32x4_t *>(p)};
 }
-__device__ __forceinline__ F8 load8(const float *p) {
-    const f32x4_t a = *reinterpret_cast<const f32x4_t *>(p);
-    const f32x4_t b = *reinterpret_cast<const f32x4_t *>(p + 4);
-    return F8{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+__device__ __forceinline__ Raw8<float> load_raw8(const float *p) {
+    return Raw8<float>{*reinterpret_cast<const f32x4_t *>(p), *reinterpret_cast<const f32x4_t *>(p + 4)};
+}
+template <typename T>
+__device__ __forceinline__ F8 load8(const T *p) {
+    return load_raw8(p).get();
 }
 __device__ __forceinline__ void store8(uint16_t *p, const F8 &x) {
     *reinterpret_cast<u32x4_t *>(p) = u32x4_t{pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]),
