@@ -7,10 +7,13 @@
 // Backward: dtable[r] = scale * sum over {t : id_t = r} (ascending) and
 // branches m of dh[m][t], in three launches whose results depend on the
 // tokens alone (no float atomics):
-//   embed_sort_kernel   stable counting sort of the token positions by id.
+//   embed_sort_kernel   stable counting sort of the token positions by id;
+//                       beside it the table is filled with zeros.
 //   embed_rows_kernel   sums of the runs inside each chunk of kRunChunk sorted
-//                       positions, and zeros for the rows no token names.
+//                       positions.
 //   embed_join_kernel   runs that cross chunks, from the chunks' parts.
+// The fill is most of the bytes (4 * vocab * d) and hides the sort, which is a
+// latency chain; rows with tokens are written a second time.
 #include <algorithm>
 
 #include "engram_internal.h"
@@ -55,11 +58,23 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t *tokens, int64
 constexpr int kSortWaves = 16;
 constexpr int kBucket = 512;
 
+// Bytes of the table that a block of the fill clears.
+constexpr int64_t kFillBytes = (int64_t)64 * kSortWaves * 16 * 16;
+
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32_t *tokens, int64_t n_tok,
                                                                      int32_t vocab, uint32_t *order, int32_t *sid,
-                                                                     uint32_t *start) {
+                                                                     uint32_t *start, uint32_t sort_blocks,
+                                                                     float *dtable, int64_t fill_bytes) {
     __shared__ uint32_t cnt[kSortWaves][kBucket];
     __shared__ uint32_t below_s[kSortWaves], wtot[kBucket / 64];
+    if (blockIdx.x >= sort_blocks) {
+        const int64_t at = (int64_t)(blockIdx.x - sort_blocks) * kFillBytes;
+        char *dst = reinterpret_cast<char *>(dtable) + at;
+        const int64_t n = min(kFillBytes, fill_bytes - at);
+        for (int64_t o = threadIdx.x * 16; o < n; o += 64 * kSortWaves * 16)
+            *reinterpret_cast<f32x4_t *>(dst + o) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        return;
+    }
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t lo64 = (int64_t)blockIdx.x * kBucket;
     const int32_t lo = (int32_t)lo64;
@@ -145,7 +160,6 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32
 }
 
 constexpr int kRunChunk = 32;  // sorted positions per wave
-constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 
 __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, bool accumulate) {
     F8 x;
@@ -159,29 +173,18 @@ __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, 
     store8(dst, x);
 }
 
-// Blocks [0, sum_blocks): one wave per (chunk of sorted positions, 512
-// channels) adds the chunk's rows in order.  A run that lies inside the chunk
-// goes to its table row; the part of one that began earlier goes to lead[c],
-// the part of one that began here and goes on to tail[c].  The other blocks
-// write zeros to the table rows without tokens.
+// One wave per (chunk of sorted positions, 512 channels) adds the chunk's rows
+// in order.  A run that lies inside the chunk goes to its table row; the part
+// of one that began earlier goes to lead[c], the part of one that began here
+// and goes on to tail[c].
 template <typename T, int BR>
 __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, const int32_t *sid,
                                                          const uint32_t *start, int64_t n_tok, int32_t vocab,
                                                          int32_t d, const T *dh, float scale, bool accumulate,
-                                                         float *dtable, float *lead, float *tail,
-                                                         uint32_t sum_blocks) {
-    constexpr int U = BR <= 2 ? 8 : 4;  // tokens whose rows are in flight
+                                                         float *dtable, float *lead, float *tail) {
+    constexpr int U = sizeof(T) == 2 ? (BR == 1 ? 16 : 8) : (BR <= 2 ? 8 : 4);  // tokens whose rows are in flight
     const int lane = threadIdx.x & 63;
     const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (blockIdx.x >= sum_blocks) {
-        const int64_t r0 = (wave - (int64_t)sum_blocks * 4) * kZeroRows;
-        for (int64_t r = r0; r < min(r0 + kZeroRows, (int64_t)vocab); ++r) {
-            if (start[r] != start[r + 1]) continue;
-            for (int32_t c = lane * 4; c < d; c += 256)
-                *reinterpret_cast<f32x4_t *>(dtable + r * d + c) = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        }
-        return;
-    }
     const int32_t strips = (d + 511) / 512;
     const int64_t c = wave / strips;
     const int32_t col = (int32_t)(wave - c * strips) * 512 + lane * 8;
@@ -200,14 +203,14 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
     bool started = __builtin_amdgcn_readlane(my_id, 0) != before;
     F8 acc = {};
     for (int k0 = 0; k0 < cnt; k0 += U) {
-        F8 x[U][BR];
+        Raw8<T> x[U][BR];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t t = (uint32_t)__builtin_amdgcn_readlane((int)my_tok, min(k0 + u, cnt - 1));
 #pragma unroll
             for (int m = 0; m < BR; ++m) {
-                x[u][m] = F8{};
-                if (in) x[u][m] = load8(dh + ((int64_t)m * n_tok + t) * d + col);
+                x[u][m] = Raw8<T>{};
+                if (in) x[u][m] = load_raw8(dh + ((int64_t)m * n_tok + t) * d + col);
             }
         }
 #pragma unroll
@@ -215,9 +218,11 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
             const int k = k0 + u;
             if (k >= cnt) break;
 #pragma unroll
-            for (int m = 0; m < BR; ++m)
+            for (int m = 0; m < BR; ++m) {
+                const F8 v = x[u][m].get();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc.v[i] += x[u][m].v[i];
+                for (int i = 0; i < 8; ++i) acc.v[i] += v.v[i];
+            }
             const int32_t id = __builtin_amdgcn_readlane(my_id, k);
             const int32_t next = k == cnt - 1 ? after : __builtin_amdgcn_readlane(my_id, min(k + 1, kRunChunk));
             const bool ends = next != id;
@@ -236,31 +241,41 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
     }
 }
 
-// One workgroup per chunk and 1024 channels: where a run starts in the chunk
-// and goes on, its tail part plus the lead parts of the chunks behind it, in order.
+// One workgroup per chunk and 256 channels: where a run starts in the chunk and
+// goes on, its tail part plus the lead parts of the chunks behind it, a
+// quarter of them each of the four waves, joined in order (a token that is a
+// tenth of 32,768 leaves a hundred parts).
 __global__ __launch_bounds__(256) void embed_join_kernel(const int32_t *sid, const uint32_t *start, int32_t vocab,
                                                          int32_t d, const float *lead, const float *tail,
                                                          float scale, bool accumulate, float *dtable) {
+    __shared__ f32x4_t part[3][64];
     const int64_t c = blockIdx.x, base = c * kRunChunk, n = start[vocab];
     if (base + kRunChunk >= n) return;
     const int32_t id = sid[base + kRunChunk - 1];
     const int64_t first = start[id], end = (int64_t)start[id + 1];
     if (first < base || end <= base + kRunChunk) return;
-    const int32_t col = (int32_t)blockIdx.y * 1024 + threadIdx.x * 4;
-    if (col >= d) return;
-    const int64_t last = (end - 1) / kRunChunk;
-    f32x4_t acc = *reinterpret_cast<const f32x4_t *>(tail + c * d + col);
-    int64_t k = c + 1;
-    for (; k + 7 <= last; k += 8) {
-        f32x4_t x[8];
+    const int64_t k0 = c + 1, k1 = (end - 1) / kRunChunk + 1;  // the chunks with a lead part
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t quarter = (k1 - k0 + 3) / 4, b = min(k0 + (w + 1) * quarter, k1);
+    int64_t k = min(k0 + w * quarter, k1);
+    const int32_t col = (int32_t)blockIdx.y * 256 + lane * 4;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    if (col < d) {
+        if (w == 0) acc = *reinterpret_cast<const f32x4_t *>(tail + c * d + col);
+        for (; k + 8 <= b; k += 8) {
+            f32x4_t x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const f32x4_t *>(lead + (k + u) * d + col);
+            for (int u = 0; u < 8; ++u) x[u] = *reinterpret_cast<const f32x4_t *>(lead + (k + u) * d + col);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) acc += x[u];
+            for (int u = 0; u < 8; ++u) acc += x[u];
+        }
+        for (; k < b; ++k) acc += *reinterpret_cast<const f32x4_t *>(lead + k * d + col);
     }
-    for (; k <= last; ++k) acc += *reinterpret_cast<const f32x4_t *>(lead + k * d + col);
+    if (w > 0) part[w - 1][lane] = acc;
+    __syncthreads();
+    if (w > 0 || col >= d) return;
     f32x4_t *dst = reinterpret_cast<f32x4_t *>(dtable + (int64_t)id * d + col);
-    acc *= scale;
+    acc = (((acc + part[0][lane]) + part[1][lane]) + part[2][lane]) * scale;
     if (accumulate) acc += *dst;
     *dst = acc;
 }
@@ -268,12 +283,10 @@ __global__ __launch_bounds__(256) void embed_join_kernel(const int32_t *sid, con
 template <typename T>
 void embed_rows(const EmbedBwdArgs &a, hipStream_t s) {
     const int64_t chunks = embed_chunks(a.n_tok), strips = (a.d + 511) / 512;
-    const uint32_t sum_blocks = (uint32_t)((chunks * strips + 3) / 4);
-    const uint32_t zero_blocks = a.accumulate ? 0u : (uint32_t)((a.vocab + 4 * kZeroRows - 1) / (4 * kZeroRows));
-    const dim3 grid(sum_blocks + zero_blocks);
+    const dim3 grid((unsigned)((chunks * strips + 3) / 4));
 #define ENGRAM_EMBED_ROWS(BR)                                                                                   \
     launch_kernel((embed_rows_kernel<T, BR>), grid, dim3(256), s, a.order, a.sid, a.start, a.n_tok, a.vocab,    \
-                  a.d, static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, a.lead, a.tail, sum_blocks)
+                  a.d, static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, a.lead, a.tail)
     switch (a.n_branches) {
         case 1: ENGRAM_EMBED_ROWS(1); break;
         case 2: ENGRAM_EMBED_ROWS(2); break;
@@ -299,23 +312,29 @@ void launch_embed(engram_dtype dt, const int32_t *tokens, int64_t n_tok, int32_t
 
 int64_t embed_chunks(int64_t n_tok) { return (n_tok + kRunChunk - 1) / kRunChunk; }
 
+namespace {
+int64_t sort_blocks(int32_t vocab) { return ((int64_t)vocab + kBucket - 1) / kBucket; }
+int64_t fill_blocks(int32_t vocab, int32_t d) { return ((int64_t)vocab * d * 4 + kFillBytes - 1) / kFillBytes; }
+}  // namespace
+
 bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d) {
     // a launch holds fewer than 2^32 threads along x, and 65535 blocks along y
     const int64_t strips = (d + 511) / 512;
-    const int64_t blocks = (embed_chunks(n_tok) * strips + 3) / 4 + ((int64_t)vocab + 31) / 32;
-    return blocks < ((int64_t)1 << 24) && embed_chunks(n_tok) < ((int64_t)1 << 24) && (d + 1023) / 1024 <= 65535;
+    return (embed_chunks(n_tok) * strips + 3) / 4 < ((int64_t)1 << 24) && embed_chunks(n_tok) < ((int64_t)1 << 24) &&
+           sort_blocks(vocab) + fill_blocks(vocab, d) < ((int64_t)1 << 22) && (d + 255) / 256 <= 65535;
 }
 
 void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s) {
-    launch_kernel(embed_sort_kernel, dim3((unsigned)(((int64_t)a.vocab + kBucket - 1) / kBucket)),
-                  dim3(64 * kSortWaves), s, a.tokens, a.n_tok, a.vocab, a.order, a.sid, a.start);
+    const int64_t sorts = sort_blocks(a.vocab), fills = a.accumulate ? 0 : fill_blocks(a.vocab, a.d);
+    launch_kernel(embed_sort_kernel, dim3((unsigned)(sorts + fills)), dim3(64 * kSortWaves), s, a.tokens, a.n_tok, a.vocab,
+                  a.order, a.sid, a.start, (uint32_t)sorts, a.dtable, (int64_t)a.vocab * a.d * 4);
     if (dt == ENGRAM_BF16)
         embed_rows<uint16_t>(a, s);
     else
         embed_rows<float>(a, s);
     const int64_t chunks = embed_chunks(a.n_tok);
     if (chunks > 1)
-        launch_kernel(embed_join_kernel, dim3((unsigned)chunks, (unsigned)((a.d + 1023) / 1024)), dim3(256), s, a.sid,
+        launch_kernel(embed_join_kernel, dim3((unsigned)chunks, (unsigned)((a.d + 255) / 256)), dim3(256), s, a.sid,
                       a.start, a.vocab, a.d, a.lead, a.tail, a.scale, a.accumulate, a.dtable);
 }
 
