@@ -40,7 +40,7 @@ engram_status embed_layout_of(const engram_plan_s &p, int64_t n_tok, EmbedLayout
         off = round_up(off + bytes, 256);
         return o;
     };
-    const size_t parts = (size_t)embed_chunks(n_tok) * (size_t)d * 4;
+    const size_t parts = (size_t)embed_chunks(n_tok, d) * (size_t)d * 4;
     L.order = take((size_t)n_tok * 4);
     L.sid = take((size_t)n_tok * 4);
     L.start = take(((size_t)V + 1) * 4);

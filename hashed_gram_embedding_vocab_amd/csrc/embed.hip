@@ -8,12 +8,15 @@
 // branches m of dh[m][t], in three launches whose results depend on the
 // tokens alone (no float atomics):
 //   embed_sort_kernel   stable counting sort of the token positions by id;
-//                       beside it the table is filled with zeros.
-//   embed_rows_kernel   sums of the runs inside each chunk of kRunChunk sorted
-//                       positions.
+//                       beside it the table's first rows are filled with zeros.
+//   embed_rows_kernel   sums of the runs inside each chunk of sorted
+//                       positions; zeros for the other rows without tokens.
 //   embed_join_kernel   runs that cross chunks, from the chunks' parts.
-// The fill is most of the bytes (4 * vocab * d) and hides the sort, which is a
-// latency chain; rows with tokens are written a second time.
+// The zeros are most of the bytes (4 * vocab * d).  The sort is a latency chain
+// of about 20 us, which kFillBeside of them hide.  Measured with a table of
+// 129,280 x 2560, 32,768 tokens and four branches: 411 us; all zeros beside the
+// sort, which writes the rows with tokens twice, 424; none there 432.  The sums
+// and zeros together move 5.3 TB/s, a large copy's rate.
 #include <algorithm>
 
 #include "engram_internal.h"
@@ -60,6 +63,7 @@ constexpr int kBucket = 512;
 
 // Bytes of the table that a block of the fill clears.
 constexpr int64_t kFillBytes = (int64_t)64 * kSortWaves * 16 * 16;
+constexpr int64_t kFillBeside = (int64_t)256 << 20;  // most bytes filled beside the sort
 
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32_t *tokens, int64_t n_tok,
                                                                      int32_t vocab, uint32_t *order, int32_t *sid,
@@ -159,7 +163,11 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32
     }
 }
 
-constexpr int kRunChunk = 32;  // sorted positions per wave
+// Sorted positions per wave: 32, or 8 where that leaves the chip short of waves
+// (333 tokens x 256 channels: the sums take 5 us instead of 12, the join of
+// longer chains of parts no longer).
+int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= 65536 ? 32 : 8; }
+constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 
 __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, bool accumulate) {
     F8 x;
@@ -173,25 +181,36 @@ __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, 
     store8(dst, x);
 }
 
-// One wave per (chunk of sorted positions, 512 channels) adds the chunk's rows
+// One wave per (run_chunk sorted positions, 512 channels) adds the chunk's rows
 // in order.  A run that lies inside the chunk goes to its table row; the part
 // of one that began earlier goes to lead[c], the part of one that began here
-// and goes on to tail[c].
+// and goes on to tail[c].  Blocks from sum_blocks on write zeros to the rows
+// from zero_row on that have no tokens.
 template <typename T, int BR>
 __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, const int32_t *sid,
                                                          const uint32_t *start, int64_t n_tok, int32_t vocab,
                                                          int32_t d, const T *dh, float scale, bool accumulate,
-                                                         float *dtable, float *lead, float *tail) {
+                                                         float *dtable, float *lead, float *tail,
+                                                         uint32_t sum_blocks, int64_t zero_row, int32_t chunk) {
     constexpr int U = sizeof(T) == 2 ? (BR == 1 ? 16 : 8) : (BR <= 2 ? 8 : 4);  // tokens whose rows are in flight
     const int lane = threadIdx.x & 63;
     const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (blockIdx.x >= sum_blocks) {
+        const int64_t r0 = zero_row + (wave - (int64_t)sum_blocks * 4) * kZeroRows;
+        for (int64_t r = r0; r < min(r0 + kZeroRows, (int64_t)vocab); ++r) {
+            if (start[r] != start[r + 1]) continue;
+            for (int32_t c = lane * 4; c < d; c += 256)
+                *reinterpret_cast<f32x4_t *>(dtable + r * d + c) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        return;
+    }
     const int32_t strips = (d + 511) / 512;
     const int64_t c = wave / strips;
     const int32_t col = (int32_t)(wave - c * strips) * 512 + lane * 8;
     const bool in = col < d;
-    const int64_t n = start[vocab], base = c * kRunChunk;
+    const int64_t n = start[vocab], base = c * chunk;
     if (base >= n) return;
-    const int cnt = (int)min((int64_t)kRunChunk, n - base);
+    const int cnt = (int)min((int64_t)chunk, n - base);
     uint32_t my_tok = 0u;
     int32_t my_id = -1;
     if (lane < cnt) {
@@ -224,7 +243,7 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
                 for (int i = 0; i < 8; ++i) acc.v[i] += v.v[i];
             }
             const int32_t id = __builtin_amdgcn_readlane(my_id, k);
-            const int32_t next = k == cnt - 1 ? after : __builtin_amdgcn_readlane(my_id, min(k + 1, kRunChunk));
+            const int32_t next = k == cnt - 1 ? after : __builtin_amdgcn_readlane(my_id, min(k + 1, 63));
             const bool ends = next != id;
             if (!ends && k < cnt - 1) continue;
             if (in) {
@@ -247,14 +266,14 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
 // tenth of 32,768 leaves a hundred parts).
 __global__ __launch_bounds__(256) void embed_join_kernel(const int32_t *sid, const uint32_t *start, int32_t vocab,
                                                          int32_t d, const float *lead, const float *tail,
-                                                         float scale, bool accumulate, float *dtable) {
+                                                         float scale, bool accumulate, float *dtable, int32_t chunk) {
     __shared__ f32x4_t part[3][64];
-    const int64_t c = blockIdx.x, base = c * kRunChunk, n = start[vocab];
-    if (base + kRunChunk >= n) return;
-    const int32_t id = sid[base + kRunChunk - 1];
+    const int64_t c = blockIdx.x, base = c * chunk, n = start[vocab];
+    if (base + chunk >= n) return;
+    const int32_t id = sid[base + chunk - 1];
     const int64_t first = start[id], end = (int64_t)start[id + 1];
-    if (first < base || end <= base + kRunChunk) return;
-    const int64_t k0 = c + 1, k1 = (end - 1) / kRunChunk + 1;  // the chunks with a lead part
+    if (first < base || end <= base + chunk) return;
+    const int64_t k0 = c + 1, k1 = (end - 1) / chunk + 1;  // the chunks with a lead part
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t quarter = (k1 - k0 + 3) / 4, b = min(k0 + (w + 1) * quarter, k1);
     int64_t k = min(k0 + w * quarter, k1);
@@ -280,13 +299,21 @@ __global__ __launch_bounds__(256) void embed_join_kernel(const int32_t *sid, con
     *dst = acc;
 }
 
+int64_t sort_blocks(int32_t vocab) { return ((int64_t)vocab + kBucket - 1) / kBucket; }
+// Rows of the table that are filled beside the sort (at least one: d is far below kFillBeside).
+int64_t fill_rows(int32_t vocab, int32_t d) {
+    return std::min<int64_t>(vocab, std::max<int64_t>(1, kFillBeside / ((int64_t)d * 4)));
+}
+
 template <typename T>
 void embed_rows(const EmbedBwdArgs &a, hipStream_t s) {
-    const int64_t chunks = embed_chunks(a.n_tok), strips = (a.d + 511) / 512;
-    const dim3 grid((unsigned)((chunks * strips + 3) / 4));
+    const int64_t chunks = embed_chunks(a.n_tok, a.d), strips = (a.d + 511) / 512;
+    const uint32_t sum_blocks = (uint32_t)((chunks * strips + 3) / 4);
+    const int64_t zero_row = a.accumulate ? a.vocab : fill_rows(a.vocab, a.d);
+    const dim3 grid(sum_blocks + (unsigned)((a.vocab - zero_row + 4 * kZeroRows - 1) / (4 * kZeroRows)));
 #define ENGRAM_EMBED_ROWS(BR)                                                                                   \
     launch_kernel((embed_rows_kernel<T, BR>), grid, dim3(256), s, a.order, a.sid, a.start, a.n_tok, a.vocab,    \
-                  a.d, static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, a.lead, a.tail)
+                  a.d, static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, a.lead, a.tail, sum_blocks, zero_row, run_chunk(a.n_tok, a.d))
     switch (a.n_branches) {
         case 1: ENGRAM_EMBED_ROWS(1); break;
         case 2: ENGRAM_EMBED_ROWS(2); break;
@@ -310,32 +337,32 @@ void launch_embed(engram_dtype dt, const int32_t *tokens, int64_t n_tok, int32_t
                       static_cast<const float *>(table), d, n_branches, scale, static_cast<float *>(h), bad);
 }
 
-int64_t embed_chunks(int64_t n_tok) { return (n_tok + kRunChunk - 1) / kRunChunk; }
-
-namespace {
-int64_t sort_blocks(int32_t vocab) { return ((int64_t)vocab + kBucket - 1) / kBucket; }
-int64_t fill_blocks(int32_t vocab, int32_t d) { return ((int64_t)vocab * d * 4 + kFillBytes - 1) / kFillBytes; }
-}  // namespace
+int64_t embed_chunks(int64_t n_tok, int32_t d) {
+    const int64_t c = run_chunk(n_tok, d);
+    return (n_tok + c - 1) / c;
+}
 
 bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d) {
     // a launch holds fewer than 2^32 threads along x, and 65535 blocks along y
     const int64_t strips = (d + 511) / 512;
-    return (embed_chunks(n_tok) * strips + 3) / 4 < ((int64_t)1 << 24) && embed_chunks(n_tok) < ((int64_t)1 << 24) &&
-           sort_blocks(vocab) + fill_blocks(vocab, d) < ((int64_t)1 << 22) && (d + 255) / 256 <= 65535;
+    return (embed_chunks(n_tok, d) * strips + 3) / 4 + ((int64_t)vocab + 31) / 32 < ((int64_t)1 << 24) &&
+           embed_chunks(n_tok, d) < ((int64_t)1 << 24) && sort_blocks(vocab) < ((int64_t)1 << 21) &&
+           (d + 255) / 256 <= 65535;
 }
 
 void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s) {
-    const int64_t sorts = sort_blocks(a.vocab), fills = a.accumulate ? 0 : fill_blocks(a.vocab, a.d);
+    const int64_t fill = a.accumulate ? 0 : fill_rows(a.vocab, a.d) * a.d * 4;
+    const int64_t sorts = sort_blocks(a.vocab), fills = (fill + kFillBytes - 1) / kFillBytes;
     launch_kernel(embed_sort_kernel, dim3((unsigned)(sorts + fills)), dim3(64 * kSortWaves), s, a.tokens, a.n_tok, a.vocab,
-                  a.order, a.sid, a.start, (uint32_t)sorts, a.dtable, (int64_t)a.vocab * a.d * 4);
+                  a.order, a.sid, a.start, (uint32_t)sorts, a.dtable, fill);
     if (dt == ENGRAM_BF16)
         embed_rows<uint16_t>(a, s);
     else
         embed_rows<float>(a, s);
-    const int64_t chunks = embed_chunks(a.n_tok);
+    const int64_t chunks = embed_chunks(a.n_tok, a.d);
     if (chunks > 1)
         launch_kernel(embed_join_kernel, dim3((unsigned)chunks, (unsigned)((a.d + 255) / 256)), dim3(256), s, a.sid,
-                      a.start, a.vocab, a.d, a.lead, a.tail, a.scale, a.accumulate, a.dtable);
+                      a.start, a.vocab, a.d, a.lead, a.tail, a.scale, a.accumulate, a.dtable, run_chunk(a.n_tok, a.d));
 }
 
 }  // namespace engram

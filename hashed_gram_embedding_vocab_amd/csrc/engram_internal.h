@@ -376,13 +376,13 @@ struct EmbedBwdArgs {
     uint32_t *order;                        // [n_tok] token positions sorted by id (those in [0, vocab))
     int32_t *sid;                           // [n_tok] their ids
     uint32_t *start;                        // [vocab + 1] first sorted position of each id; start[vocab]: how many
-    float *lead, *tail;                     // [embed_chunks(n_tok)][d] parts of runs that cross chunks
+    float *lead, *tail;                     // [embed_chunks][d] parts of runs that cross chunks
     int64_t n_tok;
     int32_t vocab, d, n_branches;
     float scale;
     bool accumulate;
 };
-int64_t embed_chunks(int64_t n_tok);
+int64_t embed_chunks(int64_t n_tok, int32_t d);
 bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d);
 void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s);
 

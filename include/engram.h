@@ -495,7 +495,8 @@ ENGRAM_API engram_status engram_embed(engram_plan p, const int32_t *d_tokens, in
                                       float scale, void *d_h, uint32_t *d_bad_tokens, hipStream_t stream);
 
 /* Bytes of device workspace engram_embed_backward needs (0 on invalid or
- * unsupported sizes): 8 bytes a token, 4 an id and n_tok * d_model / 4. */
+ * unsupported sizes): 8 bytes a token, 4 an id and two fp32 rows for every 32
+ * tokens (for every 8 of a short batch). */
 ENGRAM_API size_t engram_embed_backward_workspace_size(engram_plan p, int64_t n_tok);
 
 /*

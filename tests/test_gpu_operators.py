@@ -123,7 +123,10 @@ IDS = {
     ("zipf", 1, 1, 8, 1, 1.0), ("zipf", 333, 1000, 256, 1, 16.0), ("zipf", 4099, 1537, 264, 2, 0.3),
     ("zipf", 2048, 511, 1032, 3, 1.0), ("zipf", 1000, 513, 520, 4, -2.0), ("one", 32, 512, 64, 1, 1.0),
     ("one", 33, 513, 64, 2, 1.0), ("one", 1500, 2000, 72, 1, 1.0), ("none", 65, 600, 64, 1, 1.0),
-    ("two", 4097, 1025, 128, 1, 1.0), ("rising", 3000, 1000, 64, 4, 1.0)])
+    ("two", 4097, 1025, 128, 1, 1.0), ("rising", 3000, 1000, 64, 4, 1.0),
+    # enough tokens for chunks of 32 sorted positions
+    ("zipf", 65537, 1537, 64, 1, 0.5), ("one", 65600, 513, 64, 1, 1.0), ("two", 66001, 700, 64, 2, 1.0),
+    ("rising", 33000, 33100, 520, 1, 1.0)])
 def test_embed_backward(gpu, dtype, ids_of, n_tok, vocab, d, branches, scale):
     from hashed_gram_embedding_vocab_amd import binding as B
 
@@ -469,7 +472,8 @@ def lost_in_blocks(a, sa, abr, b, sb, bbr):
 
 PRODUCT_SHAPES = [(1, 1, 16), (1, 16, 128), (1, 2560, 1280), (2, 333, 144), (5, 128, 2048), (16, 130, 4112), (17, 257, 640),
                   (64, 64, 64), (77, 1000, 528), (128, 128, 128), (129, 255, 1264), (256, 256, 512), (300, 520, 400),
-                  (513, 129, 272), (128, 64, 16384), (1000, 24, 1024), (31, 2049, 96)]
+                  (513, 129, 272), (128, 64, 16384), (1000, 24, 1024), (31, 2049, 96),
+                  (257, 130, 8208), (700, 600, 8192), (40, 100, 20000)]
 
 
 @pytest.mark.parametrize("out", DTYPES)
