@@ -32,10 +32,54 @@ namespace {
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------- quantisation
+// Largest magnitudes of 8 columns as bit patterns (which order like the
+// values), two bf16 columns a word.  NaN and infinity are above kNotFinite.
+constexpr uint32_t kNotFinite = 0x7F800000u;
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                  __builtin_bit_cast(u16x2_t, b)));
+}
+
+template <typename T>
+struct Top8;
+template <>
+struct Top8<uint16_t> {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void add(const Raw8<uint16_t> &x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = max_u16x2(w[i], x.w[i] & 0x7FFF7FFFu);
+    }
+    __device__ __forceinline__ uint32_t column(int i) const { return (i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16; }
+    __device__ __forceinline__ uint32_t all() const {
+        const uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+        return max(m & 0xFFFF0000u, m << 16);
+    }
+};
+template <>
+struct Top8<float> {
+    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void add(const Raw8<float> &x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = max(w[i], __float_as_uint(x.a[i]) & 0x7FFFFFFFu);
+            w[4 + i] = max(w[4 + i], __float_as_uint(x.b[i]) & 0x7FFFFFFFu);
+        }
+    }
+    __device__ __forceinline__ uint32_t column(int i) const { return w[i]; }
+    __device__ __forceinline__ uint32_t all() const {
+        uint32_t m = w[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, w[i]);
+        return m;
+    }
+};
+
 // |x| as bits, 0 where x is not finite
 __device__ __forceinline__ uint32_t finite_bits(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? b : 0u;
+    return b < kNotFinite ? b : 0u;
 }
 
 // Biased exponent of the block's scale from the bits of its largest finite
@@ -48,21 +92,14 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 // 1 / scale: exact (a power of two in the normal range, 2^-120 .. 2^126)
 __device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Two values to e4m3 bytes.  Finite values are at most 448 here; infinities
-// have no e4m3 form and become NaN like NaNs.
-__device__ __forceinline__ float no_inf(float x) {
-    return (__float_as_uint(x) & 0x7FFFFFFFu) == 0x7F800000u ? __uint_as_float(0x7FC00000u) : x;
-}
-template <bool HI>
-__device__ __forceinline__ uint32_t cvt2(float a, float b, uint32_t old) {
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(no_inf(a), no_inf(b), (int)old, HI);
-}
+// To e4m3 bytes.  Finite values are at most 448 here; the conversion makes NaN
+// of infinities, which e4m3 does not have.
 __device__ __forceinline__ u32x2_t cvt8(const F8 &x, float inv) {
     u32x2_t q;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t w = cvt2<false>(x.v[4 * i] * inv, x.v[4 * i + 1] * inv, 0u);
-        q[i] = cvt2<true>(x.v[4 * i + 2] * inv, x.v[4 * i + 3] * inv, w);
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x.v[4 * i] * inv, x.v[4 * i + 1] * inv, 0, false);
+        q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x.v[4 * i + 2] * inv, x.v[4 * i + 3] * inv, w, true);
     }
     return q;
 }
@@ -70,18 +107,20 @@ __device__ __forceinline__ u32x2_t cvt8(const F8 &x, float inv) {
 // 8 values at column c of a row of `cols`, zeros past its end.  VEC: rows are
 // whole 8-value units and 16-byte aligned.
 template <bool VEC, typename T>
-__device__ __forceinline__ F8 load_cols(const T *row, int64_t c, int64_t cols) {
-    F8 x = {};
+__device__ __forceinline__ Raw8<T> load_cols(const T *row, int64_t c, int64_t cols) {
+    Raw8<T> x = {};
     if constexpr (VEC) {
-        if (c < cols) x = load8(row + c);
+        if (c < cols) x = load_raw8(row + c);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < cols) {
                 if constexpr (sizeof(T) == 2)
-                    x.v[i] = bf16_to_f32(row[c + i]);
+                    x.w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+                else if (i < 4)
+                    x.a[i & 3] = row[c + i];
                 else
-                    x.v[i] = row[c + i];
+                    x.b[i & 3] = row[c + i];
             }
     }
     return x;
@@ -98,84 +137,116 @@ __device__ __forceinline__ void store_cols(uint8_t *row, int64_t c, int64_t cols
     }
 }
 
-// One wave per (row, 512 columns): a block is 16 lanes, and the wave's four
-// scale bytes are one word of the scales' row (its blocks past the last hold 127, i.e. one).
-template <typename T, bool VEC>
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true));
+}
+// over the 16 lanes of a row (neighbours, quads, halves, the row's mirror)
+__device__ __forceinline__ uint32_t max16(uint32_t x) { return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(x)))); }
+
+// One wave per (U rows, 512 columns): a block is 16 lanes, and the wave's four
+// scale bytes of a row are one word of the scales' row (its blocks past the
+// last hold 127, i.e. one).  Bound by memory; the U rows' loads are in flight
+// together.
+template <typename T, bool VEC, int U>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const T *x, int64_t rows, int64_t cols, uint8_t *q,
                                                             uint8_t *scales) {
     const int lane = threadIdx.x & 63;
-    const int64_t strips = (cols + 511) / 512, n_items = rows * strips;
+    const int64_t strips = (cols + 511) / 512, n_items = (rows + U - 1) / U * strips;
     const int64_t kb = (cols + 127) / 128;
     for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < n_items; item += (int64_t)gridDim.x * 4) {
-        const int64_t r = item / strips, strip = item - r * strips;
+        const int64_t r0 = item / strips * U, strip = item % strips;
         const int64_t c = strip * 512 + lane * 8;
-        const F8 v = load_cols<VEC>(x + r * cols, c, cols);
-        uint32_t top = 0u;
+        Raw8<T> v[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, finite_bits(v.v[i]));
+        for (int u = 0; u < U; ++u) v[u] = load_cols<VEC>(x + min(r0 + u, rows - 1) * cols, c, cols);
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-        const uint32_t byte = scale_byte(top);
-        store_cols<VEC>(q + r * cols, c, cols, cvt8(v, scale_inverse(byte)));
-        const uint32_t mine = strip * 4 + (lane >> 4) < kb ? byte : 127u;
-        uint32_t word = 0u;
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = r0 + u;
+            if (r >= rows) break;
+            const F8 f = v[u].get();
+            Top8<T> t8;
+            t8.add(v[u]);
+            uint32_t top = max16(t8.all());
+            if (__any(top >= kNotFinite)) {
+                uint32_t m = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) word |= (uint32_t)__builtin_amdgcn_readlane((int)mine, 16 * i) << (8 * i);
-        if (lane == 0) *reinterpret_cast<uint32_t *>(scales + (r * strips + strip) * 4) = word;
+                for (int i = 0; i < 8; ++i) m = max(m, finite_bits(f.v[i]));
+                top = max16(m);
+            }
+            const uint32_t byte = scale_byte(top);
+            store_cols<VEC>(q + r * cols, c, cols, cvt8(f, scale_inverse(byte)));
+            const uint32_t mine = strip * 4 + (lane >> 4) < kb ? byte : 127u;
+            uint32_t word = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) word |= (uint32_t)__builtin_amdgcn_readlane((int)mine, 16 * i) << (8 * i);
+            if (lane == 0) *reinterpret_cast<uint32_t *>(scales + (r * strips + strip) * 4) = word;
+        }
     }
 }
 
 // One workgroup per 128 x 128 tile of x, 64 values a thread (8 rows x 8
-// columns).  TR: q is [cols][rows], its blocks run along x's rows.
-// BLOCK_ROWS 128: one scale for the tile; 1 (TR only): one per column of x.
+// columns), kept packed.  TR: q is [cols][rows], its blocks run along x's rows;
+// the tiles are taken down x's rows in groups, so that what is written at a
+// time are neighbouring pieces of q's rows (across x's columns the pieces lie
+// a row of q apart: 80 against 71 us at 32768 x 2560).  BLOCK_ROWS 128: one
+// scale for the tile; 1 (TR only): one per column of x.
 template <typename T, bool VEC, bool TR, int BLOCK_ROWS>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(const T *x, int64_t rows, int64_t cols, uint8_t *q,
                                                             uint8_t *scales) {
     static_assert(TR || BLOCK_ROWS == 128, "rows of their own scale go through quantize_rows_kernel");
-    constexpr int kPitch = 128 + 16;
-    __shared__ uint32_t top_s[4][BLOCK_ROWS == 1 ? 128 : 1];
-    __shared__ __attribute__((aligned(16))) uint8_t tile[TR ? 128 * kPitch : 16];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    constexpr int kTops = BLOCK_ROWS == 1 ? 128 : 1;
+    __shared__ __attribute__((aligned(16))) uint32_t top_s[2][kTops < 8 ? 8 : kTops];
+    __shared__ __attribute__((aligned(16))) uint8_t tile[TR ? 128 * 128 : 16];
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;  // 8 columns from 8 cg, 8 rows from 8 rg
     const int64_t col_tiles = (cols + 127) / 128, row_tiles = (rows + 127) / 128;
-    for (int64_t tl = blockIdx.x; tl < col_tiles * row_tiles; tl += gridDim.x) {
-        const int64_t tr = tl / col_tiles, tc = tl - tr * col_tiles;
+    constexpr int64_t kGroup = 16;
+    int turn = 0;
+    for (int64_t tl = blockIdx.x; tl < col_tiles * row_tiles; tl += gridDim.x, turn ^= 1) {
+        int64_t tr = tl / col_tiles, tc = tl - tr * col_tiles;
+        if constexpr (TR) {
+            const int64_t grp = tl / (kGroup * col_tiles), in = tl - grp * kGroup * col_tiles;
+            const int64_t n = min(kGroup, row_tiles - grp * kGroup);
+            tc = in / n;
+            tr = grp * kGroup + in - tc * n;
+        }
         const int64_t r0 = tr * 128, c0 = tc * 128;
-        F8 v[8];
+        Raw8<T> v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t r = r0 + 8 * rg + j;
-            v[j] = F8{};
+            v[j] = Raw8<T>{};
             if (r < rows) v[j] = load_cols<VEC>(x + r * cols, c0 + 8 * cg, cols);
         }
-        uint32_t top[8];  // of this thread's columns
+        // (two sets in turn: this one was last read before the previous tile's barriers)
+        if (threadIdx.x < kTops) top_s[turn][threadIdx.x] = 0u;
+        Top8<T> top;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            top[i] = 0u;
+        for (int j = 0; j < 8; ++j) top.add(v[j]);
+        __syncthreads();
+        if (__any(top.all() >= kNotFinite)) {
+            uint32_t m[8] = {};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top[i] = max(top[i], finite_bits(v[j].v[i]));
-        }
-        if constexpr (BLOCK_ROWS == 128) {
+            for (int j = 0; j < 8; ++j) {
+                const F8 f = v[j].get();
 #pragma unroll
-            for (int i = 1; i < 8; ++i) top[0] = max(top[0], top[i]);
+                for (int i = 0; i < 8; ++i) m[i] = max(m[i], finite_bits(f.v[i]));
+            }
 #pragma unroll
-            for (int off = 32; off > 0; off >>= 1) top[0] = max(top[0], (uint32_t)__shfl_xor((int)top[0], off));
-            if (lane == 0) top_s[w][0] = top[0];
+            for (int i = 0; i < 8; ++i) atomicMax(&top_s[turn][BLOCK_ROWS == 1 ? 8 * cg + i : 0], m[i]);
         } else {
+            if constexpr (BLOCK_ROWS == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                top[i] = max(top[i], (uint32_t)__shfl_xor((int)top[i], 16));
-                top[i] = max(top[i], (uint32_t)__shfl_xor((int)top[i], 32));
-                if (lane < 16) top_s[w][8 * cg + i] = top[i];
+                for (int i = 0; i < 8; ++i) atomicMax(&top_s[turn][8 * cg + i], top.column(i));
+            } else {
+                const uint32_t m = max16(top.all());
+                if (cg == 0) atomicMax(&top_s[turn][0], m);
             }
         }
         __syncthreads();
         uint32_t byte[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = BLOCK_ROWS == 1 ? 8 * cg + i : 0;
-            byte[i] = scale_byte(max(max(top_s[0][at], top_s[1][at]), max(top_s[2][at], top_s[3][at])));
-        }
+        for (int i = 0; i < 8; ++i) byte[i] = scale_byte(top_s[turn][BLOCK_ROWS == 1 ? 8 * cg + i : 0]);
         // the scales' rows are filled up with ones to whole words
         const int64_t kb_all = TR ? row_tiles : col_tiles, pitch = (kb_all + 3) / 4 * 4;
         const int64_t kb = TR ? tr : tc;
@@ -200,27 +271,32 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T *x, int64_t 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int64_t r = r0 + 8 * rg + j;
-                if (r < rows) store_cols<VEC>(q + r * cols, c0 + 8 * cg, cols, cvt8(v[j], inv));
+                if (r < rows) store_cols<VEC>(q + r * cols, c0 + 8 * cg, cols, cvt8(v[j].get(), inv));
             }
-            __syncthreads();  // top_s is rewritten by the next tile
         } else {
-            // q^T through LDS: 8 bytes per column of x, then 16-byte pieces of q's rows
+            // q^T through LDS: unit rg of 8 bytes of row 8 cg + i sits at place
+            // rg ^ cg (16 lanes of a row group take 16 places), read back as
+            // 16-byte pieces of q's rows
+            F8 f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = v[j].get();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 F8 col;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) col.v[j] = v[j].v[i];
-                *reinterpret_cast<u32x2_t *>(&tile[(8 * cg + i) * kPitch + 8 * rg]) =
+                for (int j = 0; j < 8; ++j) col.v[j] = f[j].v[i];
+                *reinterpret_cast<u32x2_t *>(&tile[(8 * cg + i) * 128 + (rg ^ cg) * 8]) =
                     cvt8(col, scale_inverse(byte[i]));
             }
             __syncthreads();
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int i = p * 256 + threadIdx.x;
-                const int row = i >> 3, piece = (i & 7) * 16;
-                const int64_t qr = c0 + row, qc = r0 + piece;
+                const int row = i >> 3, piece = i & 7, g = row >> 3;
+                const int64_t qr = c0 + row, qc = r0 + piece * 16;
                 if (qr >= cols || qc >= rows) continue;
-                const u32x4_t b = *reinterpret_cast<const u32x4_t *>(&tile[row * kPitch + piece]);
+                u32x4_t b = *reinterpret_cast<const u32x4_t *>(&tile[row * 128 + ((2 * piece) ^ (g & ~1)) * 8]);
+                if (g & 1) b = u32x4_t{b[2], b[3], b[0], b[1]};
                 uint8_t *dst = q + qr * rows + qc;
                 if (rows % 16 == 0) {
                     *reinterpret_cast<u32x4_t *>(dst) = b;
@@ -230,7 +306,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T *x, int64_t 
                         if (qc + z < rows) dst[z] = (uint8_t)(b[z >> 2] >> (8 * (z & 3)));
                 }
             }
-            __syncthreads();  // tile and top_s are rewritten by the next tile
+            __syncthreads();  // the tile is rewritten by the next one
         }
     }
 }
@@ -241,9 +317,15 @@ void quantize(const QuantArgs &a, hipStream_t s) {
     uint8_t *q = static_cast<uint8_t *>(a.q);
     const int64_t most = (int64_t)1 << 22;  // a launch holds fewer than 2^32 threads
     if (a.block_rows == 1 && !a.transpose) {
-        const int64_t items = a.rows * ((a.cols + 511) / 512);
-        launch_kernel((quantize_rows_kernel<T, VEC>), dim3((unsigned)std::min((items + 3) / 4, most)), dim3(256), s, x,
-                      a.rows, a.cols, q, a.scales);
+        // four rows a wave where that still leaves eight waves a SIMD
+        const int64_t strips = (a.cols + 511) / 512;
+        const bool four = a.rows * strips >= 4 * 8192;
+        const int64_t items = (four ? (a.rows + 3) / 4 : a.rows) * strips;
+        const dim3 grid((unsigned)std::min((items + 3) / 4, most));
+        if (four)
+            launch_kernel((quantize_rows_kernel<T, VEC, 4>), grid, dim3(256), s, x, a.rows, a.cols, q, a.scales);
+        else
+            launch_kernel((quantize_rows_kernel<T, VEC, 1>), grid, dim3(256), s, x, a.rows, a.cols, q, a.scales);
         return;
     }
     const dim3 grid((unsigned)std::min((a.rows + 127) / 128 * ((a.cols + 127) / 128), most));
@@ -569,6 +651,85 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
 #endif
 }
 
+// Up to 16 rows of a (decode): 16 x 16 outputs per workgroup, its four waves
+// take every fourth block of K, fragments straight from global memory to
+// registers (nothing is shared that LDS would save), four blocks of a wave in
+// flight at once, and the four sums joined in LDS in order.  Such a product is
+// one round trip to memory long: what counts is that all of b is asked for at
+// once, by as many workgroups as it has rows of 16.
+template <bool F32>
+__global__ __launch_bounds__(256) void product_skinny_kernel(ProductArgs g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int PF = 4;
+    __shared__ f32x4_t sum_s[3][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tiles_n = (g.N + 15) / 16, tiles = tiles_n * ((g.M + 15) / 16);
+    const int split = (int)(blockIdx.x / tiles);
+    const int64_t tile = blockIdx.x - split * tiles;
+    const int64_t m0 = tile / tiles_n * 16, n0 = tile % tiles_n * 16;
+    const int64_t K = g.K;
+    const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
+    const int kb_first = split * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
+    const int fr = lane & 15, piece = 16 * (lane >> 4);
+    // rows past the end repeat the last one (their results are not stored)
+    const int64_t n = min(n0 + fr, g.N - 1), m = min(m0 + fr, g.M - 1);
+    const uint8_t *brow = g.b + n * K + piece, *bsc = g.b_scales + n / g.b_block_rows * pitch;
+    const uint8_t *arow = g.a + m * K + piece, *asc = g.a_scales + m / g.a_block_rows * pitch;
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int kb = kb_first + wave; kb < kb_last; kb += 4 * PF) {
+        Frag fb[PF], fa[PF];
+        uint32_t sb[PF], sa[PF];
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+            const int k = min(kb + 4 * p, kb_last - 1);  // (past the last: loaded, not used)
+            const int64_t o = (int64_t)k * 128;
+            const bool in0 = o + piece < K, in1 = o + piece + 64 < K;
+            fb[p].half[0] = in0 ? *reinterpret_cast<const u32x4_t *>(brow + o) : zero;
+            fb[p].half[1] = in1 ? *reinterpret_cast<const u32x4_t *>(brow + o + 64) : zero;
+            fa[p].half[0] = in0 ? *reinterpret_cast<const u32x4_t *>(arow + o) : zero;
+            fa[p].half[1] = in1 ? *reinterpret_cast<const u32x4_t *>(arow + o + 64) : zero;
+            sb[p] = bsc[k];
+            sa[p] = asc[k];
+        }
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+            if (kb + 4 * p >= kb_last) break;
+            if constexpr (F32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int h = q >> 1, o = 2 * (q & 1);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16x8(fb[p].half[h][o], fb[p].half[h][o + 1], sb[p]),
+                                                                  to_bf16x8(fa[p].half[h][o], fa[p].half[h][o + 1], sa[p]),
+                                                                  acc, 0, 0, 0);
+                }
+            } else {
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(e4m3x32(fb[p]), e4m3x32(fa[p]), acc, 0, 0, 0,
+                                                                       (int)sb[p], 0, (int)sa[p]);
+            }
+        }
+    }
+    if (wave > 0) sum_s[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) acc += sum_s[w][lane];
+    const int64_t mm = m0 + fr, nn = n0 + 4 * (lane >> 4);
+    if (mm >= g.M) return;
+    if (F32 || g.splits > 1) {
+        float *c = g.splits > 1 ? static_cast<float *>(g.ws) + split * g.split_elems : static_cast<float *>(g.c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (nn + r < g.N) c[mm * g.N + nn + r] = acc[r];
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (nn + r < g.N) static_cast<__bf16 *>(g.c)[mm * g.N + nn + r] = (__bf16)acc[r];
+    }
+#endif
+}
+
 // C = the splits' sums in order, rounded to the result's type.
 __global__ __launch_bounds__(256) void product_join_kernel(const float *parts, int32_t splits, int64_t split_elems,
                                                            int64_t n, void *c, bool out_bf16) {
@@ -592,25 +753,35 @@ __global__ __launch_bounds__(256) void product_join_kernel(const float *parts, i
     }
 }
 
-// How a product is cut: 256 x 256 tiles where they (or they and parts of K of
-// at least eight blocks) come to about one workgroup a CU, else 128 x 128 (64
-// or 16 rows of a where it has no more), the blocks of K in parts of at least
-// four where the tiles leave CUs idle.
+// How a product is cut.  256 x 256 tiles where they (or they and parts of K of
+// at least eight blocks) come to about one workgroup a CU; 128 x 128 where those
+// do; else 64 x 64 (1024 x 2560 x 1280: 12.1 us against 12.4 of 128 x 128, 128 x
+// 2560 x 1280: 6.1 against 11.2), or 16 x 16 by four waves for up to 16 rows of a
+// while 64 rows of b a workgroup would leave CUs idle (1 x 2560 x 1280: 4.4 us
+// against 6; 1 x 12800 x 1280: 7.8 against 6.1).  K is cut in parts of 16 blocks
+// and more where the tiles leave CUs idle (a second launch to join shorter parts
+// costs more than it saves: 64 x 12800 x 1280 in two, 9.6 + 3.1 us, whole 6.5).
 struct ProductCut {
-    bool wide;
-    int bm;
+    int tile;
     int32_t splits, split_blocks;
 };
 
 ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
     ProductCut c{};
-    auto tiles = [&](int bn, int bm) { return ((N + bn - 1) / bn) * ((M + bm - 1) / bm); };
+    auto tiles = [&](int t) { return ((N + t - 1) / t) * ((M + t - 1) / t); };
     const int64_t kb = (K + 127) / 128;
-    const int64_t wt = tiles(256, 256), ws = std::max<int64_t>(1, std::min<int64_t>(256 / wt, kb / 8));
-    c.wide = wt * ws >= 192;
-    c.bm = c.wide ? 256 : M > 64 ? 128 : M > 16 ? 64 : 16;
-    const int64_t t = c.wide ? wt : tiles(128, c.bm);
-    int64_t s = c.wide ? ws : std::max<int64_t>(1, std::min<int64_t>(256 / t, kb / 4));
+    const int64_t wt = tiles(256), ws = std::max<int64_t>(1, std::min<int64_t>(256 / wt, kb / 8));
+    int64_t s = ws;
+    if (M <= 16 && N <= 64 * 128) {
+        c.tile = 16;
+        s = std::min<int64_t>(512 / tiles(16), kb / 16);
+    } else if (wt * ws >= 192) {
+        c.tile = 256;
+    } else {
+        c.tile = tiles(128) >= 192 ? 128 : 64;
+        s = std::min<int64_t>(256 / tiles(c.tile), kb / 16);
+    }
+    s = std::max<int64_t>(s, 1);
     int64_t per = (kb + s - 1) / s;
     per += per & 1;  // scales are read two blocks at a time
     c.splits = (int32_t)((kb + per - 1) / per);
@@ -629,14 +800,15 @@ void product(const ProductArgs &g, hipStream_t s) {
 
 template <bool F32>
 void product_of(const ProductCut &c, const ProductArgs &g, hipStream_t s) {
-    if (c.wide)
+    if (c.tile == 256)
         product<F32, 256, 256, 2, 4, 2>(g, s);
-    else if (c.bm == 128)
-        product<F32, 128, 128, 2, 2, 4>(g, s);
-    else if (c.bm == 64)
-        product<F32, 128, 64, 4, 1, 4>(g, s);
+    else if (c.tile == 128)
+        product<F32, 128, 128, 2, 2, 2>(g, s);
+    else if (c.tile == 64)
+        product<F32, 64, 64, 2, 2, 4>(g, s);
     else
-        product<F32, 128, 16, 4, 1, 4>(g, s);
+        launch_kernel(product_skinny_kernel<F32>, dim3((unsigned)((g.N + 15) / 16 * ((g.M + 15) / 16) * g.splits)), dim3(256),
+                      s, g);
 }
 
 }  // namespace
