@@ -346,14 +346,14 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // lane group takes does not matter as long as both sides agree (the sum runs
 // over the whole block): pieces (l / 16) and (l / 16) + 4 of 16 bytes.
 //
-// A workgroup makes BN x BM outputs with WN x WM waves, each FN x FM fragments
-// of 16 x 16.  Both operands go from global memory straight into LDS, one
-// block of 128 along K a stage, two stages: while one is multiplied the other
-// fills.  A load instruction takes 8 rows x 128 bytes, whole cache lines (16 rows
-// x 64 bytes took 1.63 us a stage of 256 + 256 rows without the products, whole
-// lines 1.32).  A stage is its rows, b's first, 128 bytes each, the eight pieces
-// of a row XOR-swizzled by the row so that fragment reads take distinct banks.
-// Rows past the matrix and pieces past K read as zeros (the buffer's bounds).
+// A workgroup makes T x T outputs with WN x WM waves, each FN x FM fragments of
+// 16 x 16.  Both operands go from global memory straight into LDS, one block of
+// 128 along K a stage, while earlier stages are multiplied.  A load instruction
+// takes 8 rows x 128 bytes, whole cache lines (16 rows x 64 bytes took 1.63 us
+// a stage of 256 + 256 rows without the products, whole lines 1.32).  A stage is
+// rows of 128 bytes, the eight pieces of a row XOR-swizzled by the row so that
+// fragment reads take distinct banks.  Rows past the matrix and pieces past K
+// read as zeros (the buffer's bounds).
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 struct Frag {
@@ -452,56 +452,56 @@ __device__ __forceinline__ void store_bf16(const ProductArgs &g, const f32x4_t (
     }
 }
 
-template <bool F32, int BN, int BM, int WN, int WM, int NBUF>
+// NB = 2: two stages of b and three of a (160 KB of LDS at T = 256: all there
+// is; 80 KB at T = 128, two workgroups a CU), so that a's loads have two steps
+// to land.  NB = 4: four of each.
+template <bool F32, int T, int WN, int WM, int NB>
 __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g) {
 // (The host pass only needs the launch stub, and drops it where it cannot
 // check a device builtin's template-dependent arguments.)
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int W = WN * WM, FN = BN / 16 / WN, FM = BM / 16 / WM;
-    constexpr int kStage = (BN + BM) * 128;
-    constexpr int kBPerWave = BN / 8 / W, kAPerWave = (BM / 8 + W - 1) / W;
-    static_assert(BN / 8 % W == 0, "every wave loads as many row blocks of b");
-    static_assert(NBUF == 2 || NBUF == 4, "the scales' byte goes with the stage");
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t st2[NBUF == 4 ? kStage : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t st3[NBUF == 4 ? kStage : 16];
+    constexpr int W = WN * WM, FN = T / 16 / WN, FM = T / 16 / WM;
+    constexpr int kStage = T * 128;       // of one operand
+    constexpr int kPerWave = T / 8 / W;   // loads of a wave, operand and stage
+    static_assert(T / 8 % W == 0 && (NB == 2 || NB == 4), "stages");
+    // (separate arrays: the compiler then knows which of them a fragment read
+    // and a load in flight touch, and adds no waits of its own)
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t b1[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a1[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a2[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a3[NB == 4 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b2[NB == 4 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b3[NB == 4 ? kStage : 16];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t n0, m0;
     int split;
-    tile_origin<BN, BM>(g, n0, m0, split);
+    tile_origin<T, T>(g, n0, m0, split);
 
     const int64_t K = g.K;
     const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
     const int kb_first = split * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
 
-    const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)BN, g.N - n0) * K);
-    const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)BM, g.M - m0) * K);
+    const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)T, g.N - n0) * K);
+    const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)T, g.M - m0) * K);
     // lane l of a load fills row l / 8 of its 8-row block, place l % 8; piece c
     // of row r sits at place c ^ (r / 2 % 8): 16 consecutive rows of 128 bytes
     // take the 64 banks once (a wave's blocks are all even or all odd)
     static_assert(W % 2 == 0, "one swizzle for all blocks of a wave");
     const int lr = lane >> 3, lpiece = (lane & 7) ^ (((wave & 1) * 8 + lr) >> 1);
-    uint32_t boff[kBPerWave], aoff[kAPerWave];
+    uint32_t off[kPerWave];  // the same in either operand
 #pragma unroll
-    for (int i = 0; i < kBPerWave; ++i) boff[i] = (uint32_t)((wave + W * i) * 8 + lr) * (uint32_t)K + lpiece * 16;
-#pragma unroll
-    for (int i = 0; i < kAPerWave; ++i) aoff[i] = (uint32_t)((wave + W * i) * 8 + lr) * (uint32_t)K + lpiece * 16;
-
-    auto issue = [&](uint8_t *st, int kb) {
+    for (int i = 0; i < kPerWave; ++i) off[i] = (uint32_t)((wave + W * i) * 8 + lr) * (uint32_t)K + lpiece * 16;
+    auto issue = [&](const __amdgpu_buffer_rsrc_t &res, uint8_t *st, int kb) {
         const int k = kb * 128;
         const bool in_k = k + lpiece * 16 < (int)K;
 #pragma unroll
-        for (int i = 0; i < kBPerWave; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
-                                                     in_k ? boff[i] : kPast, k, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kAPerWave; ++i)
-            if (BM / 8 % W == 0 || wave + W * i < BM / 8)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t *)(st + (BN / 8 + wave + W * i) * 1024), 16,
-                                                         in_k ? aoff[i] : kPast, k, 0, 0);
+        for (int i = 0; i < kPerWave; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
+                                                     in_k ? off[i] : kPast, k, 0, 0);
         // (the scheduler would put the fills off until they are waited for)
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         f.half[1] = read_half(st, blk, 1);
         return f;
     };
-    auto compute = [&](const uint8_t *st, auto opc) {
+    auto compute = [&](const uint8_t *sta, const uint8_t *stb, auto opc) {
         constexpr int OP = decltype(opc)::value;  // which byte of sb and sa
         if constexpr (F32) {
             // half a block at a time: its expanded a side is 8 FM registers
@@ -549,14 +549,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
                 bf16x8_t ha[FM][2];
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    const u32x4_t w = read_half(st, BN / 16 + wm + j, h);
+                    const u32x4_t w = read_half(sta, wm + j, h);
                     const uint32_t s = (sa[j] >> (8 * OP)) & 0xFFu;
                     ha[j][0] = to_bf16x8(w[0], w[1], s);
                     ha[j][1] = to_bf16x8(w[2], w[3], s);
                 }
 #pragma unroll
                 for (int i = 0; i < FN; ++i) {
-                    const u32x4_t w = read_half(st, wn + i, h);
+                    const u32x4_t w = read_half(stb, wn + i, h);
                     const uint32_t s = (sb[i] >> (8 * OP)) & 0xFFu;
                     const bf16x8_t hb[2] = {to_bf16x8(w[0], w[1], s), to_bf16x8(w[2], w[3], s)};
 #pragma unroll
@@ -569,10 +569,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         } else {
             Frag fa[FM];
 #pragma unroll
-            for (int j = 0; j < FM; ++j) fa[j] = read_frag(st, BN / 16 + wm + j);
+            for (int j = 0; j < FM; ++j) fa[j] = read_frag(sta, wm + j);
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
-                const Frag fb = read_frag(st, wn + i);
+                const Frag fb = read_frag(stb, wn + i);
 #pragma unroll
                 for (int j = 0; j < FM; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -581,24 +581,29 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         }
     };
 
-    // Block kb sits in stage (kb - kb_first) % NBUF (kb_first is even).  Each
-    // step: its loads have landed everywhere (those of the NBUF - 2 blocks
-    // behind it may be in flight) and the stage of the block before is free,
-    // fill that one, multiply.  (The last fills lie past K, or past this
-    // split: never multiplied.)  A pair's scales are loaded a pair ahead.
+    // Each step: this block's loads have landed everywhere (later ones, kAhead
+    // a wave, may be in flight) and the stages of the block before are free:
+    // fill them, multiply.  (The last fills lie past K, or past this split:
+    // never multiplied.)  kb_first is even; a pair's scales are loaded a pair
+    // ahead.
+    constexpr int kAhead = NB == 2 ? kPerWave : 4 * kPerWave;
     uint32_t sb_next[FN], sa_next[FM];
     load_scales(kb_first, sb, sa);
-    issue(st0, kb_first);
-    if constexpr (NBUF == 4) {
-        issue(st1, kb_first + 1);
-        issue(st2, kb_first + 2);
+    issue(bres, b0, kb_first);
+    issue(ares, a0, kb_first);
+    if constexpr (NB == 4) issue(bres, b1, kb_first + 1);
+    issue(ares, a1, kb_first + 1);
+    if constexpr (NB == 4) {
+        issue(bres, b2, kb_first + 2);
+        issue(ares, a2, kb_first + 2);
     }
     int kb = kb_first;
-    auto step = [&](const uint8_t *cur, uint8_t *fill, auto opc) {
-        stage_barrier<(NBUF - 2) * kBPerWave>();
+    auto step = [&](const uint8_t *cur_a, const uint8_t *cur_b, uint8_t *fill_a, uint8_t *fill_b, auto opc) {
+        stage_barrier<kAhead>();
         if constexpr (decltype(opc)::value == 0) load_scales(kb + 2, sb_next, sa_next);
-        issue(fill, kb + NBUF - 1);
-        compute(cur, opc);
+        issue(bres, fill_b, kb + NB - 1);
+        issue(ares, fill_a, kb + (NB == 2 ? 2 : 3));
+        compute(cur_a, cur_b, opc);
         if constexpr (decltype(opc)::value == 1) {
 #pragma unroll
             for (int i = 0; i < FN; ++i) sb[i] = sb_next[i];
@@ -610,14 +615,18 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
     constexpr std::integral_constant<int, 0> even{};
     constexpr std::integral_constant<int, 1> odd{};
     for (;;) {
-        if constexpr (NBUF == 2) {
-            if (step(st0, st1, even)) break;
-            if (step(st1, st0, odd)) break;
+        if constexpr (NB == 2) {
+            if (step(a0, b0, a2, b1, even)) break;
+            if (step(a1, b1, a0, b0, odd)) break;
+            if (step(a2, b0, a1, b1, even)) break;
+            if (step(a0, b1, a2, b0, odd)) break;
+            if (step(a1, b0, a0, b1, even)) break;
+            if (step(a2, b1, a1, b0, odd)) break;
         } else {
-            if (step(st0, st3, even)) break;
-            if (step(st1, st0, odd)) break;
-            if (step(st2, st1, even)) break;
-            if (step(st3, st2, odd)) break;
+            if (step(a0, b0, a3, b3, even)) break;
+            if (step(a1, b1, a0, b0, odd)) break;
+            if (step(a2, b2, a1, b1, even)) break;
+            if (step(a3, b3, a2, b2, odd)) break;
         }
     }
     stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
@@ -645,9 +654,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         }
         return;
     }
-    static_assert(W / 2 * FM * 16 * FN * 32 <= kStage, "half of the waves' tiles in each stage");
-    store_bf16<FN, FM>(g, acc, (wave < W / 2 ? st0 : st1) + (wave % (W / 2)) * FM * 16 * FN * 32, m0 + wm * 16,
-                       n0 + wn * 16, lane);
+    constexpr int kImage = FM * 16 * FN * 32, kImages = kStage / kImage;
+    static_assert(kImages * 4 >= W, "the waves' images in four stages");
+    uint8_t *const home = wave / kImages == 0 ? b0 : wave / kImages == 1 ? b1 : wave / kImages == 2 ? a0 : a1;
+    store_bf16<FN, FM>(g, acc, home + wave % kImages * kImage, m0 + wm * 16, n0 + wn * 16, lane);
 #endif
 }
 
@@ -791,21 +801,21 @@ ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
 
 int64_t split_elems_of(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
 
-template <bool F32, int BN, int BM, int WN, int WM, int NBUF>
+template <bool F32, int T, int WN, int WM, int NB>
 void product(const ProductArgs &g, hipStream_t s) {
-    const int64_t tiles = ((g.N + BN - 1) / BN) * ((g.M + BM - 1) / BM);
-    launch_kernel((product_kernel<F32, BN, BM, WN, WM, NBUF>), dim3((unsigned)(tiles * g.splits)), dim3(64 * WN * WM), s,
+    const int64_t tiles = ((g.N + T - 1) / T) * ((g.M + T - 1) / T);
+    launch_kernel((product_kernel<F32, T, WN, WM, NB>), dim3((unsigned)(tiles * g.splits)), dim3(64 * WN * WM), s,
                   g);
 }
 
 template <bool F32>
 void product_of(const ProductCut &c, const ProductArgs &g, hipStream_t s) {
     if (c.tile == 256)
-        product<F32, 256, 256, 2, 4, 2>(g, s);
+        product<F32, 256, 2, 4, 2>(g, s);
     else if (c.tile == 128)
-        product<F32, 128, 128, 2, 2, 2>(g, s);
+        product<F32, 128, 2, 2, 2>(g, s);
     else if (c.tile == 64)
-        product<F32, 64, 64, 2, 2, 4>(g, s);
+        product<F32, 64, 2, 2, 4>(g, s);
     else
         launch_kernel(product_skinny_kernel<F32>, dim3((unsigned)((g.N + 15) / 16 * ((g.M + 15) / 16) * g.splits)), dim3(256),
                       s, g);
