@@ -391,6 +391,12 @@ __device__ __forceinline__ void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// This wave's loads have landed.
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));  // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
 constexpr int kXcds = 8;
 constexpr uint32_t kPast = 0x80000000u;  // an offset behind every buffer
 
@@ -629,10 +635,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
             if (step(a3, b3, a2, b2, odd)) break;
         }
     }
-    stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
-
     if (g.splits > 1 || F32) {
-        // fp32: a lane's four n of one m, 16 bytes
+        // fp32: a lane's four n of one m, 16 bytes (the last fills have to land
+        // before the workgroup's LDS is given away)
+        wait_loads();
         float *c = g.splits > 1 ? static_cast<float *>(g.ws) + (int64_t)split * g.split_elems : static_cast<float *>(g.c);
         const bool vec = g.N % 4 == 0;
 #pragma unroll
@@ -654,6 +660,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         }
         return;
     }
+    stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
     constexpr int kImage = FM * 16 * FN * 32, kImages = kStage / kImage;
     static_assert(kImages * 4 >= W, "the waves' images in four stages");
     uint8_t *const home = wave / kImages == 0 ? b0 : wave / kImages == 1 ? b1 : wave / kImages == 2 ? a0 : a1;
