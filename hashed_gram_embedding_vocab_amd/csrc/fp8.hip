@@ -104,6 +104,19 @@ __device__ __forceinline__ u32x2_t cvt8(const F8 &x, float inv) {
     return q;
 }
 
+// Vectors at any address (the hardware splits an access where it has to):
+// rows whose length is no multiple of the vector's.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ Raw8<uint16_t> load_any8(const uint16_t *p) {
+    return Raw8<uint16_t>{*reinterpret_cast<const u32x4_any *>(p)};
+}
+__device__ __forceinline__ Raw8<float> load_any8(const float *p) {
+    return Raw8<float>{*reinterpret_cast<const f32x4_any *>(p), *reinterpret_cast<const f32x4_any *>(p + 4)};
+}
+
 // 8 values at column c of a row of `cols`, zeros past its end.  VEC: rows are
 // whole 8-value units and 16-byte aligned.
 template <bool VEC, typename T>
@@ -111,9 +124,11 @@ __device__ __forceinline__ Raw8<T> load_cols(const T *row, int64_t c, int64_t co
     Raw8<T> x = {};
     if constexpr (VEC) {
         if (c < cols) x = load_raw8(row + c);
+    } else if (c + 8 <= cols) {
+        x = load_any8(row + c);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 7; ++i)
             if (c + i < cols) {
                 if constexpr (sizeof(T) == 2)
                     x.w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
@@ -130,9 +145,11 @@ template <bool VEC>
 __device__ __forceinline__ void store_cols(uint8_t *row, int64_t c, int64_t cols, u32x2_t q) {
     if constexpr (VEC) {
         if (c < cols) *reinterpret_cast<u32x2_t *>(row + c) = q;
+    } else if (c + 8 <= cols) {
+        *reinterpret_cast<u32x2_any *>(row + c) = q;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 7; ++i)
             if (c + i < cols) row[c + i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
     }
 }
@@ -300,6 +317,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T *x, int64_t 
                 uint8_t *dst = q + qr * rows + qc;
                 if (rows % 16 == 0) {
                     *reinterpret_cast<u32x4_t *>(dst) = b;
+                } else if (qc + 16 <= rows) {
+                    *reinterpret_cast<u32x4_any *>(dst) = b;
                 } else {
 #pragma unroll
                     for (int z = 0; z < 16; ++z)
@@ -448,11 +467,14 @@ __device__ __forceinline__ void store_bf16(const ProductArgs &g, const f32x4_t (
         const int64_t m = m0 + r, n = n0 + piece * 8;
         if (m >= g.M) continue;
         uint16_t *dst = c + m * g.N + n;
-        if (vec) {
-            if (n < g.N) *reinterpret_cast<u32x4_t *>(dst) = v;
+        if (n + 8 <= g.N) {
+            if (vec)
+                *reinterpret_cast<u32x4_t *>(dst) = v;
+            else
+                *reinterpret_cast<u32x4_any *>(dst) = v;
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 7; ++e)
                 if (n + e < g.N) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
         }
     }
@@ -640,7 +662,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
         // before the workgroup's LDS is given away)
         wait_loads();
         float *c = g.splits > 1 ? static_cast<float *>(g.ws) + (int64_t)split * g.split_elems : static_cast<float *>(g.c);
-        const bool vec = g.N % 4 == 0;
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int64_t m = m0 + (wm + j) * 16 + (lane & 15);
@@ -649,11 +670,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
             for (int i = 0; i < FN; ++i) {
                 const int64_t n = n0 + (wn + i) * 16 + 4 * (lane >> 4);
                 float *dst = c + m * g.N + n;
-                if (vec) {
-                    if (n < g.N) *reinterpret_cast<f32x4_t *>(dst) = acc[i][j];
+                if (n + 4 <= g.N) {
+                    *reinterpret_cast<f32x4_any *>(dst) = acc[i][j];
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int r = 0; r < 3; ++r)
                         if (n + r < g.N) dst[r] = acc[i][j][r];
                 }
             }
