@@ -5,8 +5,9 @@
 // Forward: h[m][t] = round(scale * table[id_t]), a row copy.
 //
 // Backward: dtable[r] = scale * sum over {t : id_t = r} (ascending) and
-// branches m of dh[m][t], in three launches whose results depend on the
-// tokens alone (no float atomics):
+// branches m of dh[m][t], with no float atomics: the results depend on the
+// inputs alone.  Up to 512 tokens one launch does it all (embed_few_kernel);
+// beyond that three:
 //   embed_sort_kernel   stable counting sort of the token positions by id;
 //                       beside it the table's first rows are filled with zeros.
 //   embed_rows_kernel   sums of the runs inside each chunk of sorted
@@ -56,10 +57,11 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t *tokens, int64
 // L2).  First pass: how many tokens have a lower id (where the bucket's
 // output starts; no workgroup waits for another), and a count per id and
 // wave.  Second pass: wave w places the tokens of its contiguous share in
-// order, 64 at a time, equal ids ranked by ballot.  The cost is n_tok * (vocab
-// / kBucket) id reads.
+// order, 64 at a time, equal ids ranked by a ballot per bit of the id's place
+// in the bucket.  The cost is n_tok * (vocab / kBucket) id reads.
 constexpr int kSortWaves = 16;
-constexpr int kBucket = 512;
+constexpr int kBucketBits = 9;
+constexpr int kBucket = 1 << kBucketBits;
 
 // Bytes of the table that a block of the fill clears.
 constexpr int64_t kFillBytes = (int64_t)64 * kSortWaves * 16 * 16;
@@ -88,8 +90,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32
     const int64_t share = (n_tok + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
     const int64_t first = min(w * share, n_tok), last = min(first + share, n_tok);
     uint32_t below = 0u;
+    int32_t id[8];
     for (int64_t g = first; g < last; g += 64 * 8) {
-        int32_t id[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int64_t t = g + 64 * u + lane;
@@ -133,41 +135,37 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const int32
     }
     __syncthreads();
     for (int64_t g = first; g < last; g += 64 * 8) {
-        int32_t id[8];
+        if (share > 64 * 8) {  // (else the first pass left them in id)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t t = g + 64 * u + lane;
-            id[u] = t < last ? tokens[t] : -1;
+            for (int u = 0; u < 8; ++u) {
+                const int64_t t = g + 64 * u + lane;
+                id[u] = t < last ? tokens[t] : -1;
+            }
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const bool mine = id[u] >= lo && id[u] - lo < n_ids;
-            uint64_t left = __ballot(mine);
-            while (left) {
-                const int32_t x = __builtin_amdgcn_readlane(id[u], __builtin_ctzll(left));
-                const bool peer = mine && id[u] == x;
-                const uint64_t peers = __ballot(peer);
-                const uint32_t at = cnt[w][x - lo];
-                // (a wave's LDS accesses complete in order: every lane has read the slot)
-                asm volatile("" ::: "memory");
-                if (peer) {
-                    const uint32_t pos = at + (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
-                    order[pos] = (uint32_t)(g + 64 * u + lane);
-                    sid[pos] = x;
-                    if ((peers >> lane) == 1ull) cnt[w][x - lo] = pos + 1u;
-                }
-                asm volatile("" ::: "memory");
-                left &= ~peers;
+            uint64_t peers = __ballot(mine);
+            if (peers == 0ull) continue;
+            const uint32_t at = mine ? (uint32_t)(id[u] - lo) : 0u;
+#pragma unroll
+            for (int bit = 0; bit < kBucketBits; ++bit) {
+                const bool set = ((at >> bit) & 1u) != 0u;
+                const uint64_t m = __ballot(set);
+                peers &= set ? m : ~m;
             }
+            if (mine) {
+                const uint32_t pos = cnt[w][at] + (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
+                order[pos] = (uint32_t)(g + 64 * u + lane);
+                sid[pos] = id[u];
+                // (a wave's LDS accesses complete in order: every peer has read the slot)
+                asm volatile("" ::: "memory");
+                if ((peers >> lane) == 1ull) cnt[w][at] = pos + 1u;
+            }
+            asm volatile("" ::: "memory");
         }
     }
 }
-
-// Sorted positions per wave: 32, or 8 where that leaves the chip short of waves
-// (333 tokens x 256 channels: the sums take 5 us instead of 12, the join of
-// longer chains of parts no longer).
-int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= 65536 ? 32 : 8; }
-constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 
 __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, bool accumulate) {
     F8 x;
@@ -180,6 +178,83 @@ __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, 
     }
     store8(dst, x);
 }
+
+// Up to kFew tokens: the gradient in one launch, whose three would each be no
+// longer than their launch.  A wave per (token, 512 channels) finds the tokens
+// of the same id by ballot, leaves if one comes before, and adds all of them
+// in order.  Blocks from sum_blocks on write zeros to the rows without tokens.
+constexpr int kFew = 512;
+
+template <typename T, int BR>
+__global__ __launch_bounds__(256) void embed_few_kernel(const int32_t *tokens, int32_t n_tok, int32_t vocab, int32_t d,
+                                                        const T *dh, float scale, bool accumulate, float *dtable,
+                                                        uint32_t sum_blocks) {
+    constexpr int U = BR <= 2 ? 8 : 4;
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (blockIdx.x >= sum_blocks) {
+        const int64_t r0 = (wave - (int64_t)sum_blocks * 4) * 8;
+        uint32_t named = 0u;  // bit k: row r0 + k has a token
+        for (int32_t g = 0; g < n_tok; g += 64) {
+            const int64_t k = g + lane < n_tok ? tokens[g + lane] - r0 : -1;
+            const bool near = k >= 0 && k < 8;
+            if (__ballot(near) == 0ull) continue;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) named |= __ballot(near && k == q) != 0ull ? 1u << q : 0u;
+        }
+        for (int64_t r = r0; r < min(r0 + 8, (int64_t)vocab); ++r) {
+            if ((named >> (r - r0)) & 1u) continue;
+            for (int32_t c = lane * 4; c < d; c += 256)
+                *reinterpret_cast<f32x4_t *>(dtable + r * d + c) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        return;
+    }
+    const int32_t strips = (d + 511) / 512;
+    const int32_t t0 = (int32_t)(wave / strips), col = (int32_t)(wave % strips) * 512 + lane * 8;
+    if (t0 >= n_tok) return;
+    const int32_t id = tokens[t0];
+    if (id < 0 || id >= vocab) return;
+    for (int32_t g = 0; g < t0; g += 64)
+        if (__ballot(g + lane < t0 && tokens[g + lane] == id) != 0ull) return;  // the first one's wave does it
+    const bool in = col < d;
+    F8 acc = {};
+    for (int32_t g = t0 / 64 * 64; g < n_tok; g += 64) {
+        uint64_t left = __ballot(g + lane >= t0 && g + lane < n_tok && tokens[min(g + lane, n_tok - 1)] == id);
+        while (left) {
+            Raw8<T> x[U][BR];
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (left == 0ull) break;
+                const int32_t t = g + __builtin_ctzll(left);
+                left &= left - 1ull;
+                ++n;
+#pragma unroll
+                for (int m = 0; m < BR; ++m) {
+                    x[u][m] = Raw8<T>{};
+                    if (in) x[u][m] = load_raw8(dh + ((int64_t)m * n_tok + t) * d + col);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u >= n) break;
+#pragma unroll
+                for (int m = 0; m < BR; ++m) {
+                    const F8 v = x[u][m].get();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc.v[i] += v.v[i];
+                }
+            }
+        }
+    }
+    if (in) put_row(dtable + (int64_t)id * d + col, acc, scale, accumulate);
+}
+
+// Sorted positions per wave: 32, or 8 where that leaves the chip short of waves
+// (333 tokens x 256 channels: the sums take 5 us instead of 12, the join of
+// longer chains of parts no longer).
+int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= 65536 ? 32 : 8; }
+constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 
 // One wave per (run_chunk sorted positions, 512 channels) adds the chunk's rows
 // in order.  A run that lies inside the chunk goes to its table row; the part
@@ -306,6 +381,22 @@ int64_t fill_rows(int32_t vocab, int32_t d) {
 }
 
 template <typename T>
+void embed_few(const EmbedBwdArgs &a, hipStream_t s) {
+    const uint32_t sum_blocks = (uint32_t)((a.n_tok * ((a.d + 511) / 512) + 3) / 4);
+    const dim3 grid(sum_blocks + (a.accumulate ? 0u : (uint32_t)(((int64_t)a.vocab + 31) / 32)));
+#define ENGRAM_EMBED_FEW(BR)                                                                                      \
+    launch_kernel((embed_few_kernel<T, BR>), grid, dim3(256), s, a.tokens, (int32_t)a.n_tok, a.vocab, a.d,        \
+                  static_cast<const T *>(a.dh), a.scale, a.accumulate, a.dtable, sum_blocks)
+    switch (a.n_branches) {
+        case 1: ENGRAM_EMBED_FEW(1); break;
+        case 2: ENGRAM_EMBED_FEW(2); break;
+        case 3: ENGRAM_EMBED_FEW(3); break;
+        default: ENGRAM_EMBED_FEW(4); break;
+    }
+#undef ENGRAM_EMBED_FEW
+}
+
+template <typename T>
 void embed_rows(const EmbedBwdArgs &a, hipStream_t s) {
     const int64_t chunks = embed_chunks(a.n_tok, a.d), strips = (a.d + 511) / 512;
     const uint32_t sum_blocks = (uint32_t)((chunks * strips + 3) / 4);
@@ -351,6 +442,13 @@ bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d) {
 }
 
 void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s) {
+    if (a.n_tok <= kFew) {
+        if (dt == ENGRAM_BF16)
+            embed_few<uint16_t>(a, s);
+        else
+            embed_few<float>(a, s);
+        return;
+    }
     const int64_t fill = a.accumulate ? 0 : fill_rows(a.vocab, a.d) * a.d * 4;
     const int64_t sorts = sort_blocks(a.vocab), fills = (fill + kFillBytes - 1) / kFillBytes;
     launch_kernel(embed_sort_kernel, dim3((unsigned)(sorts + fills)), dim3(64 * kSortWaves), s, a.tokens, a.n_tok, a.vocab,

@@ -161,14 +161,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(const T *x,
     }
 }
 
-// A block's rows' dgamma and dbeta sums end as one row of `part` [2][blocks][d].
+// A block's rows' dgamma and dbeta sums end as one row of `part` [2][blocks][d],
+// or, where the launch is one block, in dgamma and dbeta themselves.
 // x and dy stay packed as loaded and are expanded twice (for the sums, for dx):
 // expanded once they would take the registers of the next row's loads.
 template <typename T, int L, int W, int NCH>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_bwd_kernel(const T *x, const T *dy, int64_t n_rows,
                                                                         int32_t d, const float *gamma,
                                                                         const float *mean, const float *rstd, T *dx,
-                                                                        float *part) {
+                                                                        float *part, bool accumulate, float *dgamma,
+                                                                        float *dbeta) {
     __shared__ float red[2][2][W];
     __shared__ float sum_s[W == 1 ? 4 : 1][W == 1 ? NCH * 512 : 1];
     const Rows<L, W> at;
@@ -260,7 +262,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_bwd_kernel(const T
                 for (int ww = 0; ww < 4; ++ww)
 #pragma unroll
                     for (int l = 0; l < 64; l += L) t += sum_s[ww][at0 + l];
-                part[((int64_t)q * gridDim.x + blockIdx.x) * d + k] = t;
+                float *dst = q == 0 ? dgamma : dbeta;
+                if (gridDim.x > 1)
+                    part[((int64_t)q * gridDim.x + blockIdx.x) * d + k] = t;
+                else if (dst)
+                    dst[k] = accumulate ? dst[k] + t : t;
             }
         }
     } else {
@@ -268,8 +274,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_bwd_kernel(const T
         for (int j = 0; j < NCH; ++j) {
             const int c = at.c0 + 512 * W * j;
             if (c < d) {
-                store8(part + (int64_t)blockIdx.x * d + c, dg[j]);
-                store8(part + ((int64_t)gridDim.x + blockIdx.x) * d + c, db[j]);
+                if (gridDim.x > 1) {
+                    store8(part + (int64_t)blockIdx.x * d + c, dg[j]);
+                    store8(part + ((int64_t)gridDim.x + blockIdx.x) * d + c, db[j]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float *dst = q == 0 ? dgamma : dbeta;
+                        if (!dst) continue;
+                        F8 s = q == 0 ? dg[j] : db[j];
+                        if (accumulate) {
+                            const F8 old = load8(dst + c);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) s.v[i] = old.v[i] + s.v[i];
+                        }
+                        store8(dst + c, s);
+                    }
+                }
             }
         }
     }
@@ -353,10 +374,11 @@ void norm_bwd(const NormArgs &a, hipStream_t s) {
 #define ENGRAM_NORM_BWD(L, W, N)                                                                                 \
     launch_kernel((norm_bwd_kernel<T, L, W, N>), dim3((unsigned)blocks), dim3(W == 1 ? 256 : 64 * W), s,         \
                   static_cast<const T *>(a.x), static_cast<const T *>(a.dy), a.n_rows, a.d, a.gamma, a.mean,     \
-                  a.rstd, static_cast<T *>(a.dx), a.part)
+                  a.rstd, static_cast<T *>(a.dx), a.part, a.accumulate, a.dgamma, a.dbeta)
     ENGRAM_NORM_SWITCH(ENGRAM_NORM_BWD, sh)
 #undef ENGRAM_NORM_BWD
-    launch_kernel(norm_bwd_sum_kernel, dim3((unsigned)((a.d + 63) / 64), 2), dim3(1024), s, a.part, blocks, a.d,
+    if (blocks > 1)
+        launch_kernel(norm_bwd_sum_kernel, dim3((unsigned)((a.d + 63) / 64), 2), dim3(1024), s, a.part, blocks, a.d,
                   a.accumulate, a.dgamma, a.dbeta);
 }
 
@@ -366,6 +388,8 @@ bool norm_fits(int32_t d) { return d <= 16 * 4 * 512; }
 
 int32_t norm_bwd_blocks(int64_t n_rows, int32_t d) {
     const RowShape sh = row_shape(d);
+    // four rows a wave take less than the second launch
+    if (n_rows <= 4 * sh.at_once()) return 1;
     return (int32_t)norm_blocks(sh, n_rows, sh.steps == 1 ? 4 : 2);
 }
 

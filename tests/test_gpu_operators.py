@@ -125,6 +125,9 @@ IDS = {
     ("one", 33, 513, 64, 2, 1.0), ("one", 1500, 2000, 72, 1, 1.0), ("none", 65, 600, 64, 1, 1.0),
     ("two", 4097, 1025, 128, 1, 1.0), ("rising", 3000, 1000, 64, 4, 1.0),
     # enough tokens for chunks of 32 sorted positions
+    # (513 tokens and more are sorted, with chunks of 8 positions)
+    ("zipf", 512, 1000, 64, 1, 1.0), ("one", 512, 33, 520, 3, 1.0), ("two", 512, 40, 64, 4, 1.0), ("zipf", 513, 20, 64, 1, 1.0),
+    ("rising", 500, 300, 1032, 2, 1.0), ("zipf", 2410, 291, 136, 1, 0.25), ("none", 1000, 600, 64, 1, 1.0),
     ("zipf", 65537, 1537, 64, 1, 0.5), ("one", 65600, 513, 64, 1, 1.0), ("two", 66001, 700, 64, 2, 1.0),
     ("rising", 33000, 33100, 520, 1, 1.0)])
 def test_embed_backward(gpu, dtype, ids_of, n_tok, vocab, d, branches, scale):
