@@ -508,6 +508,41 @@ def test_matmul(gpu, out, abr, bbr, m, n, k):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("abr,bbr", [(1, 128), (1, 1)])
+@pytest.mark.parametrize("m,n,k", [(4100, 3900, 272), (8190, 1601, 1296), (2563, 1285, 8208), (3000, 2100, 400)])
+def test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k):
+    """Shapes that take 256 x 256 tiles (the third with K cut in parts), then 128 x 128; the
+    bounds as above, with a block's largest product bounded by its operands' largest."""
+    p = make_plan()
+    a, sa = (t.to(gpu) for t in random_quantized(m, k, abr, 47))
+    b, sb = (t.to(gpu) for t in random_quantized(n, k, bbr, 49))
+    got = torch.full((m, n), 7.0, dtype=tdt(out), device=gpu)
+    p.engram_matmul_fp8(a, sa, b, sb, got, p.matmul_fp8_workspace(m, n, k), a_block_rows=abr, b_block_rows=bbr)
+    av = a.double() * spread_bytes(sa.cpu(), m, k, abr).to(gpu)
+    bv = b.double() * spread_bytes(sb.cpu(), n, k, bbr).to(gpu)
+    ref, mag = av @ bv.t().contiguous(), av.abs() @ bv.abs().t().contiguous()
+    bound = 2 * U * (k + 2) * mag
+    if out == "bf16":
+        top = lambda v: torch.nn.functional.pad(v.abs(), (0, -k % 128)).reshape(len(v), -1, 128).amax(-1)  # noqa: E731
+        bound = bound + (128 * 2.0 ** -13) * (top(av) @ top(bv).t().contiguous())
+    assert bool(((got.double() - ref).abs() <= bound + half_step(out) * (ref.abs() + bound)).all())
+
+
+def test_matmul_result_larger_than_the_caches(gpu):
+    """A bf16 result over 256 MB; sums of at most 64 ones are exact in bf16."""
+    p = make_plan()
+    m, n, k = 11600, 11704, 64
+    one = torch.full((1,), 127, dtype=torch.uint8, device=gpu)
+    a = torch.randint(-1, 2, (m, k), generator=gen(1)).float().to(gpu)
+    b = torch.randint(-1, 2, (n, k), generator=gen(2)).float().to(gpu)
+    got = torch.full((m, n), 7.0, dtype=torch.bfloat16, device=gpu)
+    f8 = torch.float8_e4m3fn
+    p.engram_matmul_fp8(a.to(f8), one.expand(m, 4).contiguous(), b.to(f8), one.expand(n, 4).contiguous(), got,
+                        p.matmul_fp8_workspace(m, n, k), b_block_rows=1)
+    assert torch.equal(got.float(), a @ b.t().contiguous())
+
+
 def test_matmul_of_whole_numbers_is_exact(gpu):
     """Small whole numbers and scales of one: every partial sum is a whole number below 2^24."""
     p = make_plan()
