@@ -519,6 +519,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
 
     const __amdgpu_buffer_rsrc_t bres = make_rsrc(g.b + n0 * K, min((int64_t)T, g.N - n0) * K);
     const __amdgpu_buffer_rsrc_t ares = make_rsrc(g.a + m0 * K, min((int64_t)T, g.M - m0) * K);
+    // (A load's row and piece are its vector offset, which the buffer's bounds
+    // cover; the position along K is the scalar one, inside the row by in_k.)
     // lane l of a load fills row l / 8 of its 8-row block, place l % 8; piece c
     // of row r sits at place c ^ (r / 2 % 8): 16 consecutive rows of 128 bytes
     // take the 64 banks once (a wave's blocks are all even or all odd)
@@ -544,19 +546,24 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
     const int64_t bs0 = n0 / g.b_block_rows, as0 = m0 / g.a_block_rows;
     const __amdgpu_buffer_rsrc_t bsres = make_rsrc(g.b_scales + bs0 * pitch, (brows - bs0) * pitch);
     const __amdgpu_buffer_rsrc_t asres = make_rsrc(g.a_scales + as0 * pitch, (arows - as0) * pitch);
-    // (a wave's rows of one side lie in one block of 128, so they share a scale row there)
+    // (a wave's rows of one side lie in one block of 128, so they share a scale
+    // row there; the whole offset is the vector one, which the buffer's bounds
+    // cover: rows and blocks past the end read as zero)
     const uint32_t bsoff = (uint32_t)((g.b_block_rows == 1 ? wn * 16 + (lane & 15) : wn / 8) * pitch);
     const uint32_t asoff = (uint32_t)((g.a_block_rows == 1 ? wm * 16 + (lane & 15) : wm / 8) * pitch);
     const int bstep = g.b_block_rows == 1 ? 16 * pitch : 0, astep = g.a_block_rows == 1 ? 16 * pitch : 0;
     static_assert(FN <= 8 && 8 % FN == 0 && FM <= 8 && 8 % FM == 0, "a wave's rows inside one block of 128");
     uint32_t sb[FN], sa[FM];
     auto load_scales = [&](int kb, uint32_t (&b2)[FN], uint32_t (&a2)[FM]) {
+        // (opaque, or the sums of all rows are kept in registers across the loop)
+        uint32_t bo = bsoff, ao = asoff;
+        asm volatile("" : "+v"(bo), "+v"(ao));
 #pragma unroll
         for (int i = 0; i < FN; ++i)
-            b2[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bsres, bsoff, i * bstep + kb, 0);
+            b2[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bsres, bo + (uint32_t)(i * bstep + kb), 0, 0);
 #pragma unroll
         for (int j = 0; j < FM; ++j)
-            a2[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(asres, asoff, j * astep + kb, 0);
+            a2[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(asres, ao + (uint32_t)(j * astep + kb), 0, 0);
     };
 
     f32x4_t acc[FN][FM] = {};

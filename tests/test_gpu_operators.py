@@ -598,6 +598,13 @@ def test_matmul_scales_of_every_size(gpu):
         p.engram_matmul_fp8(a.to(gpu), sa.to(gpu), b.to(gpu), sb.to(gpu), got, p.matmul_fp8_workspace(5, 5, k),
                             b_block_rows=1)
         assert torch.equal(got.float().cpu()[normal], want.to(dt).float()[normal]), dt
+        # byte 0 is 2^-127
+        s0, s1 = torch.zeros((1, 4), dtype=torch.uint8), torch.full((1, 4), 227, dtype=torch.uint8)
+        a0 = torch.full((1, k), 256.0).to(torch.float8_e4m3fn)
+        low = torch.empty((1, 1), dtype=dt, device=gpu)
+        p.engram_matmul_fp8(a0.to(gpu), s0.to(gpu), one.to(gpu), s1.to(gpu), low, p.matmul_fp8_workspace(1, 1, k),
+                            b_block_rows=1)
+        assert float(low) == 256.0 * k * 2.0 ** -27, dt
         zero = torch.zeros_like(got)
         z = torch.zeros((5, k)).to(torch.float8_e4m3fn)
         p.engram_matmul_fp8(z.to(gpu), sa.to(gpu), b.to(gpu), sb.to(gpu), got, p.matmul_fp8_workspace(5, 5, k),
