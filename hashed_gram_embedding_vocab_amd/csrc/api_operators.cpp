@@ -33,7 +33,8 @@ struct EmbedLayout {
 engram_status embed_layout_of(const engram_plan_s &p, int64_t n_tok, EmbedLayout &L) {
     if (n_tok <= 0) return ENGRAM_E_INVALID_ARG;
     const int32_t d = p.cfg.d_model, V = p.cfg.vocab;
-    if (n_tok > (int64_t)INT32_MAX || !embed_bwd_fits(n_tok, V, d)) return ENGRAM_E_UNSUPPORTED;
+    if (n_tok > (int64_t)INT32_MAX || n_tok > kMaxElems / d || V > kMaxElems / d || !embed_bwd_fits(n_tok, V, d))
+        return ENGRAM_E_UNSUPPORTED;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t o = off;
@@ -80,12 +81,16 @@ extern "C" {
 engram_status engram_embed(engram_plan p, const int32_t *d_tokens, int64_t n_tok, const void *d_table, float scale,
                            void *d_h, uint32_t *d_bad_tokens, hipStream_t stream) {
     if (!p || !d_tokens || !d_table || !d_h || n_tok <= 0) return ENGRAM_E_INVALID_ARG;
-    if (n_tok > (int64_t)INT32_MAX) return ENGRAM_E_UNSUPPORTED;
+    if (n_tok > (int64_t)INT32_MAX || n_tok > kMaxElems / p->cfg.d_model || p->cfg.vocab > kMaxElems / p->cfg.d_model)
+        return ENGRAM_E_UNSUPPORTED;
     if (!aligned16(d_tokens) || !aligned16(d_table) || !aligned16(d_h) || !std::isfinite(scale))
         return ENGRAM_E_INVALID_ARG;
     const size_t row = (size_t)p->cfg.d_model * p->elem;
     const size_t h_bytes = (size_t)p->cfg.n_branches * (size_t)n_tok * row;
-    if (overlap(d_h, h_bytes, d_table, (size_t)p->cfg.vocab * row) || overlap(d_h, h_bytes, d_tokens, (size_t)n_tok * 4))
+    const size_t t_bytes = (size_t)p->cfg.vocab * row, tok_bytes = (size_t)n_tok * 4;
+    if (overlap(d_h, h_bytes, d_table, t_bytes) || overlap(d_h, h_bytes, d_tokens, tok_bytes) ||
+        overlap(d_bad_tokens, 4, d_h, h_bytes) || overlap(d_bad_tokens, 4, d_table, t_bytes) ||
+        overlap(d_bad_tokens, 4, d_tokens, tok_bytes) || (reinterpret_cast<uintptr_t>(d_bad_tokens) & 3u) != 0)
         return ENGRAM_E_INVALID_ARG;
     {
         Launch l(*p, ENGRAM_K_GATHER, stream);

@@ -10,7 +10,10 @@
 // difference of two sums), all in fp32.  Both kernels are bound by memory: a
 // block walks many rows, so that gamma and beta (twice the bytes of a bf16 row)
 // and the parameters' sums stay in registers, and the next row's loads are in
-// flight while a row is worked on.
+// flight while a row is worked on.  Measured in bf16 at d = 2560: forward of
+// 32,768 rows 67 us (a block per four rows, gamma and beta read per row: 82),
+// backward of 131,072 rows 388 us (one row at a time, expanded once: 467), 5.0
+// and 5.2 TB/s; a large copy runs at 5.2.
 #include <algorithm>
 
 #include "engram_internal.h"

@@ -49,8 +49,11 @@ def test_embed_refusals(B):
     refuses(fn, good, [(0, None), (1, None), (3, None), (5, None), (2, 0), (2, -1), (1, ODD), (3, ODD), (5, ODD),
                        (4, math.nan), (4, math.inf),
                        (5, at(1)), (5, C.c_void_p(at(1).value + table_bytes - 16)),
-                       (5, C.c_void_p(at(1).value - h_bytes + 16)), (5, at(0))], B.E_INVALID_ARG)
+                       (5, C.c_void_p(at(1).value - h_bytes + 16)), (5, at(0)), (6, at(0)), (6, at(1)), (6, at(2)),
+                       (6, C.c_void_p(at(2).value + h_bytes - 4)), (6, C.c_void_p(at(7).value + 2))], B.E_INVALID_ARG)
     refuses(fn, good, [(2, 1 << 31)], B.E_UNSUPPORTED)
+    wide = plan(B, d=1 << 24, vocab=1 << 20)
+    assert fn(wide._h, *good[1:]) == B.E_UNSUPPORTED
 
 
 def test_embed_backward_refusals(B):
@@ -72,6 +75,8 @@ def test_embed_backward_refusals(B):
                        (6, at(1)), (6, at(0)), (7, at(2)), (7, at(1)), (7, at(0))], B.E_INVALID_ARG)
     refuses(fn, good, [(2, 1 << 31)], B.E_UNSUPPORTED)
     assert plan(B, vocab=(1 << 31) - 1).engram_embed_backward_workspace_size(4) == 0
+    assert plan(B, vocab=1 << 20, d=1 << 24).engram_embed_backward_workspace_size(4) == 0
+    assert plan(B, vocab=8, d=1 << 26).engram_embed_backward_workspace_size(512) == 0
 
 
 def test_layer_norm_refusals(B):
