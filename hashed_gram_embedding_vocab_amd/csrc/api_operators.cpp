@@ -239,7 +239,7 @@ engram_status engram_quantize_fp8(engram_plan p, const void *d_x, int64_t rows, 
     if (!p || !d_x || !d_q || !d_scales || rows <= 0 || cols <= 0) return ENGRAM_E_INVALID_ARG;
     if (block_rows != 1 && block_rows != 128) return ENGRAM_E_INVALID_ARG;
     if (flags & ~(uint32_t)ENGRAM_QUANTIZE_TRANSPOSE) return ENGRAM_E_INVALID_ARG;
-    if (rows > kMaxElems / cols) return ENGRAM_E_UNSUPPORTED;
+    if (rows > kMaxElems / cols || rows > (int64_t)INT32_MAX || cols > (int64_t)INT32_MAX) return ENGRAM_E_UNSUPPORTED;
     if (!aligned16(d_x) || !aligned16(d_q) || !aligned16(d_scales)) return ENGRAM_E_INVALID_ARG;
     QuantArgs a{};
     a.x = d_x;

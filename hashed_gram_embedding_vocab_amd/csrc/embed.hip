@@ -36,7 +36,7 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t *tokens, int64
     const int32_t strips = (d + 511) / 512;
     const int64_t waves = (int64_t)gridDim.x * 4, n_items = n_tok * strips;
     for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < n_items; item += waves) {
-        const int64_t t = item / strips;
+        const int64_t t = quotient(item, strips);
         const int32_t strip = (int32_t)(item - t * strips);
         const int32_t c = strip * 512 + lane * 8;
         const int32_t id = tokens[t];
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void embed_few_kernel(const int32_t *tokens, i
         return;
     }
     const int32_t strips = (d + 511) / 512;
-    const int32_t t0 = (int32_t)(wave / strips), col = (int32_t)(wave % strips) * 512 + lane * 8;
+    const int32_t t0 = (int32_t)quotient(wave, strips), col = (int32_t)(wave - (int64_t)t0 * strips) * 512 + lane * 8;
     if (t0 >= n_tok) return;
     const int32_t id = tokens[t0];
     if (id < 0 || id >= vocab) return;
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const uint32_t *order, 
         return;
     }
     const int32_t strips = (d + 511) / 512;
-    const int64_t c = wave / strips;
+    const int64_t c = quotient(wave, strips);
     const int32_t col = (int32_t)(wave - c * strips) * 512 + lane * 8;
     const bool in = col < d;
     const int64_t n = start[vocab], base = c * chunk;

@@ -169,10 +169,11 @@ template <typename T, bool VEC, int U>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const T *x, int64_t rows, int64_t cols, uint8_t *q,
                                                             uint8_t *scales) {
     const int lane = threadIdx.x & 63;
-    const int64_t strips = (cols + 511) / 512, n_items = (rows + U - 1) / U * strips;
+    const int32_t strips = (int32_t)((cols + 511) / 512);
+    const int64_t n_items = (rows + U - 1) / U * strips;
     const int64_t kb = (cols + 127) / 128;
     for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < n_items; item += (int64_t)gridDim.x * 4) {
-        const int64_t r0 = item / strips * U, strip = item % strips;
+        const int64_t group = quotient(item, strips), r0 = group * U, strip = item - group * strips;
         const int64_t c = strip * 512 + lane * 8;
         Raw8<T> v[U];
 #pragma unroll
@@ -221,12 +222,15 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const T *x, int64_t 
     constexpr int64_t kGroup = 16;
     int turn = 0;
     for (int64_t tl = blockIdx.x; tl < col_tiles * row_tiles; tl += gridDim.x, turn ^= 1) {
-        int64_t tr = tl / col_tiles, tc = tl - tr * col_tiles;
+        int64_t tr, tc;
         if constexpr (TR) {
-            const int64_t grp = tl / (kGroup * col_tiles), in = tl - grp * kGroup * col_tiles;
+            const int64_t grp = quotient(tl, (int32_t)(kGroup * col_tiles)), in = tl - grp * kGroup * col_tiles;
             const int64_t n = min(kGroup, row_tiles - grp * kGroup);
-            tc = in / n;
+            tc = quotient(in, (int32_t)n);
             tr = grp * kGroup + in - tc * n;
+        } else {
+            tr = quotient(tl, (int32_t)col_tiles);
+            tc = tl - tr * col_tiles;
         }
         const int64_t r0 = tr * 128, c0 = tc * 128;
         Raw8<T> v[8];
@@ -553,8 +557,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(ProductArgs g)
 
     // scale bytes of two blocks (kb even) for this lane's rows
     const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
-    const int64_t brows = (g.N + g.b_block_rows - 1) / g.b_block_rows, arows = (g.M + g.a_block_rows - 1) / g.a_block_rows;
-    const int64_t bs0 = n0 / g.b_block_rows, as0 = m0 / g.a_block_rows;
+    const int bshift = g.b_block_rows == 1 ? 0 : 7, ashift = g.a_block_rows == 1 ? 0 : 7;
+    const int64_t brows = ((g.N - 1) >> bshift) + 1, arows = ((g.M - 1) >> ashift) + 1;
+    const int64_t bs0 = n0 >> bshift, as0 = m0 >> ashift;
     const __amdgpu_buffer_rsrc_t bsres = make_rsrc(g.b_scales + bs0 * pitch, (brows - bs0) * pitch);
     const __amdgpu_buffer_rsrc_t asres = make_rsrc(g.a_scales + as0 * pitch, (arows - as0) * pitch);
     // (a wave's rows of one side lie in one block of 128, so they share a scale
@@ -724,18 +729,17 @@ __global__ __launch_bounds__(256) void product_skinny_kernel(ProductArgs g) {
     __shared__ f32x4_t sum_s[3][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles_n = (g.N + 15) / 16, tiles = tiles_n * ((g.M + 15) / 16);
+    const uint32_t tiles = (uint32_t)((g.N + 15) / 16);  // (16 rows of a at most)
     const int split = (int)(blockIdx.x / tiles);
-    const int64_t tile = blockIdx.x - split * tiles;
-    const int64_t m0 = tile / tiles_n * 16, n0 = tile % tiles_n * 16;
+    const int64_t n0 = (int64_t)(blockIdx.x - split * tiles) * 16;
     const int64_t K = g.K;
     const int kb_all = (int)((K + 127) / 128), pitch = (kb_all + 3) / 4 * 4;
     const int kb_first = split * g.split_blocks, kb_last = min(kb_first + g.split_blocks, kb_all);
     const int fr = lane & 15, piece = 16 * (lane >> 4);
     // rows past the end repeat the last one (their results are not stored)
-    const int64_t n = min(n0 + fr, g.N - 1), m = min(m0 + fr, g.M - 1);
-    const uint8_t *brow = g.b + n * K + piece, *bsc = g.b_scales + n / g.b_block_rows * pitch;
-    const uint8_t *arow = g.a + m * K + piece, *asc = g.a_scales + m / g.a_block_rows * pitch;
+    const int64_t n = min(n0 + fr, g.N - 1), m = min((int64_t)fr, g.M - 1);
+    const uint8_t *brow = g.b + n * K + piece, *bsc = g.b_scales + (g.b_block_rows == 1 ? n : n >> 7) * pitch;
+    const uint8_t *arow = g.a + m * K + piece, *asc = g.a_scales + (g.a_block_rows == 1 ? m : 0) * pitch;
     const u32x4_t zero = {0u, 0u, 0u, 0u};
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     for (int kb = kb_first + wave; kb < kb_last; kb += 4 * PF) {
@@ -775,7 +779,7 @@ __global__ __launch_bounds__(256) void product_skinny_kernel(ProductArgs g) {
     if (wave > 0) return;
 #pragma unroll
     for (int w = 0; w < 3; ++w) acc += sum_s[w][lane];
-    const int64_t mm = m0 + fr, nn = n0 + 4 * (lane >> 4);
+    const int64_t mm = fr, nn = n0 + 4 * (lane >> 4);
     if (mm >= g.M) return;
     if (F32 || g.splits > 1) {
         float *c = g.splits > 1 ? static_cast<float *>(g.ws) + split * g.split_elems : static_cast<float *>(g.c);
@@ -867,7 +871,7 @@ void product_of(const ProductCut &c, const ProductArgs &g, hipStream_t s) {
     else if (c.tile == 64)
         product<F32, 64, 2, 2, 4>(g, s);
     else
-        launch_kernel(product_skinny_kernel<F32>, dim3((unsigned)((g.N + 15) / 16 * ((g.M + 15) / 16) * g.splits)), dim3(256),
+        launch_kernel(product_skinny_kernel<F32>, dim3((unsigned)((g.N + 15) / 16 * g.splits)), dim3(256),
                       s, g);
 }
 

@@ -7,6 +7,12 @@
 
 namespace engram {
 
+// x / d for x >= 0, in 32 bits where x fits (a 64-bit division is a few hundred
+// instructions, which a short kernel's waves would start with).
+__device__ __forceinline__ int64_t quotient(int64_t x, int32_t d) {
+    return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
 // 8 consecutive elements as fp32, from 16 bytes of bf16 or 32 of fp32
 struct F8 {
     float v[8];

@@ -561,6 +561,7 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
  *   scale = the smallest power of two >= 2^-126 with amax / scale <= 448
  *   q     = x / scale rounded to nearest-even e4m3
  * amax over the block's finite values; NaN and infinities become e4m3's NaN.
+ * rows or cols above 2^31 - 1: ENGRAM_E_UNSUPPORTED.
  * Scale bytes behind a row's last block are set to 127 (one).
  *
  * engram_matmul_fp8 multiplies two of them:

@@ -116,7 +116,7 @@ def test_quantize_refusals(B):
     refuses(fn, good, [(0, None), (1, None), (6, None), (7, None), (2, 0), (2, -1), (3, 0), (3, -128), (4, 0), (4, 2),
                        (4, 64), (4, -1), (5, B.GRAD_ACCUMULATE), (5, 1), (1, ODD), (6, ODD), (7, ODD), (6, at(0)),
                        (7, at(0)), (7, at(1)), (6, C.c_void_p(at(0).value + 33 * 256 * 2 - 16))], B.E_INVALID_ARG)
-    refuses(fn, good, [(2, 1 << 50)], B.E_UNSUPPORTED)
+    refuses(fn, good, [(2, 1 << 50), (2, 1 << 31), (3, 1 << 31)], B.E_UNSUPPORTED)
 
 
 def test_matmul_refusals(B):
