@@ -250,9 +250,13 @@ def norm_inputs(rows, d, dtype, seed):
     return x, gamma, beta
 
 
+# more rows than a launch's blocks take at once
+MANY_ROWS = [(70001, 8), (33000, 128), (17000, 256), (8300, 512), (2100, 2560), (1030, 4104)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("with_beta", (True, False))
-@pytest.mark.parametrize("rows,d", NORM_SHAPES)
+@pytest.mark.parametrize("rows,d", NORM_SHAPES + MANY_ROWS)
 def test_layer_norm(gpu, dtype, with_beta, rows, d):
     p = make_plan(dtype, d)
     x, gamma, beta = norm_inputs(rows, d, dtype, 11)
@@ -297,7 +301,7 @@ def norm_grad_ref(x, dy, gamma, mean, rstd):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,d", NORM_SHAPES + [(2051, 256), (4100, 64), (517, 1024), (600, 6152)])
+@pytest.mark.parametrize("rows,d", NORM_SHAPES + MANY_ROWS + [(2051, 256), (4100, 64), (517, 1024), (600, 6152)])
 def test_layer_norm_backward(gpu, dtype, rows, d):
     from hashed_gram_embedding_vocab_amd import binding as B
 
@@ -529,6 +533,22 @@ def test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k):
     assert bool(((got.double() - ref).abs() <= bound + half_step(out) * (ref.abs() + bound)).all())
 
 
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(3, 5, 1 << 20), (20, 70, 1 << 18), (1, 1, 4194288)])
+def test_matmul_long_rows(gpu, out, m, n, k):
+    """K up to the largest there is, in many parts: whole numbers, exact in fp32."""
+    p = make_plan()
+    a = torch.randint(-1, 2, (m, k), generator=gen(3)).float()
+    b = torch.randint(-1, 2, (n, k), generator=gen(4)).float()
+    f8 = torch.float8_e4m3fn
+    sa = torch.full(p.fp8_scale_shape(m, k, 1), 127, dtype=torch.uint8, device=gpu)
+    sb = torch.full(p.fp8_scale_shape(n, k, 128), 127, dtype=torch.uint8, device=gpu)
+    got = torch.empty((m, n), dtype=tdt(out), device=gpu)
+    ws = p.matmul_fp8_workspace(m, n, k)
+    p.engram_matmul_fp8(a.to(f8).to(gpu), sa, b.to(f8).to(gpu), sb, got, ws)
+    assert torch.equal(got.cpu().float(), (a.double() @ b.double().t()).float().to(tdt(out)).float())
+
+
 def test_matmul_result_larger_than_the_caches(gpu):
     """A bf16 result over 256 MB; sums of at most 64 ones are exact in bf16."""
     p = make_plan()
@@ -716,9 +736,9 @@ def test_a_training_step_through_all_of_them(gpu):
     assert np.isfinite(out.float().cpu().numpy()).all()
 
 
-def _operators(gpu, seed):
-    """Every entry point once over its own buffers: (call(stream), outputs)."""
-    n_tok, d, vocab, br = 300, 512, 700, 2
+def _operators(gpu, seed, n_tok):
+    """Every entry point once over its own buffers: (call(stream), outputs, ids)."""
+    d, vocab, br = 512, 700, 2
     p = make_plan("bf16", d, vocab, br)
     f = lambda t: t.to(gpu)  # noqa: E731
     ids, table = f(zipf_ids(n_tok, vocab, seed)), f(randn((vocab, d), "bf16", seed + 1))
@@ -746,7 +766,7 @@ def _operators(gpu, seed):
 def test_captured_graphs_replay_the_eager_results(gpu):
     """Two graphs with workspaces of their own, replayed several times and at once
     on two streams, with eager work in between and inputs changed."""
-    sets = [_operators(gpu, s) for s in (60, 70)]
+    sets = [_operators(gpu, 60, 700), _operators(gpu, 70, 300)]  # the embedding's gradient sorted, and in one launch
     eager = []
     for call, outs, _ in sets:
         call()
@@ -773,7 +793,7 @@ def test_captured_graphs_replay_the_eager_results(gpu):
                 assert torch.equal(o, e), turn
         sets[0][0]()  # eager work between the replays
     # new ids in the same buffer: the replay and an eager call agree
-    sets[0][2].copy_(zipf_ids(300, 700, 99).to(gpu))
+    sets[0][2].copy_(zipf_ids(700, 700, 99).to(gpu))
     graphs[0].replay()
     torch.cuda.synchronize()
     replayed = [o.clone() for o in sets[0][1]]
@@ -785,7 +805,7 @@ def test_captured_graphs_replay_the_eager_results(gpu):
 
 def test_side_stream(gpu):
     """On a stream of the caller's, behind work of that stream, without touching the current one."""
-    call, outs, ids = _operators(gpu, 80)
+    call, outs, ids = _operators(gpu, 80, 700)
     call()
     torch.cuda.synchronize()
     want = [o.clone() for o in outs]
@@ -805,10 +825,10 @@ def test_side_stream(gpu):
 
 
 def test_profiling_counts_the_operators(gpu):
-    call, _, _ = _operators(gpu, 90)
     p = make_plan("bf16", 512, 700, 2)
     x = torch.zeros((4, 512), dtype=torch.bfloat16, device=gpu)
     g = torch.ones(512, device=gpu)
+    p.engram_layer_norm(x, g, None, x)
     p.engram_profile_begin(16, ["aux"])
     p.engram_layer_norm(x, g, None, x)
     r = p.engram_profile_end()
