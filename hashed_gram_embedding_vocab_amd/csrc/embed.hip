@@ -252,8 +252,8 @@ __global__ __launch_bounds__(256) void embed_few_kernel(const int32_t *tokens, i
 }
 
 // Sorted positions per wave: 32, or 8 where that leaves the chip short of waves
-// (333 tokens x 256 channels: the sums take 5 us instead of 12, the join of
-// longer chains of parts no longer).
+// (a whole gradient of 1000 tokens x 256 channels: 14 us instead of 20, of 2048
+// x 1024 over 32000 rows 28 instead of 34).
 int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= 65536 ? 32 : 8; }
 constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 

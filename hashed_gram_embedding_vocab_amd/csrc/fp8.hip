@@ -381,9 +381,9 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 //
 // What bounds it: a CU's loads into LDS (64 KB a step of 256 x 256 x 128, as
 // long as the step's MFMAs) and, at short K, the tile's start and stores.
-// Measured: 8192^3 2.5 PFLOP/s to bf16 and 1.40 to fp32 (the image's matrix
-// library: 2.64 and, on bf16 operands, 1.35); 32768 x 12800 x 1280 545 us (557);
-// 256 x 12800 x 1280 11.5 us.  Not kept: four waves of 128 x 128 a workgroup
+// Measured: 8192^3 2.63 PFLOP/s to bf16 and 1.40 to fp32 (the image's matrix
+// library: 2.64 and, on bf16 operands, 1.35); 32768 x 12800 x 1280 538 to 548 us
+// (557); 256 x 12800 x 1280 11.2 us.  Not kept: four waves of 128 x 128 a workgroup
 // (3 to 20% slower), workgroups that walk tiles and start the next one before
 // storing (8% slower: its first step waits for the stores), results stored
 // from the fragments without LDS (3% slower at 32768 x 12800), a start along K
@@ -818,13 +818,16 @@ __global__ __launch_bounds__(256) void product_join_kernel(const float *parts, i
 }
 
 // How a product is cut.  256 x 256 tiles where they (or they and parts of K of
-// at least eight blocks) come to about one workgroup a CU; 128 x 128 where those
-// do; else 64 x 64 (1024 x 2560 x 1280: 12.1 us against 12.4 of 128 x 128, 128 x
-// 2560 x 1280: 6.1 against 11.2), or 16 x 16 by four waves for up to 16 rows of a
-// while 64 rows of b a workgroup would leave CUs idle (1 x 2560 x 1280: 4.4 us
-// against 6; 1 x 12800 x 1280: 7.8 against 6.1).  K is cut in parts of 16 blocks
-// and more where the tiles leave CUs idle (a second launch to join shorter parts
-// costs more than it saves: 64 x 12800 x 1280 in two, 9.6 + 3.1 us, whole 6.5).
+// at least eight blocks) come to about one workgroup a CU and neither operand
+// has so few rows that half a tile is empty (1 x 129280 x 2560 to fp32: 72 us
+// against 118 of 256 x 256, 128 x 129280 x 2560: 104 against 147).  Else 64 x 64
+// while those fit the chip at once, two a CU (128 x 2560 x 1280: 5.9 us against
+// 10 of 128 x 128, 64 x 25600 x 1280: 9.0 against 10.9), and 128 x 128 beyond
+// (1024 x 2560 x 1280: 10.8 against 11.7).  Up to 16 rows of a and 8192 of b go
+// to 16 x 16 by four waves (1 x 2560 x 1280: 4.1 us against 5.8 of 64 x 64; 1 x
+// 12800 x 1280: 7.6 against 5.7).  K is cut in parts of 16 blocks and more where
+// the tiles leave CUs idle (a second launch to join shorter parts costs more
+// than it saves: 64 x 2560 x 1280 in two, 5.0 + 2.2 us, whole 5.9).
 struct ProductCut {
     int tile;
     int32_t splits, split_blocks;
@@ -839,10 +842,10 @@ ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
     if (M <= 16 && N <= 64 * 128) {
         c.tile = 16;
         s = std::min<int64_t>(512 / tiles(16), kb / 16);
-    } else if (wt * ws >= 192) {
+    } else if (wt * ws >= 192 && std::min(M, N) > 128) {
         c.tile = 256;
     } else {
-        c.tile = tiles(128) >= 192 ? 128 : 64;
+        c.tile = tiles(64) > 512 ? 128 : 64;
         s = std::min<int64_t>(256 / tiles(c.tile), kb / 16);
     }
     s = std::max<int64_t>(s, 1);

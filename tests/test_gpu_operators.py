@@ -514,10 +514,12 @@ def test_matmul(gpu, out, abr, bbr, m, n, k):
 
 @pytest.mark.parametrize("out", DTYPES)
 @pytest.mark.parametrize("abr,bbr", [(1, 128), (1, 1)])
-@pytest.mark.parametrize("m,n,k", [(4100, 3900, 272), (8190, 1601, 1296), (2563, 1285, 8208), (3000, 2100, 400)])
+@pytest.mark.parametrize("m,n,k", [(4100, 3900, 272), (8190, 1601, 1296), (2563, 1285, 8208), (3000, 2100, 400),
+                                   (20, 33100, 400), (33000, 7, 144), (128, 17000, 1296)])
 def test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k):
-    """Shapes that take 256 x 256 tiles (the third with K cut in parts), then 128 x 128; the
-    bounds as above, with a block's largest product bounded by its operands' largest."""
+    """Shapes that take 256 x 256 tiles (the third with K cut in parts), then 128 x 128, the
+    last three with a part of a tile; the bounds as above, with a block's largest
+    product bounded by its operands' largest."""
     p = make_plan()
     a, sa = (t.to(gpu) for t in random_quantized(m, k, abr, 47))
     b, sb = (t.to(gpu) for t in random_quantized(n, k, bbr, 49))
