@@ -129,7 +129,10 @@ IDS = {
     ("zipf", 512, 1000, 64, 1, 1.0), ("one", 512, 33, 520, 3, 1.0), ("two", 512, 40, 64, 4, 1.0), ("zipf", 513, 20, 64, 1, 1.0),
     ("rising", 500, 300, 1032, 2, 1.0), ("zipf", 2410, 291, 136, 1, 0.25), ("none", 1000, 600, 64, 1, 1.0),
     ("zipf", 65537, 1537, 64, 1, 0.5), ("one", 65600, 513, 64, 1, 1.0), ("two", 66001, 700, 64, 2, 1.0),
-    ("rising", 33000, 33100, 520, 1, 1.0)])
+    ("rising", 33000, 33100, 520, 1, 1.0),
+    # tokens sorted in pieces: one more than a piece, pieces left empty, as many as there are
+    ("zipf", 2049, 700, 64, 1, 1.0), ("two", 2113, 9, 8, 1, 1.0), ("zipf", 40001, 300, 8, 1, 1.0),
+    ("rising", 150001, 5000, 8, 1, 1.0), ("zipf", 270001, 513, 8, 2, 0.5), ("none", 9000, 600, 8, 1, 1.0)])
 def test_embed_backward(gpu, dtype, ids_of, n_tok, vocab, d, branches, scale):
     from hashed_gram_embedding_vocab_amd import binding as B
 
