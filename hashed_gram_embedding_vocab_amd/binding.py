@@ -558,6 +558,7 @@ class Plan:
         return int(lib().engram_embed_backward_workspace_size(self._h, n_tok))
 
     def embed_backward_workspace(self, n_tok: int, device="cuda") -> torch.Tensor:
+        """A workspace for engram_embed_backward of up to n_tok tokens."""
         return self._workspace("engram_embed_backward", self.engram_embed_backward_workspace_size(n_tok), device)
 
     def engram_embed_backward(self, tokens, dout, dtable, workspace, scale: float = 1.0, flags: int = 0, stream=None):

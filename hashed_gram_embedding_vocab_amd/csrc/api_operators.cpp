@@ -4,6 +4,7 @@
 // checks, workspace layout and launches on the caller's stream.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -101,8 +102,12 @@ engram_status engram_embed(engram_plan p, const int32_t *d_tokens, int64_t n_tok
 }
 
 size_t engram_embed_backward_workspace_size(engram_plan p, int64_t n_tok) {
-    EmbedLayout L;
+    EmbedLayout L, S;
     if (!p || embed_layout_of(*p, n_tok, L) != ENGRAM_OK) return 0;
+    // either kind of chunk takes more for more tokens, but a long batch's are
+    // four times the length: the batch before them can take more than this one
+    const int64_t n_short = embed_short_tokens(p->cfg.d_model);
+    if (n_short < n_tok && embed_layout_of(*p, n_short, S) == ENGRAM_OK) return std::max(L.total, S.total);
     return L.total;
 }
 

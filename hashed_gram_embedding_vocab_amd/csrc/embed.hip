@@ -278,7 +278,8 @@ __global__ __launch_bounds__(256) void embed_few_kernel(const int32_t *tokens, i
 // Sorted positions per wave: 32, or 8 where that leaves the chip short of waves
 // (a whole gradient of 1000 tokens x 256 channels: 14 us instead of 20, of 2048
 // x 1024 over 32000 rows 28 instead of 34).
-int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= 65536 ? 32 : 8; }
+constexpr int64_t kLongItems = 65536;  // tokens times strips of 512 channels
+int32_t run_chunk(int64_t n_tok, int32_t d) { return n_tok * ((d + 511) / 512) >= kLongItems ? 32 : 8; }
 constexpr int kZeroRows = 8;   // table rows per wave of the zero part
 
 // One wave per (run_chunk sorted positions, 512 channels) adds the chunk's rows
@@ -465,6 +466,8 @@ int64_t embed_chunks(int64_t n_tok, int32_t d) {
     const int64_t c = run_chunk(n_tok, d);
     return (n_tok + c - 1) / c;
 }
+
+int64_t embed_short_tokens(int32_t d) { return (kLongItems - 1) / ((d + 511) / 512); }
 
 bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d) {
     // a launch holds fewer than 2^32 threads along x, and 65535 blocks along y

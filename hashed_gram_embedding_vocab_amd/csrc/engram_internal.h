@@ -383,6 +383,7 @@ struct EmbedBwdArgs {
     bool accumulate;
 };
 int64_t embed_chunks(int64_t n_tok, int32_t d);
+int64_t embed_short_tokens(int32_t d);      // the most tokens whose chunks are short ones (0: none)
 bool embed_bwd_fits(int64_t n_tok, int32_t vocab, int32_t d);
 void launch_embed_bwd(engram_dtype dt, const EmbedBwdArgs &a, hipStream_t s);
 

@@ -494,9 +494,10 @@ ENGRAM_API engram_status engram_backward(engram_plan p, const uint32_t *d_idx, c
 ENGRAM_API engram_status engram_embed(engram_plan p, const int32_t *d_tokens, int64_t n_tok, const void *d_table,
                                       float scale, void *d_h, uint32_t *d_bad_tokens, hipStream_t stream);
 
-/* Bytes of device workspace engram_embed_backward needs (0 on invalid or
- * unsupported sizes): 8 bytes a token, 4 an id and two fp32 rows for every 32
- * tokens (for every 8 of a short batch). */
+/* Bytes of device workspace engram_embed_backward needs for up to n_tok tokens
+ * (0 on invalid or unsupported sizes), so one of the largest batch serves every
+ * smaller one: 8 bytes a token, 4 an id and two fp32 rows for every 32 tokens,
+ * for every 8 of them while n_tok * ceil(d_model / 512) is below 65536. */
 ENGRAM_API size_t engram_embed_backward_workspace_size(engram_plan p, int64_t n_tok);
 
 /*
@@ -509,7 +510,8 @@ ENGRAM_API size_t engram_embed_backward_workspace_size(engram_plan p, int64_t n_
  *                are not touched); without it every row is written, zeros
  *                where no token names it
  *   d_dtable     [vocab][d_model] fp32
- *   d_workspace  >= engram_embed_backward_workspace_size(p, n_tok) bytes, 256-byte aligned
+ *   d_workspace  >= engram_embed_backward_workspace_size(p, n) bytes for an
+ *                n >= n_tok, 256-byte aligned
  * Ids outside [0, vocab) contribute nothing.
  */
 ENGRAM_API engram_status engram_embed_backward(engram_plan p, const int32_t *d_tokens, int64_t n_tok,

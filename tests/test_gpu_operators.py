@@ -158,6 +158,22 @@ def test_embed_backward(gpu, dtype, ids_of, n_tok, vocab, d, branches, scale):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_embed_backward_in_the_largest_batchs_workspace(gpu, dtype):
+    """A workspace kept for the largest batch serves the smaller ones, on either
+    side of where chunks of sorted positions become longer (65536 tokens here)."""
+    vocab, d = 777, 64
+    p = make_plan(dtype, d, vocab)
+    ws = p.embed_backward_workspace(70003)
+    for n_tok in (70003, 65536, 65535, 40001, 513, 512, 1):
+        ids, dh = zipf_ids(n_tok, vocab, 15), randn((1, n_tok, d), dtype, 16)
+        ws.fill_(255)
+        got = torch.full((vocab, d), 7.0, device=gpu)
+        p.engram_embed_backward(ids.to(gpu), dh.to(gpu), got, ws)
+        ref, mag, terms = embed_grad_ref(ids, dh, vocab, 1.0)
+        close(got, ref, (terms[:, None] + 2) * U * mag, "dtable of %d tokens" % n_tok)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_embed_far_rows(gpu, dtype):
     """A table and a gradient whose element offsets pass 2^31 (and bytes 2^32)."""
     vocab, d = 300001, 8192

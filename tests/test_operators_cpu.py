@@ -280,3 +280,21 @@ def test_scale_shape(B):
     for cols, pitch in ((1, 4), (128, 4), (129, 4), (512, 4), (513, 8), (1280, 12), (16384, 128)):
         assert B.Plan.fp8_scale_shape(300, cols, 1) == (300, pitch)
         assert B.Plan.fp8_scale_shape(300, cols, 128) == (3, pitch)
+
+
+@pytest.mark.parametrize("vocab,d", [(129280, 2560), (1000, 8), (1000, 512), (50, 520), (700, 1 << 14), (9, 1 << 23)])
+def test_an_embed_backward_workspace_serves_smaller_batches(B, vocab, d):
+    """The size never falls as the batch grows, also where its chunks become longer."""
+    p = plan(B, vocab=vocab, d=d, n_branches=1)
+    turn = 65536 // ((d + 511) // 512)  # from here on a chunk is 32 tokens
+    ns = {1, 2, 7, 8, 9, 100, 512, 513, 1000, 2 * turn, 3 * turn, 4 * turn + 5, 5 * turn, 1 << 20}
+    ns |= {turn + i for i in range(-40, 41)} | {turn * i // 16 for i in range(1, 80)}
+    sizes = [s for n in sorted(ns) if n > 0 for s in [p.engram_embed_backward_workspace_size(n)] if s]
+    assert len(sizes) > 10
+    assert all(x <= y for x, y in zip(sizes, sizes[1:]))
+    # and is enough for two rows a chunk of this batch
+    for n in sorted(ns):
+        s = p.engram_embed_backward_workspace_size(n) if n > 0 else 0
+        if s:
+            chunk = 32 if n * ((d + 511) // 512) >= 65536 else 8
+            assert s >= 8 * n + 4 * (vocab + 1) + 8 * d * -(-n // chunk)
