@@ -636,7 +636,7 @@ class Plan:
         return int(lib().engram_matmul_fp8_workspace_size(self._h, m, n, k))
 
     def matmul_fp8_workspace(self, m: int, n: int, k: int, device="cuda") -> Optional[torch.Tensor]:
-        """A workspace for engram_matmul_fp8, or None where none is needed."""
+        """A workspace for engram_matmul_fp8 of up to these sizes, or None where none is needed."""
         size = self.engram_matmul_fp8_workspace_size(m, n, k)
         return torch.empty(size, dtype=torch.uint8, device=device) if size else None
 

@@ -267,7 +267,7 @@ engram_status engram_quantize_fp8(engram_plan p, const void *d_x, int64_t rows, 
 
 size_t engram_matmul_fp8_workspace_size(engram_plan p, int64_t M, int64_t N, int64_t K) {
     if (!p || check_product_sizes(M, N, K) != ENGRAM_OK) return 0;
-    return product_workspace(M, N, K);
+    return product_workspace_most(M, N, K);
 }
 
 engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const uint8_t *d_a_scales, int32_t a_block_rows,

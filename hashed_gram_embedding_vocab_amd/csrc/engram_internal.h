@@ -429,7 +429,8 @@ struct ProductArgs {
     int32_t splits, split_blocks;
     int64_t split_elems;
 };
-size_t product_workspace(int64_t M, int64_t N, int64_t K);
+size_t product_workspace(int64_t M, int64_t N, int64_t K);       // what this product uses
+size_t product_workspace_most(int64_t M, int64_t N, int64_t K);  // no smaller product uses more
 bool product_fits(int64_t M, int64_t N, int64_t K);
 void launch_product(const ProductArgs &a, hipStream_t s);
 

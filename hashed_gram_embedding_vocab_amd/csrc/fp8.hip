@@ -858,6 +858,17 @@ ProductCut cut_of(int64_t M, int64_t N, int64_t K) {
 
 int64_t split_elems_of(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
 
+// The most bytes that a product of at most M, N and K takes, or a little more,
+// and never less where one of them grows.  Parts of K come to at most `cap` /
+// tiles of them, of `blocks` blocks and more each (as in cut_of), so to at most
+// cap * tile^2 sums, and to as many as the largest result in the most parts.
+// (128 x 128 tiles are never cut: there are more than 128 of them.)
+size_t most_parts(int tile, int64_t cap, int64_t blocks, int64_t M, int64_t N, int64_t kb) {
+    const int64_t s = std::min(cap, kb / blocks);
+    if (s < 2) return 0;
+    return (size_t)std::min(cap * tile * tile, s * split_elems_of(M, N)) * 4;
+}
+
 template <bool F32, int T, int WN, int WM, int NB>
 void product(const ProductArgs &g, hipStream_t s) {
     const int64_t tiles = ((g.N + T - 1) / T) * ((g.M + T - 1) / T);
@@ -899,6 +910,15 @@ void launch_quantize(engram_dtype dt, const QuantArgs &a, hipStream_t s) {
 size_t product_workspace(int64_t M, int64_t N, int64_t K) {
     const ProductCut c = cut_of(M, N, K);
     return c.splits > 1 ? (size_t)c.splits * (size_t)split_elems_of(M, N) * 4 : 0;
+}
+
+size_t product_workspace_most(int64_t M, int64_t N, int64_t K) {
+    const int64_t kb = (K + 127) / 128, wide = ((M + 255) / 256) * ((N + 255) / 256);
+    size_t most = std::max(most_parts(64, 256, 16, M, N, kb),
+                           most_parts(16, 512, 16, std::min<int64_t>(M, 16), std::min<int64_t>(N, 64 * 128), kb));
+    if (std::min(M, N) > 128 && std::min<int64_t>(256, wide * (kb / 8)) >= 192)
+        most = std::max(most, most_parts(256, 256, 8, M, N, kb));
+    return most;
 }
 
 bool product_fits(int64_t M, int64_t N, int64_t) {

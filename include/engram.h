@@ -578,8 +578,9 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
  *                ENGRAM_E_UNSUPPORTED) and K < 2^22; the last block may be short
  *   a_block_rows, b_block_rows   1 or 128, as the scales were made
  *   d_c          [M][N] fp32 or bf16 (c_dtype)
- *   d_workspace  >= engram_matmul_fp8_workspace_size(p, M, N, K) bytes,
- *                256-byte aligned; may be NULL where that is 0
+ *   d_workspace  >= engram_matmul_fp8_workspace_size(p, M', N', K') bytes for
+ *                some M' >= M, N' >= N, K' >= K, 256-byte aligned; may be NULL
+ *                where that is 0
  * A scale byte of 255 stands for NaN.
  *
  * One projection of the layer and its gradients, E [n_tok][D_e] and W [d][D_e]:
@@ -590,7 +591,10 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
 ENGRAM_API engram_status engram_quantize_fp8(engram_plan p, const void *d_x, int64_t rows, int64_t cols,
                                              int32_t block_rows, uint32_t flags, void *d_q, uint8_t *d_scales,
                                              hipStream_t stream);
-/* 0 also on invalid or unsupported sizes (engram_matmul_fp8 then refuses the call). */
+/* Bytes that serve every product of at most M, N and K (64 MB at most): one of
+ * the largest batch serves the smaller ones, which may need more parts of K than
+ * it.  0 also on invalid or unsupported sizes (engram_matmul_fp8 then refuses
+ * the call). */
 ENGRAM_API size_t engram_matmul_fp8_workspace_size(engram_plan p, int64_t M, int64_t N, int64_t K);
 ENGRAM_API engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const uint8_t *d_a_scales,
                                            int32_t a_block_rows, const void *d_b, const uint8_t *d_b_scales,

@@ -555,6 +555,28 @@ def test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k):
 
 
 @pytest.mark.parametrize("out", DTYPES)
+def test_matmul_in_the_largest_batchs_workspace(gpu, out):
+    """A workspace kept for the largest batch serves the smaller ones: rows of a
+    (with N = K = 2560, 4096 of them take one part of K and 2560 two), and the
+    contraction; and a product of one part asks for none.  Whole numbers, exact."""
+    p = make_plan()
+    f8 = torch.float8_e4m3fn
+    ws = p.matmul_fp8_workspace(4096, 2560, 8192)
+    for m, n, k in [(4096, 2560, 2560), (2560, 2560, 2560), (1700, 2560, 2560), (2049, 1280, 8192), (2049, 1280, 6000),
+                    (77, 2560, 2560), (16, 2560, 8192), (1, 100, 8192)]:
+        a = torch.randint(-1, 2, (m, k), generator=gen(m)).float().to(gpu)
+        b = torch.randint(-1, 2, (n, k), generator=gen(n + 1)).float().to(gpu)
+        sa = torch.full(p.fp8_scale_shape(m, k, 1), 127, dtype=torch.uint8, device=gpu)
+        sb = torch.full(p.fp8_scale_shape(n, k, 128), 127, dtype=torch.uint8, device=gpu)
+        want = (a @ b.t().contiguous()).to(tdt(out))
+        for w in (ws, None) if (m, k) == (4096, 2560) else (ws,):
+            ws.fill_(255)
+            got = torch.full((m, n), 7.0, dtype=tdt(out), device=gpu)
+            p.engram_matmul_fp8(a.to(f8), sa, b.to(f8), sb, got, w)
+            assert torch.equal(got, want), (m, n, k)
+
+
+@pytest.mark.parametrize("out", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(3, 5, 1 << 20), (20, 70, 1 << 18), (1, 1, 4194288)])
 def test_matmul_long_rows(gpu, out, m, n, k):
     """K up to the largest there is, in many parts: whole numbers, exact in fp32."""

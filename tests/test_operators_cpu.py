@@ -298,3 +298,25 @@ def test_an_embed_backward_workspace_serves_smaller_batches(B, vocab, d):
         if s:
             chunk = 32 if n * ((d + 511) // 512) >= 65536 else 8
             assert s >= 8 * n + 4 * (vocab + 1) + 8 * d * -(-n // chunk)
+
+
+def test_a_matmul_workspace_serves_smaller_products(B):
+    """The size never falls as a batch grows, be it the product's rows (a
+    projection) or its contraction (a weight gradient), across the thresholds of
+    how a product is cut, and no larger size is refused its own."""
+    p = plan(B)
+    size = p.engram_matmul_fp8_workspace_size
+    steps = sorted({max(1, 2 ** i + j) for i in range(17) for j in (-1, 0, 1, 5)} | {2560, 1280, 4096, 12800, 129280})
+    ks = sorted({16 * max(1, s // 16) for s in steps} | {16 * s for s in (160, 161, 176, 255, 1024, 2047, 2048, 131072)})
+    fixed = [(1, 16), (16, 8192), (16, 8193), (17, 128), (100, 129), (129, 2560), (1280, 2560), (2560, 2560), (4096, 12800)]
+    for a, b in fixed:
+        for kk in (128, 1280, 2048, 2560, 8192, 32768, 1 << 20):
+            for along in ([size(m, a, kk) for m in steps], [size(b, n, kk) for n in steps], [size(a, n, kk) for n in steps]):
+                assert all(x <= y for x, y in zip(along, along[1:]))
+        along = [size(a, b, k) for k in ks]
+        assert all(x <= y for x, y in zip(along, along[1:]))
+    assert max(size(m, n, 4194288) for m in steps for n in steps) <= 64 << 20
+    # parts of K that a shape used before its size covered smaller ones
+    assert size(4096, 2560, 2560) >= 52428800      # 2560 rows in two parts
+    assert size(4096, 1280, 32768) >= 5 * 2560 * 1280 * 4
+    assert size(2560, 1280, 32768) >= 5 * 2560 * 1280 * 4
