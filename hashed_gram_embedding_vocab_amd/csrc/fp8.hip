@@ -921,9 +921,11 @@ size_t product_workspace_most(int64_t M, int64_t N, int64_t K) {
     return most;
 }
 
-bool product_fits(int64_t M, int64_t N, int64_t) {
-    // one launch: fewer than 2^32 threads
-    return ((N + 127) / 128) * ((M + 15) / 16) < ((int64_t)1 << 24);
+bool product_fits(int64_t M, int64_t N, int64_t K) {
+    // one launch: fewer than 2^32 threads (512 of them a 256 x 256 tile, else 256)
+    const ProductCut c = cut_of(M, N, K);
+    const int64_t tiles = ((N + c.tile - 1) / c.tile) * ((M + c.tile - 1) / c.tile);
+    return tiles * c.splits < ((int64_t)1 << (c.tile == 256 ? 23 : 24));
 }
 
 void launch_product(const ProductArgs &a, hipStream_t s) {

@@ -575,7 +575,9 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
  * 2^-13 of the largest one there (about 1.5e-5 of the result's norm, against
  * 1.7e-3 for its rounding).
  *   d_a, d_b     [M][K] and [N][K] e4m3, rows contiguous; K % 16 == 0 (else
- *                ENGRAM_E_UNSUPPORTED) and K < 2^22; the last block may be short
+ *                ENGRAM_E_UNSUPPORTED) and K < 2^22; the last block may be
+ *                short.  A result of 2^24 tiles of 128 x 128 or more (of 2^23
+ *                of 256 x 256 where M and N are above 128) is unsupported too
  *   a_block_rows, b_block_rows   1 or 128, as the scales were made
  *   d_c          [M][N] fp32 or bf16 (c_dtype)
  *   d_workspace  >= engram_matmul_fp8_workspace_size(p, M', N', K') bytes for

@@ -606,6 +606,25 @@ def test_matmul_result_larger_than_the_caches(gpu):
     assert torch.equal(got.float(), a @ b.t().contiguous())
 
 
+def test_matmul_result_of_many_tiles(gpu):
+    """More than 2^35 results (offsets past 2^32, 69 GB): sums of at most 16 ones, exact in bf16."""
+    torch.cuda.empty_cache()
+    p = make_plan()
+    m, n, k = 131077, 262153, 16
+    a = torch.randint(-1, 2, (m, k), generator=gen(1)).float().to(gpu)
+    b = torch.randint(-1, 2, (n, k), generator=gen(2)).float().to(gpu)
+    one = torch.full((1,), 127, dtype=torch.uint8, device=gpu)
+    got = torch.full((m, n), 7.0, dtype=torch.bfloat16, device=gpu)
+    f8 = torch.float8_e4m3fn
+    p.engram_matmul_fp8(a.to(f8), one.expand(m, 4).contiguous(), b.to(f8), one.expand(n, 4).contiguous(), got,
+                        p.matmul_fp8_workspace(m, n, k), b_block_rows=1)
+    bt = b.t().contiguous()
+    for r in range(0, m, 8192):
+        assert torch.equal(got[r:r + 8192], (a[r:r + 8192] @ bt).bfloat16()), r
+    del got
+    torch.cuda.empty_cache()
+
+
 def test_matmul_of_whole_numbers_is_exact(gpu):
     """Small whole numbers and scales of one: every partial sum is a whole number below 2^24."""
     p = make_plan()

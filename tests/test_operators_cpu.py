@@ -320,3 +320,16 @@ def test_a_matmul_workspace_serves_smaller_products(B):
     assert size(4096, 2560, 2560) >= 52428800      # 2560 rows in two parts
     assert size(4096, 1280, 32768) >= 5 * 2560 * 1280 * 4
     assert size(2560, 1280, 32768) >= 5 * 2560 * 1280 * 4
+
+
+def test_matmul_sizes_up_to_the_launchs(B):
+    """What is refused as unsupported is what one launch's tiles do not cover: a
+    misaligned result is found behind that check, and nothing is launched."""
+    p = plan(B)
+    fn = B.lib().engram_matmul_fp8
+    call = lambda m, n, k: fn(p._h, at(0), at(1), 1, at(2), at(3), 1, m, n, k, ODD, B.BF16, None, 0, None)  # noqa: E731
+    for m, n, k in [(131072, 262144, 128), (1048576, 32768, 1280), (1 << 20, 1 << 18, 16), (100, (1 << 31) - 128, 16),
+                    ((1 << 31) - 128, 1, 16), ((1 << 23) * 256 - 256, 256, 16)]:
+        assert call(m, n, k) == B.E_INVALID_ARG, (m, n, k)
+    for m, n, k in [(100, 1 << 31, 16), (1 << 31, 1, 16), ((1 << 23) * 256, 129, 16)]:
+        assert call(m, n, k) == B.E_UNSUPPORTED, (m, n, k)
