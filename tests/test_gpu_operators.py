@@ -353,6 +353,23 @@ def test_layer_norm_backward(gpu, dtype, rows, d):
     assert torch.equal(xx, dx) and torch.equal(dg2, dg)
 
 
+# more rows than blocks where 2, 4, 8 or 16 waves share a row (1024, 512, 256 and 256 blocks)
+WALKED_WIDE = [(1100, 2568), (1100, 4096), (530, 8192), (300, 8200), (300, 16384), (270, 16392), (270, 20488), (260, 32768)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("with_beta", (True, False))
+@pytest.mark.parametrize("rows,d", WALKED_WIDE)
+def test_layer_norm_walks_wide_rows(gpu, dtype, with_beta, rows, d):
+    test_layer_norm(gpu, dtype, with_beta, rows, d)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,d", WALKED_WIDE)
+def test_layer_norm_backward_walks_wide_rows(gpu, dtype, rows, d):
+    test_layer_norm_backward(gpu, dtype, rows, d)
+
+
 def test_layer_norm_backward_is_the_difference_of_the_forward(gpu):
     """Along a direction v: (L(x + hv) - L(x - hv)) / 2h against <dx, v>.  L = <w, y>.
     The difference misses by h^2/6 of L's third derivative, taken in 64 bits
@@ -552,6 +569,16 @@ def test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k):
         top = lambda v: torch.nn.functional.pad(v.abs(), (0, -k % 128)).reshape(len(v), -1, 128).amax(-1)  # noqa: E731
         bound = bound + (128 * 2.0 ** -13) * (top(av) @ top(bv).t().contiguous())
     assert bool(((got.double() - ref).abs() <= bound + half_step(out) * (ref.abs() + bound)).all())
+
+
+@pytest.mark.parametrize("out", DTYPES)
+@pytest.mark.parametrize("abr,bbr", [(128, 1), (128, 128)])
+@pytest.mark.parametrize("m,n,k", [(4100, 3900, 272), (2563, 1285, 8208), (3000, 2100, 400), (33000, 7, 144),
+                                   (128, 17000, 1296)])
+def test_matmul_large_tiles_with_a_scaled_by_128_rows(gpu, out, abr, bbr, m, n, k):
+    """The shared scale rows of a in 256 x 256 tiles (two of them a tile), with K
+    cut in parts, and in 128 x 128."""
+    test_matmul_large_tiles(gpu, out, abr, bbr, m, n, k)
 
 
 @pytest.mark.parametrize("out", DTYPES)
