@@ -797,6 +797,111 @@ def test_projection_and_its_gradients(gpu):
         close(got, xv @ yv.t(), slack + bound * 1.2, "unquantised")
 
 
+# ---------------------------------------------------------------- edges of buffers and of 32 bits
+
+
+class Guarded:
+    """A buffer inside a larger one whose bytes on either side must stay as they are."""
+
+    EDGE = 4096
+
+    def __init__(self, shape, dtype, gpu):
+        n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+        self.all = torch.full((n + 2 * self.EDGE,), 0xA5, dtype=torch.uint8, device=gpu)
+        self.n, self.t = n, self.all[self.EDGE:self.EDGE + n].view(dtype).view(shape)
+
+    def whole(self):
+        return bool((self.all[:self.EDGE] == 0xA5).all()) and bool((self.all[self.EDGE + self.n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d,branches", [(1, 1, 8, 1), (45, 37, 72, 3), (700, 333, 264, 2), (2049, 513, 520, 1),
+                                                    (131, 50, 2568, 1), (70, 9, 4104, 1)])
+def test_nothing_is_written_beside_the_outputs(gpu, dtype, n_tok, vocab, d, branches):
+    """Every output and workspace with bytes around it, at sizes that end inside a
+    vector, a wave's rows, a tile and a word of scales."""
+    p = make_plan(dtype, d, vocab, branches)
+    dt, f32, f8, u8 = tdt(dtype), torch.float32, torch.float8_e4m3fn, torch.uint8
+    made = []
+
+    def buf(shape, t):
+        made.append(Guarded(shape, t, gpu))
+        return made[-1].t
+
+    ids, table = zipf_ids(n_tok, vocab, 1).to(gpu), randn((vocab, d), dtype, 2).to(gpu)
+    gamma = 1.0 + randn((d,), "f32", 3, 0.1).to(gpu)
+    rows = branches * n_tok
+    h, y, dx = (buf((branches, n_tok, d), dt) for _ in range(3))
+    mean, rstd, bad = buf((rows,), f32), buf((rows,), f32), buf((1,), torch.int32)
+    p.engram_embed(ids, table, h, bad_tokens=bad)
+    p.engram_layer_norm(h, gamma, gamma, y, mean=mean, rstd=rstd)
+    dg, db, wn = buf((d,), f32), buf((d,), f32), buf((p.engram_layer_norm_backward_workspace_size(rows),), u8)
+    p.engram_layer_norm_backward(h, y, gamma, mean, rstd, dx, dg, db, wn)
+    dtab, we = buf((vocab, d), f32), buf((p.engram_embed_backward_workspace_size(n_tok),), u8)
+    p.engram_embed_backward(ids, dx, dtab, we)
+    for cols in (1, 16, 129, 520, 1288):
+        x = randn((n_tok, cols), dtype, 4).to(gpu)
+        for tr in (False, True):
+            r, c = (cols, n_tok) if tr else (n_tok, cols)
+            for br in (1, 128):
+                p.engram_quantize_fp8(x, buf((r, c), f8), buf(p.fp8_scale_shape(r, c, br), u8), block_rows=br, transpose=tr)
+    for n, k in [(1, 16), (37, 144), (129, 528), (520, 8208)]:
+        a, sa = (t.to(gpu) for t in random_quantized(n_tok, k, 1, 5))
+        b, sb = (t.to(gpu) for t in random_quantized(n, k, 128, 6))
+        size = p.engram_matmul_fp8_workspace_size(n_tok, n, k)
+        for out in (f32, torch.bfloat16):
+            p.engram_matmul_fp8(a, sa, b, sb, buf((n_tok, n), out), buf((size,), u8) if size else None)
+    torch.cuda.synchronize()
+    assert all(g.whole() for g in made), [i for i, g in enumerate(made) if not g.whole()]
+
+
+def test_rows_past_32_bits(gpu):
+    """Element and byte offsets past 2^31 and 2^32: the last rows of a long call are
+    those of a short one over them."""
+    torch.cuda.empty_cache()
+    rows, d, tail = 1 << 20, 4104, 256
+    p = make_plan("bf16", d)
+    x = torch.empty((rows, d), dtype=torch.bfloat16, device=gpu)
+    x.copy_(randn((1024, d), "bf16", 1).to(gpu).repeat(rows // 1024, 1))
+    x[-tail:] = randn((tail, d), "bf16", 2).to(gpu)
+    gamma, beta = (1.0 + randn((d,), "f32", s, 0.1).to(gpu) for s in (3, 4))
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device=gpu), torch.empty(rows, device=gpu)
+    ys, ms, rs = torch.empty_like(x[-tail:]), torch.empty(tail, device=gpu), torch.empty(tail, device=gpu)
+    p.engram_layer_norm(x, gamma, beta, y, mean=mean, rstd=rstd)
+    p.engram_layer_norm(x[-tail:], gamma, beta, ys, mean=ms, rstd=rs)
+    assert torch.equal(y[-tail:], ys) and torch.equal(mean[-tail:], ms) and torch.equal(rstd[-tail:], rs)
+    dg, db = torch.empty(d, device=gpu), torch.empty(d, device=gpu)
+    p.engram_layer_norm_backward(x, y, gamma, mean, rstd, y, dg, db, p.layer_norm_backward_workspace(rows))
+    p.engram_layer_norm_backward(x[-tail:], ys, gamma, ms, rs, ys, dg, db, p.layer_norm_backward_workspace(tail))
+    assert torch.equal(y[-tail:], ys)
+    del y
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    for br in (1, 128):
+        q, s = torch.empty((rows, d), dtype=f8, device=gpu), torch.empty(p.fp8_scale_shape(rows, d, br), dtype=u8, device=gpu)
+        p.engram_quantize_fp8(x, q, s, block_rows=br)
+        rq, rs8 = quantize_ref(x[-tail:].cpu(), br, False)
+        assert torch.equal(q[-tail:].cpu().double(), rq) and torch.equal(s[-(tail // br):].cpu(), rs8)
+        q, s = q.view(u8).view(d, rows).view(f8), torch.empty(p.fp8_scale_shape(d, rows, br), dtype=u8, device=gpu)
+        p.engram_quantize_fp8(x, q, s, block_rows=br, transpose=True)
+        rq, rs8 = quantize_ref(x[-tail:].cpu(), br, True)
+        assert torch.equal(q[:, -tail:].cpu().double(), rq) and torch.equal(s[:, -tail // 128:].cpu(), rs8[:, :tail // 128])
+    del x, q, s
+    m, n, k = (1 << 20) + 5, 2056, 2064
+    a = torch.zeros((m, k), dtype=u8, device=gpu)
+    a[-300:] = torch.randint(-1, 2, (300, k), generator=gen(5)).float().to(f8).view(u8).to(gpu)
+    b = torch.randint(-1, 2, (n, k), generator=gen(6)).float().to(f8).to(gpu)
+    one = torch.full((1,), 127, dtype=u8, device=gpu)
+    sa, sb = one.expand(*p.fp8_scale_shape(m, k, 1)).contiguous(), one.expand(*p.fp8_scale_shape(n, k, 128)).contiguous()
+    for out in (torch.bfloat16, torch.float32):
+        c = torch.full((m, n), 7.0, dtype=out, device=gpu)
+        p.engram_matmul_fp8(a.view(f8), sa, b, sb, c, p.matmul_fp8_workspace(m, n, k))
+        want = (a[-300:].view(f8).float() @ b.float().t().contiguous()).to(out)
+        assert torch.equal(c[-300:], want) and int(torch.count_nonzero(c[:-300])) == 0
+        del c
+    del a
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- together, streams, graphs
 
 
