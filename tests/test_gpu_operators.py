@@ -797,6 +797,25 @@ def test_projection_and_its_gradients(gpu):
         close(got, xv @ yv.t(), slack + bound * 1.2, "unquantised")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok", (1, 333, 1021))
+def test_weight_gradient_over_any_number_of_tokens(gpu, dtype, n_tok):
+    """dW = dv^T E with rows of zeros behind the tokens up to a multiple of 16: the
+    scales and values of the tokens alone, and the formula's product over them."""
+    p = make_plan(dtype)
+    n, k, t16 = 130, 257, -(-n_tok // 16) * 16
+    dv, e = randn((n_tok, n), dtype, 1, 1e-3), randn((n_tok, k), dtype, 2, 0.02)
+    full = lambda x: torch.nn.functional.pad(x, (0, 0, 0, t16 - n_tok))  # noqa: E731
+    (a, sa), (b, sb) = (quantize_gpu(p, full(x), 1, True, gpu, torch.uint8) for x in (dv, e))
+    (ra, rsa), (rb, rsb) = (quantize_ref(x, 1, True) for x in (dv, e))
+    assert torch.equal(sa.cpu(), rsa) and torch.equal(sb.cpu(), rsb)
+    got = torch.full((n, k), 7.0, device=gpu)
+    p.engram_matmul_fp8(a, sa, b, sb, got, p.matmul_fp8_workspace(n, k, t16), b_block_rows=1)
+    av, bv = ra * spread_bytes(rsa, n, n_tok, 1), rb * spread_bytes(rsb, k, n_tok, 1)
+    ref, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+    close(got, ref, 2 * U * (n_tok + 2) * mag + U * ref.abs(), "dW")
+
+
 # ---------------------------------------------------------------- edges of buffers and of 32 bits
 
 

@@ -333,3 +333,10 @@ def test_matmul_sizes_up_to_the_launchs(B):
         assert call(m, n, k) == B.E_INVALID_ARG, (m, n, k)
     for m, n, k in [(100, 1 << 31, 16), (1 << 31, 1, 16), ((1 << 23) * 256, 129, 16)]:
         assert call(m, n, k) == B.E_UNSUPPORTED, (m, n, k)
+
+
+def test_a_layer_norm_backward_workspace_serves_fewer_rows(B):
+    for d in (8, 64, 256, 512, 2560, 2568, 4104, 8200, 16384, 32768):
+        p = plan(B, d=d)
+        sizes = [p.engram_layer_norm_backward_workspace_size(n) for n in sorted({2 ** i + j for i in range(21) for j in (0, 1, 3)})]
+        assert sizes[0] > 0 and all(x <= y for x, y in zip(sizes, sizes[1:]))
