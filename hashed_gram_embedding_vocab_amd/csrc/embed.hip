@@ -208,6 +208,10 @@ __device__ __forceinline__ void put_row(float *dst, const F8 &acc, float scale, 
 // longer than their launch.  A wave per (token, 512 channels) finds the tokens
 // of the same id by ballot, leaves if one comes before, and adds all of them
 // in order.  Blocks from sum_blocks on write zeros to the rows without tokens.
+// What bounds it is the longest run, one wave's chain of trips to memory with U
+// tokens each: 512 tokens of 1000 x 1024 in bf16 with one branch and with four
+// take 6.4 and 6.3 us if all differ, 10.2 and 23.5 by a Zipf law, 50 and 169 if
+// all are one id; sorted (513 of them) 12.6 and 13.8, 13.7 and 14.9, 13.2 and 14.5.
 constexpr int kFew = 512;
 
 template <typename T, int BR>
@@ -404,7 +408,8 @@ int64_t sort_blocks(int32_t vocab) { return ((int64_t)vocab + kBucket - 1) / kBu
 // Pieces of the tokens: of about kPiece, and at most a workgroup for each CU in
 // all (the sort of 30,083 tokens over 1950 ids: 12.6 us against 33 in one piece,
 // of 524,288 over 32,000: 193 against 464; pieces of 4096 13.9 us, of 8192 16.1;
-// two workgroups a CU 229 us at the longest, four 346).
+// two workgroups a CU 229 us at the longest, four 346).  A vocabulary above
+// 65,536 has more than 128 buckets, which leaves one piece.
 constexpr int64_t kPiece = 2048;
 int64_t sort_parts(int64_t n_tok, int32_t vocab) {
     return std::max<int64_t>(1, std::min((n_tok + kPiece - 1) / kPiece, 256 / sort_blocks(vocab)));

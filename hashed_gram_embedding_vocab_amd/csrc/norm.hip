@@ -13,7 +13,13 @@
 // flight while a row is worked on.  Measured in bf16 at d = 2560: forward of
 // 32,768 rows 67 us (a block per four rows, gamma and beta read per row: 82),
 // backward of 131,072 rows 388 us (one row at a time, expanded once: 467), 5.0
-// and 5.2 TB/s; a large copy runs at 5.2.
+// and 5.2 TB/s; a large copy runs at 5.2.  Rows of 4096 to 16,384 channels (256 MB
+// of them) run at 4.6 to 5.5 TB/s forward and 5.0 to 5.2 backward in bf16, 5.2 to
+// 5.3 and 4.4 to 5.0 in fp32.
+// Above 16,384 channels 16 waves share a row, which leaves a lane 128
+// registers.  The forward then reads gamma and beta for every row (4.1 to 4.8
+// TB/s).  The backward keeps its state all the same and spills 216 to 544 bytes
+// a lane to scratch (in fp32 40 above 12,288 channels): 1.0 to 1.8 TB/s.
 #include <algorithm>
 
 #include "engram_internal.h"
@@ -325,7 +331,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum_kernel(const float *part, i
 }
 
 // How a row is spread: 8 to 32 lanes up to 256 channels, one wave up to 2560
-// (five steps, about 200 registers in the backward), then 2 to 16 waves.
+// (five steps; 262 registers in the bf16 backward and 308 in the fp32 one, so
+// one wave a SIMD there), then 2 to 16 waves.
 struct RowShape {
     int lanes, waves, steps;
     int at_once() const { return waves == 1 ? 256 / lanes : 1; }
@@ -338,8 +345,9 @@ RowShape row_shape(int32_t d) {
     return RowShape{64, w, (units + w - 1) / w};
 }
 
-// Blocks of 4 waves' worth that keep a CU's SIMDs full at the kernels' register
-// counts, times 256 CUs.
+// Blocks: per_cu times 4 waves for each of 256 CUs, or one for each where that
+// is less.  (Where the registers hold fewer at once, as in the five-step
+// backward with one of its two, the others follow.)
 int64_t norm_blocks(const RowShape &sh, int64_t n_rows, int per_cu) {
     const int64_t waves = sh.waves == 1 ? 4 : sh.waves;
     return std::min<int64_t>((n_rows + sh.at_once() - 1) / sh.at_once(), std::max<int64_t>(256, 256 * per_cu * 4 / waves));

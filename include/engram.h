@@ -550,7 +550,9 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
                                                     void *d_workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
- * The layer's products in 8-bit floating point, a scale for each block of 128.
+ * Matrix products in 8-bit floating point, a scale for each block of 128: a
+ * model's projections and their gradients.  (engram_forward and engram_backward
+ * project in the plan dtype; they take no 8-bit operand and no k or v made here.)
  *
  * A quantised matrix [R][C] is its e4m3 values (4 exponent bits, bias 7, no
  * infinities, largest 448), rows of C bytes, and its scales: blocks of 128
@@ -571,13 +573,18 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
  * rounded once to c_dtype.  An fp32 result is summed in fp32 throughout, over
  * the values q * scale held as bf16 (exact while they lie in bf16's normal
  * range).  A bf16 result takes the 8-bit matrix instructions at twice the rate:
- * sums across blocks are fp32, but inside a block a product counts only to
- * 2^-13 of the largest one there (about 1.5e-5 of the result's norm, against
- * 1.7e-3 for its rounding).
+ * of eight consecutive products (k = 8 i .. 8 i + 7) each counts to 2^-13 of the
+ * largest of the eight, and all else is summed in fp32.  That loses less than
+ * 8.5e-4 of the sum of the products' magnitudes (on random operands 1.5e-5 of the
+ * result's norm, beside 1.7e-3 for its rounding to bf16); where large products
+ * cancel and that is too much, ask for an fp32 result and round it.
  *   d_a, d_b     [M][K] and [N][K] e4m3, rows contiguous; K % 16 == 0 (else
  *                ENGRAM_E_UNSUPPORTED) and K < 2^22; the last block may be
  *                short.  A result of 2^24 tiles of 128 x 128 or more (of 2^23
- *                of 256 x 256 where M and N are above 128) is unsupported too
+ *                of 256 x 256 where M and N are above 128) is unsupported too.
+ *                Where K counts tokens (a weight gradient), fill the 16-bit
+ *                operands up to a multiple of 16 rows with zeros before they
+ *                are quantised: zeros change no scale and add nothing
  *   a_block_rows, b_block_rows   1 or 128, as the scales were made
  *   d_c          [M][N] fp32 or bf16 (c_dtype)
  *   d_workspace  >= engram_matmul_fp8_workspace_size(p, M', N', K') bytes for
@@ -585,7 +592,7 @@ ENGRAM_API engram_status engram_layer_norm_backward(engram_plan p, const void *d
  *                where that is 0
  * A scale byte of 255 stands for NaN.
  *
- * One projection of the layer and its gradients, E [n_tok][D_e] and W [d][D_e]:
+ * One projection and its gradients, E [n_tok][D_e] and W [d][D_e]:
  *   v  = E W^T       E by token (block_rows 1), W by 128 x 128
  *   dE = dv W        dv by token, W transposed by 128 x 128
  *   dW = dv^T E      both transposed, block_rows 1 (blocks of 128 tokens)
