@@ -12,6 +12,7 @@ from .binding import (  # noqa: F401
     F32,
     OUT_DELTA,
     EngramError,
+    GradList,
     Plan,
     Weights,
     engram_synth_fill_table,

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import atexit
 import ctypes as C
+import math
 import os
 import threading
 import weakref
@@ -28,7 +29,7 @@ CONV_LINEAR, CONV_SILU_SKIP = 0, 1
 OUT_DELTA = 1
 RETRIEVE_IN_PROJECTION = 2  # engram_forward: retrieval inside the projection launches
 WEIGHTS_PACKED = 4  # engram_forward / engram_gate_fuse: W_k and W_v as engram_pack_weight wrote them
-GRAD_ACCUMULATE = 8  # engram_embed_backward / engram_layer_norm_backward: add to the parameters' gradients
+GRAD_ACCUMULATE = 8  # the operators' backward calls: add to the parameters' gradients
 QUANTIZE_TRANSPOSE = 16  # engram_quantize_fp8: quantise the transpose
 MAX_TABLES, MAX_BRANCHES = 32, 4
 NOALLOC_SCRATCH_BYTES = 64 << 20  # ENGRAM_NOALLOC_SCRATCH_BYTES
@@ -70,6 +71,13 @@ class GradsC(C.Structure):
     _fields_ = [
         ("dw", C.c_void_p), ("dgamma_h", C.c_void_p), ("dgamma_k", C.c_void_p), ("dconv_w", C.c_void_p),
         ("row_ids", C.c_void_p), ("row_grads", C.c_void_p), ("row_counts", C.c_void_p),
+    ]
+
+
+class GradC(C.Structure):
+    _fields_ = [
+        ("data", C.c_void_p), ("out", C.c_void_p), ("row_counts", C.c_void_p),
+        ("n_groups", C.c_int64), ("rows", C.c_int64), ("row_len", C.c_int64), ("dtype", C.c_int),
     ]
 
 
@@ -141,6 +149,24 @@ def lib() -> C.CDLL:
         L.engram_matmul_fp8_workspace_size.argtypes = [P, i64, i64, i64]
         L.engram_matmul_fp8.restype = C.c_int
         L.engram_matmul_fp8.argtypes = [P, P, P, i32, P, P, i32, i64, i64, i64, P, C.c_int, P, C.c_size_t, P]
+        L.engram_rms_norm.restype = C.c_int
+        L.engram_rms_norm.argtypes = [P, P, P, i64, P, f32, P, P, P, P, P, P]
+        L.engram_rms_norm_backward_workspace_size.restype = C.c_size_t
+        L.engram_rms_norm_backward_workspace_size.argtypes = [P, i64]
+        L.engram_rms_norm_backward.restype = C.c_int
+        L.engram_rms_norm_backward.argtypes = [P, P, P, P, i64, P, P, u32, P, P, P, C.c_size_t, P]
+        L.engram_cross_entropy_workspace_size.restype = C.c_size_t
+        L.engram_cross_entropy_workspace_size.argtypes = [P, i64]
+        L.engram_cross_entropy.restype = C.c_int
+        L.engram_cross_entropy.argtypes = [P, P, P, P, i64, f32, P, P, P, C.c_size_t, P]
+        L.engram_cross_entropy_backward_workspace_size.restype = C.c_size_t
+        L.engram_cross_entropy_backward_workspace_size.argtypes = [P, i64, C.c_int]
+        L.engram_cross_entropy_backward.restype = C.c_int
+        L.engram_cross_entropy_backward.argtypes = [P, P, P, P, i64, f32, P, P, f32, u32, P, P, C.c_int, P, C.c_size_t, P]
+        L.engram_clip_grads_workspace_size.restype = C.c_size_t
+        L.engram_clip_grads_workspace_size.argtypes = [P, i32]
+        L.engram_clip_grads.restype = C.c_int
+        L.engram_clip_grads.argtypes = [P, P, i32, f32, P, P, C.c_size_t, P]
         L.engram_profile_begin.restype = C.c_int
         L.engram_profile_begin.argtypes = [P, i32, u32]
         L.engram_profile_end.restype = C.c_int
@@ -347,6 +373,12 @@ def _call(fn: str, stream, tensors, *args):
         _check(fn, status)
 
 
+def _grad_dtype(dtype) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("a gradient's dtype is float32 or bfloat16, not %s" % dtype)
+    return F32 if dtype == torch.float32 else BF16
+
+
 def _torch_dtype(dt: int):
     return torch.bfloat16 if dt == BF16 else torch.float32
 
@@ -366,6 +398,44 @@ class Grads:
         self.row_counts = torch.zeros((n_tables,), dtype=torch.int32, device=device)
         self.c = GradsC(*[C.c_void_p(t.data_ptr()) for t in (self.dw, self.dgamma_h, self.dgamma_k, self.dconv_w,
                                                             self.row_ids, self.row_grads, self.row_counts)])
+
+
+class GradList:
+    """The gradients that engram_clip_grads takes together, plus their C array.
+
+    grads: fp32 or bf16 tensors.  outs: where each is written scaled: the tensor
+    itself (outs=None: all in place), another one like it, or None (only its norm
+    counts).  row_counts: for each tensor None, or an int32 tensor [n_groups] on
+    the device for a tensor [n_groups][rows][...]: of every group only so many
+    rows, the first, take part (Grads.row_grads with Grads.row_counts)."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                 row_counts: Optional[Sequence[Optional[torch.Tensor]]] = None):
+        self.grads = list(grads)
+        self.outs = list(self.grads if outs is None else outs)
+        self.row_counts = list([None] * len(self.grads) if row_counts is None else row_counts)
+        if not self.grads or not len(self.grads) == len(self.outs) == len(self.row_counts):
+            raise ValueError("a list of gradients with as many outs and row_counts, got %d, %d and %d"
+                             % (len(self.grads), len(self.outs), len(self.row_counts)))
+        kinds = (torch.float32, torch.bfloat16)
+        self.c = (GradC * len(self.grads))()
+        for i, (g, o, n) in enumerate(zip(self.grads, self.outs, self.row_counts)):
+            e = self.c[i]
+            e.data, e.out = _addr(g, "grads[%d]" % i, *kinds), _addr(o, "outs[%d]" % i, g.dtype)
+            e.row_counts = _addr(n, "row_counts[%d]" % i, torch.int32)
+            _shape(o, "outs[%d]" % i, *g.shape)
+            e.n_groups, e.rows, e.row_len = 1, 1, g.numel()
+            if n is not None:
+                if g.dim() < 2 or n.shape != g.shape[:1]:
+                    raise ValueError("row_counts[%d] has shape %s, expected a count for each of the groups of %s"
+                                     % (i, tuple(n.shape), tuple(g.shape)))
+                e.n_groups, e.rows, e.row_len = g.shape[0], g.shape[1], math.prod(g.shape[2:])
+            e.dtype = F32 if g.dtype == torch.float32 else BF16
+        # what a call checks to be on one device
+        self.tensors = tuple(t for t in self.grads + self.outs + self.row_counts if t is not None)
+        dev = self.tensors[0].get_device()
+        if any(t.get_device() != dev for t in self.tensors):
+            raise ValueError("the gradients of a list are on several devices")
 
 
 class Weights:
@@ -657,6 +727,114 @@ class Plan:
             _shape(a_scales, "a_scales", *self.fp8_scale_shape(m, k, a_block_rows))
             _shape(b_scales, "b_scales", *self.fp8_scale_shape(n, k, b_block_rows))
         _call("engram_matmul_fp8", stream, (a, a_scales, b, b_scales, out, workspace), self._h, *args)
+
+    def engram_rms_norm(self, x, gamma, y=None, residual=None, total=None, q=None, scales=None, rrms=None,
+                        eps: float = 1e-6, stream=None):
+        """total = x + residual (neither: x itself), y = RMS norm of total's rows
+        ([..., d]) times gamma; q and scales = y in 8 bits (float8_e4m3fn like x, and
+        float8_e8m0fnu or uint8 of fp8_scale_shape(n_rows, d, 1)).  y or q or both;
+        rrms (fp32, one a row) is kept for the backward if given."""
+        dt, f32, d = self.torch_dtype, torch.float32, self._d
+        n_rows = self._rows(x, "x")
+        args = (_addr(x, "x", dt), _addr(residual, "residual", dt), n_rows, _addr(gamma, "gamma", f32), eps,
+                _addr(total, "total", dt), _addr(y, "y", dt), _addr(q, "q", torch.float8_e4m3fn),
+                _addr(scales, "scales", *_E8M0), _addr(rrms, "rrms", f32))
+        for t, name in ((residual, "residual"), (total, "total"), (y, "y"), (q, "q")):
+            _shape(t, name, *x.shape)
+        _shape(gamma, "gamma", d)
+        _shape(scales, "scales", *self.fp8_scale_shape(n_rows, d, 1))
+        _count(rrms, "rrms", n_rows)
+        _call("engram_rms_norm", stream, (x, residual, gamma, total, y, q, scales, rrms), self._h, *args)
+
+    def engram_rms_norm_backward_workspace_size(self, n_rows: int) -> int:
+        return int(lib().engram_rms_norm_backward_workspace_size(self._h, n_rows))
+
+    def rms_norm_backward_workspace(self, n_rows: int, device="cuda") -> torch.Tensor:
+        """A workspace for engram_rms_norm_backward of up to n_rows rows."""
+        return self._workspace("engram_rms_norm_backward", self.engram_rms_norm_backward_workspace_size(n_rows), device)
+
+    def engram_rms_norm_backward(self, s, dy, gamma, rrms, dx, dgamma, workspace, dtotal=None, flags: int = 0,
+                                 stream=None):
+        """dx (of x and of the residual alike; it may be s, dy or dtotal) and dgamma
+        of engram_rms_norm: s is what was normed, dtotal the gradient that reaches it
+        through the residual stream; flags=GRAD_ACCUMULATE adds to dgamma."""
+        dt, f32, d = self.torch_dtype, torch.float32, self._d
+        n_rows = self._rows(s, "s")
+        args = (_addr(s, "s", dt), _addr(dy, "dy", dt), _addr(dtotal, "dtotal", dt), n_rows,
+                _addr(gamma, "gamma", f32), _addr(rrms, "rrms", f32), flags, _addr(dx, "dx", dt),
+                _addr(dgamma, "dgamma", f32), _addr(workspace, "workspace"), workspace.nbytes)
+        for t, name in ((dy, "dy"), (dtotal, "dtotal"), (dx, "dx")):
+            _shape(t, name, *s.shape)
+        _shape(gamma, "gamma", d)
+        _shape(dgamma, "dgamma", d)
+        _count(rrms, "rrms", n_rows)
+        _call("engram_rms_norm_backward", stream, (s, dy, dtotal, gamma, rrms, dx, dgamma, workspace), self._h, *args)
+
+    def engram_cross_entropy_workspace_size(self, n_tok: int) -> int:
+        return int(lib().engram_cross_entropy_workspace_size(self._h, n_tok))
+
+    def cross_entropy_workspace(self, n_tok: int, device="cuda") -> torch.Tensor:
+        """A workspace for engram_cross_entropy of up to n_tok tokens."""
+        return self._workspace("engram_cross_entropy", self.engram_cross_entropy_workspace_size(n_tok), device)
+
+    def engram_cross_entropy(self, h, weight, targets, loss, lse, workspace, scale: float = 1.0, stream=None):
+        """loss and lse (fp32, one a token) of the logits scale * h @ weight.T, which
+        are never in memory.  h: [..., d]; weight: [vocab][d]; targets: int32, one a
+        token; one outside [0, vocab) does not count (loss and lse 0)."""
+        dt, f32 = self.torch_dtype, torch.float32
+        n_tok = self._rows(h, "h")
+        args = (_addr(h, "h", dt), _addr(weight, "weight", dt), _addr(targets, "targets", torch.int32), n_tok, scale,
+                _addr(loss, "loss", f32), _addr(lse, "lse", f32), _addr(workspace, "workspace"), workspace.nbytes)
+        _shape(weight, "weight", self._vocab, self._d)
+        for t, name in ((targets, "targets"), (loss, "loss"), (lse, "lse")):
+            _count(t, name, n_tok)
+        _call("engram_cross_entropy", stream, (h, weight, targets, loss, lse, workspace), self._h, *args)
+
+    def engram_cross_entropy_backward_workspace_size(self, n_tok: int, dweight_dtype=torch.float32) -> int:
+        return int(lib().engram_cross_entropy_backward_workspace_size(self._h, n_tok, _grad_dtype(dweight_dtype)))
+
+    def cross_entropy_backward_workspace(self, n_tok: int, dweight_dtype=torch.float32, device="cuda") -> torch.Tensor:
+        """A workspace for engram_cross_entropy_backward of up to n_tok tokens."""
+        return self._workspace("engram_cross_entropy_backward",
+                               self.engram_cross_entropy_backward_workspace_size(n_tok, dweight_dtype), device)
+
+    def engram_cross_entropy_backward(self, h, weight, targets, lse, dloss, dh, dweight, workspace, scale: float = 1.0,
+                                      dloss_scale: float = 1.0, flags: int = 0, stream=None):
+        """dh (plan dtype) and dweight (fp32, or bf16 in bf16 plans), either of them
+        None where it is not wanted, from the forward's lse and each token's loss
+        gradient dloss (fp32; None: ones) times dloss_scale; flags=GRAD_ACCUMULATE
+        adds to dweight."""
+        dt, f32 = self.torch_dtype, torch.float32
+        n_tok = self._rows(h, "h")
+        # without dweight the smaller workspace does
+        wdt = _grad_dtype(dt if dweight is None else dweight.dtype)
+        args = (_addr(h, "h", dt), _addr(weight, "weight", dt), _addr(targets, "targets", torch.int32), n_tok, scale,
+                _addr(lse, "lse", f32), _addr(dloss, "dloss", f32), dloss_scale, flags, _addr(dh, "dh", dt),
+                _addr(dweight, "dweight", f32, torch.bfloat16), wdt, _addr(workspace, "workspace"), workspace.nbytes)
+        _shape(weight, "weight", self._vocab, self._d)
+        _shape(dweight, "dweight", self._vocab, self._d)
+        _shape(dh, "dh", *h.shape)
+        for t, name in ((targets, "targets"), (lse, "lse"), (dloss, "dloss")):
+            _count(t, name, n_tok)
+        _call("engram_cross_entropy_backward", stream, (h, weight, targets, lse, dloss, dh, dweight, workspace), self._h,
+              *args)
+
+    def engram_clip_grads_workspace_size(self, n_grads: int) -> int:
+        return int(lib().engram_clip_grads_workspace_size(self._h, n_grads))
+
+    def clip_grads_workspace(self, grads, device="cuda") -> torch.Tensor:
+        """A workspace for engram_clip_grads of a GradList, or of up to so many gradients."""
+        n = grads if isinstance(grads, int) else len(grads.grads)
+        return self._workspace("engram_clip_grads", self.engram_clip_grads_workspace_size(n), device)
+
+    def engram_clip_grads(self, grads: GradList, norm, workspace, max_norm: float = math.inf, stream=None):
+        """norm (fp32 [2]) = the norm of all gradients together and the factor that
+        brings it down to max_norm (1 where it is not above it, or not finite); the
+        list's outs = the gradients times the factor."""
+        args = (C.addressof(grads.c), len(grads.grads), max_norm, _addr(norm, "norm", torch.float32),
+                _addr(workspace, "workspace"), workspace.nbytes)
+        _count(norm, "norm", 2)
+        _call("engram_clip_grads", stream, (norm, workspace, grads.tensors[0]), self._h, *args)
 
     def _rows(self, x, name: str) -> int:
         d = self._d

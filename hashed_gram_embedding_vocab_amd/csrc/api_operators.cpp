@@ -15,18 +15,6 @@ using namespace engram::host;
 
 namespace {
 
-// Whether two buffers share a byte.
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
-}
-
-bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-
-// More elements than any GPU's memory holds: such sizes are refused before
-// products of them can overflow.
-constexpr int64_t kMaxElems = (int64_t)1 << 42;
-
 struct EmbedLayout {
     size_t order, sid, start, lead, tail, total;
 };

@@ -405,6 +405,56 @@ int32_t norm_bwd_blocks(int64_t n_rows, int32_t d);
 void launch_norm(engram_dtype dt, const NormArgs &a, hipStream_t s);
 void launch_norm_bwd(engram_dtype dt, const NormArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------- RMS norm
+struct RmsArgs {
+    const void *x, *res;                    // [n_rows][d] plan dtype; res may be null
+    void *total, *y;                        // [n_rows][d] plan dtype: x + res; the normed rows, or null
+    uint8_t *q, *scales;                    // [n_rows][d] e4m3 and its scales, or null
+    const void *dy, *ds;                    // backward: [n_rows][d]; ds (the total's gradient) may be null
+    void *dx;
+    const float *gamma;                     // [d]
+    float *rrms;                            // [n_rows]: written by the forward (if given), read by the backward
+    float *part;                            // [rms_bwd_blocks][d] partial sums of dgamma
+    float *dgamma;                          // [d]
+    int64_t n_rows;
+    int32_t d;
+    float eps;
+    bool accumulate;
+};
+int32_t rms_bwd_blocks(int64_t n_rows, int32_t d);
+void launch_rms(engram_dtype dt, const RmsArgs &a, hipStream_t s);
+void launch_rms_bwd(engram_dtype dt, const RmsArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- cross entropy
+struct LossArgs {
+    const void *h, *w;                      // [n_tok][d], [vocab][d] plan dtype
+    const int32_t *targets;                 // [n_tok]
+    float *loss;                            // [n_tok]
+    float *lse;                             // [n_tok]: written by the forward, read by the backward
+    const float *dloss;                     // [n_tok] or null: ones
+    void *dh, *dw;                          // [n_tok][d] plan dtype, [vocab][d]; either may be null
+    void *ws;
+    int64_t n_tok;
+    int32_t vocab, d;
+    float scale, dloss_scale;
+    bool bf16;                              // the plan's dtype
+    bool dw_bf16, accumulate;               // dw's dtype (bf16 too where dw is null and the plan is bf16)
+};
+// Byte offsets in the workspace and its size; the size never falls as n_tok grows.
+struct LossLayout {
+    size_t xt, part, h, w, sum, wsum, total;
+};
+LossLayout loss_layout(const LossArgs &a);
+LossLayout loss_bwd_layout(const LossArgs &a);
+bool loss_fits(int64_t n_tok, int32_t vocab, int32_t d);
+void launch_loss(const LossArgs &a, hipStream_t s);
+void launch_loss_bwd(const LossArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- clipping
+int64_t clip_chunks(const engram_grad &g);  // pieces of a tensor: a list's come to less than 2^31
+size_t clip_workspace(int64_t n_grads);
+void launch_clip(const engram_grad *grads, int32_t n_grads, float max_norm, float *norm, double *part, hipStream_t s);
+
 // ---------------------------------------------------------------- 8-bit product
 struct QuantArgs {
     const void *x;                          // [rows][cols] plan dtype

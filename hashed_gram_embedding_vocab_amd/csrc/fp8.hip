@@ -26,7 +26,9 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "block8.h"
 #include "engram_internal.h"
+#include "stage.h"
 #include "vec8.h"
 
 namespace engram {
@@ -35,91 +37,6 @@ namespace {
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------- quantisation
-// Largest magnitudes of 8 columns as bit patterns (which order like the
-// values), two bf16 columns a word.  NaN and infinity are above kNotFinite.
-constexpr uint32_t kNotFinite = 0x7F800000u;
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
-                                                                  __builtin_bit_cast(u16x2_t, b)));
-}
-
-template <typename T>
-struct Top8;
-template <>
-struct Top8<uint16_t> {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    __device__ __forceinline__ void add(const Raw8<uint16_t> &x) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = max_u16x2(w[i], x.w[i] & 0x7FFF7FFFu);
-    }
-    __device__ __forceinline__ uint32_t column(int i) const { return (i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16; }
-    __device__ __forceinline__ uint32_t all() const {
-        const uint32_t m = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
-        return max(m & 0xFFFF0000u, m << 16);
-    }
-};
-template <>
-struct Top8<float> {
-    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    __device__ __forceinline__ void add(const Raw8<float> &x) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = max(w[i], __float_as_uint(x.a[i]) & 0x7FFFFFFFu);
-            w[4 + i] = max(w[4 + i], __float_as_uint(x.b[i]) & 0x7FFFFFFFu);
-        }
-    }
-    __device__ __forceinline__ uint32_t column(int i) const { return w[i]; }
-    __device__ __forceinline__ uint32_t all() const {
-        uint32_t m = w[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) m = max(m, w[i]);
-        return m;
-    }
-};
-
-// |x| as bits, 0 where x is not finite
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-    return b < kNotFinite ? b : 0u;
-}
-
-// Biased exponent of the block's scale from the bits of its largest finite
-// magnitude (448 = 1.75 * 2^8).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
-    const int e = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return (uint32_t)max(e, 1);
-}
-
-// 1 / scale: exact (a power of two in the normal range, 2^-120 .. 2^126)
-__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-// To e4m3 bytes.  Finite values are at most 448 here; the conversion makes NaN
-// of infinities, which e4m3 does not have.
-__device__ __forceinline__ u32x2_t cvt8(const F8 &x, float inv) {
-    u32x2_t q;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x.v[4 * i] * inv, x.v[4 * i + 1] * inv, 0, false);
-        q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x.v[4 * i + 2] * inv, x.v[4 * i + 3] * inv, w, true);
-    }
-    return q;
-}
-
-// Vectors at any address (the hardware splits an access where it has to):
-// rows whose length is no multiple of the vector's.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-__device__ __forceinline__ Raw8<uint16_t> load_any8(const uint16_t *p) {
-    return Raw8<uint16_t>{*reinterpret_cast<const u32x4_any *>(p)};
-}
-__device__ __forceinline__ Raw8<float> load_any8(const float *p) {
-    return Raw8<float>{*reinterpret_cast<const f32x4_any *>(p), *reinterpret_cast<const f32x4_any *>(p + 4)};
-}
-
 // 8 values at column c of a row of `cols`, zeros past its end.  VEC: rows are
 // whole 8-value units and 16-byte aligned.
 template <bool VEC, typename T>
@@ -156,13 +73,6 @@ __device__ __forceinline__ void store_cols(uint8_t *row, int64_t c, int64_t cols
             if (c + i < cols) row[c + i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
     }
 }
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
-    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true));
-}
-// over the 16 lanes of a row (neighbours, quads, halves, the row's mirror)
-__device__ __forceinline__ uint32_t max16(uint32_t x) { return dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(x)))); }
 
 // One wave per (U rows, 512 columns): a block is 16 lanes, and the wave's four
 // scale bytes of a row are one word of the scales' row (its blocks past the
@@ -365,8 +275,6 @@ void quantize(const QuantArgs &a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- product
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-
 // The MFMA's A side is rows of b (n), its B side rows of a (m), both
 // K-contiguous: lane l holds row l % 16 and 32 of the block's 128 bytes, and
 // result lane l holds C[m = l % 16][n = 4 (l / 16) .. + 3].  Which 32 bytes a
@@ -391,8 +299,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // storing (8% slower: its first step waits for the stores), results stored
 // from the fragments without LDS (3% slower at 32768 x 12800), a start along K
 // rotated by workgroup against equal channels of K = 2^n (no change).
-typedef __attribute__((address_space(3))) void lds_void_t;
-
 struct Frag {
     u32x4_t half[2];
 };
@@ -411,31 +317,6 @@ __device__ __forceinline__ bf16x8_t to_bf16x8(uint32_t w0, uint32_t w1, uint32_t
     const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
     return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0,
-                                             (int)min(bytes, (int64_t)0x7FFFFFFF), 0x00020000);
-}
-
-// All but this wave's last N loads have landed and its LDS reads are done, then
-// the workgroup's barrier: every wave's are.
-template <int N>
-__device__ __forceinline__ void stage_barrier() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));  // vmcnt(N) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-// This wave's loads have landed.
-__device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));  // vmcnt(0)
-    asm volatile("" ::: "memory");
-}
-
-constexpr int kXcds = 8;
-constexpr uint32_t kPast = 0x80000000u;  // an offset behind every buffer
 
 // First row of b and of a of this workgroup's tile, and its part of K.
 // Consecutive workgroups go to the XCDs in turn: each XCD gets a contiguous

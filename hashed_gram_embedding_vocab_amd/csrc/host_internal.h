@@ -1,7 +1,7 @@
 // host_internal.h -- what the host side of the C ABI shares between its
 // files (api.cpp: plans, retrieval and fusion; api_backward.cpp: the
-// backward; api_offload.cpp: host-resident tables and the prefetcher): the
-// plan, the profiling scope of a launch, argument checks and the row gather.
+// backward; api_offload.cpp: host-resident tables and the prefetcher;
+// api_operators.cpp, api_ends.cpp: the operators beside the layer): the plan, the profiling scope of a launch, argument checks and the row gather.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -36,6 +36,18 @@ namespace engram {
 namespace host {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether two buffers share a byte.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+inline bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// More elements than any GPU's memory holds: such sizes are refused before
+// products of them can overflow.
+constexpr int64_t kMaxElems = (int64_t)1 << 42;
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -1,5 +1,5 @@
 // vec8.h -- eight consecutive bf16 or fp32 elements moved as fp32 values: the
-// unit in which the row kernels (embed.hip, norm.hip, fp8.hip) read and write.
+// unit in which the row kernels (embed.hip, norm.hip, rms.hip, fp8.hip, clip.hip) read and write.
 // Rounding to bf16 is to nearest even and keeps NaN and infinity.
 #pragma once
 
@@ -56,6 +56,27 @@ __device__ __forceinline__ void store8(uint16_t *p, const F8 &x) {
 __device__ __forceinline__ void store8(float *p, const F8 &x) {
     *reinterpret_cast<f32x4_t *>(p) = f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]};
     *reinterpret_cast<f32x4_t *>(p + 4) = f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]};
+}
+
+// The same units at any address (the hardware splits an access where it has to):
+// rows whose length is no multiple of the vector's.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ Raw8<uint16_t> load_any8(const uint16_t *p) {
+    return Raw8<uint16_t>{*reinterpret_cast<const u32x4_any *>(p)};
+}
+__device__ __forceinline__ Raw8<float> load_any8(const float *p) {
+    return Raw8<float>{*reinterpret_cast<const f32x4_any *>(p), *reinterpret_cast<const f32x4_any *>(p + 4)};
+}
+__device__ __forceinline__ void store_any8(uint16_t *p, const F8 &x) {
+    *reinterpret_cast<u32x4_any *>(p) = u32x4_t{pack_bf16x2(x.v[0], x.v[1]), pack_bf16x2(x.v[2], x.v[3]),
+                                                pack_bf16x2(x.v[4], x.v[5]), pack_bf16x2(x.v[6], x.v[7])};
+}
+__device__ __forceinline__ void store_any8(float *p, const F8 &x) {
+    *reinterpret_cast<f32x4_any *>(p) = f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]};
+    *reinterpret_cast<f32x4_any *>(p + 4) = f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]};
 }
 
 }  // namespace engram

@@ -82,9 +82,10 @@ enum { ENGRAM_RETRIEVE_IN_PROJECTION = 1u << 1 };
  * (bf16 plans only; engram_backward takes the [d][D_e] matrices and rejects
  * the flag).  Same results bit for bit. */
 enum { ENGRAM_WEIGHTS_PACKED = 1u << 2 };
-/* engram_embed_backward / engram_layer_norm_backward flag: the parameters'
- * gradients are added to what their buffers hold instead of overwriting it
- * (micro-batches of one optimizer step). */
+/* engram_embed_backward / engram_layer_norm_backward / engram_rms_norm_backward /
+ * engram_cross_entropy_backward flag: the parameters' gradients are added to
+ * what their buffers hold instead of overwriting it (micro-batches of one
+ * optimizer step). */
 enum { ENGRAM_GRAD_ACCUMULATE = 1u << 3 };
 /* engram_quantize_fp8 flag: quantise the transpose of x. */
 enum { ENGRAM_QUANTIZE_TRANSPOSE = 1u << 4 };
@@ -135,18 +136,20 @@ enum {
     ENGRAM_K_GATHER = 1,  /* engram_gather, or the fused hash + gather of engram_forward;
                              engram_embed                                                    */
     ENGRAM_K_GEMM = 2,    /* projections W_k e of every branch with the gate partials fused
-                             (and W_v e on the fusion-kernel path); engram_matmul_fp8        */
+                             (and W_v e on the fusion-kernel path); engram_matmul_fp8,
+                             engram_cross_entropy                                           */
     ENGRAM_K_FUSE = 3,    /* fusion-kernel path (short chunks, fp32): gated value, conv,
                              residual, state                                                 */
     ENGRAM_K_AUX = 4,     /* context / state bookkeeping, packing; engram_layer_norm,
-                             engram_quantize_fp8                                             */
+                             engram_rms_norm, engram_quantize_fp8, engram_clip_grads        */
     ENGRAM_K_GEMM_V = 5,  /* W_v e with gated value, conv, residual, state fused (prefill)     */
     ENGRAM_K_GATE = 6,    /* gate per token and branch from the partial sums                  */
     ENGRAM_K_SEAM = 7,    /* rows at 256-token tile seams left by ENGRAM_K_GEMM_V             */
-    ENGRAM_K_BWD_GEMM = 8,  /* engram_backward: the MFMA contractions (k and v again, dE, dW)  */
+    ENGRAM_K_BWD_GEMM = 8,  /* engram_backward: the MFMA contractions (k and v again, dE, dW);
+                               engram_cross_entropy_backward                                 */
     ENGRAM_K_BWD_FUSE = 9,  /* engram_backward: gate statistics, conv / gate / RMSNorm backward,
                                transposes and the reductions of the small gradients;
-                               engram_layer_norm_backward                                    */
+                               engram_layer_norm_backward, engram_rms_norm_backward          */
     ENGRAM_K_BWD_TABLE = 10,/* engram_backward: sort, scan and per-row sums of the table gradient;
                                engram_embed_backward                                         */
     ENGRAM_K_COUNT = 11
@@ -609,6 +612,147 @@ ENGRAM_API engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const
                                            int32_t a_block_rows, const void *d_b, const uint8_t *d_b_scales,
                                            int32_t b_block_rows, int64_t M, int64_t N, int64_t K, void *d_c,
                                            engram_dtype c_dtype, void *d_workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
+
+/*
+ * RMS norm of the residual stream's rows, with the residual's addition before it
+ * and 8 bits behind it:
+ *   s = x + residual (rounded to the plan dtype; s = x without a residual)
+ *   y = s * rrms * gamma,  rrms = 1 / sqrt(mean(s^2) + eps)
+ * with the sums in fp32; y is rounded once to the plan dtype in d_y, and once to
+ * e4m3 in d_q with a scale for each 128 channels of a row, as
+ * engram_quantize_fp8 (block_rows 1) makes them: the operand of
+ * engram_matmul_fp8.
+ *   d_x          [n_rows][d_model] plan dtype
+ *   d_residual   the same, or NULL
+ *   d_total      the same: s, where a residual is given (else NULL); it may be
+ *                d_x or d_residual
+ *   d_gamma      [d_model] fp32
+ *   d_y          [n_rows][d_model] plan dtype, or NULL; it may be d_x or
+ *                d_residual (where d_total is not)
+ *   d_q, d_scales  [n_rows][d_model] e4m3 and [n_rows][ceil(d_model / 512) * 4]
+ *                e8m0, or both NULL; one of d_y and d_q is wanted
+ *   d_rrms       [n_rows] fp32 for the backward, or NULL
+ * A row with an infinity or a NaN gives NaN throughout or zeros beside NaN, as
+ * the formula has it (and its blocks' scales those of their finite values).
+ * d_model above 32768: ENGRAM_E_UNSUPPORTED.
+ */
+ENGRAM_API engram_status engram_rms_norm(engram_plan p, const void *d_x, const void *d_residual, int64_t n_rows,
+                                         const float *d_gamma, float eps, void *d_total, void *d_y, void *d_q,
+                                         uint8_t *d_scales, float *d_rrms, hipStream_t stream);
+
+/* Bytes of device workspace engram_rms_norm_backward needs for up to n_rows rows
+ * (0 on invalid or unsupported sizes). */
+ENGRAM_API size_t engram_rms_norm_backward_workspace_size(engram_plan p, int64_t n_rows);
+
+/*
+ * The gradients of engram_rms_norm (its 8-bit output taken as y): with
+ * g = dy * gamma and sh = s * rrms,
+ *   dx = rrms * (g - sh * mean(g * sh)) + dtotal,  dgamma = sum dy * sh.
+ * dx is the gradient of x and of the residual alike.
+ *   d_s           [n_rows][d_model] plan dtype: what was normed (d_total, or d_x
+ *                 where there was no residual)
+ *   d_dy          the gradient of y
+ *   d_dtotal      the gradient that reaches s through the residual stream, or NULL
+ *   d_rrms        as the forward wrote it
+ *   flags         ENGRAM_GRAD_ACCUMULATE: add to d_dgamma
+ *   d_dx          may be d_s, d_dy or d_dtotal
+ *   d_workspace   >= engram_rms_norm_backward_workspace_size(p, n) bytes for an
+ *                 n >= n_rows, 256-byte aligned
+ */
+ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s, const void *d_dy, const void *d_dtotal,
+                                                  int64_t n_rows, const float *d_gamma, const float *d_rrms,
+                                                  uint32_t flags, void *d_dx, float *d_dgamma, void *d_workspace,
+                                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Softmax cross entropy of the output head, from the hidden state and the head's
+ * weights, the logits never in memory:
+ *   x[t][v] = scale * <h_t, W_v>,  lse_t = log sum_v exp x[t][v],  loss_t = lse_t - x[t][target t]
+ * A target outside [0, vocab) marks a token that does not count (a prompt's,
+ * padding): its loss and lse are 0, whatever its h holds.
+ *   d_h          [n_tok][d_model] plan dtype
+ *   d_weight     [vocab][d_model] plan dtype (the token embedding's table, where tied)
+ *   d_targets    [n_tok] int32
+ *   scale        finite factor of the logits
+ *   d_loss, d_lse  [n_tok] fp32 (natural logarithms)
+ *   d_workspace  >= engram_cross_entropy_workspace_size(p, n) bytes for an
+ *                n >= n_tok, 256-byte aligned
+ * Logits and sums are fp32 (an fp32 plan's values are multiplied as three bf16
+ * parts each, six products, with fp32 sums; they have to be finite).  A NaN in a
+ * token's h, or in a weight, gives NaN losses.  n_tok above 2^27, vocab above
+ * 2^22, d_model above 2^20 or 2^22 tiles of 256 x 256 logits and more:
+ * ENGRAM_E_UNSUPPORTED.
+ */
+/* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported sizes). */
+ENGRAM_API size_t engram_cross_entropy_workspace_size(engram_plan p, int64_t n_tok);
+ENGRAM_API engram_status engram_cross_entropy(engram_plan p, const void *d_h, const void *d_weight,
+                                              const int32_t *d_targets, int64_t n_tok, float scale, float *d_loss,
+                                              float *d_lse, void *d_workspace, size_t workspace_bytes,
+                                              hipStream_t stream);
+
+/*
+ * Its gradients, from the logits made once more in pieces of the vocabulary (1 GB
+ * of their gradients at a time):
+ *   P[t][v] = g_t * scale * (exp(x[t][v] - lse_t) - [v = target t]),  g_t = dloss_t * dloss_scale
+ *   dh = P W,  dW = P^T h, over the tokens that count (the others' dh is 0)
+ *   d_lse        as the forward wrote it
+ *   d_dloss      [n_tok] fp32 gradient of each token's loss, or NULL: ones
+ *   dloss_scale  finite factor of it (one over the number of tokens, a loss scale)
+ *   flags        ENGRAM_GRAD_ACCUMULATE: add to d_dweight
+ *   d_dh         [n_tok][d_model] plan dtype, or NULL
+ *   d_dweight    [vocab][d_model] in dweight_dtype, or NULL (one of both is
+ *                wanted): fp32, where tied the same buffer as
+ *                engram_embed_backward's d_dtable; or bf16 (bf16 plans only)
+ *   d_workspace  >= engram_cross_entropy_backward_workspace_size(p, n,
+ *                dweight_dtype) bytes for an n >= n_tok, 256-byte aligned
+ * For bf16 results P is rounded to bf16, as the operand beside it is; for an
+ * fp32 d_dweight P is held in two bf16 parts (16 bits), and in an fp32 plan every
+ * value in three.
+ */
+/* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported
+ * sizes; 1.3 GB and some copies of h at most, and 1 GB more in an fp32 plan). */
+ENGRAM_API size_t engram_cross_entropy_backward_workspace_size(engram_plan p, int64_t n_tok, engram_dtype dweight_dtype);
+ENGRAM_API engram_status engram_cross_entropy_backward(engram_plan p, const void *d_h, const void *d_weight,
+                                                       const int32_t *d_targets, int64_t n_tok, float scale,
+                                                       const float *d_lse, const float *d_dloss, float dloss_scale,
+                                                       uint32_t flags, void *d_dh, void *d_dweight,
+                                                       engram_dtype dweight_dtype, void *d_workspace,
+                                                       size_t workspace_bytes, hipStream_t stream);
+
+/* One tensor of a list of gradients: n_groups groups of `rows` rows of row_len
+ * values, one after the other (a plain tensor: 1, 1 and its size). */
+typedef struct {
+    const void *data;          /* 16-byte aligned device memory; any number of values, also none   */
+    void *out;                 /* where the scaled values go: data itself, another buffer of the
+                                  same size, or NULL (only the norm is wanted)                      */
+    const int32_t *row_counts; /* [n_groups] device counts: of each group only so many rows, the
+                                  first, take part and are written (engram_backward's row_grads and
+                                  row_counts: n_groups = n_tables, rows = batch*seqlen, row_len =
+                                  d_e); counts outside [0, rows] count as the nearer end.  NULL: all */
+    int64_t n_groups, rows, row_len;
+    engram_dtype dtype;        /* of data and out */
+} engram_grad;
+
+/*
+ * Clipping by the global norm:
+ *   norm = sqrt(sum over all tensors of x^2)       (squares and sums in 64 bits)
+ *   factor = max_norm / norm where norm is finite and above max_norm, else 1
+ *   out = factor * x, rounded once
+ * A norm that is infinite or NaN (an overflow: the step is to be skipped) scales
+ * nothing.  Tensors in place are not written where the factor is 1.
+ *   grads        HOST array of n_grads tensors, read before the call returns
+ *   max_norm     above 0; INFINITY for the norm alone
+ *   d_norm       [2] fp32: the norm and the factor (for an optimizer that scales
+ *                by itself, with every out NULL)
+ *   d_workspace  >= engram_clip_grads_workspace_size(p, n) bytes for an n >=
+ *                n_grads, 256-byte aligned
+ * No two buffers may overlap but a tensor's own data and out where they are the
+ * same, and counts.  Tensors of 2^42 values and more together: ENGRAM_E_UNSUPPORTED.
+ */
+ENGRAM_API size_t engram_clip_grads_workspace_size(engram_plan p, int32_t n_grads);
+ENGRAM_API engram_status engram_clip_grads(engram_plan p, const engram_grad *grads, int32_t n_grads, float max_norm,
+                                           float *d_norm, void *d_workspace, size_t workspace_bytes,
                                            hipStream_t stream);
 
 /*

@@ -1,0 +1,467 @@
+"""The operators at a model's ends on the GPU (RMS norm with the residual's
+addition, cross entropy of the output head, clipping of gradients) against plain
+64-bit implementations.
+
+Tolerances count roundings: u = 2^-24 is fp32's half step.  A product over K is a
+chain of ceil(K / 32) matrix instructions for each product of parts, whose
+rounded adds and the sums of 32 inside one are taken as off by 2 u each of the
+magnitudes' sum; an output rounded to bf16 is off by 2^-8 of its value (fp32: u).
+"""
+
+import math
+
+import pytest
+import torch
+
+from test_gpu_operators import Guarded, close, gen, half_step, make_plan, randn, tdt, zipf_ids
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DTYPES = ("bf16", "f32")
+
+
+def nan_like(t):
+    """A buffer whose old values would show."""
+    return t.fill_(math.nan)
+
+
+# ---------------------------------------------------------------- cross entropy
+
+
+def head(dtype, n_tok, vocab, d, scale, seed, gpu, skip=True):
+    """A head's inputs: some tokens nearly certain, a few that do not count."""
+    w = randn((vocab, d), dtype, seed, 1.0 / math.sqrt(d) / abs(scale))
+    y = zipf_ids(n_tok, vocab, seed + 1, bad=skip)
+    h = torch.randn((n_tok, d), generator=gen(seed + 2))
+    sure = torch.rand((n_tok, 1), generator=gen(seed + 3)) * 10
+    h = (h + sure * scale * w[y.clamp(0, vocab - 1).long()].float()).to(tdt(dtype))
+    return h.to(gpu), w.to(gpu), y.to(gpu)
+
+
+def chain(k, segs):
+    return 2 * (segs * -(-k // 32) + 40)
+
+
+class HeadRef:
+    """Losses, gradients and bounds of their errors in 64 bits, some tokens at a time."""
+
+    def __init__(self, h, w, y, scale, dtype):
+        self.h, self.w, self.y, self.scale = h.double(), w.double(), y.long(), scale
+        self.V, self.d = w.shape
+        self.segs = 1 if dtype == "bf16" else 6
+        self.dtype = dtype
+        self.counts = (self.y >= 0) & (self.y < self.V)
+
+    def logits(self, at):
+        """Logits of tokens `at` and how far the kernel's may be off: sums, and the
+        5 u that products of three parts leave out."""
+        h = self.h[at]
+        x = h @ self.w.t() * self.scale
+        mag = h.abs() @ self.w.abs().t() * abs(self.scale)
+        return x, (chain(self.d, self.segs) + 6) * U * mag + U * x.abs()
+
+    def forward(self):
+        n = len(self.y)
+        out = [torch.zeros(n, dtype=torch.float64, device=self.h.device) for _ in range(4)]
+        for at in self.counts.nonzero()[:, 0].split(1024):
+            x, e = self.logits(at)
+            lse = x.logsumexp(1)
+            xy = x.gather(1, self.y[at][:, None])[:, 0]
+            # exponentials and their sum: 300 roundings at most, and those of the join
+            off = e.amax(1) + 300 * U + 4 * U * (lse.abs() + x.amax(1).abs())
+            out[0][at], out[1][at] = lse - xy, lse
+            out[2][at], out[3][at] = 2 * off + 4 * U * xy.abs(), off
+        return out
+
+    def backward(self, lse, g, dw_dtype):
+        """dh, dW and their bounds, from the lse that the kernel is given."""
+        n, V, d = len(self.y), self.V, self.d
+        dev = self.h.device
+        dh, dh_off = (torch.zeros((n, d), dtype=torch.float64, device=dev) for _ in range(2))
+        dw, dw_off = (torch.zeros((V, d), dtype=torch.float64, device=dev) for _ in range(2))
+        rh = 2.0 ** -8 if self.dtype == "bf16" else 2.0 ** -22  # what P's parts leave out, and the products of parts
+        rw = 2.0 ** -22 if self.dtype == "f32" else 2.0 ** -8 if dw_dtype == torch.bfloat16 else 2.0 ** -16
+        sh, sw = chain(V, self.segs) + 40, chain(n, 6 if self.dtype == "f32" else 2) + 40
+        for at in self.counts.nonzero()[:, 0].split(1024):
+            x, e = self.logits(at)
+            l = lse[at].double()[:, None]
+            f = (g[at].double() * self.scale)[:, None]
+            p = (x - l).exp()
+            off = p * (e + 4 * U * (x - l).abs() + U * l.abs() + 8 * U)
+            p[torch.arange(len(at), device=dev), self.y[at]] -= 1.0
+            p, off = p * f, (off + 2 * U * p.abs()) * f.abs() + 2.0 ** -126
+            h, w = self.h[at], self.w
+            mag_h, mag_w = p.abs() @ w.abs(), p.abs().t() @ h.abs()
+            dh[at] = p @ w
+            dh_off[at] = off @ w.abs() + (rh + sh * U) * mag_h
+            dw += p.t() @ h
+            dw_off += off.t() @ h.abs() + (rw + sw * U) * mag_w
+        return dh, dh_off + half_step(self.dtype) * dh.abs(), dw, dw_off + torch.finfo(dw_dtype).eps / 2 * dw.abs()
+
+
+HEADS = [  # n_tok, vocab, d, scale
+    (1, 1, 8, 1.0), (1, 50, 64, 1.0), (2, 300, 72, -0.5), (63, 257, 264, 1.0), (64, 4099, 128, 0.25),
+    (65, 1000, 256, 1.0), (130, 33, 520, 1.0), (333, 1000, 256, 0.0625), (300, 5003, 72, 1.0), (1100, 2111, 136, 1.0),
+    (513, 260, 8, 1.0), (2049, 50, 64, 1.0), (700, 16500, 64, 2.0), (3, 70000, 128, 1.0)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d,scale", HEADS)
+def test_cross_entropy(gpu, dtype, n_tok, vocab, d, scale):
+    p = make_plan(dtype, d, vocab)
+    h, w, y = head(dtype, n_tok, vocab, d, scale, 3, gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok), scale=scale)
+    ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, scale, dtype).forward())
+    close(loss, ref, off, "loss")
+    close(lse, ref_lse, off_lse, "lse")
+
+
+GRADS = [("bf16", torch.bfloat16), ("bf16", torch.float32), ("f32", torch.float32)]
+
+
+def check_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale, with_dloss=True):
+    p = make_plan(dtype, d, vocab)
+    h, w, y = head(dtype, n_tok, vocab, d, scale, 5, gpu)
+    ref = HeadRef(h, w, y, scale, dtype)
+    lse = ref.forward()[1].float()
+    dloss = torch.rand(n_tok, generator=gen(8)).to(gpu) if with_dloss else None
+    dh = nan_like(torch.empty_like(h))
+    dw = nan_like(torch.empty((vocab, d), dtype=dw_dtype, device=gpu))
+    ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+    ws.fill_(255)  # NaN in every type
+    p.engram_cross_entropy_backward(h, w, y, lse, dloss, dh, dw, ws, scale=scale, dloss_scale=0.125)
+    g = (dloss.double() if with_dloss else torch.ones(n_tok, device=gpu, dtype=torch.float64)) * 0.125
+    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse, g, dw_dtype))
+    close(dh, rdh, off_h, "dh")
+    close(dw, rdw, off_w, "dw")
+    assert not dh[~ref.counts].count_nonzero()
+    return p, (h, w, y, lse, dloss), (dh, dw), ws
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+@pytest.mark.parametrize("n_tok,vocab,d,scale", HEADS)
+def test_cross_entropy_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale):
+    p, (h, w, y, lse, dloss), (dh, dw), ws = check_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale)
+    # one of both alone, and again: the same bits
+    dh2, dw2 = torch.empty_like(dh), torch.empty_like(dw)
+    p.engram_cross_entropy_backward(h, w, y, lse, dloss, None, dw2, ws, scale=scale, dloss_scale=0.125)
+    p.engram_cross_entropy_backward(h, w, y, lse, dloss, dh2, None, ws, scale=scale, dloss_scale=0.125)
+    assert torch.equal(dw2, dw) and torch.equal(dh2, dh)
+    # accumulated: once more what is there
+    p.engram_cross_entropy_backward(h, w, y, lse, dloss, None, dw2, ws, scale=scale, dloss_scale=0.125, flags=8)
+    assert torch.allclose(dw2.double(), 2 * dw.double(), rtol=2.0 ** -7 if dw_dtype == torch.bfloat16 else 1e-5,
+                          atol=2e-5 * float(dw.double().abs().max()) if dw_dtype == torch.float32 else
+                          2.0 ** -8 * float(dw.double().abs().max()))
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+def test_cross_entropy_backward_without_dloss(gpu, dtype, dw_dtype):
+    check_backward(gpu, dtype, dw_dtype, 200, 777, 136, 1.0, with_dloss=False)
+
+
+def test_cross_entropy_backward_is_the_difference_of_the_loss(gpu):
+    """Along random directions, by central differences of the loss in 64 bits."""
+    n, V, d, scale = 150, 700, 136, 0.7
+    p = make_plan("f32", d, V)
+    h, w, y = head("f32", n, V, d, scale, 7, gpu)
+    dloss = torch.rand(n, generator=gen(9)).to(gpu)
+    loss, lse = torch.empty(n, device=gpu), torch.empty(n, device=gpu)
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n), scale=scale)
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    p.engram_cross_entropy_backward(h, w, y, lse, dloss, dh, dw, p.cross_entropy_backward_workspace(n), scale=scale)
+    counts = (y >= 0) & (y < V)
+
+    def total(hh, ww):
+        x = hh @ ww.t() * scale
+        each = x.logsumexp(1) - x.gather(1, y.clamp(0, V - 1).long()[:, None])[:, 0]
+        return (each * dloss.double())[counts].sum()
+
+    for seed in range(3):
+        uh, uw = randn((n, d), "f32", 20 + seed).to(gpu).double(), randn((V, d), "f32", 30 + seed).to(gpu).double()
+        for dirs, got in (((uh, 0 * uw), (dh.double() * uh).sum()), ((0 * uh, uw), (dw.double() * uw).sum())):
+            step = 1e-4  # the third derivative's term: about step^2 of the difference
+            diff = (total(h.double() + step * dirs[0], w.double() + step * dirs[1]) -
+                    total(h.double() - step * dirs[0], w.double() - step * dirs[1])) / (2 * step)
+            scale_of = float(((dh.double() * uh).abs().sum() if dirs[0].any() else (dw.double() * uw).abs().sum()))
+            assert abs(float(got - diff)) < 1e-5 * scale_of
+
+
+# ---------------------------------------------------------------- RMS norm
+
+RMS_SHAPES = [(1, 8), (3, 64), (9, 72), (17, 128), (33, 136), (5, 256), (130, 264), (77, 512), (4, 520), (41, 1024),
+              (2, 1032), (7, 1544), (300, 2560), (6, 2568), (5, 4104), (3, 8200), (2, 16384), (3, 16392), (2, 32768),
+              (1, 32760)]
+RMS_MANY = [(70000, 64), (30011, 256), (9001, 512), (2600, 2560), (1100, 5000), (700, 9000)]
+
+
+def rms_sums(d):
+    """Roundings of a row's sum: a lane's steps of eight, the lanes and the waves, 16 at most of each."""
+    return 8 * 5 + 6 + 16
+
+
+def rms_ref(x, res, gamma, eps, dtype):
+    s = x if res is None else (x.float() + res.float()).to(tdt(dtype))
+    rr = (s.double().square().mean(1) + eps).rsqrt()
+    return s, rr, s.double() * rr[:, None] * gamma.double()
+
+
+def check_8bit(q, sc, y, rel):
+    """q and sc are y in 8 bits, where y may be off by `rel` of its value before it is rounded."""
+    rows, d = y.shape
+    kb = -(-d // 128)
+    q, sc, y = q.cpu().double(), sc.cpu().view(torch.uint8).to(torch.int64), y.cpu()
+    assert (sc[:, kb:] == 127).all()
+    top = torch.nn.functional.pad(y.abs(), (0, -d % 128)).reshape(rows, kb, 128).amax(2)
+    exps = []
+    for f in (1 - rel, 1 + rel):
+        e = torch.ceil(torch.log2(top * f / 448.0)).clamp(min=-126)
+        exps.append(torch.where(top > 0, e, torch.full_like(e, -126.0)).to(torch.int64) + 127)
+    assert ((sc[:, :kb] == exps[0]) | (sc[:, :kb] == exps[1])).all()
+    unit = torch.exp2((sc[:, :kb] - 127).double()).repeat_interleave(128, 1)[:, :d]
+    # e4m3: half a step is 2^-4 of the value, 2^-10 below its normal range
+    assert ((q * unit - y).abs() <= torch.maximum(2.0 ** -4 * y.abs() * (1 + rel), 2.0 ** -10 * unit) + rel * y.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("residual", (True, False))
+@pytest.mark.parametrize("rows,d", RMS_SHAPES + RMS_MANY)
+def test_rms_norm(gpu, dtype, residual, rows, d):
+    p = make_plan(dtype, d)
+    x, gamma = randn((rows, d), dtype, 1).to(gpu), (1.0 + randn((d,), "f32", 2, 0.1)).to(gpu)
+    res = randn((rows, d), dtype, 3, 2.0).to(gpu) if residual else None
+    x[rows // 2] = 0.0
+    if residual:
+        res[rows // 2] = 0.0  # a row of padding
+    total = nan_like(torch.empty_like(x)) if residual else None
+    y, rr = nan_like(torch.empty_like(x)), nan_like(torch.empty(rows, device=gpu))
+    q = torch.full((rows, d), 0x7F, dtype=torch.uint8, device=gpu).view(torch.float8_e4m3fn)
+    sc = torch.full(p.fp8_scale_shape(rows, d, 1), 255, dtype=torch.uint8, device=gpu)
+    p.engram_rms_norm(x, gamma, y, residual=res, total=total, q=q, scales=sc, rrms=rr, eps=1e-6)
+    s, ref_rr, ref = rms_ref(x, res, gamma, 1e-6, dtype)
+    if residual:
+        assert torch.equal(total, s)
+    rel = (rms_sums(d) / 2 + 6) * U
+    close(rr, ref_rr.cpu(), rel * ref_rr.cpu(), "rrms")
+    close(y, ref.cpu(), ((rel + 3 * U) + half_step(dtype) * 1.01) * ref.abs().cpu(), "y")
+    check_8bit(q, sc, ref, rel + 3 * U)
+    # each output alone is the same; the operator in 8 bits is its fp32 self quantised
+    y2, q2, sc2 = torch.empty_like(y), torch.empty_like(q), torch.empty_like(sc)
+    p.engram_rms_norm(x, gamma, y2, residual=res, total=total)
+    p.engram_rms_norm(x, gamma, residual=res, total=total, q=q2, scales=sc2)
+    assert torch.equal(y2, y) and torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(sc2, sc)
+    if dtype == "f32":
+        p.engram_quantize_fp8(y, q2, sc2)
+        assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(sc2, sc)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,d", [(70, 64), (600, 136), (257, 1024), (66, 4104)])
+def test_rms_norm_in_place(gpu, dtype, rows, d):
+    p = make_plan(dtype, d)
+    x, res, gamma = randn((rows, d), dtype, 1).to(gpu), randn((rows, d), dtype, 2).to(gpu), randn((d,), "f32", 3).to(gpu)
+    total, y, rr = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=gpu)
+    p.engram_rms_norm(x, gamma, y, residual=res, total=total, rrms=rr)
+    for t_at, y_at in ((0, 1), (1, 0), (0, None), (1, None), (None, 0), (None, 1)):
+        bufs = [x.clone(), res.clone()]
+        t = bufs[t_at] if t_at is not None else torch.empty_like(x)
+        o = bufs[y_at] if y_at is not None else torch.empty_like(x)
+        p.engram_rms_norm(bufs[0], gamma, o, residual=bufs[1], total=t)
+        assert torch.equal(t, total) and torch.equal(o, y)
+    alone = x.clone()
+    p.engram_rms_norm(alone, gamma, alone)
+    p.engram_rms_norm(x, gamma, y)
+    assert torch.equal(alone, y)
+    # x twice: the sum of a row with itself
+    p.engram_rms_norm(x, gamma, y, residual=x, total=total)
+    assert torch.equal(total, (x.float() + x.float()).to(x.dtype))
+    # the backward in place of each of its inputs
+    dy, dt = randn((rows, d), dtype, 4).to(gpu), randn((rows, d), dtype, 5).to(gpu)
+    p.engram_rms_norm(x, gamma, y, residual=res, total=total, rrms=rr)
+    ws, dg, dx = p.rms_norm_backward_workspace(rows), torch.empty(d, device=gpu), torch.empty_like(x)
+    p.engram_rms_norm_backward(total, dy, gamma, rr, dx, dg, ws, dtotal=dt)
+    for at in range(3):
+        b = [total.clone(), dy.clone(), dt.clone()]
+        dg2 = torch.empty_like(dg)
+        p.engram_rms_norm_backward(b[0], b[1], gamma, rr, b[at], dg2, ws, dtotal=b[2])
+        assert torch.equal(b[at], dx) and torch.equal(dg2, dg)
+
+
+def test_rms_norm_rows_are_apart(gpu):
+    """An infinity, a NaN or the type's largest values in a row change no other row."""
+    for d in (64, 128, 256, 1024, 4104):
+        p = make_plan("bf16", d)
+        x, gamma = randn((70, d), "bf16", 1).to(gpu), torch.ones(d, device=gpu)
+        sc_shape = p.fp8_scale_shape(70, d, 1)
+
+        def call(x):
+            y, q, sc = torch.empty_like(x), torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=gpu), \
+                torch.empty(sc_shape, dtype=torch.uint8, device=gpu)
+            p.engram_rms_norm(x, gamma, y, q=q, scales=sc)
+            return y, q.view(torch.uint8), sc
+
+        clean = call(x)
+        bad = x.clone()
+        bad[5, 3], bad[9, d - 1], bad[33, 0], bad[40] = math.inf, math.nan, -math.inf, torch.finfo(torch.bfloat16).max
+        got = call(bad)
+        ok = torch.ones(70, dtype=torch.bool, device=gpu)
+        ok[[5, 9, 33, 40]] = False
+        for a, b in zip(clean, got):
+            assert torch.equal(a[ok], b[ok])
+        assert got[0][9].isnan().all() and got[0][5, 3].isnan() and (got[0][5, :3] == 0).all()
+        assert ((got[1][9] & 0x7F) == 0x7F).all() and int(got[1][5, 3]) & 0x7F == 0x7F
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("residual", (True, False))
+@pytest.mark.parametrize("rows,d", RMS_SHAPES + RMS_MANY)
+def test_rms_norm_backward(gpu, dtype, residual, rows, d):
+    p = make_plan(dtype, d)
+    s, dy = randn((rows, d), dtype, 1).to(gpu), randn((rows, d), dtype, 2).to(gpu)
+    gamma = (1.0 + randn((d,), "f32", 3, 0.1)).to(gpu)
+    dt = randn((rows, d), dtype, 4).to(gpu) if residual else None
+    rr = (s.double().square().mean(1) + 1e-6).rsqrt().float()
+    dx, dg = nan_like(torch.empty_like(s)), nan_like(torch.empty(d, device=gpu))
+    ws = p.rms_norm_backward_workspace(rows)
+    ws.fill_(255)
+    p.engram_rms_norm_backward(s, dy, gamma, rr, dx, dg, ws, dtotal=dt)
+    r, xh = rr.double()[:, None], s.double() * rr.double()[:, None]
+    g = dy.double() * gamma.double()
+    m = (g * xh).mean(1, keepdim=True)
+    ref = r * (g - xh * m) + (0 if dt is None else dt.double())
+    mag_m = (g * xh).abs().mean(1, keepdim=True)
+    off = r * (3 * U * g.abs() + xh.abs() * ((rms_sums(d) + 8) * U * mag_m)) + 4 * U * ref.abs() + half_step(dtype) * ref.abs()
+    off = off + 4 * U * (r * (g.abs() + (xh * m).abs()))
+    close(dx, ref.cpu(), off.cpu(), "dx")
+    # a lane's rows, the blocks' parts by 16 waves
+    n_sum = rows / 64 + 200
+    ref_g, mag_g = (dy.double() * xh).sum(0), (dy.double() * xh).abs().sum(0)
+    close(dg, ref_g.cpu(), ((min(rows, n_sum) + 4) * U * mag_g).cpu(), "dgamma")
+    before = randn((d,), "f32", 6).to(gpu)
+    acc = before.clone()
+    p.engram_rms_norm_backward(s, dy, gamma, rr, dx, acc, ws, dtotal=dt, flags=8)
+    assert torch.equal(acc, before + dg)
+
+
+def test_rms_norm_backward_is_the_difference_of_the_norm(gpu):
+    rows, d, eps = 7, 264, 1e-6
+    p = make_plan("f32", d)
+    x, dy, gamma = randn((rows, d), "f32", 1).to(gpu), randn((rows, d), "f32", 2).to(gpu), randn((d,), "f32", 3).to(gpu)
+    y, rr = torch.empty_like(x), torch.empty(rows, device=gpu)
+    p.engram_rms_norm(x, gamma, y, rrms=rr, eps=eps)
+    dx, dg = torch.empty_like(x), torch.empty(d, device=gpu)
+    p.engram_rms_norm_backward(x, dy, gamma, rr, dx, dg, p.rms_norm_backward_workspace(rows))
+
+    def total(xx, gg):
+        return (dy.double() * xx * (xx.square().mean(1, keepdim=True) + eps).rsqrt() * gg).sum()
+
+    for seed in range(4):
+        ux, ug = randn((rows, d), "f32", 20 + seed).to(gpu).double(), randn((d,), "f32", 30 + seed).to(gpu).double()
+        step = 1e-4
+        for a, b, got, mag in ((ux, 0 * ug, (dx.double() * ux).sum(), (dx.double() * ux).abs().sum()),
+                               (0 * ux, ug, (dg.double() * ug).sum(), (dg.double() * ug).abs().sum())):
+            diff = (total(x.double() + step * a, gamma.double() + step * b) -
+                    total(x.double() - step * a, gamma.double() - step * b)) / (2 * step)
+            assert abs(float(got - diff)) < 1e-5 * float(mag)
+
+
+# ---------------------------------------------------------------- clipping
+
+
+def grads_of(sizes, dtypes, seed, gpu, sd=1.0):
+    return [(torch.randn(n, generator=gen(seed + i)) * sd * 10.0 ** (i % 3 - 1)).to(tdt(t)).to(gpu)
+            for i, (n, t) in enumerate(zip(sizes, dtypes))]
+
+
+def norm_ref(grads, counts=None):
+    total = 0.0
+    for i, g in enumerate(grads):
+        x = g.double().cpu()
+        if counts is not None and counts[i] is not None:
+            x = torch.cat([x[k, :max(0, min(int(c), x.shape[1]))].flatten() for k, c in enumerate(counts[i])])
+        total += float(x.square().sum())
+    return math.sqrt(total)
+
+
+def check_clip(p, B, grads, max_norm, counts=None, in_place=False):
+    outs = None if in_place else [torch.full_like(g, 5.0) for g in grads]
+    before = [g.clone() for g in grads]
+    lst = B.GradList(grads, outs=outs, row_counts=counts)
+    norm = nan_like(torch.empty(2, device=grads[0].device))
+    p.engram_clip_grads(lst, norm, p.clip_grads_workspace(lst), max_norm=max_norm)
+    ref = norm_ref(before, counts)
+    n, f = norm.tolist()
+    assert abs(n - ref) <= 1.01 * U * ref
+    top = float(torch.tensor(max_norm, dtype=torch.float32))  # the argument is an fp32 number: 1e-3 is off by up to u
+    want = top / ref if ref > top else 1.0
+    assert abs(f - want) <= 1.01 * U * want
+    for i, (b, o) in enumerate(zip(before, grads if in_place else outs)):
+        exp = (b.float() * torch.tensor(f, dtype=torch.float32, device=b.device)).to(b.dtype)
+        if counts is not None and counts[i] is not None:
+            rest = b if in_place else torch.full_like(b, 5.0)
+            live = torch.arange(b.shape[1], device=b.device)[None, :] < counts[i][:, None]
+            exp = torch.where(live.reshape(live.shape + (1,) * (b.dim() - 2)), exp, rest)
+        assert torch.equal(o, exp), i
+    if not in_place:
+        assert all(torch.equal(a, b) for a, b in zip(grads, before))
+
+
+@pytest.mark.parametrize("in_place", (False, True))
+@pytest.mark.parametrize("max_norm", (1e-3, 1.0, 1e30, math.inf))
+@pytest.mark.parametrize("sizes", [(1,), (7, 8, 9), (0, 5, 0), (8191, 8192, 8193, 0), (100003, 1, 33, 4097),
+                                   tuple(range(1, 130)), (20_000_001, 17, 3_000_000)])
+def test_clip_grads(gpu, in_place, max_norm, sizes):
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    dtypes = ["bf16" if i % 3 == 1 else "f32" for i in range(len(sizes))]
+    check_clip(make_plan(), B, grads_of(sizes, dtypes, 3, gpu), max_norm, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", (False, True))
+@pytest.mark.parametrize("groups,rows,tail", [(1, 1, (1,)), (3, 5, (7,)), (8, 333, (32,)), (2, 3000, (4, 3)), (16, 1, (8,)), (5, 40, ())])
+def test_clip_grads_takes_the_first_rows_of_a_group(gpu, in_place, groups, rows, tail):
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    for dtype in DTYPES:
+        g = randn((groups, rows) + tail, dtype, 1).to(gpu)
+        counts = torch.randint(-2, rows + 3, (groups,), generator=gen(2)).to(torch.int32)
+        counts[0], counts[-1] = 0, rows
+        counts = counts.to(gpu)
+        for k in range(groups):  # what takes no part may hold anything
+            g[k, max(0, int(counts[k])):] = 3e38
+        plain = randn((1001,), "f32", 3).to(gpu)
+        check_clip(make_plan(), B, [g, plain], 0.5, counts=[counts, None], in_place=in_place)
+
+
+def test_clip_grads_norms_of_every_size(gpu):
+    """Squares below and above fp32's range, and norms that are not finite."""
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    p = make_plan()
+    norm = torch.empty(2, device=gpu)
+    for v in (1e-38, 1e-30, 1e30, 3e38):
+        g = torch.full((1000,), v, device=gpu)
+        lst = B.GradList([g], outs=[torch.empty_like(g)])
+        p.engram_clip_grads(lst, norm, p.clip_grads_workspace(1), max_norm=1.0)
+        ref = float(g[0].double()) * math.sqrt(1000)
+        n, f = norm.tolist()
+        assert (abs(n - ref) <= 1.01 * U * ref) if ref < 3.4e38 else n == math.inf
+        assert abs(f - min(1.0, 1.0 / ref)) <= 1.01 * U * f + 2.0 ** -149
+    for v in (math.inf, -math.inf, math.nan):
+        g = torch.ones(5000, device=gpu)
+        g[4321] = v
+        keep = g.clone()
+        out = torch.zeros_like(g)
+        p.engram_clip_grads(B.GradList([g]), norm, p.clip_grads_workspace(1), max_norm=1.0)
+        p.engram_clip_grads(B.GradList([g], outs=[out]), norm, p.clip_grads_workspace(1), max_norm=1.0)
+        n, f = norm.tolist()
+        assert not math.isfinite(n) and f == 1.0
+        for t in (g, out):
+            assert torch.equal(t.nan_to_num(9.0, 8.0, 7.0), keep.nan_to_num(9.0, 8.0, 7.0))
+    g = torch.zeros(77, device=gpu)
+    p.engram_clip_grads(B.GradList([g]), norm, p.clip_grads_workspace(1), max_norm=1.0)
+    assert norm.tolist() == [0.0, 1.0]
+    g = torch.ones(77, device=gpu)  # only the norm is wanted
+    p.engram_clip_grads(B.GradList([g], outs=[None]), norm, p.clip_grads_workspace(1), max_norm=0.5)
+    assert abs(float(norm[0]) - math.sqrt(77)) < 1e-6 and (g == 1).all()
