@@ -27,6 +27,7 @@
 // where the results are bf16.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "engram_internal.h"
 #include "stage.h"
@@ -36,17 +37,33 @@ namespace engram {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kStep = 64;  // k of a stage: 128 bytes
+constexpr int kBlock = 64;  // rows and columns of a block of the workspaces' matrices
 
 // ---------------------------------------------------------------- operands
-// rows x k values in bf16, `parts` of them one after the other.
-// along: value (row, k) at row * ld + k; across: at k * ld + row.
+// A matrix of rows (of m or n) and columns of k values ("along"), or of rows (one
+// for each k) of m or n values ("across"), whole or in blocks of 64 x 64 that
+// are each contiguous, with zeros up to whole blocks: then a stage is a few runs of
+// 8 KB, and not one line each of as many rows, pages and channels.
 struct Operand {
-    const uint16_t *p;
-    int64_t ld;
-    int64_t part;   // values from one part to the next
-    int64_t rows;   // along: rows; across: values of a k (a multiple of 8)
+    const void *p;
+    int64_t row, row64;      // values from a row to the next, and to the one after 64
+    int64_t col64;           // values from a column to the one after 64
+    int64_t part, size;      // values from one part to the next, and of a part
 };
+
+// Rows of `cols` values.
+Operand rows_of(const void *p, int64_t rows, int64_t cols) {
+    return Operand{p, cols, kBlock * cols, kBlock, rows * cols, rows * cols};
+}
+int64_t round64(int64_t x) { return (x + kBlock - 1) / kBlock * kBlock; }
+Operand blocks_of(const void *p, int64_t rows, int64_t cols) {
+    const int64_t n = round64(rows) * round64(cols);
+    return Operand{p, kBlock, round64(cols) * kBlock, kBlock * kBlock, n, n};
+}
+// Value (r, c) of a matrix in blocks, `row64` as in its Operand.
+__device__ __forceinline__ int64_t block_at(int64_t r, int64_t c, int64_t row64) {
+    return (r >> 6) * row64 + (c >> 6) * (kBlock * kBlock) + (r & 63) * kBlock + (c & 63);
+}
 
 struct GemmArgs {
     Operand a, b;
@@ -54,199 +71,405 @@ struct GemmArgs {
     int32_t segs;              // products of parts: one after the other along k
     uint32_t a_parts, b_parts; // four bits each: the parts of product z
     int32_t splits, split_steps;  // parts of K, in stages
+    int32_t items;             // tiles times splits
+    int32_t round;             // an item's stages are a multiple of this
 };
 
-__device__ __forceinline__ int64_t steps_of(int64_t K) { return (K + kStep - 1) / kStep; }
+// ---------------------------------------------------------------- tiles
+// The items (tile, part of K) of a workgroup.  Consecutive workgroups go to the
+// XCDs in turn: each XCD gets a contiguous range of (part, tile), all n tiles of
+// kGroup m tiles before the next, so that the workgroups of an L2 share operand
+// rows of the same part.
+template <int TN, int TM>
+struct Items {
+    static constexpr uint32_t kGroup = 4;
+    uint32_t at, end, stride;
+    uint32_t tiles_n, tiles_m;
+    __device__ __forceinline__ Items(const GemmArgs &g) {
+        tiles_n = (uint32_t)((g.N + TN - 1) / TN);
+        tiles_m = (uint32_t)((g.M + TM - 1) / TM);
+        const uint32_t all = (uint32_t)g.items, x = blockIdx.x % kXcds, q = all / kXcds, r = all % kXcds;
+        const uint32_t from = x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q;
+        stride = (gridDim.x + kXcds - 1 - x) / kXcds;  // workgroups of this XCD
+        at = from + blockIdx.x / kXcds;
+        end = from + q + (x < r ? 1u : 0u);
+    }
+    __device__ __forceinline__ void origin(uint32_t item, int64_t &n0, int64_t &m0, int &split) const {
+        const uint32_t tiles = tiles_n * tiles_m;
+        split = (int)(item / tiles);
+        const uint32_t tile = item - (uint32_t)split * tiles;
+        const uint32_t grp = tile / (kGroup * tiles_n), in = tile - grp * (kGroup * tiles_n);
+        const uint32_t gm = min(kGroup, tiles_m - grp * kGroup);
+        n0 = (int64_t)(in / gm) * TN;
+        m0 = (int64_t)(grp * kGroup + in % gm) * TM;
+    }
+};
 
-// Fills stages of T rows x 64 k with T / 8 loads of 1 KB, shared by W waves.
-// Along: 8 rows x 128 bytes a load, piece c (16 bytes) of row r at place
-// c ^ (r / 2 % 8).  Across: 512 / T rows of k of 2 T bytes, their 32-byte
-// granules XOR-swizzled by k, so that the eight rows that half a wave reads at a
-// time (k % 4 and k / 8 % 2 vary) lie in distinct banks.
-template <int T, int W, bool ACROSS>
+// Stages of an item and product of parts: whole rounds of two or four where a
+// workgroup takes several items (`round`), the last of them zeros past K.
+template <class E>
+__device__ __forceinline__ int steps_in(const GemmArgs &g, int split) {
+    const int all = (int)((g.K + 128 / (int)sizeof(E) - 1) / (128 / (int)sizeof(E)));
+    const int n = min(g.split_steps, all - split * g.split_steps);
+    return (n + g.round - 1) & -g.round;
+}
+
+// Fills stages of T rows x 128 bytes of k (64 bf16, 32 fp32), one after the other
+// through a workgroup's items, with T / 8 loads of 1 KB shared by W waves.
+// Along: 8 rows x 128 bytes a load, the eight pieces of 16 bytes of a row
+// XOR-swizzled so that the 16 rows that are read at a time lie in distinct banks
+// (two rows fill the banks once): piece c of row r at place c ^ (r / 2 % 8), or,
+// where a lane's results are to be eight neighbours (PAIRS), where the rows are
+// 8 a + b (a, b < 4), at c ^ (r / 2 % 2 + r / 8 % 4 * 2).
+// Across: rows of k of T values.  bf16: the 32-byte granules XOR-swizzled by k, so that
+// the eight rows that half a wave reads at a time (k % 4 and k / 8 % 2 vary) lie
+// in distinct banks.  fp32: the 64-byte ones, by k / 4 % 4.
+// A leg is the stages of one item and product of parts.  What issue() does after
+// its loads is branch-free, so that it is scheduled between multiplications; the
+// leg after the present one is worked out in turn(), called between steps at
+// least once a leg.
+template <class E, int T, int W, bool ACROSS, bool PAIRS, class ItemsT>
 struct Feed {
+    static constexpr int kStep = 128 / (int)sizeof(E);
     static constexpr int kLoads = T / 8 / W;
-    static_assert(T / 8 % W == 0 && W % 2 == 0, "whole loads, one swizzle for all blocks of a wave");
-    Operand o;
-    int64_t K, first, r0;
-    uint32_t off, step_off;
-    int lk;             // along: this lane's k in a stage; across: whether its column is inside
-    int kb, kb_first, kb_last, seg, segs;
-    uint32_t parts;
+    static_assert(T / 8 % W == 0 && W % 4 == 0, "whole loads, one swizzle for all blocks of a wave");
+    struct Leg {
+        int64_t at, bytes;     // of the next stage in the operand, and from there to the part's end
+        int kb, left;          // its number along k, and the leg's stages from there on
+    };
+    const Operand &o;
+    const GemmArgs &g;
+    const ItemsT &it;
+    const uint32_t parts;
+    const bool is_a;
+    const int64_t inc;         // bytes from a stage to the next
+    uint32_t off[kLoads];
+    int lk;                    // along: this lane's k in a stage
+    uint32_t item;             // of the leg after
+    int seg;
+    bool turned;
+    Leg now, after;
 
-    __device__ __forceinline__ void init(const Operand &op, int64_t row0, int64_t K_, int wave, int lane, int first_step,
-                                         int last_step, int n_segs, uint32_t part_list) {
-        o = op;
-        K = K_;
-        r0 = row0;
-        kb = kb_first = first_step;
-        kb_last = last_step;
-        seg = 0;
-        segs = n_segs;
-        parts = part_list;
+    __device__ __forceinline__ Feed(const Operand &op, const GemmArgs &ga, uint32_t part_list, bool a_side, int wave,
+                                    int lane, const ItemsT &items)
+        : o(op), g(ga), it(items), parts(part_list), is_a(a_side),
+          // (64 k a stage of bf16; two stages to 64 k of fp32, whose operands are not in blocks)
+          inc((sizeof(E) == 2 ? (ACROSS ? op.row64 : op.col64) : (ACROSS ? kStep * op.row : kStep)) * (int64_t)sizeof(E)) {
         if constexpr (!ACROSS) {
-            const int lr = lane >> 3, piece = (lane & 7) ^ (((wave & 1) * 8 + lr) >> 1);
-            off = (uint32_t)(((int64_t)(wave * 8 + lr) * o.ld + piece * 8) * 2);
-            step_off = (uint32_t)(W * 8 * o.ld * 2);
-            lk = piece * 8;
+            const int lr = lane >> 3;
+            const int swz = PAIRS ? ((lr >> 1) & 1) | (wave & 3) << 1 : ((wave & 1) * 8 + lr) >> 1;
+            const int piece = (lane & 7) ^ swz;
+            lk = piece * (16 / (int)sizeof(E));
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = (wave + W * i) * 8 + lr;
+                off[i] = (uint32_t)(((r >> 6) * o.row64 + (r & 63) * o.row + lk) * (int64_t)sizeof(E));
+            }
         } else {
-            constexpr int kRows = 512 / T, kLanes = T / 8;  // k rows of a load, lanes of a row
-            const int k = wave * kRows + lane / kLanes, place = lane % kLanes;
-            const int f = T == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
-            static_assert(W * kRows % 16 == 0, "one swizzle for all loads of a lane");
-            const int col = ((place >> 1) ^ f) * 16 + (place & 1) * 8;
-            off = (uint32_t)(((int64_t)k * o.ld + col) * 2);
-            step_off = (uint32_t)((int64_t)W * kRows * o.ld * 2);
-            lk = row0 + col < o.rows;
+            constexpr int kRowBytes = T * (int)sizeof(E), kLanes = kRowBytes / 16;  // lanes of a row of k
+            static_assert(sizeof(E) == 2 || T == 64, "fp32 tiles");
+            lk = 0;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int k = (wave + W * i) * (64 / kLanes) + lane / kLanes, place = lane % kLanes;
+                int piece;
+                if constexpr (sizeof(E) == 2) {
+                    const int f = T == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
+                    piece = place ^ (f << 1);
+                } else {
+                    piece = place ^ ((k >> 2) & 3) << 2;
+                }
+                const int col = piece * (16 / (int)sizeof(E));
+                off[i] = (uint32_t)(((col >> 6) * o.col64 + (col & 63) + k * o.row) * (int64_t)sizeof(E));
+            }
+        }
+        item = it.at;
+        seg = 0;
+        now = leg();
+        next();
+        after = leg();
+        turned = false;
+    }
+    // the leg of `item` and `seg`: no bytes behind the last item
+    __device__ __forceinline__ Leg leg() const {
+        Leg l{0, 0, 0, 1 << 30};
+        if (item < it.end) {
+            int64_t n0, m0;
+            int split;
+            it.origin(item, n0, m0, split);
+            const int64_t r0 = is_a ? m0 : n0, part = (int64_t)((parts >> (4 * seg)) & 15u) * o.part;
+            l.kb = split * g.split_steps;
+            l.left = steps_in<E>(g, split);
+            // (kStep divides 64, and a tile starts at a multiple of 64)
+            const int64_t k = (int64_t)l.kb * kStep;
+            const int64_t at = ACROSS ? (r0 >> 6) * o.col64 + (k >> 6) * o.row64 + (k & 63) * o.row
+                                      : (r0 >> 6) * o.row64 + (k >> 6) * o.col64 + (k & 63);
+            l.at = (part + at) * (int64_t)sizeof(E);
+            l.bytes = (o.size - at) * (int64_t)sizeof(E);
+        }
+        return l;
+    }
+    __device__ __forceinline__ void next() {
+        if (++seg == g.segs) {
+            seg = 0;
+            item += it.stride;
         }
     }
-    // the next stage's loads (none past the last)
+    __device__ __forceinline__ void turn() {
+        if (turned) {
+            next();
+            after = leg();
+            turned = false;
+        }
+    }
+    // the next stage's loads (zeros past the last item's, and past k)
     __device__ __forceinline__ void issue(uint8_t *st, int wave) {
-        const bool live = seg < segs;
-        const uint16_t *base = o.p + (int64_t)((parts >> (4 * (live ? seg : 0))) & 15u) * o.part;
-        const int64_t k = (int64_t)kb * kStep;
-        uint32_t at = off;
-        if constexpr (!ACROSS) {
-            const __amdgpu_buffer_rsrc_t res = make_rsrc(base + r0 * o.ld, live ? min((int64_t)T, o.rows - r0) * o.ld * 2 : 0);
-            const bool in = k + lk < K;
+        // (a round's last stages may lie behind the matrix: no bytes, never fewer)
+        const int hi = (int)(now.bytes >> 32);
+        const uint32_t low = (uint32_t)now.bytes, cut = low < 0x7FFFFFFFu ? low : 0x7FFFFFFFu;
+        const int bytes = hi < 0 ? 0 : hi > 0 ? 0x7FFFFFFF : (int)cut;
+        const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(static_cast<const char *>(o.p)) + now.at, (short)0, bytes, 0x00020000);
+        const bool in = ACROSS || now.kb * kStep + lk < (int)g.K;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
-                                                         in ? at : kPast, (int)(k * 2), 0, 0);
-                at += step_off;
-            }
-        } else {
-            const __amdgpu_buffer_rsrc_t res =
-                make_rsrc(base + k * o.ld + r0, live ? (min((int64_t)kStep, K - k) * o.ld - r0) * 2 : 0);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
-                                                         lk ? at : kPast, 0, 0, 0);
-                at += step_off;
-            }
-        }
-        // (the scheduler would put the fills off until they are waited for)
-        __builtin_amdgcn_sched_barrier(0);
-        if (++kb == kb_last) {
-            kb = kb_first;
-            ++seg;
-        }
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_void_t *)(st + (wave + W * i) * 1024), 16,
+                                                     in ? off[i] : kPast, 0, 0, 0);
+        const bool last = --now.left == 0;
+        now.at = last ? after.at : now.at + inc;
+        now.bytes = last ? after.bytes : now.bytes - inc;
+        now.kb = last ? after.kb : now.kb + 1;
+        now.left = last ? after.left : now.left;
+        turned = turned || last;
     }
 };
 
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
+typedef short v8i16_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
 
-// This lane's operand of the matrix instruction for half H of a stage (k from
-// 32 H): row l % 16 of block `blk` of 16 rows, k = 8 (l / 16) .. + 7.
-// Across: two transposing reads, each of 4 k (the lanes of a group of 16 give
+// This lane's operand of the matrix instructions for half H of a stage: row
+// l % 16 of block `blk` of 16 rows; bf16: k = 32 H + 8 (l / 16) .. + 7 of one
+// instruction; fp32: k = 16 H + 4 (l / 16) .. + 3, one each of four instructions
+// (which k go together does not matter as long as both sides agree).
+// PAIRS: rows l / 4 * 8 + l % 4 (+ 4 in the odd block) of the 32 of two blocks.
+// Across in bf16: two transposing reads, each of 4 k (the lanes of a group of 16 give
 // four values of one k each and get four k of one row).
-template <int T, bool ACROSS>
+template <class E, int T, bool ACROSS, bool PAIRS>
 struct Reader {
     uint32_t p0, p1;
     __device__ __forceinline__ Reader(int lane) {
+        const int fr = lane & 15, g = lane >> 4;
         if constexpr (!ACROSS) {
-            const int fr = lane & 15, g = lane >> 4;
-            p0 = fr * 128 + (g ^ (fr >> 1)) * 16;
-            p1 = fr * 128 + ((g + 4) ^ (fr >> 1)) * 16;
-        } else {
-            const int g = lane >> 4, q = (lane >> 2) & 3;  // k = 8 g + q (+ 4)
+            const int r = PAIRS ? (fr >> 2) * 8 + (fr & 3) : fr;
+            const int swz = PAIRS ? ((fr >> 1) & 1) | (fr >> 2) << 1 : fr >> 1;
+            p0 = r * 128 + (g ^ swz) * 16;
+            p1 = r * 128 + ((g + 4) ^ swz) * 16;
+        } else if constexpr (sizeof(E) == 2) {
+            const int q = (lane >> 2) & 3;  // k = 8 g + q (+ 4)
             p0 = (8 * g + q) * (2 * T) + (lane & 3) * 8;
             p1 = T == 64 ? (q >> 1) | (g & 1) << 1 : q | (g & 1) << 2;
+        } else {
+            p0 = 4 * g * (4 * T) + fr * 4;
+            p1 = g;
         }
     }
     template <int H>
-    __device__ __forceinline__ bf16x8_t read(const uint8_t *st, int blk) const {
+    __device__ __forceinline__ u32x4_t read(const uint8_t *st, int blk) const {
         if constexpr (!ACROSS) {
-            return *reinterpret_cast<const bf16x8_t *>(st + blk * 2048 + (H == 0 ? p0 : p1));
-        } else {
+            const int at = PAIRS ? (blk >> 1) * 4096 + (blk & 1) * 512 : blk * 2048;
+            return *reinterpret_cast<const u32x4_t *>(st + at + (H == 0 ? p0 : p1));
+        } else if constexpr (sizeof(E) == 2) {
 #if defined(__HIP_DEVICE_COMPILE__)
             const uint8_t *at = st + p0 + (blk ^ p1) * 32 + H * 32 * 2 * T;
             const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)(at));
             const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_t *)(at + 4 * 2 * T));
-            typedef short v8i16_t __attribute__((ext_vector_type(8)));
-            return __builtin_bit_cast(bf16x8_t, v8i16_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+            return __builtin_bit_cast(u32x4_t, v8i16_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 #else
-            return bf16x8_t{};
+            return u32x4_t{};
 #endif
+        } else {
+            const uint8_t *at = st + p0 + (blk ^ p1) * 64 + H * 16 * 4 * T;
+            u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t *>(at + e * 4 * T);
+            return v;
         }
     }
 };
 
-// First row of b and of a of this workgroup's tile, and its part of K.
-// Consecutive workgroups go to the XCDs in turn: each XCD gets a contiguous
-// range of (part, tile), all n tiles of kGroup m tiles before the next, so
-// that the workgroups of an L2 share operand rows of the same part.
-template <int TN, int TM>
-__device__ __forceinline__ void tile_of(const GemmArgs &g, int64_t &n0, int64_t &m0, int &split) {
-    constexpr uint32_t kGroup = 4;
-    const uint32_t tiles_n = (uint32_t)((g.N + TN - 1) / TN), tiles_m = (uint32_t)((g.M + TM - 1) / TM);
-    const uint32_t tiles = tiles_n * tiles_m, all = gridDim.x;
-    const uint32_t xq = all / kXcds, xr = all % kXcds, x = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    const uint32_t logical = x < xr ? x * (xq + 1) + slot : xr * (xq + 1) + (x - xr) * xq + slot;
-    split = (int)(logical / tiles);
-    const uint32_t tile = logical - (uint32_t)split * tiles;
-    const uint32_t grp = tile / (kGroup * tiles_n), in = tile - grp * (kGroup * tiles_n);
-    const uint32_t gm = min(kGroup, tiles_m - grp * kGroup);
-    n0 = (int64_t)(in / gm) * TN;
-    m0 = (int64_t)(grp * kGroup + in % gm) * TM;
-}
-
 // ---------------------------------------------------------------- what a tile ends as
 // A wave's part of a tile: lane l holds C[m][n .. n + 3] of fragment (i, j),
-// m = m0 + 16 j + l % 16, n = n0 + 16 i + 4 (l / 16).
+// m = m0 + 16 j + l % 16, n = n0 + 16 i + 4 (l / 16); PAIRS: of fragments 2 p and 2 p + 1
+// together the eight n = n0 + 32 p + 8 (l / 16) ...
+// kImage: an end that passes through the stages' LDS, so that its workgroup has
+// one item; the others' workgroups take items until there are none, and the next
+// one's first stages land while a tile ends.
 
 // Rows' maxima and sums of exponentials over the wave's columns, and the
 // targets' logits.
 struct LseEnd {
+    static constexpr bool kImage = false, kPairs = false;
     float scale;
     const int32_t *targets;
     float *xt;                 // [n_tok]
     float2 *part;              // [columns / (16 FN)][n_tok]
     int64_t v0;                // the first column's id
-    template <int FN, int FM>
+    template <class E, int FN, int FM>
     __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *, int64_t m0, int64_t n0, int,
                                         int lane) const {
-        const int64_t nl = n0 + 4 * (lane >> 4);
+        const int nl = 4 * (lane >> 4);
+        int32_t y[FM];  // the target's column in the wave's, if it has one
 #pragma unroll
-        for (int j = 0; j < FM; ++j)
+        for (int j = 0; j < FM; ++j) {
+            const int64_t m = m0 + 16 * j + (lane & 15), at = (int64_t)targets[min(m, g.M - 1)] - v0 - n0;
+            y[j] = m < g.M && at >= 0 && at < 16 * FN && n0 + at < g.N ? (int32_t)at : -1;
+        }
 #pragma unroll
-            for (int i = 0; i < FN; ++i) acc[i][j] *= scale;
+        for (int j = 0; j < FM; ++j) {
+            if (!__any(y[j] >= 0)) continue;
+            float at_y = 0.f;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (y[j] == 16 * i + nl + r) at_y = acc[i][j][r] * scale;
+            if (y[j] >= 0 && ((y[j] >> 2) & 3) == (lane >> 4)) xt[m0 + 16 * j + (lane & 15)] = at_y;
+        }
+        float c = scale * kLog2e;
+        if (c < 0.f) {  // (the largest logit is the smallest sum)
+            c = -c;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = -acc[i][j];
+        }
         if (n0 + 16 * FN > g.N) {
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (nl + 16 * i + r >= g.N)
+                    if (n0 + nl + 16 * i + r >= g.N)
 #pragma unroll
                         for (int j = 0; j < FM; ++j) acc[i][j][r] = -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int64_t m = m0 + 16 * j + (lane & 15);
-            const bool in = m < g.M;
-            const int64_t y = in ? (int64_t)targets[m] - v0 - n0 : -1;
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
+                top = fmaxf(fmaxf(fmaxf(top, acc[i][j][0]), fmaxf(acc[i][j][1], acc[i][j][2])), acc[i][j][3]);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float from = top == -INFINITY ? 0.f : top;
-            float sum = 0.f, at_y = 0.f;
-            const bool mine = y >= 0 && y < 16 * FN && n0 + y < g.N && ((y >> 2) & 3) == (lane >> 4);
+            // (no finite one: the sum is of NaN, or of nothing)
+            const float from = top == -INFINITY ? 0.f : -top * c;
+            float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (y == 16 * i + 4 * (lane >> 4) + r) at_y = acc[i][j][r];
-                    sum += __builtin_amdgcn_exp2f((acc[i][j][r] - from) * kLog2e);
-                }
+                for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], c, from));
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (mine) xt[m] = at_y;
-            if (in && lane < 16) part[(v0 + n0) / (16 * FN) * g.M + m] = float2{top, sum};
+            const int64_t m = m0 + 16 * j + (lane & 15);
+            if (m < g.M && lane < 16)
+                part[(v0 + n0) / (16 * FN) * g.M + m] = float2{top == -INFINITY ? top : top * c, sum};
+        }
+    }
+};
+
+// What the gradient of a token's logits needs: lse, the factor g_t scale (0 for a
+// token that does not count) and the target.
+struct Token {
+    float lse, factor;
+    int32_t target, unused;
+};
+
+// A tile of P, in `parts` parts of bf16 in blocks, or in fp32 rows of ld: zeros
+// behind the vocabulary's end and for tokens that do not count.
+struct GradEnd {
+    static constexpr bool kImage = false, kPairs = true;
+    float scale;
+    const Token *token;        // [n_tok]
+    void *p;
+    int64_t row64, part, ld;   // blocks: as in their Operand, whole columns
+    int32_t parts;
+    int64_t v0;
+    template <class E, int FN, int FM>
+    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *, int64_t m0, int64_t n0,
+                                        int, int lane) const {
+        constexpr bool PAIRS = sizeof(E) == 2;
+        // this lane's columns: nl + col(i) + r
+        const int64_t nl = n0 + (PAIRS ? 8 : 4) * (lane >> 4);
+        auto col = [](int i) { return PAIRS ? (i >> 1) * 32 + (i & 1) * 4 : i * 16; };
+        u32x4_t tok[FM];
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            tok[j] = *reinterpret_cast<const u32x4_t *>(token + min(m0 + 16 * j + (lane & 15), g.M - 1));
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int64_t m = m0 + 16 * j + (lane & 15);
+            const float l = __uint_as_float(tok[j][0]), f = m < g.M ? __uint_as_float(tok[j][1]) : 0.f;
+            const int64_t y = (int64_t)(int32_t)tok[j][2] - v0 - nl;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[i][j][r] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], scale, -l) * kLog2e);
+            if (__any(y >= 0 && y < 16 * FN)) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (y == col(i) + r) acc[i][j][r] -= 1.f;
+            }
+#pragma unroll
+            for (int i = 0; i < FN; ++i) acc[i][j] *= f;
+        }
+        if (n0 + 16 * FN > g.N) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (nl + col(i) + r >= g.N)
+#pragma unroll
+                        for (int j = 0; j < FM; ++j) acc[i][j][r] = 0.f;
+        }
+        if constexpr (PAIRS) {
+            for (int q = 0; q < parts; ++q) {
+                uint16_t *to = static_cast<uint16_t *>(p) + q * part;
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    // (rows and columns past the last are zeros up to whole blocks)
+                    const int64_t m = m0 + 16 * j + (lane & 15);
+                    if (m >= (g.M + kBlock - 1) / kBlock * kBlock) continue;
+#pragma unroll
+                    for (int i = 0; i < FN; i += 2) {
+                        const int64_t n = nl + col(i);
+                        if (n >= ld) continue;
+                        const f32x4_t &x = acc[i][j], &z = acc[i + 1][j];
+                        *reinterpret_cast<u32x4_t *>(to + block_at(m, n, row64)) =
+                            u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(z[0], z[1]),
+                                    pack_bf16x2(z[2], z[3])};
+                    }
+                }
+                if (q + 1 < parts)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j)
+#pragma unroll
+                        for (int i = 0; i < FN; ++i)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[i][j][r] -= (float)(__bf16)acc[i][j][r];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int64_t m = m0 + 16 * j + (lane & 15);
+                if (m >= g.M) continue;
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+                    if (nl + col(i) < ld)
+                        *reinterpret_cast<f32x4_t *>(static_cast<float *>(p) + m * ld + nl + col(i)) = acc[i][j];
+            }
         }
     }
 };
@@ -288,61 +511,16 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[FN][FM], uint8_t
             }
         }
     }
-    asm volatile("" ::: "memory");
 }
-
-// A tile of P, in `parts` parts: zeros behind the vocabulary's end and for tokens
-// that do not count.
-struct GradEnd {
-    float scale, dloss_scale;
-    const int32_t *targets;
-    const float *lse, *dloss;  // [n_tok]; dloss may be null: ones
-    uint16_t *p;               // [parts][n_tok][ld]
-    int64_t ld;
-    int32_t parts, vocab;
-    int64_t v0;
-    template <int FN, int FM>
-    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *img, int64_t m0, int64_t n0,
-                                        int, int lane) const {
-        const int64_t nl = n0 + 4 * (lane >> 4);
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const int64_t m = m0 + 16 * j + (lane & 15);
-            const int64_t t = min(m, g.M - 1);
-            const int32_t id = targets[t];
-            const bool counts = id >= 0 && id < vocab;
-            const int64_t y = (int64_t)id - v0 - nl;
-            const float l = lse[t], f = (dloss ? dloss[t] : 1.f) * dloss_scale * scale;
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float x = __builtin_amdgcn_exp2f((acc[i][j][r] * scale - l) * kLog2e);
-                    if (y == 16 * i + r) x -= 1.f;
-                    x *= f;
-                    acc[i][j][r] = counts && nl + 16 * i + r < g.N ? x : 0.f;
-                }
-        }
-        for (int q = 0; q < parts; ++q) {
-            store_rows<FN, FM>(acc, img, p + q * g.M * ld, ld, g.M, ld, m0, n0, lane, false);
-            if (q + 1 < parts)
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-#pragma unroll
-                    for (int i = 0; i < FN; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][j][r] -= (float)(__bf16)acc[i][j][r];
-        }
-    }
-};
 
 // The sums themselves: fp32 (a split's at `split_elems` from the one before), or
 // bf16; over what is there or added to it.
 struct SumEnd {
+    static constexpr bool kImage = true, kPairs = false;
     void *c;
     int64_t ld, split_elems;
     bool bf16, accumulate;
-    template <int FN, int FM>
+    template <class E, int FN, int FM>
     __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *img, int64_t m0, int64_t n0,
                                         int split, int lane) const {
         if (bf16) {
@@ -366,128 +544,233 @@ struct SumEnd {
 };
 
 // ---------------------------------------------------------------- the product
-// A workgroup makes TN x TM outputs with WN x WM waves, each FN x FM fragments of
+// The order the scheduler is to keep: N instructions of a kind (0x20: loads from
+// global memory, 0x100: reads of LDS) spread over M matrix instructions.
+template <int KIND, int N, int M, int... I>
+__device__ __forceinline__ void spread_of(std::integer_sequence<int, I...>) {
+    ((__builtin_amdgcn_sched_group_barrier(KIND, 1, 0),
+      __builtin_amdgcn_sched_group_barrier(0x8, M * (I + 1) / N - M * I / N, 0)), ...);
+}
+template <int KIND, int N, int M>
+__device__ __forceinline__ void spread() {
+    spread_of<KIND, N, M>(std::make_integer_sequence<int, N>{});
+}
+
+// A workgroup makes T x T outputs with WN x WM waves, each FN x FM fragments of
 // 16 x 16; b's rows are the matrix instruction's A side.  Operands go from global
-// memory straight into LDS, 64 k a stage, while earlier stages are multiplied.
+// memory straight into LDS, 128 bytes of k a stage, while earlier stages are multiplied.
 // NB = 2: two stages of b and three of a (160 KB at 256 x 256; 80 KB at 128 x
 // 128, two workgroups a CU), so that a's loads have two steps to land.  NB = 4:
 // four of each.
-template <class End, int TN, int TM, int WN, int WM, int NB, bool AX, bool BX>
+//
+// A step multiplies the first half of its stage, which the step before has
+// read, while it reads the second; then every wave has read this stage and
+// the next one has landed (the barrier): it is filled again, and the next
+// stage's first half is read while the second is multiplied.  So no multiply
+// waits for a read behind a barrier.
+template <class E, class End, int T, int WN, int WM, int NB, int NA, bool AX, bool BX>
 __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End end) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int W = WN * WM, FN = TN / 16 / WN, FM = TM / 16 / WM;
-    constexpr int kStageB = TN * 128, kStageA = TM * 128;
-    static_assert(TN == TM && (NB == 2 || NB == 4), "stages");
+    constexpr int W = WN * WM, FN = T / 16 / WN, FM = T / 16 / WM;
+    constexpr int kStage = T * 128;
+    constexpr bool PAIRS = End::kPairs && sizeof(E) == 2;
+    static_assert(NA == 2 || NA == 3 || NB == 4, "stages");
+    static_assert(!PAIRS || !BX, "pairs of rows along k");
     // (separate arrays: the compiler then knows which of them a fragment read
     // and a load in flight touch, and adds no waits of its own)
-    __shared__ __attribute__((aligned(1024))) uint8_t b0[kStageB];
-    __shared__ __attribute__((aligned(1024))) uint8_t b1[kStageB];
-    __shared__ __attribute__((aligned(1024))) uint8_t a0[kStageA];
-    __shared__ __attribute__((aligned(1024))) uint8_t a1[kStageA];
-    __shared__ __attribute__((aligned(1024))) uint8_t a2[kStageA];
-    __shared__ __attribute__((aligned(1024))) uint8_t a3[NB == 4 ? kStageA : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b2[NB == 4 ? kStageB : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b3[NB == 4 ? kStageB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t b1[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a1[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t a2[NA >= 3 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t a3[NA == 4 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b2[NB == 4 ? kStage : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b3[NB == 4 ? kStage : 16];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t n0, m0;
-    int split;
-    tile_of<TN, TM>(g, n0, m0, split);
-    const int all = (int)steps_of(g.K), first = split * g.split_steps, last = min(first + g.split_steps, all);
-    Feed<TM, W, AX> fa;
-    Feed<TN, W, BX> fb;
-    fa.init(g.a, m0, g.K, wave, lane, first, last, g.segs, g.a_parts);
-    fb.init(g.b, n0, g.K, wave, lane, first, last, g.segs, g.b_parts);
-    const Reader<TM, AX> ra(lane);
-    const Reader<TN, BX> rb(lane);
+    typedef Items<T, T> ItemsT;
+    const ItemsT it(g);
+    if (it.at >= it.end) return;  // (all of its waves)
+    Feed<E, T, W, AX, false, ItemsT> fa(g.a, g, g.a_parts, true, wave, lane, it);
+    Feed<E, T, W, BX, PAIRS, ItemsT> fb(g.b, g, g.b_parts, false, wave, lane, it);
+    auto turn = [&] {
+        fa.turn();
+        fb.turn();
+    };
+    const Reader<E, T, AX, false> ra(lane);
+    const Reader<E, T, BX, PAIRS> rb(lane);
     const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
 
     f32x4_t acc[FN][FM] = {};
-    auto half = [&](const uint8_t *sta, const uint8_t *stb, auto hc) {
+    struct Half {
+        u32x4_t a[FM], b[FN];
+    };
+    auto read = [&](const uint8_t *sta, const uint8_t *stb, Half &h, auto hc) {
         constexpr int H = decltype(hc)::value;
-        bf16x8_t va[FM];
 #pragma unroll
-        for (int j = 0; j < FM; ++j) va[j] = ra.template read<H>(sta, wm + j);
+        for (int j = 0; j < FM; ++j) h.a[j] = ra.template read<H>(sta, wm + j);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const bf16x8_t vb = rb.template read<H>(stb, wn + i);
+        for (int i = 0; i < FN; ++i) h.b[i] = rb.template read<H>(stb, wn + i);
+    };
+    auto multiply = [&](const Half &h) {
+        if constexpr (sizeof(E) == 2) {
 #pragma unroll
-            for (int j = 0; j < FM; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, va[j], acc[i][j], 0, 0, 0);
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, h.b[i]),
+                                                                        __builtin_bit_cast(bf16x8_t, h.a[j]), acc[i][j], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]),
+                                                                         acc[i][j], 0, 0, 0);
         }
     };
-    // Each step: this stage's loads have landed everywhere (later ones, kAhead
-    // a wave, may be in flight) and the stages of the step before are free:
-    // fill them, multiply.  (The last fills lie past the last step: zeros.)
-    constexpr int kAhead = NB == 2 ? Feed<TM, W, AX>::kLoads : 2 * (Feed<TM, W, AX>::kLoads + Feed<TN, W, BX>::kLoads);
-    fb.issue(b0, wave);
-    fa.issue(a0, wave);
-    if constexpr (NB == 4) fb.issue(b1, wave);
-    fa.issue(a1, wave);
+    // (kAhead loads a wave may be in flight at a step's barrier.  The last fills
+    // and reads lie past the last item: zeros, not used.)
+    constexpr int kL = T / 8 / W;
+    constexpr int kAhead = NB == 4 ? 4 * kL : NA == 3 ? kL : 0;
+    constexpr std::integral_constant<int, 0> lo{};
+    constexpr std::integral_constant<int, 1> hi{};
+    // (a step's fills may end a leg, which turn() has to see before the next one's)
+    auto fill = [&](uint8_t *st_b, uint8_t *st_a) {
+        fb.issue(st_b, wave);
+        fa.issue(st_a, wave);
+    };
+    fill(b0, a0);
+    turn();
+    fill(b1, a1);
+    turn();
     if constexpr (NB == 4) {
-        fb.issue(b2, wave);
+        fill(b2, a2);
+        turn();
+        fill(b3, a3);
+    } else if constexpr (NA == 3) {
         fa.issue(a2, wave);
     }
-    int left = (last - first) * g.segs;
-    auto step = [&](const uint8_t *cur_a, const uint8_t *cur_b, uint8_t *fill_a, uint8_t *fill_b) {
+    turn();
+    Half h0, h1;
+    stage_barrier<NB == 4 ? 6 * kL : NA * kL>();
+    read(a0, b0, h0, lo);
+    int left = 0;
+    auto step = [&](uint8_t *cur_a, uint8_t *cur_b, const uint8_t *next_a, const uint8_t *next_b)
+                    __attribute__((always_inline)) {
+        // (256 x 256: the order is set, or the scheduler gathers the reads and fills
+        // and the multiplications wait for them: P 1.29 PFLOP/s against 1.20)
+        constexpr bool SET = T == 256;
+        constexpr int kReads = (AX ? 2 : 1) * FM + (BX ? 2 : 1) * FN, kMul = FM * FN;
+        read(cur_a, cur_b, h1, hi);
+        multiply(h0);
+        if constexpr (SET) {
+            spread<0x100, kReads, kMul - 8>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
         stage_barrier<kAhead>();
-        fb.issue(fill_b, wave);
-        fa.issue(fill_a, wave);
-        half(cur_a, cur_b, std::integral_constant<int, 0>{});
-        half(cur_a, cur_b, std::integral_constant<int, 1>{});
+        if constexpr (SET) __builtin_amdgcn_sched_barrier(0);
+        fill(cur_b, cur_a);
+        read(next_a, next_b, h0, lo);
+        multiply(h1);
+        if constexpr (SET) {
+            spread<0x20, 2 * kL, 4 * kL>();
+            spread<0x100, kReads, kMul - 4 * kL>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
         return --left == 0;
     };
-    for (;;) {
-        if constexpr (NB == 2) {
-            if (step(a0, b0, a2, b1)) break;
-            if (step(a1, b1, a0, b0)) break;
-            if (step(a2, b0, a1, b1)) break;
-            if (step(a0, b1, a2, b0)) break;
-            if (step(a1, b0, a0, b1)) break;
-            if (step(a2, b1, a1, b0)) break;
-        } else {
-            if (step(a0, b0, a3, b3)) break;
-            if (step(a1, b1, a0, b0)) break;
-            if (step(a2, b2, a1, b1)) break;
-            if (step(a3, b3, a2, b2)) break;
+    for (uint32_t item = it.at; item < it.end; item += it.stride) {
+        int64_t n0, m0;
+        int split;
+        it.origin(item, n0, m0, split);
+        left = steps_in<E>(g, split) * g.segs;
+        for (;;) {  // (whole rounds of the stages, or one item; a leg is a round at least)
+            if constexpr (NA == 2) {
+                step(a0, b0, a1, b1);
+                if (step(a1, b1, a0, b0)) break;
+                turn();
+            } else if constexpr (NB == 2) {
+                if (step(a0, b0, a1, b1)) break;
+                turn();
+                if (step(a1, b1, a2, b0)) break;
+                turn();
+                if (step(a2, b0, a0, b1)) break;
+                turn();
+                if (step(a0, b1, a1, b0)) break;
+                turn();
+                if (step(a1, b0, a2, b1)) break;
+                turn();
+                if (step(a2, b1, a0, b0)) break;
+                turn();
+            } else {
+                step(a0, b0, a1, b1);
+                step(a1, b1, a2, b2);
+                step(a2, b2, a3, b3);
+                if (step(a3, b3, a0, b0)) break;
+                turn();
+            }
         }
+        turn();
+        if constexpr (End::kImage) stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
+        constexpr int kImage = FM * 16 * FN * 32, kImages = kStage / kImage;
+        static_assert(kImages * 4 >= W, "the waves' images in four stages");
+        uint8_t *const home = wave / kImages == 0 ? b0 : wave / kImages == 1 ? b1 : wave / kImages == 2 ? a0 : a1;
+        end.template run<E, FN, FM>(g, acc, home + wave % kImages * kImage, m0 + wm * 16, n0 + wn * 16, split, lane);
+        if constexpr (End::kImage) return;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        read(a0, b0, h0, lo);  // (once more: its registers are free while the tile ends)
     }
-    stage_barrier<0>();  // the last fills have landed and every read is done: the stages are free
-    constexpr int kImage = FM * 16 * FN * 32, kImages = kStageB / kImage;
-    static_assert(kImages * 4 >= W, "the waves' images in four stages");
-    uint8_t *const home = wave / kImages == 0 ? b0 : wave / kImages == 1 ? b1 : wave / kImages == 2 ? a0 : a1;
-    end.run(g, acc, home + wave % kImages * kImage, m0 + wm * 16, n0 + wn * 16, split, lane);
+    wait_loads();  // (the last fills land before the workgroup's LDS is given away)
 #endif
 }
 
 // ---------------------------------------------------------------- the rest
-// Parts of x [rows][d] in bf16, rows of tokens that do not count as zeros
-// (targets given): with one part a masked copy.
-template <typename T, int PARTS>
+// Copies of x [rows][d] for the products: parts in bf16 in blocks, or (T = Out = float,
+// one part) whole rows of fp32; zeros in the rows of tokens that do not count
+// (targets given) and up to whole blocks.  Beside it the tokens' constants.
+template <typename T, typename Out, int PARTS>
 __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, int32_t d, const int32_t *targets,
-                                                    int32_t vocab, uint16_t *out) {
-    const int32_t units = d / 8;
-    const int64_t n = rows * units;
+                                                    int32_t vocab, Out *out, const float *lse, const float *dloss,
+                                                    float factor, Token *token) {
+    constexpr bool BLOCKS = sizeof(Out) == 2;
+    const int32_t cols = BLOCKS ? (d + kBlock - 1) / kBlock * kBlock : d, units = cols / 8;
+    const int64_t all = BLOCKS ? (rows + kBlock - 1) / kBlock * kBlock : rows, n = all * units;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
-        bool counts = true;
-        if (targets) {
-            const int32_t id = targets[quotient(u, units)];
+        const int64_t r = quotient(u, units);
+        const int32_t c = (int32_t)(u - r * units) * 8;
+        bool counts = r < rows;
+        if (targets && counts) {
+            const int32_t id = targets[r];
             counts = id >= 0 && id < vocab;
+            if (token && c == 0)
+                token[r] = Token{lse[r], counts ? (dloss ? dloss[r] : 1.f) * factor : 0.f, id, 0};
         }
         F8 v = {};
-        if (counts) v = load8(x + u * 8);
+        if (counts && c < d) v = load8(x + r * d + c);
+        if constexpr (BLOCKS) {
+            const int64_t at = block_at(r, c, (int64_t)cols * kBlock);
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
-            store8(out + (int64_t)q * n * 8 + u * 8, v);
-            if (q + 1 < PARTS)
+            for (int q = 0; q < PARTS; ++q) {
+                store8(out + q * n * 8 + at, v);
+                if (q + 1 < PARTS)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v.v[i] -= (float)(__bf16)v.v[i];
+                    for (int i = 0; i < 8; ++i) v.v[i] -= (float)(__bf16)v.v[i];
+            }
+        } else {
+            store8(out + r * d + c, v);
         }
     }
 }
 
-// lse and loss of 8 tokens a workgroup, their parts shared by 32 lanes each.
+// lse and loss of 8 tokens a workgroup, their parts (maxima in powers of two)
+// shared by 32 lanes each.
 __global__ __launch_bounds__(256) void lse_join_kernel(const float2 *part, int64_t n_parts, int64_t n_tok,
                                                        const int32_t *targets, int32_t vocab, const float *xt, float *loss,
                                                        float *lse) {
@@ -497,10 +780,10 @@ __global__ __launch_bounds__(256) void lse_join_kernel(const float2 *part, int64
     float top = -INFINITY, sum = 0.f;
     auto add = [&](float2 p) {
         const float m = fmaxf(top, p.x), from = m == -INFINITY ? 0.f : m;
-        sum = sum * __builtin_amdgcn_exp2f((top - from) * kLog2e) + p.y * __builtin_amdgcn_exp2f((p.x - from) * kLog2e);
+        sum = sum * __builtin_amdgcn_exp2f(top - from) + p.y * __builtin_amdgcn_exp2f(p.x - from);
         top = m;
     };
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = sl; i < n_parts; i += 32) add(part[i * n_tok + tc]);
     red[sl][tl] = float2{top, sum};
     __syncthreads();
@@ -510,7 +793,7 @@ __global__ __launch_bounds__(256) void lse_join_kernel(const float2 *part, int64
     for (int i = 0; i < 32; ++i) add(red[i][tl]);
     const int32_t id = targets[t];
     const bool counts = id >= 0 && id < vocab;
-    const float l = (top == -INFINITY ? 0.f : top) + logf(sum);
+    const float l = (float)((top == -INFINITY ? 0. : (double)top * 0.69314718055994530942) + (double)logf(sum));
     loss[t] = counts ? l - xt[t] : 0.f;
     lse[t] = counts ? l : 0.f;
 }
@@ -544,77 +827,113 @@ __global__ __launch_bounds__(256) void sum_join_kernel(const float *part, int32_
 }
 
 // ---------------------------------------------------------------- host side
-// How an M x N product is tiled: 256 x 256 where such tiles come to about one
-// workgroup a CU, else 64 x 64 while those fit the chip at once or M is that
-// short, and 128 x 128 beyond.
-int tile_for(int64_t M, int64_t N) {
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class E>
+constexpr int64_t step_of() {
+    return 128 / (int64_t)sizeof(E);
+}
+
+// How an M x N product is tiled: 256 x 256 where such tiles (or they and parts of
+// K of at least eight stages, where K may be split) come to about one workgroup
+// a CU, else 64 x 64 while those fit the chip at once or M is that short, and
+// 128 x 128 beyond.  fp32 tiles are 64 x 64.
+int tile_for(int64_t M, int64_t N, int64_t k_steps = 0) {
     auto tiles = [&](int64_t t) { return ((N + t - 1) / t) * ((M + t - 1) / t); };
-    if (M > 128 && tiles(256) >= 192) return 256;
+    const int64_t wide = tiles(256), parts = std::max<int64_t>(1, std::min<int64_t>(256 / wide, k_steps / 8));
+    if (std::min(M, k_steps ? N : M) > 128 && wide * parts >= 192) return 256;
     return M <= 64 || tiles(64) <= 512 ? 64 : 128;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+template <class E, bool AX, bool BX, class End>
+void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
+    g.items = (int32_t)(ceil_div(g.N, tile) * ceil_div(g.M, tile) * g.splits);
+    // one 256 x 256 tile's stages fill a CU's LDS, two of the others fit
+    const unsigned most = tile == 256 ? 256 : 512, grid = End::kImage ? (unsigned)g.items : std::min((unsigned)g.items, most);
+    constexpr int NA = End::kImage ? 3 : 2;
+    g.round = tile == 64 ? 4 : NA == 3 ? 1 : 2;
+    if constexpr (sizeof(E) == 4) {
+        launch_kernel((gemm_kernel<E, End, 64, 2, 2, 4, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
+    } else {
+        if (tile == 256)
+            launch_kernel((gemm_kernel<E, End, 256, 2, 4, 2, NA, AX, BX>), dim3(grid), dim3(512), s, g, end);
+        else if (tile == 128)
+            launch_kernel((gemm_kernel<E, End, 128, 2, 2, 2, NA, AX, BX>), dim3(grid), dim3(256), s, g, end);
+        else
+            launch_kernel((gemm_kernel<E, End, 64, 2, 2, 4, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
+    }
+}
 
-template <bool AX, bool BX, class End>
-void gemm(const GemmArgs &g, const End &end, int tile, hipStream_t s) {
-    const unsigned grid = (unsigned)(ceil_div(g.N, tile) * ceil_div(g.M, tile) * g.splits);
-    if (tile == 256)
-        launch_kernel((gemm_kernel<End, 256, 256, 2, 4, 2, AX, BX>), dim3(grid), dim3(512), s, g, end);
-    else if (tile == 128)
-        launch_kernel((gemm_kernel<End, 128, 128, 2, 2, 2, AX, BX>), dim3(grid), dim3(256), s, g, end);
+template <typename T, typename Out, int PARTS>
+void make_parts(const void *x, int64_t rows, int32_t d, const LossArgs *a, Out *out, Token *token, hipStream_t s) {
+    const int64_t n = sizeof(Out) == 2 ? round64(rows) * (round64(d) / 8) : rows * (d / 8);
+    launch_kernel((parts_kernel<T, Out, PARTS>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), s,
+                  static_cast<const T *>(x), rows, d, a ? a->targets : static_cast<const int32_t *>(nullptr),
+                  a ? a->vocab : 0, out, a ? static_cast<const float *>(a->lse) : static_cast<const float *>(nullptr),
+                  a ? a->dloss : static_cast<const float *>(nullptr), a ? a->dloss_scale * a->scale : 0.f, token);
+}
+
+// A copy in blocks of rows of h or W: a bf16 plan's as they are, an fp32 plan's in
+// three parts.
+void make_blocks(const LossArgs &a, const void *x, int64_t rows, const LossArgs *mask, uint16_t *out, Token *token,
+                 hipStream_t s) {
+    if (a.bf16)
+        make_parts<uint16_t, uint16_t, 1>(x, rows, a.d, mask, out, token, s);
     else
-        launch_kernel((gemm_kernel<End, 64, 64, 2, 2, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
+        make_parts<float, uint16_t, 3>(x, rows, a.d, mask, out, token, s);
 }
 
-template <typename T, int PARTS>
-void make_parts(const void *x, int64_t rows, int32_t d, const int32_t *targets, int32_t vocab, uint16_t *out,
-                hipStream_t s) {
-    const int64_t n = rows * (d / 8);
-    launch_kernel((parts_kernel<T, PARTS>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), s,
-                  static_cast<const T *>(x), rows, d, targets, vocab, out);
-}
-
-// Products of parts: all pairs whose weight is 2^-16 and more.
+// Products of parts: all pairs whose weight is 2^-16 and more, the lightest first,
+// so that only the last one's sums are rounded at their full size.
 void parts_of(GemmArgs &g, int a_parts, int b_parts) {
     g.segs = 0;
     g.a_parts = g.b_parts = 0;
-    for (int i = 0; i < a_parts; ++i)
-        for (int j = 0; j < b_parts; ++j)
-            if (i + j < 3) {
-                g.a_parts |= (uint32_t)i << (4 * g.segs);
-                g.b_parts |= (uint32_t)j << (4 * g.segs);
-                ++g.segs;
-            }
+    for (int w = 2; w >= 0; --w)
+        for (int i = 0; i < a_parts; ++i) {
+            const int j = w - i;
+            if (j < 0 || j >= b_parts) continue;
+            g.a_parts |= (uint32_t)i << (4 * g.segs);
+            g.b_parts |= (uint32_t)j << (4 * g.segs);
+            ++g.segs;
+        }
 }
 
+template <class E>
 void whole(GemmArgs &g) {
     g.splits = 1;
-    g.split_steps = (int32_t)ceil_div(g.K, kStep);
+    g.split_steps = (int32_t)ceil_div(g.K, step_of<E>());
+}
+
+// At most n parts of K, of whole rounds of stages (an item's last ones are zeros
+// past K, not the next part's).
+void split_steps(GemmArgs &g, int64_t steps, int64_t n) {
+    const int64_t per = ceil_div(ceil_div(steps, n), 4) * 4;
+    g.split_steps = (int32_t)per;
+    g.splits = (int32_t)ceil_div(steps, per);
 }
 
 // Parts of K for a product of few tiles: as many as fill the chip's slots (one
 // 256 x 256 tile a CU, two of the others) evenly, of at least eight stages.
+template <class E>
 void split_k(GemmArgs &g, int tile, int64_t most) {
-    const int64_t tiles = ceil_div(g.M, tile) * ceil_div(g.N, tile), steps = ceil_div(g.K, kStep);
+    const int64_t tiles = ceil_div(g.M, tile) * ceil_div(g.N, tile), steps = ceil_div(g.K, step_of<E>());
     const int64_t slots = tile == 256 ? 256 : 512;
-    most = std::min<int64_t>({most, steps / 8, tiles >= 4 * slots ? 1 : 4 * slots / tiles});
+    most = std::min<int64_t>({most, steps / 8, tiles >= 8 * slots ? 1 : 8 * slots / tiles});
     int64_t best = 1;
     double best_cost = 1e30;
     for (int64_t s = 1; s <= most; ++s) {
-        // rounds of the chip times a tile's stages, and a stage's worth for its start and end
+        // rounds of the chip times a tile's stages, and a dozen stages' worth for its start and end
         const double cost = (double)ceil_div(tiles * s, slots) * ((double)ceil_div(steps, s) + 12.);
         if (cost < best_cost * 0.97) {
             best_cost = cost;
             best = s;
         }
     }
-    const int64_t per = ceil_div(steps, best);
-    g.split_steps = (int32_t)per;
-    g.splits = (int32_t)ceil_div(steps, per);
+    split_steps(g, steps, best);
 }
 
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;     // of P, and of W's parts, at a time
-constexpr int64_t kSumBytes = (int64_t)256 << 20;     // of dh's sums in several splits
+constexpr int64_t kSumBytes = (int64_t)512 << 20;     // of dh's sums in several splits
 constexpr int64_t kMostSplits = 16;
 
 int64_t padded(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
@@ -636,10 +955,27 @@ int64_t sum_bytes(int64_t n_tok, int32_t d) {
     return std::max(one, std::min(kSumBytes, kMostSplits * one));
 }
 
-// dW's sums in several splits: at most 64 MB (a tile of each slot).
+// dW's sums in several splits: at most 64 MB.
 int64_t weight_sum_bytes(int64_t vocab, int32_t d) { return std::min<int64_t>((int64_t)64 << 20, kMostSplits * vocab * d * 4); }
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Whether an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
+// of the bf16 ones' rate, or in six products of bf16 parts: those need W's parts
+// made first.
+bool direct32(const LossArgs &a) { return a.n_tok <= 128; }
+
+// Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
+// d = 2560 put a stage's 256 lines on four of an L2's sixteen channels; in blocks
+// the logits of 8192 tokens and 64,640 columns take 2.03 ms (h) and 1.92 ms (h and W)
+// against 2.13 ms, their gradient's product with W 2.08 ms against 2.35 ms.  The
+// copy of W costs 4 bytes a value, 0.14 ms there, so it takes this many tokens.
+bool blocks_h(const LossArgs &a) { return a.bf16 && a.n_tok >= 1024 && a.vocab >= 16384; }
+bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (forward ? 12288 : 4096); }
+
+// Parts of P, and bytes of P for a token and column.
+int p_parts(const LossArgs &a) { return a.bf16 && a.dw_bf16 ? 1 : 3; }
+int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a) ? 4 : 2 * p_parts(a); }
 
 }  // namespace
 
@@ -650,8 +986,6 @@ LossLayout loss_layout(const LossArgs &a) {
     LossLayout L{};
     const int64_t v = padded(a.vocab), T = a.n_tok;
     const int64_t n128 = v / 128, n64 = v / 64, n32 = v / 32;
-    const int64_t most = std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 512 * 128 * 4),
-                                   std::min<int64_t>(T, 128) * n64, std::min<int64_t>(T * n64, 192 * 1024 * 4)});
     int64_t off = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = off;
@@ -659,11 +993,11 @@ LossLayout loss_layout(const LossArgs &a) {
         return (size_t)o;
     };
     L.xt = take(T * 4);
-    L.part = take(most * 8);
-    if (!a.bf16) {
-        L.h = take(3 * T * a.d * 2);
-        L.w = take(piece_bytes(a.vocab, (int64_t)a.d * 6));
-    }
+    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 128) * n32, std::min<int64_t>(T * n32, 512 * 128 * 4),
+                                std::min<int64_t>(T, 128) * n64, std::min<int64_t>(T * n64, 192 * 1024 * 4)}));
+    const int64_t each = a.bf16 ? 2 : 6;
+    if (a.bf16 ? blocks_h(a) : !direct32(a)) L.h = take(each * round64(T) * round64(a.d));
+    if (a.bf16 ? blocks_w(a, true) : !direct32(a)) L.w = take(piece_bytes(a.vocab, round64(a.d) * each));
     L.total = (size_t)off;
     return L;
 }
@@ -676,129 +1010,129 @@ LossLayout loss_bwd_layout(const LossArgs &a) {
         off = round256(off + bytes);
         return (size_t)o;
     };
-    const int64_t pp = a.bf16 ? (a.dw_bf16 ? 1 : 2) : 3;
-    L.h = take((a.bf16 ? 1 : 3) * a.n_tok * a.d * 2);
-    L.part = take(piece_bytes(a.vocab, pp * a.n_tok * 2));
+    L.xt = take(a.n_tok * (int64_t)sizeof(Token));
+    L.h = take((a.bf16 ? 2 : direct32(a) ? 4 : 6) * round64(a.n_tok) * round64(a.d));
+    L.part = take(piece_bytes(a.vocab, p_bytes(a) * round64(a.n_tok)));
     L.sum = take(sum_bytes(a.n_tok, a.d));
     L.wsum = take(weight_sum_bytes(a.vocab, a.d));
-    if (!a.bf16) L.w = take(piece_bytes(a.vocab, (int64_t)a.d * 6));
+    if (a.bf16 ? blocks_w(a, false) : !direct32(a)) L.w = take(piece_bytes(a.vocab, round64(a.d) * (a.bf16 ? 2 : 6)));
     L.total = (size_t)off;
     return L;
 }
 
 bool loss_fits(int64_t n_tok, int32_t vocab, int32_t d) {
-    // tiles of one launch (fewer than 2^32 threads), and 31-bit offsets in a tile's
-    // rows of d or of a piece of the vocabulary
+    // items of one launch, and 31-bit offsets in a tile's rows of d or of a piece
+    // of the vocabulary
     return ceil_div(n_tok, 256) * ceil_div(vocab, 256) < ((int64_t)1 << 22) &&
            ceil_div(n_tok, 256) * ceil_div(d, 256) < ((int64_t)1 << 18) && d <= (1 << 20) && vocab <= (1 << 22) &&
            n_tok <= (1 << 27);
 }
 
-void launch_loss(const LossArgs &a, hipStream_t s) {
+namespace {
+
+template <class E>
+void forward(const LossArgs &a, hipStream_t s) {
+    constexpr bool F32 = sizeof(E) == 4;
     const LossLayout L = loss_layout(a);
     char *ws = static_cast<char *>(a.ws);
     LseEnd end{a.scale, a.targets, reinterpret_cast<float *>(ws + L.xt), reinterpret_cast<float2 *>(ws + L.part), 0};
     GemmArgs g{};
-    g.M = a.n_tok;
-    g.K = a.d;
-    whole(g);
-    const int64_t d = a.d, V = a.vocab;
-    const int64_t piece = a.bf16 ? padded(V) : piece_for(V, d * 6);
-    const int tile = tile_for(a.n_tok, std::min(piece, V));
-    if (!a.bf16)
-        make_parts<float, 3>(a.h, a.n_tok, a.d, nullptr, 0, reinterpret_cast<uint16_t *>(ws + L.h), s);
+    const int64_t d = a.d, V = a.vocab, T = a.n_tok;
+    const bool parts = !F32 && !a.bf16;
+    g.M = T;
+    g.K = d;
+    whole<E>(g);
+    const bool bh = parts || blocks_h(a), bw = parts || blocks_w(a, true);
+    const int64_t piece = bw ? piece_for(V, round64(d) * (parts ? 6 : 2)) : padded(V);
+    const int tile = F32 ? 64 : tile_for(T, std::min(piece, V));
+    uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
+    if (bh) make_blocks(a, a.h, T, nullptr, h, nullptr, s);
+    g.a = bh ? blocks_of(h, T, d) : rows_of(a.h, T, d);
+    parts_of(g, parts ? 3 : 1, parts ? 3 : 1);
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         g.N = std::min(piece, V - v0);
         end.v0 = v0;
-        if (a.bf16) {
-            g.a = Operand{static_cast<const uint16_t *>(a.h), d, 0, a.n_tok};
-            g.b = Operand{static_cast<const uint16_t *>(a.w), d, 0, V};
-            parts_of(g, 1, 1);
-        } else {
-            uint16_t *w = reinterpret_cast<uint16_t *>(ws + L.w);
-            make_parts<float, 3>(static_cast<const float *>(a.w) + v0 * d, g.N, a.d, nullptr, 0, w, s);
-            g.a = Operand{reinterpret_cast<const uint16_t *>(ws + L.h), d, a.n_tok * d, a.n_tok};
-            g.b = Operand{w, d, g.N * d, g.N};
-            parts_of(g, 3, 3);
-        }
-        gemm<false, false>(g, end, tile, s);
+        const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
+        if (bw) make_blocks(a, rows, g.N, nullptr, w, nullptr, s);
+        g.b = bw ? blocks_of(w, g.N, d) : rows_of(rows, g.N, d);
+        gemm<E, false, false>(g, end, tile, s);
     }
-    const int64_t wave_cols = tile / 2;
-    launch_kernel(lse_join_kernel, dim3((unsigned)ceil_div(a.n_tok, 8)), dim3(256), s, end.part,
-                  ceil_div(V, tile) * (tile / wave_cols), a.n_tok, a.targets, a.vocab, end.xt, a.loss, a.lse);
+    launch_kernel(lse_join_kernel, dim3((unsigned)ceil_div(T, 8)), dim3(256), s, end.part, 2 * ceil_div(V, tile), T,
+                  a.targets, a.vocab, end.xt, a.loss, a.lse);
 }
 
-void launch_loss_bwd(const LossArgs &a, hipStream_t s) {
+template <class E>
+void backward(const LossArgs &a, hipStream_t s) {
+    constexpr bool F32 = sizeof(E) == 4;
     const LossLayout L = loss_bwd_layout(a);
     char *ws = static_cast<char *>(a.ws);
     const int64_t d = a.d, V = a.vocab, T = a.n_tok;
-    const int hp = a.bf16 ? 1 : 3, pp = a.bf16 ? (a.dw_bf16 ? 1 : 2) : 3;
-    uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *p = reinterpret_cast<uint16_t *>(ws + L.part);
+    const bool parts = !F32 && !a.bf16;
+    const int hp = parts ? 3 : 1, pp = F32 ? 1 : p_parts(a);
+    Token *token = reinterpret_cast<Token *>(ws + L.xt);
+    void *h = ws + L.h, *p = ws + L.part;
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.w);
     float *sum = reinterpret_cast<float *>(ws + L.sum), *wsum = reinterpret_cast<float *>(ws + L.wsum);
-    if (a.bf16)
-        make_parts<uint16_t, 1>(a.h, T, a.d, a.targets, a.vocab, h, s);
+    const bool bw = parts || blocks_w(a, false);
+    if constexpr (F32)
+        make_parts<float, float, 1>(a.h, T, a.d, &a, static_cast<float *>(h), token, s);
     else
-        make_parts<float, 3>(a.h, T, a.d, a.targets, a.vocab, h, s);
-    int64_t piece = piece_for(V, (int64_t)pp * T * 2);
-    if (!a.bf16) piece = std::min(piece, piece_for(V, d * 6));
+        make_blocks(a, a.h, T, &a, static_cast<uint16_t *>(h), token, s);
+    const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, T, d);
+    int64_t piece = piece_for(V, p_bytes(a) * round64(T));
+    if (bw) piece = std::min(piece, piece_for(V, round64(d) * (parts ? 6 : 2)));
     int32_t dh_splits = 1;
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
-        const int64_t n = std::min(piece, V - v0), ld = ceil_div(n, kStep) * kStep;
-        const Operand ph{p, ld, T * ld, T}, pw{p, ld, T * ld, ld};
-        Operand w{static_cast<const uint16_t *>(a.w) + v0 * d, d, 0, n};
-        if (!a.bf16) {
-            make_parts<float, 3>(static_cast<const float *>(a.w) + v0 * d, n, a.d, nullptr, 0, wp, s);
-            w = Operand{wp, d, n * d, n};
-        }
+        const int64_t n = std::min(piece, V - v0), ld = round64(n);
+        const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, T, n);
+        const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
+        if (bw) make_blocks(a, rows, n, nullptr, wp, nullptr, s);
+        const Operand ow = bw ? blocks_of(wp, n, d) : rows_of(rows, n, d);
         GemmArgs g{};
         {  // P
             g.M = T;
             g.N = n;
             g.K = d;
-            g.a = Operand{h, d, T * d, T};
-            g.b = w;
-            whole(g);
+            g.a = oh;
+            g.b = ow;
+            whole<E>(g);
             parts_of(g, hp, hp);
-            const GradEnd end{a.scale, a.dloss_scale, a.targets, a.lse, a.dloss, p, ld, pp, a.vocab, v0};
-            gemm<false, false>(g, end, tile_for(T, n), s);
+            const GradEnd end{a.scale, token, p, op.row64, op.part, ld, pp, v0};
+            gemm<E, false, false>(g, end, F32 ? 64 : tile_for(T, n), s);
         }
         if (a.dh) {
             g.M = T;
             g.N = d;
             g.K = n;
-            g.a = ph;
-            g.b = w;
-            g.b.rows = d;
-            parts_of(g, a.bf16 ? 1 : 3, hp);
-            const int tile = tile_for(T, d);
+            g.a = op;
+            g.b = ow;
+            parts_of(g, hp, hp);
+            const int64_t steps = ceil_div(n, step_of<E>());
+            const int tile = F32 ? 64 : tile_for(T, d, ceil_div(std::min(piece, V), step_of<E>()));
             // (the same split for every piece: its sums go on from one to the next)
             if (v0 == 0) {
-                split_k(g, tile, std::min(kMostSplits, sum_bytes(T, a.d) / (T * d * 4)));
+                split_k<E>(g, tile, std::min(kMostSplits, sum_bytes(T, a.d) / (T * d * 4)));
                 dh_splits = g.splits;
             } else {
-                const int64_t steps = ceil_div(n, kStep);
-                g.splits = dh_splits;
-                g.split_steps = (int32_t)ceil_div(steps, dh_splits);
-                g.splits = (int32_t)ceil_div(steps, g.split_steps);
+                split_steps(g, steps, dh_splits);
             }
             const SumEnd end{sum, d, T * d, false, v0 > 0};
-            gemm<false, true>(g, end, tile, s);
+            gemm<E, false, true>(g, end, tile, s);
         }
         if (a.dw) {
             g.M = n;
             g.N = d;
             g.K = T;
-            g.a = pw;
-            g.b = Operand{h, d, T * d, d};
+            g.a = op;
+            g.b = oh;
             parts_of(g, pp, hp);
-            const int tile = tile_for(n, d);
-            split_k(g, tile, std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4)));
+            const int tile = F32 ? 64 : tile_for(n, d, ceil_div(T, step_of<E>()));
+            split_k<E>(g, tile, std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4)));
             char *out = static_cast<char *>(a.dw) + v0 * d * (a.dw_bf16 ? 2 : 4);
-            const bool parts = g.splits > 1;
-            const SumEnd end{parts ? static_cast<void *>(wsum) : out, d, n * d, !parts && a.dw_bf16, !parts && a.accumulate};
-            gemm<true, true>(g, end, tile, s);
-            if (parts) {
+            const bool split = g.splits > 1;
+            const SumEnd end{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16, !split && a.accumulate};
+            gemm<E, true, true>(g, end, tile, s);
+            if (split) {
                 const dim3 grid((unsigned)std::min<int64_t>((n * d / 8 + 255) / 256, 1 << 20));
                 if (a.dw_bf16)
                     launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, wsum, g.splits, n * d, n, a.d,
@@ -819,6 +1153,22 @@ void launch_loss_bwd(const LossArgs &a, hipStream_t s) {
             launch_kernel(sum_join_kernel<float>, grid, dim3(256), s, sum, dh_splits, T * d, T, a.d, a.targets, a.vocab,
                           static_cast<float *>(a.dh), false);
     }
+}
+
+}  // namespace
+
+void launch_loss(const LossArgs &a, hipStream_t s) {
+    if (!a.bf16 && direct32(a))
+        forward<float>(a, s);
+    else
+        forward<uint16_t>(a, s);
+}
+
+void launch_loss_bwd(const LossArgs &a, hipStream_t s) {
+    if (!a.bf16 && direct32(a))
+        backward<float>(a, s);
+    else
+        backward<uint16_t>(a, s);
 }
 
 }  // namespace engram
