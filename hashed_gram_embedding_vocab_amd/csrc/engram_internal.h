@@ -442,7 +442,7 @@ struct LossArgs {
 };
 // Byte offsets in the workspace and its size; the size never falls as n_tok grows.
 struct LossLayout {
-    size_t xt, part, h, w, sum, wsum, total;
+    size_t xt, part, few, h, unit, w, sum, wsum, total;
 };
 LossLayout loss_layout(const LossArgs &a);
 LossLayout loss_bwd_layout(const LossArgs &a);

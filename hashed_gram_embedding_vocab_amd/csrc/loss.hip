@@ -244,6 +244,7 @@ struct Feed {
     }
 };
 
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
@@ -309,21 +310,45 @@ struct Reader {
 // Rows' maxima and sums of exponentials over the wave's columns, and the
 // targets' logits.
 struct LseEnd {
-    static constexpr bool kImage = false, kPairs = false;
+    static constexpr bool kImage = false, kPairs = false, kEarly = true;
     float scale;
     const int32_t *targets;
     float *xt;                 // [n_tok]
     float2 *part;              // [columns / (16 FN)][n_tok]
     int64_t v0;                // the first column's id
+    const float *a_unit, *b_unit;  // fp16 operands: the units of their rows
+    template <int FM>
+    struct Row {
+        int32_t id[FM];
+    };
+    template <int FM>
+    __device__ __forceinline__ Row<FM> rows(const GemmArgs &g, int64_t m0, int lane) const {
+        Row<FM> r;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) r.id[j] = targets[min(m0 + 16 * j + (lane & 15), g.M - 1)];
+        return r;
+    }
     template <class E, int FN, int FM>
-    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *, int64_t m0, int64_t n0, int,
-                                        int lane) const {
+    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], const Row<FM> &row, uint8_t *,
+                                        int64_t m0, int64_t n0, int, int lane) const {
         const int nl = 4 * (lane >> 4);
         int32_t y[FM];  // the target's column in the wave's, if it has one
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int64_t m = m0 + 16 * j + (lane & 15), at = (int64_t)targets[min(m, g.M - 1)] - v0 - n0;
+            const int64_t m = m0 + 16 * j + (lane & 15), at = (int64_t)row.id[j] - v0 - n0;
             y[j] = m < g.M && at >= 0 && at < 16 * FN && n0 + at < g.N ? (int32_t)at : -1;
+        }
+        if constexpr (std::is_same<E, _Float16>::value) {
+            float u[FM];
+#pragma unroll
+            for (int j = 0; j < FM; ++j) u[j] = a_unit[min(m0 + 16 * j + (lane & 15), g.M - 1)];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(b_unit + min(n0 + nl + 16 * i, (g.N - 1) & ~(int64_t)3));
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] *= v * u[j];
+                if (i % 2) __builtin_amdgcn_sched_barrier(0);  // (not all units' registers at once)
+            }
         }
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
@@ -387,29 +412,38 @@ struct Token {
 // A tile of P, in `parts` parts of bf16 in blocks, or in fp32 rows of ld: zeros
 // behind the vocabulary's end and for tokens that do not count.
 struct GradEnd {
-    static constexpr bool kImage = false, kPairs = true;
+    static constexpr bool kImage = false, kPairs = true, kEarly = false;
     float scale;
     const Token *token;        // [n_tok]
     void *p;
     int64_t row64, part, ld;   // blocks: as in their Operand, whole columns
     int32_t parts;
     int64_t v0;
+    template <int FM>
+    struct Row {
+        u32x4_t tok[FM];
+    };
+    template <int FM>
+    __device__ __forceinline__ Row<FM> rows(const GemmArgs &g, int64_t m0, int lane) const {
+        Row<FM> r;
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            r.tok[j] = *reinterpret_cast<const u32x4_t *>(token + min(m0 + 16 * j + (lane & 15), g.M - 1));
+        return r;
+    }
     template <class E, int FN, int FM>
-    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *, int64_t m0, int64_t n0,
-                                        int, int lane) const {
+    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], const Row<FM> &row, uint8_t *,
+                                        int64_t m0, int64_t n0, int, int lane) const {
         constexpr bool PAIRS = sizeof(E) == 2;
         // this lane's columns: nl + col(i) + r
         const int64_t nl = n0 + (PAIRS ? 8 : 4) * (lane >> 4);
         auto col = [](int i) { return PAIRS ? (i >> 1) * 32 + (i & 1) * 4 : i * 16; };
-        u32x4_t tok[FM];
-#pragma unroll
-        for (int j = 0; j < FM; ++j)
-            tok[j] = *reinterpret_cast<const u32x4_t *>(token + min(m0 + 16 * j + (lane & 15), g.M - 1));
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int64_t m = m0 + 16 * j + (lane & 15);
-            const float l = __uint_as_float(tok[j][0]), f = m < g.M ? __uint_as_float(tok[j][1]) : 0.f;
-            const int64_t y = (int64_t)(int32_t)tok[j][2] - v0 - nl;
+            const u32x4_t &tok = row.tok[j];
+            const float l = __uint_as_float(tok[0]), f = m < g.M ? __uint_as_float(tok[1]) : 0.f;
+            const int64_t y = (int64_t)(int32_t)tok[2] - v0 - nl;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -516,13 +550,37 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[FN][FM], uint8_t
 // The sums themselves: fp32 (a split's at `split_elems` from the one before), or
 // bf16; over what is there or added to it.
 struct SumEnd {
-    static constexpr bool kImage = true, kPairs = false;
+    static constexpr bool kImage = true, kPairs = false, kEarly = false;
     void *c;
     int64_t ld, split_elems;
     bool bf16, accumulate;
+    const int32_t *targets;    // given: rows of tokens that do not count are zeros
+    int32_t vocab;
+    template <int FM>
+    struct Row {
+        bool counts[FM];
+    };
+    template <int FM>
+    __device__ __forceinline__ Row<FM> rows(const GemmArgs &g, int64_t m0, int lane) const {
+        Row<FM> r;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            r.counts[j] = true;
+            if (targets) {
+                const int32_t id = targets[min(m0 + 16 * j + (lane & 15), g.M - 1)];
+                r.counts[j] = id >= 0 && id < vocab;
+            }
+        }
+        return r;
+    }
     template <class E, int FN, int FM>
-    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], uint8_t *img, int64_t m0, int64_t n0,
-                                        int split, int lane) const {
+    __device__ __forceinline__ void run(const GemmArgs &g, f32x4_t (&acc)[FN][FM], const Row<FM> &row, uint8_t *img,
+                                        int64_t m0, int64_t n0, int split, int lane) const {
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            if (!row.counts[j])
+#pragma unroll
+                for (int i = 0; i < FN; ++i) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if (bf16) {
             store_rows<FN, FM>(acc, img, static_cast<uint16_t *>(c), ld, g.M, g.N, m0, n0, lane, accumulate);
             return;
@@ -602,7 +660,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
     const Reader<E, T, BX, PAIRS> rb(lane);
     const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
 
-    f32x4_t acc[FN][FM] = {};
+    // (64 x 64: sums of their own for each half of a stage, in fp32 for each
+    // instruction of it, so that long rows round less)
+    constexpr int SETS = T != 64 ? 1 : sizeof(E) == 2 ? 2 : 8;
+    f32x4_t acc[SETS][FN][FM] = {};
     struct Half {
         u32x4_t a[FM], b[FN];
     };
@@ -613,14 +674,21 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 #pragma unroll
         for (int i = 0; i < FN; ++i) h.b[i] = rb.template read<H>(stb, wn + i);
     };
-    auto multiply = [&](const Half &h) {
+    auto multiply = [&](const Half &h, auto hc) {
+        constexpr int H = decltype(hc)::value;
         if constexpr (sizeof(E) == 2) {
+            f32x4_t(&sum)[FN][FM] = acc[SETS > 1 ? H : 0];
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
-                for (int j = 0; j < FM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, h.b[i]),
-                                                                        __builtin_bit_cast(bf16x8_t, h.a[j]), acc[i][j], 0, 0, 0);
+                for (int j = 0; j < FM; ++j) {
+                    if constexpr (std::is_same<E, _Float16>::value)
+                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, h.b[i]),
+                                                                           __builtin_bit_cast(f16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
+                    else
+                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, h.b[i]),
+                                                                            __builtin_bit_cast(bf16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
+                }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -628,8 +696,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
                 for (int i = 0; i < FN; ++i)
 #pragma unroll
                     for (int j = 0; j < FM; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]),
-                                                                         acc[i][j], 0, 0, 0);
+                        acc[4 * H + e][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            __uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]), acc[4 * H + e][i][j], 0, 0, 0);
         }
     };
     // (kAhead loads a wave may be in flight at a step's barrier.  The last fills
@@ -666,7 +734,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         constexpr bool SET = T == 256;
         constexpr int kReads = (AX ? 2 : 1) * FM + (BX ? 2 : 1) * FN, kMul = FM * FN;
         read(cur_a, cur_b, h1, hi);
-        multiply(h0);
+        multiply(h0, lo);
         if constexpr (SET) {
             spread<0x100, kReads, kMul - 8>();
             __builtin_amdgcn_sched_barrier(0);
@@ -675,7 +743,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         if constexpr (SET) __builtin_amdgcn_sched_barrier(0);
         fill(cur_b, cur_a);
         read(next_a, next_b, h0, lo);
-        multiply(h1);
+        multiply(h1, hi);
         if constexpr (SET) {
             spread<0x20, 2 * kL, 4 * kL>();
             spread<0x100, kReads, kMul - 4 * kL>();
@@ -688,6 +756,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         int split;
         it.origin(item, n0, m0, split);
         left = steps_in<E>(g, split) * g.segs;
+        // (a tile's rows are asked for ahead of its stages, whose waits then cover
+        // them: behind them they would wait for the next tile's first stages.  The
+        // 256 x 256 tile of P has no registers left for that.)
+        constexpr bool EARLY = End::kEarly || T != 256;
+        typename End::template Row<FM> row;
+        if constexpr (EARLY) row = end.template rows<FM>(g, m0 + wm * 16, lane);
         for (;;) {  // (whole rounds of the stages, or one item; a leg is a round at least)
             if constexpr (NA == 2) {
                 step(a0, b0, a1, b1);
@@ -719,12 +793,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         constexpr int kImage = FM * 16 * FN * 32, kImages = kStage / kImage;
         static_assert(kImages * 4 >= W, "the waves' images in four stages");
         uint8_t *const home = wave / kImages == 0 ? b0 : wave / kImages == 1 ? b1 : wave / kImages == 2 ? a0 : a1;
-        end.template run<E, FN, FM>(g, acc, home + wave % kImages * kImage, m0 + wm * 16, n0 + wn * 16, split, lane);
+        if constexpr (!EARLY) row = end.template rows<FM>(g, m0 + wm * 16, lane);
+#pragma unroll
+        for (int q = SETS / 2; q > 0; q /= 2)
+#pragma unroll
+            for (int z = 0; z < q; ++z)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) acc[z][i][j] += acc[z + q][i][j];
+        end.template run<E, FN, FM>(g, acc[0], row, home + wave % kImages * kImage, m0 + wm * 16, n0 + wn * 16, split, lane);
         if constexpr (End::kImage) return;
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+        for (int z = 0; z < SETS; ++z)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[z][i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         read(a0, b0, h0, lo);  // (once more: its registers are free while the tile ends)
     }
     wait_loads();  // (the last fills land before the workgroup's LDS is given away)
@@ -750,7 +835,7 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
             const int32_t id = targets[r];
             counts = id >= 0 && id < vocab;
             if (token && c == 0)
-                token[r] = Token{lse[r], counts ? (dloss ? dloss[r] : 1.f) * factor : 0.f, id, 0};
+                token[r] = counts ? Token{lse[r], (dloss ? dloss[r] : 1.f) * factor, id, 0} : Token{0.f, 0.f, -1, 0};
         }
         F8 v = {};
         if (counts && c < d) v = load8(x + r * d + c);
@@ -769,33 +854,152 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
     }
 }
 
-// lse and loss of 8 tokens a workgroup, their parts (maxima in powers of two)
-// shared by 32 lanes each.
+// Two fp16 parts of x's rows over their units, in blocks: a row's unit is the power
+// of two over which its largest value lies in [2^14, 2^15), so that the parts hold
+// 22 bits of whatever is not below 2^-18 of that, and 2^-40 of it otherwise.  One
+// wave a row.
+__global__ __launch_bounds__(256) void half_parts_kernel(const float *x, int64_t rows, int32_t d, _Float16 *out,
+                                                         float *unit) {
+    const int lane = threadIdx.x & 63;
+    const int32_t cols = (d + kBlock - 1) / kBlock * kBlock;
+    const int64_t all = (rows + kBlock - 1) / kBlock * kBlock;
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < all; r += (int64_t)gridDim.x * 4) {
+        uint32_t top = 0u;
+        if (r < rows)
+            for (int32_t c = lane * 8; c < d; c += 512) {
+                const F8 v = load8(x + r * d + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t b = __float_as_uint(v.v[i]) & 0x7FFFFFFFu;
+                    top = max(top, b < 0x7F800000u ? b : 0u);
+                }
+            }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+        // exponents of the unit and its inverse, both normal numbers
+        const int e = min(max((int)(top >> 23) - 14, 1), 253);
+        const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+        if (lane == 0) unit[r] = __uint_as_float((uint32_t)e << 23);
+        for (int32_t c = lane * 8; c < cols; c += 512) {
+            F8 v = {};
+            if (r < rows && c < d) v = load8(x + r * d + c);
+            h8 p0, p1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = v.v[i] * inv;
+                p0[i] = (_Float16)y;
+                p1[i] = (_Float16)(y - (float)p0[i]);
+            }
+            _Float16 *to = out + block_at(r, c, (int64_t)cols * kBlock);
+            *reinterpret_cast<h8 *>(to) = p0;
+            *reinterpret_cast<h8 *>(to + all * cols) = p1;
+        }
+    }
+}
+
+// The largest and the sum of 256 / TB threads' values for each of TB tokens (a
+// token's threads lie TB apart); every thread gets them.
+template <int TB, bool MAX>
+__device__ __forceinline__ float join_threads(float x, float (&red)[256]) {
+    red[threadIdx.x] = x;
+    __syncthreads();
+#pragma unroll
+    for (int n = 128; n >= TB; n >>= 1) {
+        if ((int)threadIdx.x < n) {
+            const float a = red[threadIdx.x], b = red[threadIdx.x + n];
+            red[threadIdx.x] = MAX ? fmaxf(a, b) : a + b;
+        }
+        __syncthreads();
+    }
+    x = red[threadIdx.x % TB];
+    __syncthreads();
+    return x;
+}
+
+__device__ __forceinline__ void store_loss(int64_t t, float top2, float sum, int32_t id, int32_t vocab, float x_y,
+                                           float *loss, float *lse) {
+    const bool counts = id >= 0 && id < vocab;
+    const float l = (float)((top2 == -INFINITY ? 0. : (double)top2 * 0.69314718055994530942) + (double)logf(sum));
+    loss[t] = counts ? l - x_y : 0.f;
+    lse[t] = counts ? l : 0.f;
+}
+
+// lse and loss of TB tokens a workgroup from their parts (maxima in powers of two).
+template <int TB>
 __global__ __launch_bounds__(256) void lse_join_kernel(const float2 *part, int64_t n_parts, int64_t n_tok,
                                                        const int32_t *targets, int32_t vocab, const float *xt, float *loss,
                                                        float *lse) {
-    __shared__ float2 red[32][8];
-    const int tl = threadIdx.x & 7, sl = threadIdx.x >> 3;
-    const int64_t t = (int64_t)blockIdx.x * 8 + tl, tc = min(t, n_tok - 1);
+    __shared__ float red[256];
+    const int64_t t = (int64_t)blockIdx.x * TB + threadIdx.x % TB, tc = min(t, n_tok - 1);
     float top = -INFINITY, sum = 0.f;
-    auto add = [&](float2 p) {
-        const float m = fmaxf(top, p.x), from = m == -INFINITY ? 0.f : m;
-        sum = sum * __builtin_amdgcn_exp2f(top - from) + p.y * __builtin_amdgcn_exp2f(p.x - from);
-        top = m;
-    };
 #pragma unroll 8
-    for (int64_t i = sl; i < n_parts; i += 32) add(part[i * n_tok + tc]);
-    red[sl][tl] = float2{top, sum};
-    __syncthreads();
-    if (threadIdx.x >= 8 || t >= n_tok) return;
-    top = -INFINITY;
-    sum = 0.f;
-    for (int i = 0; i < 32; ++i) add(red[i][tl]);
-    const int32_t id = targets[t];
-    const bool counts = id >= 0 && id < vocab;
-    const float l = (float)((top == -INFINITY ? 0. : (double)top * 0.69314718055994530942) + (double)logf(sum));
-    loss[t] = counts ? l - xt[t] : 0.f;
-    lse[t] = counts ? l : 0.f;
+    for (int64_t i = threadIdx.x / TB; i < n_parts; i += 256 / TB) top = fmaxf(top, part[i * n_tok + tc].x);
+    top = join_threads<TB, true>(top, red);
+    const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x / TB; i < n_parts; i += 256 / TB) {
+        const float2 p = part[i * n_tok + tc];
+        sum += p.y * __builtin_amdgcn_exp2f(p.x - from);
+    }
+    sum = join_threads<TB, false>(sum, red);
+    if (threadIdx.x < TB && t < n_tok) store_loss(t, top, sum, targets[t], vocab, xt[t], loss, lse);
+}
+
+// From logits in memory (a few tokens of a small vocabulary): the sums of the
+// splits of K, in order.
+__device__ __forceinline__ float few_logit(const float *x, int64_t at, int32_t splits, int64_t split_elems) {
+    float v = x[at];
+    for (int32_t z = 1; z < splits; ++z) v += x[z * split_elems + at];
+    return v;
+}
+
+// One workgroup a token.
+__global__ __launch_bounds__(256) void few_loss_kernel(const float *x, int32_t splits, int64_t split_elems, int64_t ld,
+                                                       int32_t vocab, float scale, const int32_t *targets, float *loss,
+                                                       float *lse) {
+    __shared__ float red[256];
+    const int64_t t = blockIdx.x;
+    float top = -INFINITY, sum = 0.f;
+    for (int32_t v = threadIdx.x; v < vocab; v += 256)
+        top = fmaxf(top, few_logit(x, t * ld + v, splits, split_elems) * scale);
+    top = join_threads<1, true>(top, red);
+    const float from = top == -INFINITY ? 0.f : top;
+    for (int32_t v = threadIdx.x; v < vocab; v += 256)
+        sum += __builtin_amdgcn_exp2f((few_logit(x, t * ld + v, splits, split_elems) * scale - from) * kLog2e);
+    sum = join_threads<1, false>(sum, red);
+    if (threadIdx.x == 0) {
+        const int32_t id = targets[t];
+        const float l = from + logf(sum);
+        const bool counts = id >= 0 && id < vocab;
+        loss[t] = counts ? l - few_logit(x, t * ld + id, splits, split_elems) * scale : 0.f;
+        lse[t] = counts ? l : 0.f;
+    }
+}
+
+// P of a few tokens: as GradEnd writes it.
+__global__ __launch_bounds__(256) void few_grad_kernel(const float *x, int32_t splits, int64_t split_elems, int64_t ldx,
+                                                       int64_t n_tok, int32_t vocab, float scale, const Token *token,
+                                                       void *p, int64_t row64, int64_t part, int64_t ld, int32_t parts,
+                                                       bool f32) {
+    const int64_t rows = f32 ? n_tok : (n_tok + kBlock - 1) / kBlock * kBlock;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / ld, v = i - t * ld;
+    if (t >= rows) return;
+    float y = 0.f;
+    if (t < n_tok && v < vocab) {
+        const Token k = token[t];
+        y = __builtin_amdgcn_exp2f(fmaf(few_logit(x, t * ldx + v, splits, split_elems), scale, -k.lse) * kLog2e);
+        if (v == k.target) y -= 1.f;
+        y = k.factor == 0.f ? 0.f : y * k.factor;
+    }
+    if (f32) {
+        static_cast<float *>(p)[t * ld + v] = y;
+        return;
+    }
+    for (int32_t q = 0; q < parts; ++q) {
+        static_cast<__bf16 *>(p)[q * part + block_at(t, v, row64)] = (__bf16)y;
+        y -= (float)(__bf16)y;
+    }
 }
 
 // out[m][i] (+)= sum over the splits, in order, rounded to the output's type;
@@ -834,15 +1038,52 @@ constexpr int64_t step_of() {
     return 128 / (int64_t)sizeof(E);
 }
 
-// How an M x N product is tiled: 256 x 256 where such tiles (or they and parts of
-// K of at least eight stages, where K may be split) come to about one workgroup
-// a CU, else 64 x 64 while those fit the chip at once or M is that short, and
-// 128 x 128 beyond.  fp32 tiles are 64 x 64.
-int tile_for(int64_t M, int64_t N, int64_t k_steps = 0) {
-    auto tiles = [&](int64_t t) { return ((N + t - 1) / t) * ((M + t - 1) / t); };
-    const int64_t wide = tiles(256), parts = std::max<int64_t>(1, std::min<int64_t>(256 / wide, k_steps / 8));
-    if (std::min(M, k_steps ? N : M) > 128 && wide * parts >= 192) return 256;
-    return M <= 64 || tiles(64) <= 512 ? 64 : 128;
+// How a product is cut: square tiles, and parts of K.  The tile and the parts are
+// those that should take least, by what a stage takes on a CU (measured, us): 1.48
+// with one workgroup of 256 x 256, 0.92 with two of 128 x 128 (0.62 with one),
+// 0.44 with two of 64 x 64 (0.30), and at its start and end a few us more, which
+// grow with the bytes of a result.  (A 256 x 256 tile's 1.33 PFLOP/s are 1.05 of
+// 128 x 128 and 0.53 of 64 x 64; but 96 tiles of 64 x 64 are six of 256 x 256.)
+// Parts of K cost a second launch that joins them.  fp32 tiles are 64 x 64.
+struct Cut {
+    int tile;
+    int64_t splits;
+    double cost;
+};
+
+// (the parts of a token's sums, whose number goes with the tile, stay few: loss_layout)
+bool may_tile(int tile, int64_t M, int64_t N) {
+    const int64_t items = ceil_div(M, tile) * ceil_div(N, tile);
+    return tile == 256 || (tile == 128 ? items <= 2048 : M <= 64 || items <= 1024);
+}
+
+template <class E>
+Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_bytes) {
+    struct Rate {
+        int tile;
+        double one, two, start1, start2, byte1, byte2;
+    };
+    static constexpr Rate kRates[3] = {{64, 0.30, 0.44, 3., 4., 0.25, 0.5},
+                                       {128, 0.62, 0.92, 5., 6., 0.7, 1.3},
+                                       {256, 1.48, 1.48, 5., 5., 2.3, 2.3}};
+    Cut best{64, 1, 1e30};
+    const int64_t steps = ceil_div(K, step_of<E>());
+    for (const Rate &r : kRates) {
+        if (!may_tile(r.tile, M, N) || (sizeof(E) == 4 && r.tile != 64)) continue;
+        // (an fp32 stage: 32 k at a sixteenth of the bf16 rate)
+        const double one = sizeof(E) == 4 ? 0.5 : r.one, two = sizeof(E) == 4 ? 0.95 : r.two;
+        const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
+        for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
+            const int64_t items = tiles * n, full = items / slots, rest = items % slots;
+            const double each = (double)(ceil_div(ceil_div(steps, n), 4) * 4 * segs);
+            const int bytes = n > 1 ? 4 : out_bytes;
+            double t = (double)full * (each * two + r.start2 + r.byte2 * bytes);
+            if (rest > 0) t += rest <= 256 ? each * one + r.start1 + r.byte1 * bytes : each * two + r.start2 + r.byte2 * bytes;
+            if (n > 1) t += 4. + (double)(n * M) * (double)N * 4. / 4.5e6;
+            if (t < best.cost * 0.98) best = Cut{r.tile, n, t};
+        }
+    }
+    return best;
 }
 
 template <class E, bool AX, bool BX, class End>
@@ -912,29 +1153,10 @@ void split_steps(GemmArgs &g, int64_t steps, int64_t n) {
     g.splits = (int32_t)ceil_div(steps, per);
 }
 
-// Parts of K for a product of few tiles: as many as fill the chip's slots (one
-// 256 x 256 tile a CU, two of the others) evenly, of at least eight stages.
-template <class E>
-void split_k(GemmArgs &g, int tile, int64_t most) {
-    const int64_t tiles = ceil_div(g.M, tile) * ceil_div(g.N, tile), steps = ceil_div(g.K, step_of<E>());
-    const int64_t slots = tile == 256 ? 256 : 512;
-    most = std::min<int64_t>({most, steps / 8, tiles >= 8 * slots ? 1 : 8 * slots / tiles});
-    int64_t best = 1;
-    double best_cost = 1e30;
-    for (int64_t s = 1; s <= most; ++s) {
-        // rounds of the chip times a tile's stages, and a dozen stages' worth for its start and end
-        const double cost = (double)ceil_div(tiles * s, slots) * ((double)ceil_div(steps, s) + 12.);
-        if (cost < best_cost * 0.97) {
-            best_cost = cost;
-            best = s;
-        }
-    }
-    split_steps(g, steps, best);
-}
-
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;     // of P, and of W's parts, at a time
 constexpr int64_t kSumBytes = (int64_t)512 << 20;     // of dh's sums in several splits
-constexpr int64_t kMostSplits = 16;
+constexpr int64_t kMostSplits = 64;
+constexpr int64_t kFewBytes = (int64_t)32 << 20;      // of a few tokens' logits in several splits
 
 int64_t padded(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
 
@@ -961,9 +1183,12 @@ int64_t weight_sum_bytes(int64_t vocab, int32_t d) { return std::min<int64_t>((i
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Whether an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
-// of the bf16 ones' rate, or in six products of bf16 parts: those need W's parts
-// made first.
-bool direct32(const LossArgs &a) { return a.n_tok <= 128; }
+// of the bf16 ones' rate, or as products of parts (three of fp16 parts forward, six of
+// bf16 parts backward): those need W's parts made first, and take more stages.
+bool direct32(const LossArgs &a, bool forward) {
+    const int64_t T = a.n_tok, V = a.vocab;
+    return forward ? T * V <= 135 * V + 1100000 : T * V <= 333 * V + 6750000;
+}
 
 // Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
 // d = 2560 put a stage's 256 lines on four of an L2's sixteen channels; in blocks
@@ -975,7 +1200,22 @@ bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (fo
 
 // Parts of P, and bytes of P for a token and column.
 int p_parts(const LossArgs &a) { return a.bf16 && a.dw_bf16 ? 1 : 3; }
-int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a) ? 4 : 2 * p_parts(a); }
+int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a, false) ? 4 : 2 * p_parts(a); }
+
+int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t few_bytes(const LossArgs &a) { return std::min(kFewBytes, kMostSplits * a.n_tok * round8(a.vocab) * 4); }
+
+// A few tokens of a small vocabulary: the logits in parts of K, where that is
+// faster than whole rows by the tiles there are (122 tokens x 75 x 7680 in fp32: two
+// workgroups would do 240 stages each).  splits 1: not.
+template <class E>
+Cut few_cut(const LossArgs &a, const GemmArgs &g, int out_bytes) {
+    Cut whole = cut_for<E>(g.M, g.N, g.K, g.segs, 1, out_bytes);
+    const int64_t one = a.n_tok * round8(a.vocab) * 4;
+    if (one > kFewBytes / 2 || ceil_div(g.M, 64) * ceil_div(g.N, 64) > 128) return whole;
+    const Cut parts = cut_for<E>(g.M, g.N, g.K, g.segs, few_bytes(a) / one, 4);
+    return parts.splits > 1 && parts.cost + 5. < whole.cost ? parts : whole;
+}
 
 }  // namespace
 
@@ -993,11 +1233,15 @@ LossLayout loss_layout(const LossArgs &a) {
         return (size_t)o;
     };
     L.xt = take(T * 4);
-    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 128) * n32, std::min<int64_t>(T * n32, 512 * 128 * 4),
-                                std::min<int64_t>(T, 128) * n64, std::min<int64_t>(T * n64, 192 * 1024 * 4)}));
-    const int64_t each = a.bf16 ? 2 : 6;
-    if (a.bf16 ? blocks_h(a) : !direct32(a)) L.h = take(each * round64(T) * round64(a.d));
-    if (a.bf16 ? blocks_w(a, true) : !direct32(a)) L.w = take(piece_bytes(a.vocab, round64(a.d) * each));
+    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2),
+                                std::min<int64_t>(T * n64, 2048 * 128 * 2)}));
+    L.few = take(few_bytes(a));
+    const int64_t each = a.bf16 ? 2 : 4;
+    if (a.bf16 ? blocks_h(a) : !direct32(a, true)) {
+        L.h = take(each * round64(T) * round64(a.d));
+        L.unit = take(4 * (round64(T) + padded(a.vocab)));
+    }
+    if (a.bf16 ? blocks_w(a, true) : !direct32(a, true)) L.w = take(piece_bytes(a.vocab, round64(a.d) * each));
     L.total = (size_t)off;
     return L;
 }
@@ -1010,12 +1254,14 @@ LossLayout loss_bwd_layout(const LossArgs &a) {
         off = round256(off + bytes);
         return (size_t)o;
     };
+    const bool direct = !a.bf16 && direct32(a, false);
     L.xt = take(a.n_tok * (int64_t)sizeof(Token));
-    L.h = take((a.bf16 ? 2 : direct32(a) ? 4 : 6) * round64(a.n_tok) * round64(a.d));
+    L.h = take((a.bf16 ? 2 : direct ? 4 : 6) * round64(a.n_tok) * round64(a.d));
     L.part = take(piece_bytes(a.vocab, p_bytes(a) * round64(a.n_tok)));
     L.sum = take(sum_bytes(a.n_tok, a.d));
     L.wsum = take(weight_sum_bytes(a.vocab, a.d));
-    if (a.bf16 ? blocks_w(a, false) : !direct32(a)) L.w = take(piece_bytes(a.vocab, round64(a.d) * (a.bf16 ? 2 : 6)));
+    L.few = take(few_bytes(a));
+    if (a.bf16 ? blocks_w(a, false) : !direct) L.w = take(piece_bytes(a.vocab, round64(a.d) * (a.bf16 ? 2 : 6)));
     L.total = (size_t)off;
     return L;
 }
@@ -1032,33 +1278,60 @@ namespace {
 
 template <class E>
 void forward(const LossArgs &a, hipStream_t s) {
-    constexpr bool F32 = sizeof(E) == 4;
+    constexpr bool F32 = sizeof(E) == 4, F16 = std::is_same<E, _Float16>::value;
     const LossLayout L = loss_layout(a);
     char *ws = static_cast<char *>(a.ws);
-    LseEnd end{a.scale, a.targets, reinterpret_cast<float *>(ws + L.xt), reinterpret_cast<float2 *>(ws + L.part), 0};
-    GemmArgs g{};
     const int64_t d = a.d, V = a.vocab, T = a.n_tok;
-    const bool parts = !F32 && !a.bf16;
+    GemmArgs g{};
     g.M = T;
     g.K = d;
-    whole<E>(g);
-    const bool bh = parts || blocks_h(a), bw = parts || blocks_w(a, true);
-    const int64_t piece = bw ? piece_for(V, round64(d) * (parts ? 6 : 2)) : padded(V);
-    const int tile = F32 ? 64 : tile_for(T, std::min(piece, V));
+    parts_of(g, F16 ? 2 : 1, F16 ? 2 : 1);
+    const bool bh = F16 || (!F32 && blocks_h(a)), bw = F16 || (!F32 && blocks_w(a, true));
+    const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
-    if (bh) make_blocks(a, a.h, T, nullptr, h, nullptr, s);
+    float *h_unit = reinterpret_cast<float *>(ws + L.unit), *w_unit = h_unit + round64(T);
+    auto copy = [&](const void *x, int64_t rows, uint16_t *out, float *unit) {
+        if constexpr (F16)
+            launch_kernel(half_parts_kernel, dim3((unsigned)std::min<int64_t>(round64(rows) / 4, 1 << 20)), dim3(256), s,
+                          static_cast<const float *>(x), rows, a.d, reinterpret_cast<_Float16 *>(out), unit);
+        else
+            make_blocks(a, x, rows, nullptr, out, nullptr, s);
+    };
+    g.N = std::min(piece, V);
+    const Cut few = F16 ? cut_for<E>(T, g.N, d, g.segs, 1, 0) : few_cut<E>(a, g, 0);
+    if (bh) copy(a.h, T, h, h_unit);
     g.a = bh ? blocks_of(h, T, d) : rows_of(a.h, T, d);
-    parts_of(g, parts ? 3 : 1, parts ? 3 : 1);
+    if constexpr (!F16) {
+        if (few.splits > 1) {
+            float *x = reinterpret_cast<float *>(ws + L.few);
+            const int64_t ld = round8(V);
+            g.b = rows_of(a.w, V, d);
+            split_steps(g, ceil_div(d, step_of<E>()), few.splits);
+            gemm<E, false, false>(g, SumEnd{x, ld, T * ld, false, false, nullptr, 0}, few.tile, s);
+            launch_kernel(few_loss_kernel, dim3((unsigned)T), dim3(256), s, x, g.splits, T * ld, ld, a.vocab, a.scale,
+                          a.targets, a.loss, a.lse);
+            return;
+        }
+    }
+    whole<E>(g);
+    LseEnd end{a.scale, a.targets, reinterpret_cast<float *>(ws + L.xt), reinterpret_cast<float2 *>(ws + L.part), 0,
+               h_unit, w_unit};
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         g.N = std::min(piece, V - v0);
         end.v0 = v0;
         const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
-        if (bw) make_blocks(a, rows, g.N, nullptr, w, nullptr, s);
+        if (bw) copy(rows, g.N, w, w_unit);
         g.b = bw ? blocks_of(w, g.N, d) : rows_of(rows, g.N, d);
-        gemm<E, false, false>(g, end, tile, s);
+        gemm<E, false, false>(g, end, few.tile, s);
     }
-    launch_kernel(lse_join_kernel, dim3((unsigned)ceil_div(T, 8)), dim3(256), s, end.part, 2 * ceil_div(V, tile), T,
-                  a.targets, a.vocab, end.xt, a.loss, a.lse);
+    // (a workgroup a token where its parts are many and tokens are few)
+    const int64_t n_parts = 2 * ceil_div(V, few.tile);
+    if (T <= 256 && n_parts >= 256)
+        launch_kernel(lse_join_kernel<1>, dim3((unsigned)T), dim3(256), s, end.part, n_parts, T, a.targets, a.vocab, end.xt,
+                      a.loss, a.lse);
+    else
+        launch_kernel(lse_join_kernel<8>, dim3((unsigned)ceil_div(T, 8)), dim3(256), s, end.part, n_parts, T, a.targets,
+                      a.vocab, end.xt, a.loss, a.lse);
 }
 
 template <class E>
@@ -1073,7 +1346,7 @@ void backward(const LossArgs &a, hipStream_t s) {
     void *h = ws + L.h, *p = ws + L.part;
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.w);
     float *sum = reinterpret_cast<float *>(ws + L.sum), *wsum = reinterpret_cast<float *>(ws + L.wsum);
-    const bool bw = parts || blocks_w(a, false);
+    const bool bw = parts || (!F32 && blocks_w(a, false));
     if constexpr (F32)
         make_parts<float, float, 1>(a.h, T, a.d, &a, static_cast<float *>(h), token, s);
     else
@@ -1081,7 +1354,8 @@ void backward(const LossArgs &a, hipStream_t s) {
     const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, T, d);
     int64_t piece = piece_for(V, p_bytes(a) * round64(T));
     if (bw) piece = std::min(piece, piece_for(V, round64(d) * (parts ? 6 : 2)));
-    int32_t dh_splits = 1;
+    const bool one_piece = piece >= V;
+    Cut cut_h{};
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         const int64_t n = std::min(piece, V - v0), ld = round64(n);
         const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, T, n);
@@ -1095,10 +1369,19 @@ void backward(const LossArgs &a, hipStream_t s) {
             g.K = d;
             g.a = oh;
             g.b = ow;
-            whole<E>(g);
             parts_of(g, hp, hp);
-            const GradEnd end{a.scale, token, p, op.row64, op.part, ld, pp, v0};
-            gemm<E, false, false>(g, end, F32 ? 64 : tile_for(T, n), s);
+            const Cut few = one_piece ? few_cut<E>(a, g, F32 ? 4 : 2 * pp) : cut_for<E>(T, n, d, g.segs, 1, F32 ? 4 : 2 * pp);
+            if (few.splits > 1) {
+                float *x = reinterpret_cast<float *>(ws + L.few);
+                const int64_t ldx = round8(V);
+                split_steps(g, ceil_div(d, step_of<E>()), few.splits);
+                gemm<E, false, false>(g, SumEnd{x, ldx, T * ldx, false, false, nullptr, 0}, few.tile, s);
+                launch_kernel(few_grad_kernel, dim3((unsigned)ceil_div((F32 ? T : round64(T)) * ld, 256)), dim3(256), s, x,
+                              g.splits, T * ldx, ldx, T, a.vocab, a.scale, token, p, op.row64, op.part, ld, pp, F32);
+            } else {
+                whole<E>(g);
+                gemm<E, false, false>(g, GradEnd{a.scale, token, p, op.row64, op.part, ld, pp, v0}, few.tile, s);
+            }
         }
         if (a.dh) {
             g.M = T;
@@ -1107,17 +1390,15 @@ void backward(const LossArgs &a, hipStream_t s) {
             g.a = op;
             g.b = ow;
             parts_of(g, hp, hp);
-            const int64_t steps = ceil_div(n, step_of<E>());
-            const int tile = F32 ? 64 : tile_for(T, d, ceil_div(std::min(piece, V), step_of<E>()));
-            // (the same split for every piece: its sums go on from one to the next)
-            if (v0 == 0) {
-                split_k<E>(g, tile, std::min(kMostSplits, sum_bytes(T, a.d) / (T * d * 4)));
-                dh_splits = g.splits;
-            } else {
-                split_steps(g, steps, dh_splits);
-            }
-            const SumEnd end{sum, d, T * d, false, v0 > 0};
-            gemm<E, false, true>(g, end, tile, s);
+            // (the same cut for every piece: its sums go on from one to the next)
+            if (v0 == 0)
+                cut_h = cut_for<E>(T, d, n, g.segs, std::min(kMostSplits, sum_bytes(T, a.d) / (T * d * 4)), a.bf16 ? 2 : 4);
+            split_steps(g, ceil_div(n, step_of<E>()), cut_h.splits);
+            if (v0 == 0) cut_h.splits = g.splits;
+            if (one_piece && cut_h.splits == 1)
+                gemm<E, false, true>(g, SumEnd{a.dh, d, 0, a.bf16, false, a.targets, a.vocab}, cut_h.tile, s);
+            else
+                gemm<E, false, true>(g, SumEnd{sum, d, T * d, false, v0 > 0, nullptr, 0}, cut_h.tile, s);
         }
         if (a.dw) {
             g.M = n;
@@ -1126,12 +1407,13 @@ void backward(const LossArgs &a, hipStream_t s) {
             g.a = op;
             g.b = oh;
             parts_of(g, pp, hp);
-            const int tile = F32 ? 64 : tile_for(n, d, ceil_div(T, step_of<E>()));
-            split_k<E>(g, tile, std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4)));
+            const Cut cut = cut_for<E>(n, d, T, g.segs, std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4)),
+                                       a.dw_bf16 ? 2 : 4);
+            split_steps(g, ceil_div(T, step_of<E>()), cut.splits);
             char *out = static_cast<char *>(a.dw) + v0 * d * (a.dw_bf16 ? 2 : 4);
             const bool split = g.splits > 1;
-            const SumEnd end{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16, !split && a.accumulate};
-            gemm<E, true, true>(g, end, tile, s);
+            gemm<E, true, true>(g, SumEnd{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16,
+                                          !split && a.accumulate, nullptr, 0}, cut.tile, s);
             if (split) {
                 const dim3 grid((unsigned)std::min<int64_t>((n * d / 8 + 255) / 256, 1 << 20));
                 if (a.dw_bf16)
@@ -1144,13 +1426,14 @@ void backward(const LossArgs &a, hipStream_t s) {
             }
         }
     }
-    if (a.dh) {
+    if (a.dh && !(one_piece && cut_h.splits == 1)) {
         const dim3 grid((unsigned)std::min<int64_t>((T * d / 8 + 255) / 256, 1 << 20));
+        const int32_t splits = (int32_t)cut_h.splits;
         if (a.bf16)
-            launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, sum, dh_splits, T * d, T, a.d, a.targets,
-                          a.vocab, static_cast<uint16_t *>(a.dh), false);
+            launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, sum, splits, T * d, T, a.d, a.targets, a.vocab,
+                          static_cast<uint16_t *>(a.dh), false);
         else
-            launch_kernel(sum_join_kernel<float>, grid, dim3(256), s, sum, dh_splits, T * d, T, a.d, a.targets, a.vocab,
+            launch_kernel(sum_join_kernel<float>, grid, dim3(256), s, sum, splits, T * d, T, a.d, a.targets, a.vocab,
                           static_cast<float *>(a.dh), false);
     }
 }
@@ -1158,14 +1441,16 @@ void backward(const LossArgs &a, hipStream_t s) {
 }  // namespace
 
 void launch_loss(const LossArgs &a, hipStream_t s) {
-    if (!a.bf16 && direct32(a))
+    if (a.bf16)
+        forward<uint16_t>(a, s);
+    else if (direct32(a, true))
         forward<float>(a, s);
     else
-        forward<uint16_t>(a, s);
+        forward<_Float16>(a, s);
 }
 
 void launch_loss_bwd(const LossArgs &a, hipStream_t s) {
-    if (!a.bf16 && direct32(a))
+    if (!a.bf16 && direct32(a, false))
         backward<float>(a, s);
     else
         backward<uint16_t>(a, s);
