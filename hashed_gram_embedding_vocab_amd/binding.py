@@ -92,6 +92,8 @@ _lock = threading.Lock()
 def lib() -> C.CDLL:
     """Load libengram.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -335,13 +337,13 @@ def _addr(t: Optional[torch.Tensor], name: str, *dtypes) -> Optional[int]:
     kernels take no longer than their host side."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (t.dtype in dtypes or not dtypes):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA (HIP) tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if dtypes and t.dtype not in dtypes:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-    return t.data_ptr()
+    raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
 
 
 # the current stream of a device as an address; torch.cuda.current_stream builds a Stream object around it (2 us)
@@ -349,10 +351,21 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_one_device = None  # whether the process sees one GPU only: then all its tensors are on it
+
+
 def _call(fn: str, stream, tensors, *args):
     """One library call on one device: every tensor must be on it, it is made the
     current device around the launch, and `stream` must be one of its streams
     (None: its current one).  The stream is the call's last argument."""
+    global _one_device
+    if stream is None and _one_device:
+        status = getattr(lib(), fn)(*args, _current_raw_stream(0))
+        if status != OK:
+            _check(fn, status)
+        return
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
@@ -739,10 +752,13 @@ class Plan:
         args = (_addr(x, "x", dt), _addr(residual, "residual", dt), n_rows, _addr(gamma, "gamma", f32), eps,
                 _addr(total, "total", dt), _addr(y, "y", dt), _addr(q, "q", torch.float8_e4m3fn),
                 _addr(scales, "scales", *_E8M0), _addr(rrms, "rrms", f32))
+        shape = x.shape
         for t, name in ((residual, "residual"), (total, "total"), (y, "y"), (q, "q")):
-            _shape(t, name, *x.shape)
+            if t is not None and t.shape != shape:
+                _shape(t, name, *shape)
         _shape(gamma, "gamma", d)
-        _shape(scales, "scales", *self.fp8_scale_shape(n_rows, d, 1))
+        if scales is not None:
+            _shape(scales, "scales", *self.fp8_scale_shape(n_rows, d, 1))
         _count(rrms, "rrms", n_rows)
         _call("engram_rms_norm", stream, (x, residual, gamma, total, y, q, scales, rrms), self._h, *args)
 

@@ -780,6 +780,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
                 turn();
                 if (step(a2, b1, a0, b0)) break;
                 turn();
+            } else if constexpr (End::kImage) {
+                if (step(a0, b0, a1, b1)) break;
+                turn();
+                if (step(a1, b1, a2, b2)) break;
+                turn();
+                if (step(a2, b2, a3, b3)) break;
+                turn();
+                if (step(a3, b3, a0, b0)) break;
+                turn();
             } else {
                 step(a0, b0, a1, b1);
                 step(a1, b1, a2, b2);
@@ -926,21 +935,37 @@ __device__ __forceinline__ void store_loss(int64_t t, float top2, float sum, int
 }
 
 // lse and loss of TB tokens a workgroup from their parts (maxima in powers of two).
+// TB = 1, where the parts are many and few workgroups read them, takes the maximum
+// first: a thread's loads are then all in flight, with no exponential between them.
 template <int TB>
 __global__ __launch_bounds__(256) void lse_join_kernel(const float2 *part, int64_t n_parts, int64_t n_tok,
                                                        const int32_t *targets, int32_t vocab, const float *xt, float *loss,
                                                        float *lse) {
     __shared__ float red[256];
     const int64_t t = (int64_t)blockIdx.x * TB + threadIdx.x % TB, tc = min(t, n_tok - 1);
-    float top = -INFINITY, sum = 0.f;
+    float top = -INFINITY, sum = 0.f, from;
+    if constexpr (TB == 1) {
 #pragma unroll 8
-    for (int64_t i = threadIdx.x / TB; i < n_parts; i += 256 / TB) top = fmaxf(top, part[i * n_tok + tc].x);
-    top = join_threads<TB, true>(top, red);
-    const float from = top == -INFINITY ? 0.f : top;
+        for (int64_t i = threadIdx.x; i < n_parts; i += 256) top = fmaxf(top, part[i * n_tok + tc].x);
+        top = join_threads<TB, true>(top, red);
+        from = top == -INFINITY ? 0.f : top;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x / TB; i < n_parts; i += 256 / TB) {
-        const float2 p = part[i * n_tok + tc];
-        sum += p.y * __builtin_amdgcn_exp2f(p.x - from);
+        for (int64_t i = threadIdx.x; i < n_parts; i += 256) {
+            const float2 p = part[i * n_tok + tc];
+            sum += p.y * __builtin_amdgcn_exp2f(p.x - from);
+        }
+    } else {
+#pragma unroll 8
+        for (int64_t i = threadIdx.x / TB; i < n_parts; i += 256 / TB) {
+            const float2 p = part[i * n_tok + tc];
+            const float m = fmaxf(top, p.x), f = m == -INFINITY ? 0.f : m;
+            sum = sum * __builtin_amdgcn_exp2f(top - f) + p.y * __builtin_amdgcn_exp2f(p.x - f);
+            top = m;
+        }
+        const float own = top;
+        top = join_threads<TB, true>(top, red);
+        from = top == -INFINITY ? 0.f : top;
+        sum *= __builtin_amdgcn_exp2f(own - from);
     }
     sum = join_threads<TB, false>(sum, red);
     if (threadIdx.x < TB && t < n_tok) store_loss(t, top, sum, targets[t], vocab, xt[t], loss, lse);
@@ -954,25 +979,53 @@ __device__ __forceinline__ float few_logit(const float *x, int64_t at, int32_t s
     return v;
 }
 
-// One workgroup a token.
-__global__ __launch_bounds__(256) void few_loss_kernel(const float *x, int32_t splits, int64_t split_elems, int64_t ld,
-                                                       int32_t vocab, float scale, const int32_t *targets, float *loss,
-                                                       float *lse) {
-    __shared__ float red[256];
+// One workgroup a token; a thread's logits stay in its registers.
+constexpr int kFewThreads = 1024, kFewEach = 8;
+__global__ __launch_bounds__(kFewThreads) void few_loss_kernel(const float *x, int32_t splits, int64_t split_elems,
+                                                               int64_t ld, int32_t vocab, float scale,
+                                                               const int32_t *targets, float *loss, float *lse) {
+    __shared__ float red[2][kFewThreads / 64];
+    __shared__ float at_y;
     const int64_t t = blockIdx.x;
-    float top = -INFINITY, sum = 0.f;
-    for (int32_t v = threadIdx.x; v < vocab; v += 256)
-        top = fmaxf(top, few_logit(x, t * ld + v, splits, split_elems) * scale);
-    top = join_threads<1, true>(top, red);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int32_t id = targets[t];
+    float v[kFewEach], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFewEach; ++i) {
+        const int32_t c = i * kFewThreads + (int32_t)threadIdx.x;
+        v[i] = c < vocab ? x[t * ld + c] : -INFINITY;
+    }
+    for (int32_t z = 1; z < splits; ++z)
+#pragma unroll
+        for (int i = 0; i < kFewEach; ++i) {
+            const int32_t c = i * kFewThreads + (int32_t)threadIdx.x;
+            if (c < vocab) v[i] += x[z * split_elems + t * ld + c];
+        }
+#pragma unroll
+    for (int i = 0; i < kFewEach; ++i) {
+        const int32_t c = i * kFewThreads + (int32_t)threadIdx.x;
+        if (c < vocab) v[i] *= scale;
+        if (c == id && c < vocab) at_y = v[i];
+        top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if (lane == 0) red[0][w] = top;
+    __syncthreads();
+    for (int i = 0; i < kFewThreads / 64; ++i) top = fmaxf(top, red[0][i]);
     const float from = top == -INFINITY ? 0.f : top;
-    for (int32_t v = threadIdx.x; v < vocab; v += 256)
-        sum += __builtin_amdgcn_exp2f((few_logit(x, t * ld + v, splits, split_elems) * scale - from) * kLog2e);
-    sum = join_threads<1, false>(sum, red);
+#pragma unroll
+    for (int i = 0; i < kFewEach; ++i) sum += __builtin_amdgcn_exp2f((v[i] - from) * kLog2e);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    if (lane == 0) red[1][w] = sum;
+    __syncthreads();
     if (threadIdx.x == 0) {
-        const int32_t id = targets[t];
+        sum = red[1][0];
+        for (int i = 1; i < kFewThreads / 64; ++i) sum += red[1][i];
         const float l = from + logf(sum);
         const bool counts = id >= 0 && id < vocab;
-        loss[t] = counts ? l - few_logit(x, t * ld + id, splits, split_elems) * scale : 0.f;
+        loss[t] = counts ? l - at_y : 0.f;
         lse[t] = counts ? l : 0.f;
     }
 }
@@ -1075,7 +1128,7 @@ Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_byt
         const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
         for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
             const int64_t items = tiles * n, full = items / slots, rest = items % slots;
-            const double each = (double)(ceil_div(ceil_div(steps, n), 4) * 4 * segs);
+            const double each = (double)(ceil_div(steps, n) * segs);
             const int bytes = n > 1 ? 4 : out_bytes;
             double t = (double)full * (each * two + r.start2 + r.byte2 * bytes);
             if (rest > 0) t += rest <= 256 ? each * one + r.start1 + r.byte1 * bytes : each * two + r.start2 + r.byte2 * bytes;
@@ -1092,7 +1145,7 @@ void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
     // one 256 x 256 tile's stages fill a CU's LDS, two of the others fit
     const unsigned most = tile == 256 ? 256 : 512, grid = End::kImage ? (unsigned)g.items : std::min((unsigned)g.items, most);
     constexpr int NA = End::kImage ? 3 : 2;
-    g.round = tile == 64 ? 4 : NA == 3 ? 1 : 2;
+    g.round = End::kImage ? 1 : tile == 64 ? 4 : 2;
     if constexpr (sizeof(E) == 4) {
         launch_kernel((gemm_kernel<E, End, 64, 2, 2, 4, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
     } else {
@@ -1145,10 +1198,10 @@ void whole(GemmArgs &g) {
     g.split_steps = (int32_t)ceil_div(g.K, step_of<E>());
 }
 
-// At most n parts of K, of whole rounds of stages (an item's last ones are zeros
-// past K, not the next part's).
+// At most n parts of K, for an end whose workgroups take one item each (another's
+// item is a whole round of stages, which would run into the next part).
 void split_steps(GemmArgs &g, int64_t steps, int64_t n) {
-    const int64_t per = ceil_div(ceil_div(steps, n), 4) * 4;
+    const int64_t per = ceil_div(steps, n);
     g.split_steps = (int32_t)per;
     g.splits = (int32_t)ceil_div(steps, per);
 }
@@ -1212,7 +1265,7 @@ template <class E>
 Cut few_cut(const LossArgs &a, const GemmArgs &g, int out_bytes) {
     Cut whole = cut_for<E>(g.M, g.N, g.K, g.segs, 1, out_bytes);
     const int64_t one = a.n_tok * round8(a.vocab) * 4;
-    if (one > kFewBytes / 2 || ceil_div(g.M, 64) * ceil_div(g.N, 64) > 128) return whole;
+    if (one > kFewBytes / 2 || g.N > kFewThreads * kFewEach || ceil_div(g.M, 64) * ceil_div(g.N, 64) > 128) return whole;
     const Cut parts = cut_for<E>(g.M, g.N, g.K, g.segs, few_bytes(a) / one, 4);
     return parts.splits > 1 && parts.cost + 5. < whole.cost ? parts : whole;
 }
@@ -1308,7 +1361,7 @@ void forward(const LossArgs &a, hipStream_t s) {
             g.b = rows_of(a.w, V, d);
             split_steps(g, ceil_div(d, step_of<E>()), few.splits);
             gemm<E, false, false>(g, SumEnd{x, ld, T * ld, false, false, nullptr, 0}, few.tile, s);
-            launch_kernel(few_loss_kernel, dim3((unsigned)T), dim3(256), s, x, g.splits, T * ld, ld, a.vocab, a.scale,
+            launch_kernel(few_loss_kernel, dim3((unsigned)T), dim3(kFewThreads), s, x, g.splits, T * ld, ld, a.vocab, a.scale,
                           a.targets, a.loss, a.lse);
             return;
         }
