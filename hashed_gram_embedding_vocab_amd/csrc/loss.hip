@@ -1320,11 +1320,11 @@ LossLayout loss_bwd_layout(const LossArgs &a) {
 }
 
 bool loss_fits(int64_t n_tok, int32_t vocab, int32_t d) {
-    // items of one launch, and 31-bit offsets in a tile's rows of d or of a piece
-    // of the vocabulary
-    return ceil_div(n_tok, 256) * ceil_div(vocab, 256) < ((int64_t)1 << 22) &&
-           ceil_div(n_tok, 256) * ceil_div(d, 256) < ((int64_t)1 << 18) && d <= (1 << 20) && vocab <= (1 << 22) &&
-           n_tok <= (1 << 27);
+    // items of one launch (fewer than 2^32 threads), and 31-bit offsets in a tile's
+    // rows of d or of a piece of the vocabulary
+    const int64_t t = ceil_div(n_tok, 256), v = ceil_div(vocab, 256), c = ceil_div(d, 256);
+    return t * v < ((int64_t)1 << 22) && v * c < ((int64_t)1 << 22) && t * c < ((int64_t)1 << 18) && d <= (1 << 20) &&
+           vocab <= (1 << 22) && n_tok <= (1 << 26);
 }
 
 namespace {
@@ -1423,7 +1423,9 @@ void backward(const LossArgs &a, hipStream_t s) {
             g.a = oh;
             g.b = ow;
             parts_of(g, hp, hp);
-            const Cut few = one_piece ? few_cut<E>(a, g, F32 ? 4 : 2 * pp) : cut_for<E>(T, n, d, g.segs, 1, F32 ? 4 : 2 * pp);
+            // (cut as for one part, so that dh does not change with dW's type)
+            const int out = F32 ? 4 : 2;
+            const Cut few = one_piece ? few_cut<E>(a, g, out) : cut_for<E>(T, n, d, g.segs, 1, out);
             if (few.splits > 1) {
                 float *x = reinterpret_cast<float *>(ws + L.few);
                 const int64_t ldx = round8(V);

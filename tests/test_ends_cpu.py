@@ -76,8 +76,8 @@ def test_cross_entropy_refusals(B):
             [(4, 0), (4, -1), (5, math.nan), (5, -math.inf), (9, ws - 1), (8, off(at(5), 16)),
              (6, at(0)), (6, at(1)), (6, at(2)), (7, at(2)), (7, at(3)), (8, at(0)), (8, at(1)), (8, at(3)), (8, at(4)),
              (8, off(at(1), 1000 * 256 * 2 - 256))], B.E_INVALID_ARG)
-    refuses(fn, good, [(4, (1 << 27) + 1), (4, 1 << 50)], B.E_UNSUPPORTED)
-    for other in (plan(B, vocab=(1 << 22) + 1), plan(B, d=(1 << 20) + 8)):
+    refuses(fn, good, [(4, (1 << 26) + 1), (4, 1 << 50)], B.E_UNSUPPORTED)
+    for other in (plan(B, vocab=(1 << 22) + 1), plan(B, d=(1 << 20) + 8), plan(B, vocab=1 << 22, d=1 << 16)):
         assert fn(other._h, *good[1:]) == B.E_UNSUPPORTED
         assert other.engram_cross_entropy_workspace_size(n) == 0
         assert other.engram_cross_entropy_backward_workspace_size(n) == 0
@@ -107,7 +107,7 @@ def test_cross_entropy_backward_refusals(B):
     a = list(good)
     a[10] = a[11] = None
     assert fn(*a) == B.E_INVALID_ARG  # nothing is wanted
-    refuses(fn, good, [(4, (1 << 27) + 1)], B.E_UNSUPPORTED)
+    refuses(fn, good, [(4, (1 << 26) + 1)], B.E_UNSUPPORTED)
     a = list(good)
     a[0], a[12], a[14] = f._h, B.BF16, 1 << 40
     assert fn(*a) == B.E_UNSUPPORTED

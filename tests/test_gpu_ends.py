@@ -103,7 +103,10 @@ class HeadRef:
 HEADS = [  # n_tok, vocab, d, scale
     (1, 1, 8, 1.0), (1, 50, 64, 1.0), (2, 300, 72, -0.5), (63, 257, 264, 1.0), (64, 4099, 128, 0.25),
     (65, 1000, 256, 1.0), (130, 33, 520, 1.0), (333, 1000, 256, 0.0625), (300, 5003, 72, 1.0), (1100, 2111, 136, 1.0),
-    (513, 260, 8, 1.0), (2049, 50, 64, 1.0), (700, 16500, 64, 2.0), (3, 70000, 128, 1.0)]
+    (513, 260, 8, 1.0), (2049, 50, 64, 1.0), (700, 16500, 64, 2.0), (3, 70000, 128, 1.0),
+    # h in blocks, W in blocks (backward; forward), long rows of few tokens, many tiles of 128
+    (1030, 16500, 72, 1.0), (4100, 300, 136, 1.0), (12290, 270, 72, 1.0), (5, 130, 5000, 1.0), (70, 90, 4104, -0.3),
+    (150, 1100, 3080, 1.0), (260, 9000, 200, 1.0), (1500, 1500, 264, 1.0)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -159,6 +162,192 @@ def test_cross_entropy_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale):
 @pytest.mark.parametrize("dtype,dw_dtype", GRADS)
 def test_cross_entropy_backward_without_dloss(gpu, dtype, dw_dtype):
     check_backward(gpu, dtype, dw_dtype, 200, 777, 136, 1.0, with_dloss=False)
+
+
+PATHS = [(9, 300, 72), (200, 1000, 264), (600, 5003, 136), (1100, 17000, 72), (4200, 270, 72)]
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+@pytest.mark.parametrize("n_tok,vocab,d", PATHS)
+def test_tokens_that_do_not_count_may_hold_anything(gpu, dtype, dw_dtype, n_tok, vocab, d):
+    """NaN and infinity in their h, lse and dloss reach nothing; their own results are zeros."""
+    p = make_plan(dtype, d, vocab)
+    h, w, y = head(dtype, n_tok, vocab, d, 1.0, 3, gpu, skip=False)
+    out = torch.arange(n_tok, device=gpu) % 3 == 1
+    out[-1] = True
+    y[out] = torch.tensor([-1, vocab, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=gpu)[torch.arange(int(out.sum()), device=gpu) % 4]
+    dloss = torch.rand(n_tok, generator=gen(8)).to(gpu)
+    results = []
+    for junk in (0.0, math.nan, math.inf):
+        h[out] = junk
+        loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+        p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+        assert not loss[out].count_nonzero() and not lse[out].count_nonzero()
+        lse_in, g = lse.clone(), dloss.clone()
+        lse_in[out] = g[out] = junk
+        dh, dw = nan_like(torch.empty_like(h)), nan_like(torch.empty((vocab, d), dtype=dw_dtype, device=gpu))
+        ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+        ws.fill_(255)
+        p.engram_cross_entropy_backward(h, w, y, lse_in, g, dh, dw, ws)
+        assert not dh[out].count_nonzero() and torch.isfinite(dh).all() and torch.isfinite(dw).all()
+        results.append((loss, lse, dh, dw))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+def test_no_token_counts(gpu, dtype, dw_dtype):
+    for n_tok, vocab, d in PATHS:
+        p = make_plan(dtype, d, vocab)
+        h, w, y = head(dtype, n_tok, vocab, d, 1.0, 3, gpu)
+        y.fill_(-1)
+        loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+        p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+        dh, dw = nan_like(torch.empty_like(h)), nan_like(torch.empty((vocab, d), dtype=dw_dtype, device=gpu))
+        ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+        p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, ws)
+        assert not any(t.count_nonzero() for t in (loss, lse, dh, dw))
+        dw.fill_(3.0)
+        p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, ws, flags=8)
+        assert (dw == 3.0).all()
+
+
+def test_nan_stays_in_its_token(gpu):
+    for n_tok, vocab, d in PATHS:
+        p = make_plan("bf16", d, vocab)
+        h, w, y = head("bf16", n_tok, vocab, d, 1.0, 3, gpu, skip=False)
+
+        def call():
+            loss, lse = torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu)
+            p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+            dh, dw = torch.empty_like(h), torch.empty_like(w)
+            p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, p.cross_entropy_backward_workspace(n_tok, torch.bfloat16))
+            return loss, lse, dh
+
+        clean = call()
+        h[4, 3] = math.nan
+        got = call()
+        ok = torch.arange(n_tok, device=gpu) != 4
+        for a, b in zip(clean, got):
+            assert torch.equal(a[ok], b[ok]) and b[4].isnan().all()
+        h[4, 3] = 0.0
+        w[vocab // 2, 1] = math.nan
+        assert all(t.isnan().all() for t in call())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_far_logits(gpu, dtype):
+    """Logits of some ten thousand, all the same, and one far above: no overflow, and
+    the loss of the one that is certain is zero."""
+    for n_tok, vocab, d in PATHS:
+        p = make_plan(dtype, d, vocab)
+        h, w = torch.ones((n_tok, d), dtype=tdt(dtype), device=gpu), torch.zeros((vocab, d), dtype=tdt(dtype), device=gpu)
+        y = (torch.arange(n_tok, device=gpu) % vocab).to(torch.int32)
+        loss, lse = torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu)
+        ws = p.cross_entropy_workspace(n_tok)
+        for level in (0.0, 128.0, -128.0):
+            w.fill_(level)
+            p.engram_cross_entropy(h, w, y, loss, lse, ws)
+            want = level * d + math.log(vocab)
+            assert (lse.double() - want).abs().max() <= 4 * U * abs(want) + 1e-6
+            assert (loss.double() - math.log(vocab)).abs().max() <= 4 * U * abs(want) + 1e-6
+        w.fill_(-128.0)
+        w[vocab - 1] = 128.0
+        y.fill_(vocab - 1)
+        p.engram_cross_entropy(h, w, y, loss, lse, ws)
+        assert (loss == 0).all() and (lse == 128.0 * d).all()
+        y.fill_(0)
+        p.engram_cross_entropy(h, w, y, loss, lse, ws)
+        assert (loss == 256.0 * d).all()
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, p.cross_entropy_backward_workspace(n_tok, tdt(dtype)))
+        assert (dh == 256.0).all() and (dw[0] == -n_tok).all() and (dw[vocab - 1] == n_tok).all() and not dw[1:-1].any()
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+def test_cross_entropy_backward_in_pieces(gpu, dtype, dw_dtype):
+    """More than 1 GB of the logits' gradients: pieces of the vocabulary, dh's sums going on."""
+    check_backward(gpu, dtype, dw_dtype, 8190, 70010, 72, 1.0)
+
+
+def test_cross_entropy_in_pieces(gpu):
+    """An fp32 plan's W in more than 1 GB of parts."""
+    n_tok, vocab, d = 150, 140001, 2056
+    p = make_plan("f32", d, vocab)
+    h, w, y = head("f32", n_tok, vocab, d, 1.0, 3, gpu)
+    loss, lse = torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu)
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+    ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, 1.0, "f32").forward())
+    close(loss, ref, off, "loss")
+    close(lse, ref_lse, off_lse, "lse")
+
+
+def test_cross_entropy_past_32_bits(gpu):
+    """Offsets past 2^31 and 2^32 bytes in W, its gradient, h and dh: the results of
+    few rows and columns there are those of a small call."""
+    torch.cuda.empty_cache()
+    # W: all rows but the last 300 far below, so that these alone make the loss
+    vocab, d, n_tok, tail = 270000, 8200, 5, 300
+    p, small = make_plan("bf16", d, vocab), make_plan("bf16", d, tail)
+    h = randn((n_tok, d), "bf16", 1).abs().to(gpu)
+    w = torch.full((vocab, d), -1.0, dtype=torch.bfloat16, device=gpu)  # logits of thousands below zero
+    w[-tail:] = randn((tail, d), "bf16", 2, 0.01).to(gpu)
+    y = torch.tensor([0, 7, 299, 100, 298], dtype=torch.int32, device=gpu)
+    out = [[torch.empty(n_tok, device=gpu) for _ in range(2)] for _ in range(2)]
+    p.engram_cross_entropy(h, w, y + (vocab - tail), *out[0], p.cross_entropy_workspace(n_tok))
+    small.engram_cross_entropy(h, w[-tail:], y, *out[1], small.cross_entropy_workspace(n_tok))
+    for a, b in zip(*out):
+        assert torch.allclose(a, b, rtol=1e-6, atol=1e-6)
+    dh, dw = torch.empty_like(h), nan_like(torch.empty_like(w))
+    dhs, dws = torch.empty_like(h), torch.empty_like(w[-tail:])
+    p.engram_cross_entropy_backward(h, w, y + (vocab - tail), out[1][1], None, dh, dw,
+                                    p.cross_entropy_backward_workspace(n_tok, torch.bfloat16))
+    small.engram_cross_entropy_backward(h, w[-tail:], y, out[1][1], None, dhs, dws,
+                                        small.cross_entropy_backward_workspace(n_tok, torch.bfloat16))
+    # (both round P of 8 bits; its sums' order differs)
+    assert (dw[-tail:].double() - dws.double()).abs().max() <= 2.0 ** -7 * float(dws.double().abs().max())
+    assert (dh.double() - dhs.double()).abs().max() <= 2.0 ** -7 * float(dhs.double().abs().max())
+    assert not dw[:-tail].count_nonzero()
+    del w, dw
+    torch.cuda.empty_cache()
+    n_tok, d, vocab, tail = (1 << 20) + 77, 2056, 40, 301
+    p = make_plan("bf16", d, vocab)
+    w = randn((vocab, d), "bf16", 3, 0.02).to(gpu)
+    h = torch.zeros((n_tok, d), dtype=torch.bfloat16, device=gpu)
+    h[-tail:] = randn((tail, d), "bf16", 4).to(gpu)
+    y = torch.full((n_tok,), -1, dtype=torch.int32, device=gpu)
+    y[-tail:] = zipf_ids(tail, vocab, 5, bad=False).to(gpu)
+    loss, lse, dh = (torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu), nan_like(torch.empty_like(h)))
+    dw = torch.empty((vocab, d), device=gpu)
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+    p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, p.cross_entropy_backward_workspace(n_tok))
+    ref = HeadRef(h[-tail:], w, y[-tail:], 1.0, "bf16")
+    r = [t.cpu() for t in ref.forward()]
+    close(loss[-tail:], r[0], r[2], "loss")
+    g = torch.ones(tail, dtype=torch.float64, device=gpu)
+    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse[-tail:], g, torch.float32))
+    close(dh[-tail:], rdh, off_h, "dh")
+    close(dw, rdw, off_w + 2 * (-(-n_tok // 32)) * 3 * U * rdw.abs(), "dw")  # (a longer chain, of zeros)
+    assert not dh[:-tail].count_nonzero() and not loss[:-tail].count_nonzero()
+    del h, dh
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+def test_cross_entropy_in_the_largest_batchs_workspace(gpu, dtype, dw_dtype):
+    p = make_plan(dtype, 136, 3000)
+    big = p.cross_entropy_workspace(5000), p.cross_entropy_backward_workspace(5000, dw_dtype)
+    for n_tok in (1, 65, 700, 2049):
+        h, w, y = head(dtype, n_tok, 3000, 136, 1.0, 3, gpu)
+        res = []
+        for f, b in (big, (p.cross_entropy_workspace(n_tok), p.cross_entropy_backward_workspace(n_tok, dw_dtype))):
+            f.fill_(255), b.fill_(255)
+            loss, lse, dh = torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu), torch.empty_like(h)
+            dw = torch.empty((3000, 136), dtype=dw_dtype, device=gpu)
+            p.engram_cross_entropy(h, w, y, loss, lse, f)
+            p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, b)
+            res.append((loss, lse, dh, dw))
+        assert all(torch.equal(a, b) for a, b in zip(*res))
 
 
 def test_cross_entropy_backward_is_the_difference_of_the_loss(gpu):
@@ -465,3 +654,214 @@ def test_clip_grads_norms_of_every_size(gpu):
     g = torch.ones(77, device=gpu)  # only the norm is wanted
     p.engram_clip_grads(B.GradList([g], outs=[None]), norm, p.clip_grads_workspace(1), max_norm=0.5)
     assert abs(float(norm[0]) - math.sqrt(77)) < 1e-6 and (g == 1).all()
+
+
+# ---------------------------------------------------------------- together, streams, graphs
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d", [(1, 1, 8), (45, 37, 72), (300, 333, 264), (700, 1111, 520), (1030, 16500, 72),
+                                           (131, 50, 2568), (4100, 70, 136)])
+def test_nothing_is_written_beside_the_outputs(gpu, dtype, n_tok, vocab, d):
+    """Every output and workspace with bytes around it, at sizes that end inside a
+    vector, a block, a tile and a word of scales."""
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    p = make_plan(dtype, d, vocab)
+    dt, f32, u8 = tdt(dtype), torch.float32, torch.uint8
+    made = []
+
+    def buf(shape, t):
+        made.append(Guarded(shape, t, gpu))
+        return made[-1].t
+
+    h, w, y = head(dtype, n_tok, vocab, d, 1.0, 3, gpu)
+    gamma = 1.0 + randn((d,), "f32", 3, 0.1).to(gpu)
+    total, yn, rr = buf((n_tok, d), dt), buf((n_tok, d), dt), buf((n_tok,), f32)
+    p.engram_rms_norm(h, gamma, yn, residual=h, total=total, q=buf((n_tok, d), torch.float8_e4m3fn),
+                      scales=buf(p.fp8_scale_shape(n_tok, d, 1), u8), rrms=rr)
+    dg = buf((d,), f32)
+    p.engram_rms_norm_backward(total, yn, gamma, rr, buf((n_tok, d), dt), dg,
+                               buf((p.engram_rms_norm_backward_workspace_size(n_tok),), u8), dtotal=h)
+    loss, lse = buf((n_tok,), f32), buf((n_tok,), f32)
+    p.engram_cross_entropy(h, w, y, loss, lse, buf((p.engram_cross_entropy_workspace_size(n_tok),), u8))
+    outs = []
+    for dw_dtype in (f32, torch.bfloat16) if dtype == "bf16" else (f32,):
+        ws = buf((p.engram_cross_entropy_backward_workspace_size(n_tok, dw_dtype),), u8)
+        outs += [buf((n_tok, d), dt), buf((vocab, d), dw_dtype)]
+        p.engram_cross_entropy_backward(h, w, y, lse, None, outs[-2], outs[-1], ws)
+    counts = torch.tensor([0, n_tok, n_tok // 2], dtype=torch.int32, device=gpu)
+    rows = randn((3, n_tok, 7), "f32", 5).to(gpu)
+    grads, row_counts = outs + [dg, rows, rows[0, 0].clone()], [None] * (len(outs) + 1) + [counts, None]
+    lst = B.GradList(grads, outs=[buf(tuple(g.shape), g.dtype) for g in grads], row_counts=row_counts)
+    p.engram_clip_grads(lst, buf((2,), f32), buf((p.engram_clip_grads_workspace_size(len(grads)),), u8), max_norm=1e-3)
+    torch.cuda.synchronize()
+    assert all(g.whole() for g in made), [i for i, g in enumerate(made) if not g.whole()]
+
+
+def test_a_training_step_through_all_of_them(gpu):
+    """Tokens -> tied embedding -> residual and RMS norm in 8 bits -> a projection ->
+    residual and norm -> loss, and back, the tied table's gradient from both ends in
+    one buffer, clipped together.  Every stage against 64 bits on what the stage
+    before gave."""
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    n, V, d = 300, 1111, 264
+    p = make_plan("bf16", d, V)
+    bf, f32 = dict(dtype=torch.bfloat16, device=gpu), dict(dtype=torch.float32, device=gpu)
+    ids, targets = zipf_ids(n, V, 1).to(gpu), zipf_ids(n, V, 2).to(gpu)
+    table, gamma1, gamma2 = randn((V, d), "bf16", 3, 0.3).to(gpu), torch.ones(d, **f32), 1.0 + randn((d,), "f32", 4, 0.1).to(gpu)
+    wp = randn((d, d), "bf16", 5, 0.05).to(gpu)
+    h0, x1, t2, y2 = (torch.empty((n, d), **bf) for _ in range(4))
+    p.engram_embed(ids, table, h0.view(1, n, d))
+    q, sc = torch.empty((n, d), dtype=torch.float8_e4m3fn, device=gpu), torch.empty(p.fp8_scale_shape(n, d, 1), dtype=torch.uint8, device=gpu)
+    rr1, rr2 = torch.empty(n, **f32), torch.empty(n, **f32)
+    y1 = torch.empty((n, d), **bf)
+    p.engram_rms_norm(h0, gamma1, y1, q=q, scales=sc, rrms=rr1)
+    kp = 272  # (a product's K is a multiple of 16)
+    qp, sp = torch.zeros((n, kp), dtype=torch.uint8, device=gpu), sc
+    qp[:, :d] = q.view(torch.uint8)
+    wq, ws8 = torch.empty((d, kp), dtype=torch.float8_e4m3fn, device=gpu), torch.empty(p.fp8_scale_shape(d, kp, 128), dtype=torch.uint8, device=gpu)
+    p.engram_quantize_fp8(torch.nn.functional.pad(wp, (0, kp - d)), wq, ws8, block_rows=128)
+    p.engram_matmul_fp8(qp.view(torch.float8_e4m3fn), sp, wq, ws8, x1, p.matmul_fp8_workspace(n, d, kp))
+    p.engram_rms_norm(x1, gamma2, y2, residual=h0, total=t2, rrms=rr2)
+    s2, ref_rr, ref_y = rms_ref(x1, h0, gamma2, 1e-6, "bf16")
+    assert torch.equal(t2, s2)
+    close(y2, ref_y.cpu(), 2.0 ** -8 * 1.02 * ref_y.abs().cpu(), "y2")
+    loss, lse = torch.empty(n, **f32), torch.empty(n, **f32)
+    p.engram_cross_entropy(y2, table, targets, loss, lse, p.cross_entropy_workspace(n))
+    ref = HeadRef(y2, table, targets, 1.0, "bf16")
+    r = [t.cpu() for t in ref.forward()]
+    close(loss, r[0], r[2], "loss")
+    counted = int(ref.counts.sum())
+    dy2, dtable = torch.empty((n, d), **bf), torch.empty((V, d), **f32)
+    p.engram_cross_entropy_backward(y2, table, targets, lse, None, dy2, dtable, p.cross_entropy_backward_workspace(n),
+                                    dloss_scale=1.0 / counted)
+    g = torch.full((n,), 1.0 / counted, dtype=torch.float64, device=gpu)
+    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse, g, torch.float32))
+    close(dy2, rdh, off_h, "dy2")
+    close(dtable, rdw, off_w, "dtable, the head's part")
+    dt2, dg2 = torch.empty((n, d), **bf), torch.empty(d, **f32)
+    p.engram_rms_norm_backward(t2, dy2, gamma2, rr2, dt2, dg2, p.rms_norm_backward_workspace(n))
+    # (the projection's own gradients go the way of the 8-bit product; here its input's is taken in 16 bits)
+    dy1 = (dt2.float() @ wp.float()).to(torch.bfloat16)
+    dh0, dg1 = torch.empty((n, d), **bf), torch.empty(d, **f32)
+    p.engram_rms_norm_backward(h0, dy1, gamma1, rr1, dh0, dg1, p.rms_norm_backward_workspace(n), dtotal=dt2)
+    head_part = dtable.clone()
+    p.engram_embed_backward(ids, dh0.view(1, n, d), dtable, p.embed_backward_workspace(n), flags=B.GRAD_ACCUMULATE)
+    ok = (ids >= 0) & (ids < V)
+    both = head_part.double().index_add_(0, ids[ok].long(), dh0.double()[ok])
+    mag = head_part.double().abs().index_add_(0, ids[ok].long(), dh0.double().abs()[ok])
+    close(dtable, both.cpu(), (n * U * mag).cpu(), "dtable")
+    lst = B.GradList([dtable, dg1, dg2])
+    norm = torch.empty(2, **f32)
+    before = [t.clone() for t in lst.grads]
+    ref_norm = norm_ref(before)
+    p.engram_clip_grads(lst, norm, p.clip_grads_workspace(lst), max_norm=0.5 * ref_norm)
+    assert abs(float(norm[0]) - ref_norm) <= 1.01 * U * ref_norm and abs(float(norm[1]) - 0.5) <= 4 * U
+    assert all(torch.equal(a, b * norm[1]) for a, b in zip(lst.grads, before))
+    assert abs(norm_ref(lst.grads) - 0.5 * ref_norm) <= 1e-6 * ref_norm
+
+
+def _ends(gpu, seed, n, V=1030, d=136, dw_dtype=torch.float32):
+    """A call of every operator on buffers of its own."""
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    p = make_plan("bf16", d, V)
+    h, w, y = head("bf16", n, V, d, 1.0, seed, gpu)
+    gamma = 1.0 + randn((d,), "f32", seed, 0.1).to(gpu)
+    e = torch.empty_like
+    total, yn, dx, dh = e(h), e(h), e(h), e(h)
+    q, sc = torch.empty(h.shape, dtype=torch.float8_e4m3fn, device=gpu), torch.empty(p.fp8_scale_shape(n, d, 1), dtype=torch.uint8, device=gpu)
+    rr, loss, lse = (torch.empty(n, device=gpu) for _ in range(3))
+    dg, dw = torch.empty(d, device=gpu), torch.empty((V, d), dtype=dw_dtype, device=gpu)
+    rows, counts = randn((4, 50, 16), "f32", seed).to(gpu), torch.tensor([0, 50, 7, 21], dtype=torch.int32, device=gpu)
+    ro = torch.zeros_like(rows)
+    outs = [e(dg), e(dw), ro]
+    lst = B.GradList([dg, dw, rows], outs=outs, row_counts=[None, None, counts])
+    norm = torch.empty(2, device=gpu)
+    ws = (p.rms_norm_backward_workspace(n), p.cross_entropy_workspace(n), p.cross_entropy_backward_workspace(n, dw_dtype),
+          p.clip_grads_workspace(lst))
+
+    def call(stream=None):
+        p.engram_rms_norm(h, gamma, yn, residual=h, total=total, q=q, scales=sc, rrms=rr, stream=stream)
+        p.engram_cross_entropy(yn, w, y, loss, lse, ws[1], stream=stream)
+        p.engram_cross_entropy_backward(yn, w, y, lse, None, dh, dw, ws[2], stream=stream)
+        p.engram_rms_norm_backward(total, dh, gamma, rr, dx, dg, ws[0], dtotal=dh, stream=stream)
+        p.engram_clip_grads(lst, norm, ws[3], max_norm=0.01, stream=stream)
+
+    return call, [total, yn, q.view(torch.uint8), sc, rr, loss, lse, dh, dw, dx, dg, norm] + outs, y
+
+
+def test_captured_graphs_replay_the_eager_results(gpu):
+    """Two graphs with workspaces of their own, replayed several times and at once
+    on two streams, with eager work in between and inputs changed."""
+    sets = [_ends(gpu, 60, 700), _ends(gpu, 70, 33, dw_dtype=torch.bfloat16)]
+    eager = []
+    for call, outs, _ in sets:
+        call()
+        torch.cuda.synchronize()
+        eager.append([o.clone() for o in outs])
+    graphs = []
+    for call, outs, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for turn in range(4):
+        for _, outs, _ in sets:
+            for o in outs:
+                o.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, outs, _), want in zip(sets, eager):
+            for o, e in zip(outs, want):
+                assert torch.equal(o, e), turn
+        sets[0][0]()  # eager work between the replays
+    sets[0][2].copy_(zipf_ids(700, 1030, 99).to(gpu))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    replayed = [o.clone() for o in sets[0][1]]
+    sets[0][0]()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(replayed, sets[0][1]))
+    assert not torch.equal(replayed[5], eager[0][5])
+
+
+def test_side_stream(gpu):
+    """On a stream of the caller's, behind work of that stream, without touching the current one."""
+    call, outs, y = _ends(gpu, 80, 700)
+    call()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    keep = y.clone()
+    y.fill_(0)
+    for o in outs:
+        o.zero_()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        big = torch.zeros(1 << 28, device=gpu)  # work the calls have to wait behind
+        big += 1
+        y.copy_(keep)
+    call(st)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_profiling_counts_the_operators(gpu):
+    call, _, _ = _ends(gpu, 90, 40)
+    p = call.__closure__  # (a plan of its own would count the same; the call's is used below)
+    from hashed_gram_embedding_vocab_amd import binding as B
+
+    plan = [c.cell_contents for c in p if isinstance(c.cell_contents, B.Plan)][0]
+    call()
+    plan.engram_profile_begin(16)
+    call()
+    r = plan.engram_profile_end()
+    assert r["aux"]["launches"] == 2 and r["gemm"]["launches"] == 1 and r["bwd_gemm"]["launches"] == 1
+    assert r["bwd_fuse"]["launches"] == 1 and r["bwd_gemm"]["total_ms"] > 0
