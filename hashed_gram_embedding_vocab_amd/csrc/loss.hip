@@ -674,6 +674,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 #pragma unroll
         for (int i = 0; i < FN; ++i) h.b[i] = rb.template read<H>(stb, wn + i);
     };
+    int rows_left = 0;  // of the tile's rows, those of the result (fp32)
     auto multiply = [&](const Half &h, auto hc) {
         constexpr int H = decltype(hc)::value;
         if constexpr (sizeof(E) == 2) {
@@ -690,14 +691,17 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
                                                                             __builtin_bit_cast(bf16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
                 }
         } else {
+            // (fragments of rows past the last are left out: a few tokens are bound
+            // by W's bytes then, and not by products with nothing)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int j = 0; j < FM; ++j)
+                if (16 * (wm + j) < rows_left)
 #pragma unroll
-                for (int i = 0; i < FN; ++i)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int j = 0; j < FM; ++j)
-                        acc[4 * H + e][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            __uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]), acc[4 * H + e][i][j], 0, 0, 0);
+                        for (int i = 0; i < FN; ++i)
+                            acc[4 * H + e][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]), acc[4 * H + e][i][j], 0, 0, 0);
         }
     };
     // (kAhead loads a wave may be in flight at a step's barrier.  The last fills
@@ -755,6 +759,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         int64_t n0, m0;
         int split;
         it.origin(item, n0, m0, split);
+        rows_left = (int)min(g.M - m0, (int64_t)T);
         left = steps_in<E>(g, split) * g.segs;
         // (a tile's rows are asked for ahead of its stages, whose waits then cover
         // them: behind them they would wait for the next tile's first stages.  The
@@ -1065,7 +1070,8 @@ __global__ __launch_bounds__(256) void sum_join_kernel(const float *part, int32_
     const int64_t n = rows * units;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
         F8 v = load8(part + u * 8);
-        for (int32_t z = 1; z < splits; ++z) {
+#pragma unroll 8
+        for (int32_t z = 1; z < splits; ++z) {  // (eight loads in flight)
             const F8 w = load8(part + z * split_elems + u * 8);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v.v[i] += w.v[i];
