@@ -419,6 +419,7 @@ struct GradEnd {
     int64_t row64, part, ld;   // blocks: as in their Operand, whole columns
     int32_t parts;
     int64_t v0;
+    int64_t stack;             // rows from a token's part to its next one; 0: parts apart
     template <int FM>
     struct Row {
         u32x4_t tok[FM];
@@ -469,13 +470,15 @@ struct GradEnd {
                         for (int j = 0; j < FM; ++j) acc[i][j][r] = 0.f;
         }
         if constexpr (PAIRS) {
+            const int64_t all = (stack ? parts : 1) * g.M;
             for (int q = 0; q < parts; ++q) {
-                uint16_t *to = static_cast<uint16_t *>(p) + q * part;
+                uint16_t *to = static_cast<uint16_t *>(p) + (stack ? 0 : q * part);
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    // (rows and columns past the last are zeros up to whole blocks)
-                    const int64_t m = m0 + 16 * j + (lane & 15);
-                    if (m >= (g.M + kBlock - 1) / kBlock * kBlock) continue;
+                    // (rows and columns past the last are zeros up to whole blocks:
+                    // of stacked parts, of one block then, behind the last part's)
+                    const int64_t mine = m0 + 16 * j + (lane & 15), m = mine + q * stack;
+                    if (m >= (all + kBlock - 1) / kBlock * kBlock || (stack && q + 1 < parts && mine >= g.M)) continue;
 #pragma unroll
                     for (int i = 0; i < FN; i += 2) {
                         const int64_t n = nl + col(i);
@@ -548,9 +551,11 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[FN][FM], uint8_t
 }
 
 // The sums themselves: fp32 (a split's at `split_elems` from the one before), or
-// bf16; over what is there or added to it.
+// bf16; over what is there or added to it.  WALKS: fp32, by workgroups that take
+// several items of few stages.
+template <bool WALKS>
 struct SumEnd {
-    static constexpr bool kImage = true, kPairs = false, kEarly = false;
+    static constexpr bool kImage = !WALKS, kPairs = false, kEarly = false;
     void *c;
     int64_t ld, split_elems;
     bool bf16, accumulate;
@@ -581,9 +586,11 @@ struct SumEnd {
             if (!row.counts[j])
 #pragma unroll
                 for (int i = 0; i < FN; ++i) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if (bf16) {
-            store_rows<FN, FM>(acc, img, static_cast<uint16_t *>(c), ld, g.M, g.N, m0, n0, lane, accumulate);
-            return;
+        if constexpr (!WALKS) {
+            if (bf16) {
+                store_rows<FN, FM>(acc, img, static_cast<uint16_t *>(c), ld, g.M, g.N, m0, n0, lane, accumulate);
+                return;
+            }
         }
         float *base = static_cast<float *>(c) + split * split_elems;
 #pragma unroll
@@ -837,24 +844,25 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 template <typename T, typename Out, int PARTS>
 __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, int32_t d, const int32_t *targets,
                                                     int32_t vocab, Out *out, const float *lse, const float *dloss,
-                                                    float factor, Token *token) {
+                                                    float factor, Token *token, int32_t copies) {
     constexpr bool BLOCKS = sizeof(Out) == 2;
     const int32_t cols = BLOCKS ? (d + kBlock - 1) / kBlock * kBlock : d, units = cols / 8;
-    const int64_t all = BLOCKS ? (rows + kBlock - 1) / kBlock * kBlock : rows, n = all * units;
+    const int64_t all = BLOCKS ? (rows * copies + kBlock - 1) / kBlock * kBlock : rows, n = all * units;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
-        const int64_t r = quotient(u, units);
-        const int32_t c = (int32_t)(u - r * units) * 8;
+        const int64_t to = quotient(u, units), copy = copies > 1 ? min(to / rows, (int64_t)copies - 1) : 0;
+        const int64_t r = to - copy * rows;  // (copies of all rows one after the other)
+        const int32_t c = (int32_t)(u - to * units) * 8;
         bool counts = r < rows;
         if (targets && counts) {
             const int32_t id = targets[r];
             counts = id >= 0 && id < vocab;
-            if (token && c == 0)
+            if (token && c == 0 && copy == 0)
                 token[r] = counts ? Token{lse[r], (dloss ? dloss[r] : 1.f) * factor, id, 0} : Token{0.f, 0.f, -1, 0};
         }
         F8 v = {};
         if (counts && c < d) v = load8(x + r * d + c);
         if constexpr (BLOCKS) {
-            const int64_t at = block_at(r, c, (int64_t)cols * kBlock);
+            const int64_t at = block_at(to, c, (int64_t)cols * kBlock);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) {
                 store8(out + q * n * 8 + at, v);
@@ -1039,7 +1047,7 @@ __global__ __launch_bounds__(kFewThreads) void few_loss_kernel(const float *x, i
 __global__ __launch_bounds__(256) void few_grad_kernel(const float *x, int32_t splits, int64_t split_elems, int64_t ldx,
                                                        int64_t n_tok, int32_t vocab, float scale, const Token *token,
                                                        void *p, int64_t row64, int64_t part, int64_t ld, int32_t parts,
-                                                       bool f32) {
+                                                       int64_t stack, bool f32) {
     const int64_t rows = f32 ? n_tok : (n_tok + kBlock - 1) / kBlock * kBlock;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / ld, v = i - t * ld;
     if (t >= rows) return;
@@ -1055,7 +1063,9 @@ __global__ __launch_bounds__(256) void few_grad_kernel(const float *x, int32_t s
         return;
     }
     for (int32_t q = 0; q < parts; ++q) {
-        static_cast<__bf16 *>(p)[q * part + block_at(t, v, row64)] = (__bf16)y;
+        const int64_t r = t + q * stack;
+        if (!stack || (r < kBlock && (q + 1 == parts || t < n_tok)))
+            static_cast<__bf16 *>(p)[(stack ? 0 : q * part) + block_at(r, v, row64)] = (__bf16)y;
         y -= (float)(__bf16)y;
     }
 }
@@ -1117,7 +1127,7 @@ bool may_tile(int tile, int64_t M, int64_t N) {
 }
 
 template <class E>
-Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_bytes) {
+Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_bytes, bool walks = false) {
     struct Rate {
         int tile;
         double one, two, start1, start2, byte1, byte2;
@@ -1128,16 +1138,18 @@ Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_byt
     Cut best{64, 1, 1e30};
     const int64_t steps = ceil_div(K, step_of<E>());
     for (const Rate &r : kRates) {
-        if (!may_tile(r.tile, M, N) || (sizeof(E) == 4 && r.tile != 64)) continue;
+        if ((walks ? r.tile == 256 : !may_tile(r.tile, M, N)) || (sizeof(E) == 4 && r.tile != 64)) continue;
         // (an fp32 stage: 32 k at a sixteenth of the bf16 rate)
         const double one = sizeof(E) == 4 ? 0.5 : r.one, two = sizeof(E) == 4 ? 0.95 : r.two;
         const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
         for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
             const int64_t items = tiles * n, full = items / slots, rest = items % slots;
-            const double each = (double)(ceil_div(steps, n) * segs);
+            const double each = (double)((walks ? ceil_div(steps, 2) * 2 : ceil_div(steps, n)) * segs);
             const int bytes = n > 1 ? 4 : out_bytes;
-            double t = (double)full * (each * two + r.start2 + r.byte2 * bytes);
-            if (rest > 0) t += rest <= 256 ? each * one + r.start1 + r.byte1 * bytes : each * two + r.start2 + r.byte2 * bytes;
+            const double less = walks ? 0.6 : 1.;  // (the next item's first stages land while one ends)
+            double t = (double)full * (each * two + less * (r.start2 + r.byte2 * bytes));
+            if (rest > 0)
+                t += rest <= 256 ? each * one + less * (r.start1 + r.byte1 * bytes) : each * two + less * (r.start2 + r.byte2 * bytes);
             if (n > 1) t += 4. + (double)(n * M) * (double)N * 4. / 4.5e6;
             if (t < best.cost * 0.98) best = Cut{r.tile, n, t};
         }
@@ -1151,34 +1163,40 @@ void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
     // one 256 x 256 tile's stages fill a CU's LDS, two of the others fit
     const unsigned most = tile == 256 ? 256 : 512, grid = End::kImage ? (unsigned)g.items : std::min((unsigned)g.items, most);
     constexpr int NA = End::kImage ? 3 : 2;
-    g.round = End::kImage ? 1 : tile == 64 ? 4 : 2;
+    constexpr bool SHORT = std::is_same<End, SumEnd<true>>::value;  // few stages an item: two of each do
+    constexpr int NS = SHORT ? 2 : 4;
+    g.round = End::kImage ? 1 : tile == 64 ? NS : 2;
     if constexpr (sizeof(E) == 4) {
-        launch_kernel((gemm_kernel<E, End, 64, 2, 2, 4, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
+        launch_kernel((gemm_kernel<E, End, 64, 2, 2, NS, NS, AX, BX>), dim3(grid), dim3(256), s, g, end);
     } else {
-        if (tile == 256)
-            launch_kernel((gemm_kernel<E, End, 256, 2, 4, 2, NA, AX, BX>), dim3(grid), dim3(512), s, g, end);
-        else if (tile == 128)
+        if constexpr (!SHORT)
+            if (tile == 256) {
+                launch_kernel((gemm_kernel<E, End, 256, 2, 4, 2, NA, AX, BX>), dim3(grid), dim3(512), s, g, end);
+                return;
+            }
+        if (tile == 128)
             launch_kernel((gemm_kernel<E, End, 128, 2, 2, 2, NA, AX, BX>), dim3(grid), dim3(256), s, g, end);
         else
-            launch_kernel((gemm_kernel<E, End, 64, 2, 2, 4, 4, AX, BX>), dim3(grid), dim3(256), s, g, end);
+            launch_kernel((gemm_kernel<E, End, 64, 2, 2, NS, NS, AX, BX>), dim3(grid), dim3(256), s, g, end);
     }
 }
 
 template <typename T, typename Out, int PARTS>
-void make_parts(const void *x, int64_t rows, int32_t d, const LossArgs *a, Out *out, Token *token, hipStream_t s) {
-    const int64_t n = sizeof(Out) == 2 ? round64(rows) * (round64(d) / 8) : rows * (d / 8);
+void make_parts(const void *x, int64_t rows, int32_t d, const LossArgs *a, Out *out, Token *token, hipStream_t s,
+                int32_t copies = 1) {
+    const int64_t n = sizeof(Out) == 2 ? round64(rows * copies) * (round64(d) / 8) : rows * (d / 8);
     launch_kernel((parts_kernel<T, Out, PARTS>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), s,
                   static_cast<const T *>(x), rows, d, a ? a->targets : static_cast<const int32_t *>(nullptr),
                   a ? a->vocab : 0, out, a ? static_cast<const float *>(a->lse) : static_cast<const float *>(nullptr),
-                  a ? a->dloss : static_cast<const float *>(nullptr), a ? a->dloss_scale * a->scale : 0.f, token);
+                  a ? a->dloss : static_cast<const float *>(nullptr), a ? a->dloss_scale * a->scale : 0.f, token, copies);
 }
 
 // A copy in blocks of rows of h or W: a bf16 plan's as they are, an fp32 plan's in
 // three parts.
 void make_blocks(const LossArgs &a, const void *x, int64_t rows, const LossArgs *mask, uint16_t *out, Token *token,
-                 hipStream_t s) {
+                 hipStream_t s, int32_t copies = 1) {
     if (a.bf16)
-        make_parts<uint16_t, uint16_t, 1>(x, rows, a.d, mask, out, token, s);
+        make_parts<uint16_t, uint16_t, 1>(x, rows, a.d, mask, out, token, s, copies);
     else
         make_parts<float, uint16_t, 3>(x, rows, a.d, mask, out, token, s);
 }
@@ -1243,10 +1261,16 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Whether an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
 // of the bf16 ones' rate, or as products of parts (three of fp16 parts forward, six of
-// bf16 parts backward): those need W's parts made first, and take more stages.
+// bf16 parts backward), which need W's parts made first: as long as a second
+// reading of W takes (some 100 tokens' products), and where V is small their
+// launches (a time of its own) and, forward, tiles of too few workgroups along
+// all of d.  Measured, us, instructions of fp32 against parts: forward 59 tokens x
+// 61016 x 2832 237 : 567, 517 x 32000 x 1024 373 : 220, 1000 x 773 x 5952 135 : 144,
+// 2500 x 1000 x 256 25 : 28, 6000 x 1000 x 256 44 : 35; backward 59 x 61016 x 2832
+// 850 : 1374, 275 x 22940 x 1496 711 : 571, 521 x 773 x 5952 214 : 175,
+// 1000 x 1000 x 256 45 : 59.
 bool direct32(const LossArgs &a, bool forward) {
-    const int64_t T = a.n_tok, V = a.vocab;
-    return forward ? T * V <= 135 * V + 1100000 : T * V <= 333 * V + 6750000;
+    return forward ? (a.n_tok - 130) * a.vocab <= 600000000 / a.d + 550000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
 }
 
 // Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
@@ -1257,9 +1281,16 @@ bool direct32(const LossArgs &a, bool forward) {
 bool blocks_h(const LossArgs &a) { return a.bf16 && a.n_tok >= 1024 && a.vocab >= 16384; }
 bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (forward ? 12288 : 4096); }
 
+// A bf16 plan's few tokens: the parts of P are further rows of it, and h's rows
+// stand as often, so that a tile of 64 rows, which these tokens do not fill, holds
+// two parts for dh and dW at no cost (three for an fp32 dW).  One token's gradient
+// is a few products, whose one rounding to bf16 would not average out (up to 2^-8 of
+// its norm, twice what a result's own rounding is).
+bool stacked(const LossArgs &a) { return a.bf16 && a.n_tok <= 21; }
+
 // Parts of P, and bytes of P for a token and column.
-int p_parts(const LossArgs &a) { return a.bf16 && a.dw_bf16 ? 1 : 3; }
-int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a, false) ? 4 : 2 * p_parts(a); }
+int p_parts(const LossArgs &a) { return !a.bf16 || !a.dw_bf16 ? 3 : stacked(a) ? 2 : 1; }
+int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a, false) ? 4 : stacked(a) ? 2 : 2 * p_parts(a); }
 
 int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
 int64_t few_bytes(const LossArgs &a) { return std::min(kFewBytes, kMostSplits * a.n_tok * round8(a.vocab) * 4); }
@@ -1366,7 +1397,7 @@ void forward(const LossArgs &a, hipStream_t s) {
             const int64_t ld = round8(V);
             g.b = rows_of(a.w, V, d);
             split_steps(g, ceil_div(d, step_of<E>()), few.splits);
-            gemm<E, false, false>(g, SumEnd{x, ld, T * ld, false, false, nullptr, 0}, few.tile, s);
+            gemm<E, false, false>(g, SumEnd<false>{x, ld, T * ld, false, false, nullptr, 0}, few.tile, s);
             launch_kernel(few_loss_kernel, dim3((unsigned)T), dim3(kFewThreads), s, x, g.splits, T * ld, ld, a.vocab, a.scale,
                           a.targets, a.loss, a.lse);
             return;
@@ -1405,19 +1436,20 @@ void backward(const LossArgs &a, hipStream_t s) {
     void *h = ws + L.h, *p = ws + L.part;
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.w);
     float *sum = reinterpret_cast<float *>(ws + L.sum), *wsum = reinterpret_cast<float *>(ws + L.wsum);
-    const bool bw = parts || (!F32 && blocks_w(a, false));
+    const bool bw = parts || (!F32 && blocks_w(a, false)), stack = stacked(a);
     if constexpr (F32)
         make_parts<float, float, 1>(a.h, T, a.d, &a, static_cast<float *>(h), token, s);
     else
-        make_blocks(a, a.h, T, &a, static_cast<uint16_t *>(h), token, s);
-    const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, T, d);
+        make_blocks(a, a.h, T, &a, static_cast<uint16_t *>(h), token, s, stack ? pp : 1);
+    const int64_t p_rows = stack ? pp * T : T;
+    const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, p_rows, d);
     int64_t piece = piece_for(V, p_bytes(a) * round64(T));
     if (bw) piece = std::min(piece, piece_for(V, round64(d) * (parts ? 6 : 2)));
     const bool one_piece = piece >= V;
     Cut cut_h{};
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         const int64_t n = std::min(piece, V - v0), ld = round64(n);
-        const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, T, n);
+        const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, p_rows, n);
         const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
         if (bw) make_blocks(a, rows, n, nullptr, wp, nullptr, s);
         const Operand ow = bw ? blocks_of(wp, n, d) : rows_of(rows, n, d);
@@ -1436,16 +1468,17 @@ void backward(const LossArgs &a, hipStream_t s) {
                 float *x = reinterpret_cast<float *>(ws + L.few);
                 const int64_t ldx = round8(V);
                 split_steps(g, ceil_div(d, step_of<E>()), few.splits);
-                gemm<E, false, false>(g, SumEnd{x, ldx, T * ldx, false, false, nullptr, 0}, few.tile, s);
+                gemm<E, false, false>(g, SumEnd<false>{x, ldx, T * ldx, false, false, nullptr, 0}, few.tile, s);
                 launch_kernel(few_grad_kernel, dim3((unsigned)ceil_div((F32 ? T : round64(T)) * ld, 256)), dim3(256), s, x,
-                              g.splits, T * ldx, ldx, T, a.vocab, a.scale, token, p, op.row64, op.part, ld, pp, F32);
+                              g.splits, T * ldx, ldx, T, a.vocab, a.scale, token, p, op.row64, op.part, ld, pp, stack ? T : 0, F32);
             } else {
                 whole<E>(g);
-                gemm<E, false, false>(g, GradEnd{a.scale, token, p, op.row64, op.part, ld, pp, v0}, few.tile, s);
+                gemm<E, false, false>(g, GradEnd{a.scale, token, p, op.row64, op.part, ld, pp, v0, stack ? T : 0}, few.tile, s);
             }
         }
         if (a.dh) {
-            g.M = T;
+            const int64_t M = (stack ? 2 : 1) * T;
+            g.M = M;
             g.N = d;
             g.K = n;
             g.a = op;
@@ -1453,28 +1486,34 @@ void backward(const LossArgs &a, hipStream_t s) {
             parts_of(g, hp, hp);
             // (the same cut for every piece: its sums go on from one to the next)
             if (v0 == 0)
-                cut_h = cut_for<E>(T, d, n, g.segs, std::min(kMostSplits, sum_bytes(T, a.d) / (T * d * 4)), a.bf16 ? 2 : 4);
+                cut_h = cut_for<E>(M, d, n, g.segs, std::min(kMostSplits, sum_bytes(T, a.d) / (M * d * 4)), a.bf16 ? 2 : 4);
             split_steps(g, ceil_div(n, step_of<E>()), cut_h.splits);
             if (v0 == 0) cut_h.splits = g.splits;
-            if (one_piece && cut_h.splits == 1)
-                gemm<E, false, true>(g, SumEnd{a.dh, d, 0, a.bf16, false, a.targets, a.vocab}, cut_h.tile, s);
+            if (one_piece && cut_h.splits == 1 && !stack)
+                gemm<E, false, true>(g, SumEnd<false>{a.dh, d, 0, a.bf16, false, a.targets, a.vocab}, cut_h.tile, s);
             else
-                gemm<E, false, true>(g, SumEnd{sum, d, T * d, false, v0 > 0, nullptr, 0}, cut_h.tile, s);
+                gemm<E, false, true>(g, SumEnd<false>{sum, d, M * d, false, v0 > 0, nullptr, 0}, cut_h.tile, s);
         }
         if (a.dw) {
             g.M = n;
             g.N = d;
-            g.K = T;
+            g.K = p_rows;
             g.a = op;
             g.b = oh;
-            parts_of(g, pp, hp);
-            const Cut cut = cut_for<E>(n, d, T, g.segs, std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4)),
-                                       a.dw_bf16 ? 2 : 4);
-            split_steps(g, ceil_div(T, step_of<E>()), cut.splits);
+            parts_of(g, stack ? 1 : pp, hp);
+            const int64_t most = std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4));
+            Cut cut = cut_for<E>(n, d, p_rows, g.segs, most, a.dw_bf16 ? 2 : 4);
+            const Cut walk = cut_for<E>(n, d, p_rows, g.segs, 1, 4, true);
+            const bool walks = !a.dw_bf16 && walk.cost < cut.cost;
+            if (walks) cut = walk;
+            split_steps(g, ceil_div(p_rows, step_of<E>()), cut.splits);
             char *out = static_cast<char *>(a.dw) + v0 * d * (a.dw_bf16 ? 2 : 4);
             const bool split = g.splits > 1;
-            gemm<E, true, true>(g, SumEnd{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16,
-                                          !split && a.accumulate, nullptr, 0}, cut.tile, s);
+            if (walks)
+                gemm<E, true, true>(g, SumEnd<true>{out, d, 0, false, a.accumulate, nullptr, 0}, cut.tile, s);
+            else
+                gemm<E, true, true>(g, SumEnd<false>{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16,
+                                                     !split && a.accumulate, nullptr, 0}, cut.tile, s);
             if (split) {
                 const dim3 grid((unsigned)std::min<int64_t>((n * d / 8 + 255) / 256, 1 << 20));
                 if (a.dw_bf16)
@@ -1487,9 +1526,9 @@ void backward(const LossArgs &a, hipStream_t s) {
             }
         }
     }
-    if (a.dh && !(one_piece && cut_h.splits == 1)) {
+    if (a.dh && !(one_piece && cut_h.splits == 1 && !stack)) {
         const dim3 grid((unsigned)std::min<int64_t>((T * d / 8 + 255) / 256, 1 << 20));
-        const int32_t splits = (int32_t)cut_h.splits;
+        const int32_t splits = (int32_t)cut_h.splits * (stack ? 2 : 1);  // (a split's two parts of P follow each other)
         if (a.bf16)
             launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, sum, splits, T * d, T, a.d, a.targets, a.vocab,
                           static_cast<uint16_t *>(a.dh), false);

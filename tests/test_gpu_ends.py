@@ -74,14 +74,15 @@ class HeadRef:
             out[2][at], out[3][at] = 2 * off + 4 * U * xy.abs(), off
         return out
 
-    def backward(self, lse, g, dw_dtype):
-        """dh, dW and their bounds, from the lse that the kernel is given."""
+    def backward(self, lse, g, dw_dtype, p_bits=8):
+        """dh, dW and their bounds, from the lse that the kernel is given.  p_bits: of a
+        bf16 plan's P, for dh and a bf16 dW."""
         n, V, d = len(self.y), self.V, self.d
         dev = self.h.device
         dh, dh_off = (torch.zeros((n, d), dtype=torch.float64, device=dev) for _ in range(2))
         dw, dw_off = (torch.zeros((V, d), dtype=torch.float64, device=dev) for _ in range(2))
-        rh = 2.0 ** -8 if self.dtype == "bf16" else 2.0 ** -22  # what P's parts leave out, and the products of parts
-        rw = 2.0 ** -22 if self.dtype == "f32" else 2.0 ** -8 if dw_dtype == torch.bfloat16 else 2.0 ** -16
+        rh = 2.0 ** -p_bits if self.dtype == "bf16" else 2.0 ** -22  # what P's parts leave out, and the products of parts
+        rw = 2.0 ** -22 if self.dtype == "f32" else 2.0 ** -p_bits if dw_dtype == torch.bfloat16 else 2.0 ** -16
         sh, sw = chain(V, self.segs) + 40, chain(n, 6 if self.dtype == "f32" else 2) + 40
         for at in self.counts.nonzero()[:, 0].split(1024):
             x, e = self.logits(at)
@@ -157,6 +158,30 @@ def test_cross_entropy_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale):
     assert torch.allclose(dw2.double(), 2 * dw.double(), rtol=2.0 ** -7 if dw_dtype == torch.bfloat16 else 1e-5,
                           atol=2e-5 * float(dw.double().abs().max()) if dw_dtype == torch.float32 else
                           2.0 ** -8 * float(dw.double().abs().max()))
+
+
+@pytest.mark.parametrize("dw_dtype", (torch.bfloat16, torch.float32))
+@pytest.mark.parametrize("n_tok", (1, 3, 20, 21, 22))
+@pytest.mark.parametrize("vocab,d", [(1, 8), (77, 72), (300, 4104), (9001, 264), (40000, 64)])
+def test_few_tokens_keep_two_parts_of_p(gpu, vocab, d, n_tok, dw_dtype):
+    """Two roundings to bf16 in turn leave 2^-16 of P, up to 21 tokens; one alone 2^-8."""
+    p = make_plan("bf16", d, vocab)
+    h, w, y = head("bf16", n_tok, vocab, d, 1.0, 5, gpu)
+    y[n_tok // 2] = -1  # (its h reaches nothing)
+    ref = HeadRef(h, w, y, 1.0, "bf16")
+    lse, g = ref.forward()[1].float(), torch.rand(n_tok, generator=gen(8)).to(gpu)
+    h[n_tok // 2] = math.nan
+    dh, dw = nan_like(torch.empty_like(h)), Guarded((vocab, d), dw_dtype, gpu)
+    ws = Guarded((p.engram_cross_entropy_backward_workspace_size(n_tok, dw_dtype),), torch.uint8, gpu)
+    p.engram_cross_entropy_backward(h, w, y, lse, g, dh, dw.t, ws.t)
+    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse, g, dw_dtype, p_bits=16 if n_tok <= 21 else 8))
+    close(dh, rdh, off_h, "dh")
+    close(dw.t, rdw, off_w, "dw")
+    once = dw.t.clone()
+    p.engram_cross_entropy_backward(h, w, y, lse, g, None, dw.t, ws.t, flags=8)
+    assert torch.equal(dw.t, 2 * once) or dw_dtype == torch.bfloat16
+    torch.cuda.synchronize()
+    assert dw.whole() and ws.whole()
 
 
 @pytest.mark.parametrize("dtype,dw_dtype", GRADS)
@@ -337,7 +362,7 @@ def test_cross_entropy_past_32_bits(gpu):
 def test_cross_entropy_in_the_largest_batchs_workspace(gpu, dtype, dw_dtype):
     p = make_plan(dtype, 136, 3000)
     big = p.cross_entropy_workspace(5000), p.cross_entropy_backward_workspace(5000, dw_dtype)
-    for n_tok in (1, 65, 700, 2049):
+    for n_tok in (1, 21, 22, 65, 700, 2049):
         h, w, y = head(dtype, n_tok, 3000, 136, 1.0, 3, gpu)
         res = []
         for f, b in (big, (p.cross_entropy_workspace(n_tok), p.cross_entropy_backward_workspace(n_tok, dw_dtype))):
