@@ -123,7 +123,8 @@ __device__ __forceinline__ int steps_in(const GemmArgs &g, int split) {
 // 8 a + b (a, b < 4), at c ^ (r / 2 % 2 + r / 8 % 4 * 2).
 // Across: rows of k of T values.  bf16: the 32-byte granules XOR-swizzled by k, so that
 // the eight rows that half a wave reads at a time (k % 4 and k / 8 % 2 vary) lie
-// in distinct banks.  fp32: the 64-byte ones, by k / 4 % 4.
+// in distinct banks.  fp32: the 64-byte ones, by k / 4 (two of four then share
+// their banks where a row has two: a tile of 32).
 // A leg is the stages of one item and product of parts.  What issue() does after
 // its loads is branch-free, so that it is scheduled between multiplications; the
 // leg after the present one is worked out in turn(), called between steps at
@@ -167,7 +168,7 @@ struct Feed {
             }
         } else {
             constexpr int kRowBytes = T * (int)sizeof(E), kLanes = kRowBytes / 16;  // lanes of a row of k
-            static_assert(sizeof(E) == 2 || T == 64, "fp32 tiles");
+            static_assert(sizeof(E) == 2 || T <= 64, "fp32 tiles");
             lk = 0;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -177,7 +178,7 @@ struct Feed {
                     const int f = T == 64 ? ((k >> 1) & 1) | ((k >> 3) & 1) << 1 : (k & 3) | ((k >> 3) & 1) << 2;
                     piece = place ^ (f << 1);
                 } else {
-                    piece = place ^ ((k >> 2) & 3) << 2;
+                    piece = place ^ ((k >> 2) & (T / 16 - 1)) << 2;
                 }
                 const int col = piece * (16 / (int)sizeof(E));
                 off[i] = (uint32_t)(((col >> 6) * o.col64 + (col & 63) + k * o.row) * (int64_t)sizeof(E));
@@ -200,10 +201,10 @@ struct Feed {
             const int64_t r0 = is_a ? m0 : n0, part = (int64_t)((parts >> (4 * seg)) & 15u) * o.part;
             l.kb = split * g.split_steps;
             l.left = steps_in<E>(g, split);
-            // (kStep divides 64, and a tile starts at a multiple of 64)
-            const int64_t k = (int64_t)l.kb * kStep;
-            const int64_t at = ACROSS ? (r0 >> 6) * o.col64 + (k >> 6) * o.row64 + (k & 63) * o.row
-                                      : (r0 >> 6) * o.row64 + (k >> 6) * o.col64 + (k & 63);
+            // (kStep divides 64; a tile starts at a multiple of 64, or in the middle of two)
+            const int64_t k = (int64_t)l.kb * kStep, r = T < 64 ? r0 & 63 : 0;
+            const int64_t at = ACROSS ? (r0 >> 6) * o.col64 + r + (k >> 6) * o.row64 + (k & 63) * o.row
+                                      : (r0 >> 6) * o.row64 + r * o.row + (k >> 6) * o.col64 + (k & 63);
             l.at = (part + at) * (int64_t)sizeof(E);
             l.bytes = (o.size - at) * (int64_t)sizeof(E);
         }
@@ -272,7 +273,7 @@ struct Reader {
             p1 = T == 64 ? (q >> 1) | (g & 1) << 1 : q | (g & 1) << 2;
         } else {
             p0 = 4 * g * (4 * T) + fr * 4;
-            p1 = g;
+            p1 = g & (T / 16 - 1);
         }
     }
     template <int H>
@@ -354,11 +355,12 @@ struct LseEnd {
         for (int j = 0; j < FM; ++j) {
             if (!__any(y[j] >= 0)) continue;
             float at_y = 0.f;
+            const int32_t mine = y[j] - nl;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (y[j] == 16 * i + nl + r) at_y = acc[i][j][r] * scale;
+                    if (mine == 16 * i + r) at_y = acc[i][j][r] * scale;
             if (y[j] >= 0 && ((y[j] >> 2) & 3) == (lane >> 4)) xt[m0 + 16 * j + (lane & 15)] = at_y;
         }
         float c = scale * kLog2e;
@@ -370,11 +372,12 @@ struct LseEnd {
                 for (int j = 0; j < FM; ++j) acc[i][j] = -acc[i][j];
         }
         if (n0 + 16 * FN > g.N) {
+            const int32_t left = (int32_t)max(g.N - n0, (int64_t)0) - nl;
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (n0 + nl + 16 * i + r >= g.N)
+                    if (16 * i + r >= left)
 #pragma unroll
                         for (int j = 0; j < FM; ++j) acc[i][j][r] = -INFINITY;
         }
@@ -667,9 +670,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
     const Reader<E, T, BX, PAIRS> rb(lane);
     const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
 
-    // (64 x 64: sums of their own for each half of a stage, in fp32 for each
+    // (64 x 64 and less: sums of their own for each half of a stage, in fp32 for each
     // instruction of it, so that long rows round less)
-    constexpr int SETS = T != 64 ? 1 : sizeof(E) == 2 ? 2 : 8;
+    constexpr int SETS = T > 64 ? 1 : sizeof(E) == 2 ? 2 : 8;
     f32x4_t acc[SETS][FN][FM] = {};
     struct Half {
         u32x4_t a[FM], b[FN];
@@ -1071,21 +1074,41 @@ __global__ __launch_bounds__(256) void few_grad_kernel(const float *x, int32_t s
 }
 
 // out[m][i] (+)= sum over the splits, in order, rounded to the output's type;
-// rows of tokens that do not count are zeros (targets given).
-template <typename T>
+// rows of tokens that do not count are zeros (targets given).  SHARE threads of a
+// workgroup take every SHARE-th split each, where few values come in many splits: the
+// time is that of loads one behind the other (64 splits of 2560 values 13 -> 5 us).
+template <typename T, int SHARE>
 __global__ __launch_bounds__(256) void sum_join_kernel(const float *part, int32_t splits, int64_t split_elems,
                                                        int64_t rows, int32_t d, const int32_t *targets, int32_t vocab,
                                                        T *out, bool accumulate) {
     const int32_t units = d / 8;
     const int64_t n = rows * units;
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
-        F8 v = load8(part + u * 8);
+    constexpr int kUnits = 256 / SHARE;
+    const int first = threadIdx.x / kUnits, mine = threadIdx.x % kUnits;
+    for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < n; u0 += (int64_t)gridDim.x * kUnits) {
+        const int64_t u = u0 + mine;
+        F8 v = {};
+        if (u < n) {
+            if (first < splits) v = load8(part + first * split_elems + u * 8);
 #pragma unroll 8
-        for (int32_t z = 1; z < splits; ++z) {  // (eight loads in flight)
-            const F8 w = load8(part + z * split_elems + u * 8);
+            for (int32_t z = first + SHARE; z < splits; z += SHARE) {  // (eight loads in flight)
+                const F8 w = load8(part + z * split_elems + u * 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v.v[i] += w.v[i];
+                for (int i = 0; i < 8; ++i) v.v[i] += w.v[i];
+            }
         }
+        if constexpr (SHARE > 1) {
+            __shared__ F8 red[SHARE][kUnits];
+            __syncthreads();  // (the last units' sums are read)
+            red[first][mine] = v;
+            __syncthreads();
+            if (first > 0) continue;
+#pragma unroll
+            for (int z = 1; z < SHARE; ++z)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v.v[i] += red[z][mine].v[i];
+        }
+        if (u >= n) continue;
         if (targets) {
             const int32_t id = targets[quotient(u, units)];
             if (id < 0 || id >= vocab) v = F8{};
@@ -1113,7 +1136,10 @@ constexpr int64_t step_of() {
 // 0.44 with two of 64 x 64 (0.30), and at its start and end a few us more, which
 // grow with the bytes of a result.  (A 256 x 256 tile's 1.33 PFLOP/s are 1.05 of
 // 128 x 128 and 0.53 of 64 x 64; but 96 tiles of 64 x 64 are six of 256 x 256.)
-// Parts of K cost a second launch that joins them.  fp32 tiles are 64 x 64.
+// fp32 tiles are 64 x 64 (0.95, 0.55) or 32 x 32 (0.58, 0.36): 33 tokens x 1000 x 256
+// are 16 of the one or 64 of the other, 13.4 us against 10.0.  Parts of K cost a
+// second launch that joins them.  Against the best of each tile forced, and of
+// parts or none, the choice loses 5% and less in 100 drawn shapes but two (8%).
 struct Cut {
     int tile;
     int64_t splits;
@@ -1123,7 +1149,7 @@ struct Cut {
 // (the parts of a token's sums, whose number goes with the tile, stay few: loss_layout)
 bool may_tile(int tile, int64_t M, int64_t N) {
     const int64_t items = ceil_div(M, tile) * ceil_div(N, tile);
-    return tile == 256 || (tile == 128 ? items <= 2048 : M <= 64 || items <= 1024);
+    return tile == 256 || (tile == 128 ? items <= 2048 : tile == 64 ? M <= 64 || items <= 1024 : items <= 512);
 }
 
 template <class E>
@@ -1132,24 +1158,29 @@ Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_byt
         int tile;
         double one, two, start1, start2, byte1, byte2;
     };
-    static constexpr Rate kRates[3] = {{64, 0.30, 0.44, 3., 4., 0.25, 0.5},
-                                       {128, 0.62, 0.92, 5., 6., 0.7, 1.3},
-                                       {256, 1.48, 1.48, 5., 5., 2.3, 2.3}};
+    constexpr bool F32 = sizeof(E) == 4;
+    static constexpr Rate kRates16[3] = {{64, 0.30, 0.44, 3., 4., 0.25, 0.5},
+                                         {128, 0.62, 0.92, 5., 6., 0.7, 1.3},
+                                         {256, 1.48, 1.48, 5., 5., 2.3, 2.3}};
+    // (a stage of fp32: 32 k at a sixteenth of the rate)
+    static constexpr Rate kRates32[2] = {{32, 0.36, 0.58, 3., 4., 0.1, 0.2}, {64, 0.55, 0.95, 4., 5., 0.25, 0.5}};
+    auto &rates = [&]() -> auto & {
+        if constexpr (F32) return kRates32;
+        else return kRates16;
+    }();
     Cut best{64, 1, 1e30};
     const int64_t steps = ceil_div(K, step_of<E>());
-    for (const Rate &r : kRates) {
-        if ((walks ? r.tile == 256 : !may_tile(r.tile, M, N)) || (sizeof(E) == 4 && r.tile != 64)) continue;
-        // (an fp32 stage: 32 k at a sixteenth of the bf16 rate)
-        const double one = sizeof(E) == 4 ? 0.5 : r.one, two = sizeof(E) == 4 ? 0.95 : r.two;
+    for (const Rate &r : rates) {
+        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile(r.tile, M, N)) continue;
         const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
         for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
             const int64_t items = tiles * n, full = items / slots, rest = items % slots;
             const double each = (double)((walks ? ceil_div(steps, 2) * 2 : ceil_div(steps, n)) * segs);
             const int bytes = n > 1 ? 4 : out_bytes;
             const double less = walks ? 0.6 : 1.;  // (the next item's first stages land while one ends)
-            double t = (double)full * (each * two + less * (r.start2 + r.byte2 * bytes));
+            double t = (double)full * (each * r.two + less * (r.start2 + r.byte2 * bytes));
             if (rest > 0)
-                t += rest <= 256 ? each * one + less * (r.start1 + r.byte1 * bytes) : each * two + less * (r.start2 + r.byte2 * bytes);
+                t += rest <= 256 ? each * r.one + less * (r.start1 + r.byte1 * bytes) : each * r.two + less * (r.start2 + r.byte2 * bytes);
             if (n > 1) t += 4. + (double)(n * M) * (double)N * 4. / 4.5e6;
             if (t < best.cost * 0.98) best = Cut{r.tile, n, t};
         }
@@ -1165,8 +1196,13 @@ void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
     constexpr int NA = End::kImage ? 3 : 2;
     constexpr bool SHORT = std::is_same<End, SumEnd<true>>::value;  // few stages an item: two of each do
     constexpr int NS = SHORT ? 2 : 4;
-    g.round = End::kImage ? 1 : tile == 64 ? NS : 2;
+    g.round = End::kImage ? 1 : tile <= 64 ? NS : 2;
     if constexpr (sizeof(E) == 4) {
+        if constexpr (!SHORT)
+            if (tile == 32) {
+                launch_kernel((gemm_kernel<E, End, 32, 2, 2, NS, NS, AX, BX>), dim3(grid), dim3(256), s, g, end);
+                return;
+            }
         launch_kernel((gemm_kernel<E, End, 64, 2, 2, NS, NS, AX, BX>), dim3(grid), dim3(256), s, g, end);
     } else {
         if constexpr (!SHORT)
@@ -1201,12 +1237,13 @@ void make_blocks(const LossArgs &a, const void *x, int64_t rows, const LossArgs 
         make_parts<float, uint16_t, 3>(x, rows, a.d, mask, out, token, s);
 }
 
-// Products of parts: all pairs whose weight is 2^-16 and more, the lightest first,
-// so that only the last one's sums are rounded at their full size.
-void parts_of(GemmArgs &g, int a_parts, int b_parts) {
+// Products of parts: all pairs (i, j) with i + j up to `most` (2: weights of 2^-16 in
+// bf16; 1: of 2^-11 in fp16, whose two smaller parts' is 2^-22), the lightest first, so
+// that only the last one's sums are rounded at their full size.
+void parts_of(GemmArgs &g, int a_parts, int b_parts, int most = 2) {
     g.segs = 0;
     g.a_parts = g.b_parts = 0;
-    for (int w = 2; w >= 0; --w)
+    for (int w = most; w >= 0; --w)
         for (int i = 0; i < a_parts; ++i) {
             const int j = w - i;
             if (j < 0 || j >= b_parts) continue;
@@ -1265,12 +1302,12 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 // reading of W takes (some 100 tokens' products), and where V is small their
 // launches (a time of its own) and, forward, tiles of too few workgroups along
 // all of d.  Measured, us, instructions of fp32 against parts: forward 59 tokens x
-// 61016 x 2832 237 : 567, 517 x 32000 x 1024 373 : 220, 1000 x 773 x 5952 135 : 144,
-// 2500 x 1000 x 256 25 : 28, 6000 x 1000 x 256 44 : 35; backward 59 x 61016 x 2832
+// 61016 x 2832 236 : 525, 517 x 32000 x 1024 374 : 185, 521 x 773 x 5952 78 : 117,
+// 1000 x 773 x 5952 134 : 118, 2500 x 1000 x 256 25 : 26, 6000 x 1000 x 256 44 : 32; backward 59 x 61016 x 2832
 // 850 : 1374, 275 x 22940 x 1496 711 : 571, 521 x 773 x 5952 214 : 175,
 // 1000 x 1000 x 256 45 : 59.
 bool direct32(const LossArgs &a, bool forward) {
-    return forward ? (a.n_tok - 130) * a.vocab <= 600000000 / a.d + 550000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
+    return forward ? (a.n_tok - 100) * a.vocab <= 600000000 / a.d + 400000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
 }
 
 // Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
@@ -1304,7 +1341,10 @@ Cut few_cut(const LossArgs &a, const GemmArgs &g, int out_bytes) {
     const int64_t one = a.n_tok * round8(a.vocab) * 4;
     if (one > kFewBytes / 2 || g.N > kFewThreads * kFewEach || ceil_div(g.M, 64) * ceil_div(g.N, 64) > 128) return whole;
     const Cut parts = cut_for<E>(g.M, g.N, g.K, g.segs, few_bytes(a) / one, 4);
-    return parts.splits > 1 && parts.cost + 5. < whole.cost ? parts : whole;
+    // (the forward's maxima and sums are joined by a launch of their own anyway, which
+    // takes less than one of a workgroup for each token)
+    const double more = out_bytes ? 1. : (double)a.n_tok / 200 - 3.;
+    return parts.splits > 1 && parts.cost + more < whole.cost ? parts : whole;
 }
 
 }  // namespace
@@ -1323,7 +1363,7 @@ LossLayout loss_layout(const LossArgs &a) {
         return (size_t)o;
     };
     L.xt = take(T * 4);
-    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2),
+    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2), std::min<int64_t>(2 * T * n32, 512 * 32 * 2),
                                 std::min<int64_t>(T * n64, 2048 * 128 * 2)}));
     L.few = take(few_bytes(a));
     const int64_t each = a.bf16 ? 2 : 4;
@@ -1366,6 +1406,20 @@ bool loss_fits(int64_t n_tok, int32_t vocab, int32_t d) {
 
 namespace {
 
+void join_sums(const float *part, int64_t splits, int64_t split_elems, int64_t rows, int32_t d, const int32_t *targets,
+               int32_t vocab, bool bf16, void *out, bool accumulate, hipStream_t s) {
+    const int64_t units = rows * d / 8;
+    const bool share = splits >= 16 && units <= 32768;
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(units, share ? 32 : 256), 1 << 20));
+    auto go = [&](auto kernel, auto *to) {
+        launch_kernel(kernel, grid, dim3(256), s, part, (int32_t)splits, split_elems, rows, d, targets, vocab, to, accumulate);
+    };
+    if (bf16)
+        go(share ? sum_join_kernel<uint16_t, 8> : sum_join_kernel<uint16_t, 1>, static_cast<uint16_t *>(out));
+    else
+        go(share ? sum_join_kernel<float, 8> : sum_join_kernel<float, 1>, static_cast<float *>(out));
+}
+
 template <class E>
 void forward(const LossArgs &a, hipStream_t s) {
     constexpr bool F32 = sizeof(E) == 4, F16 = std::is_same<E, _Float16>::value;
@@ -1375,7 +1429,7 @@ void forward(const LossArgs &a, hipStream_t s) {
     GemmArgs g{};
     g.M = T;
     g.K = d;
-    parts_of(g, F16 ? 2 : 1, F16 ? 2 : 1);
+    parts_of(g, F16 ? 2 : 1, F16 ? 2 : 1, 1);
     const bool bh = F16 || (!F32 && blocks_h(a)), bw = F16 || (!F32 && blocks_w(a, true));
     const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
@@ -1514,28 +1568,11 @@ void backward(const LossArgs &a, hipStream_t s) {
             else
                 gemm<E, true, true>(g, SumEnd<false>{split ? static_cast<void *>(wsum) : out, d, n * d, !split && a.dw_bf16,
                                                      !split && a.accumulate, nullptr, 0}, cut.tile, s);
-            if (split) {
-                const dim3 grid((unsigned)std::min<int64_t>((n * d / 8 + 255) / 256, 1 << 20));
-                if (a.dw_bf16)
-                    launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, wsum, g.splits, n * d, n, a.d,
-                                  static_cast<const int32_t *>(nullptr), 0, reinterpret_cast<uint16_t *>(out),
-                                  a.accumulate);
-                else
-                    launch_kernel(sum_join_kernel<float>, grid, dim3(256), s, wsum, g.splits, n * d, n, a.d,
-                                  static_cast<const int32_t *>(nullptr), 0, reinterpret_cast<float *>(out), a.accumulate);
-            }
+            if (split) join_sums(wsum, g.splits, n * d, n, a.d, nullptr, 0, a.dw_bf16, out, a.accumulate, s);
         }
     }
-    if (a.dh && !(one_piece && cut_h.splits == 1 && !stack)) {
-        const dim3 grid((unsigned)std::min<int64_t>((T * d / 8 + 255) / 256, 1 << 20));
-        const int32_t splits = (int32_t)cut_h.splits * (stack ? 2 : 1);  // (a split's two parts of P follow each other)
-        if (a.bf16)
-            launch_kernel(sum_join_kernel<uint16_t>, grid, dim3(256), s, sum, splits, T * d, T, a.d, a.targets, a.vocab,
-                          static_cast<uint16_t *>(a.dh), false);
-        else
-            launch_kernel(sum_join_kernel<float>, grid, dim3(256), s, sum, splits, T * d, T, a.d, a.targets, a.vocab,
-                          static_cast<float *>(a.dh), false);
-    }
+    if (a.dh && !(one_piece && cut_h.splits == 1 && !stack))  // (a split's two parts of P follow each other)
+        join_sums(sum, cut_h.splits * (stack ? 2 : 1), T * d, T, a.d, a.targets, a.vocab, a.bf16, a.dh, false, s);
 }
 
 }  // namespace
