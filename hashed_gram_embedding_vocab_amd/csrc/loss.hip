@@ -882,14 +882,23 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
 // Two fp16 parts of x's rows over their units, in blocks: a row's unit is the power
 // of two over which its largest value lies in [2^14, 2^15), so that the parts hold
 // 22 bits of whatever is not below 2^-18 of that, and 2^-40 of it otherwise.  One
-// wave a row.
-__global__ __launch_bounds__(256) void half_parts_kernel(const float *x, int64_t rows, int32_t d, _Float16 *out,
-                                                         float *unit) {
+// wave a row, of one matrix or behind it of a second one (no rows: none).
+struct Halves {
+    const float *x;
+    int64_t rows, all;         // with those up to whole blocks
+    _Float16 *out;
+    float *unit;
+};
+__global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves second, int32_t d) {
     const int lane = threadIdx.x & 63;
     const int32_t cols = (d + kBlock - 1) / kBlock * kBlock;
-    const int64_t all = (rows + kBlock - 1) / kBlock * kBlock;
     typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < all; r += (int64_t)gridDim.x * 4) {
+    for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < first.all + second.all; at += (int64_t)gridDim.x * 4) {
+        const bool one = at < first.all;
+        const float *const x = one ? first.x : second.x;
+        _Float16 *const out = one ? first.out : second.out;
+        float *const unit = one ? first.unit : second.unit;
+        const int64_t r = one ? at : at - first.all, rows = one ? first.rows : second.rows, all = one ? first.all : second.all;
         uint32_t top = 0u;
         if (r < rows)
             for (int32_t c = lane * 8; c < d; c += 512) {
@@ -1434,16 +1443,12 @@ void forward(const LossArgs &a, hipStream_t s) {
     const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
     float *h_unit = reinterpret_cast<float *>(ws + L.unit), *w_unit = h_unit + round64(T);
-    auto copy = [&](const void *x, int64_t rows, uint16_t *out, float *unit) {
-        if constexpr (F16)
-            launch_kernel(half_parts_kernel, dim3((unsigned)std::min<int64_t>(round64(rows) / 4, 1 << 20)), dim3(256), s,
-                          static_cast<const float *>(x), rows, a.d, reinterpret_cast<_Float16 *>(out), unit);
-        else
-            make_blocks(a, x, rows, nullptr, out, nullptr, s);
+    auto halves = [&](const void *x, int64_t rows, uint16_t *out, float *unit) {
+        return Halves{static_cast<const float *>(x), rows, round64(rows), reinterpret_cast<_Float16 *>(out), unit};
     };
     g.N = std::min(piece, V);
     const Cut few = F16 ? cut_for<E>(T, g.N, d, g.segs, 1, 0) : few_cut<E>(a, g, 0);
-    if (bh) copy(a.h, T, h, h_unit);
+    if (bh && !F16) make_blocks(a, a.h, T, nullptr, h, nullptr, s);
     g.a = bh ? blocks_of(h, T, d) : rows_of(a.h, T, d);
     if constexpr (!F16) {
         if (few.splits > 1) {
@@ -1464,7 +1469,13 @@ void forward(const LossArgs &a, hipStream_t s) {
         g.N = std::min(piece, V - v0);
         end.v0 = v0;
         const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
-        if (bw) copy(rows, g.N, w, w_unit);
+        if constexpr (F16) {  // (and h with the first piece)
+            const Halves hh = v0 == 0 ? halves(a.h, T, h, h_unit) : Halves{}, hw = halves(rows, g.N, w, w_unit);
+            launch_kernel(half_parts_kernel, dim3((unsigned)std::min<int64_t>((hh.all + hw.all) / 4, 1 << 20)), dim3(256), s,
+                          hh, hw, a.d);
+        } else if (bw) {
+            make_blocks(a, rows, g.N, nullptr, w, nullptr, s);
+        }
         g.b = bw ? blocks_of(w, g.N, d) : rows_of(rows, g.N, d);
         gemm<E, false, false>(g, end, few.tile, s);
     }
