@@ -420,7 +420,8 @@ class GradList:
     itself (outs=None: all in place), another one like it, or None (only its norm
     counts).  row_counts: for each tensor None, or an int32 tensor [n_groups] on
     the device for a tensor [n_groups][rows][...]: of every group only so many
-    rows, the first, take part (Grads.row_grads with Grads.row_counts)."""
+    rows, the first, take part (Grads.row_grads with Grads.row_counts).  The list
+    holds the tensors' addresses: make it anew if one gets other memory."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[Optional[torch.Tensor]]] = None,
                  row_counts: Optional[Sequence[Optional[torch.Tensor]]] = None):
@@ -818,8 +819,8 @@ class Plan:
                                       dloss_scale: float = 1.0, flags: int = 0, stream=None):
         """dh (plan dtype) and dweight (fp32, or bf16 in bf16 plans), either of them
         None where it is not wanted, from the forward's lse and each token's loss
-        gradient dloss (fp32; None: ones) times dloss_scale; flags=GRAD_ACCUMULATE
-        adds to dweight."""
+        gradient dloss (fp32; None: ones; 0: the token has no part) times dloss_scale;
+        flags=GRAD_ACCUMULATE adds to dweight."""
         dt, f32 = self.torch_dtype, torch.float32
         n_tok = self._rows(h, "h")
         # without dweight the smaller workspace does

@@ -246,6 +246,7 @@ struct Feed {
 };
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16_t lds_v4i16_t;
@@ -317,7 +318,7 @@ struct LseEnd {
     float *xt;                 // [n_tok]
     float2 *part;              // [columns / (16 FN)][n_tok]
     int64_t v0;                // the first column's id
-    const float *a_unit, *b_unit;  // fp16 operands: the units of their rows
+    const int32_t *a_unit, *b_unit;  // fp16 operands: the units of their rows (powers of two)
     template <int FM>
     struct Row {
         int32_t id[FM];
@@ -340,14 +341,17 @@ struct LseEnd {
             y[j] = m < g.M && at >= 0 && at < 16 * FN && n0 + at < g.N ? (int32_t)at : -1;
         }
         if constexpr (std::is_same<E, _Float16>::value) {
-            float u[FM];
+            int32_t u[FM];
 #pragma unroll
             for (int j = 0; j < FM; ++j) u[j] = a_unit[min(m0 + 16 * j + (lane & 15), g.M - 1)];
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
-                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(b_unit + min(n0 + nl + 16 * i, (g.N - 1) & ~(int64_t)3));
+                const i32x4_t v = *reinterpret_cast<const i32x4_t *>(b_unit + min(n0 + nl + 16 * i, (g.N - 1) & ~(int64_t)3));
+                // (one of the two alone may pass the range of fp32, where the logit does not)
 #pragma unroll
-                for (int j = 0; j < FM; ++j) acc[i][j] *= v * u[j];
+                for (int j = 0; j < FM; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_amdgcn_ldexpf(acc[i][j][r], v[r] + u[j]);
                 if (i % 2) __builtin_amdgcn_sched_barrier(0);  // (not all units' registers at once)
             }
         }
@@ -459,6 +463,12 @@ struct GradEnd {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (y == col(i) + r) acc[i][j][r] -= 1.f;
+            }
+            if (__any(f == 0.f)) {  // (nothing, whatever their logits are)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = f == 0.f ? 0.f : acc[i][j][r];
             }
 #pragma unroll
             for (int i = 0; i < FN; ++i) acc[i][j] *= f;
@@ -842,8 +852,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 
 // ---------------------------------------------------------------- the rest
 // Copies of x [rows][d] for the products: parts in bf16 in blocks, or (T = Out = float,
-// one part) whole rows of fp32; zeros in the rows of tokens that do not count
-// (targets given) and up to whole blocks.  Beside it the tokens' constants.
+// one part) whole rows of fp32; with targets, lse, dloss and token given zeros in the
+// rows of tokens that do not count or whose factor is 0, and the tokens' constants;
+// zeros up to whole blocks.
 template <typename T, typename Out, int PARTS>
 __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, int32_t d, const int32_t *targets,
                                                     int32_t vocab, Out *out, const float *lse, const float *dloss,
@@ -858,9 +869,9 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
         bool counts = r < rows;
         if (targets && counts) {
             const int32_t id = targets[r];
-            counts = id >= 0 && id < vocab;
-            if (token && c == 0 && copy == 0)
-                token[r] = counts ? Token{lse[r], (dloss ? dloss[r] : 1.f) * factor, id, 0} : Token{0.f, 0.f, -1, 0};
+            const float f = (dloss ? dloss[r] : 1.f) * factor;
+            counts = id >= 0 && id < vocab && f != 0.f;
+            if (c == 0 && copy == 0) token[r] = counts ? Token{lse[r], f, id, 0} : Token{0.f, 0.f, -1, 0};
         }
         F8 v = {};
         if (counts && c < d) v = load8(x + r * d + c);
@@ -887,7 +898,7 @@ struct Halves {
     const float *x;
     int64_t rows, all;         // with those up to whole blocks
     _Float16 *out;
-    float *unit;
+    int32_t *unit;             // exponents
 };
 __global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves second, int32_t d) {
     const int lane = threadIdx.x & 63;
@@ -897,7 +908,7 @@ __global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves se
         const bool one = at < first.all;
         const float *const x = one ? first.x : second.x;
         _Float16 *const out = one ? first.out : second.out;
-        float *const unit = one ? first.unit : second.unit;
+        int32_t *const unit = one ? first.unit : second.unit;
         const int64_t r = one ? at : at - first.all, rows = one ? first.rows : second.rows, all = one ? first.all : second.all;
         uint32_t top = 0u;
         if (r < rows)
@@ -914,7 +925,7 @@ __global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves se
         // exponents of the unit and its inverse, both normal numbers
         const int e = min(max((int)(top >> 23) - 14, 1), 253);
         const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-        if (lane == 0) unit[r] = __uint_as_float((uint32_t)e << 23);
+        if (lane == 0) unit[r] = e - 127;
         for (int32_t c = lane * 8; c < cols; c += 512) {
             F8 v = {};
             if (r < rows && c < d) v = load8(x + r * d + c);
@@ -1442,8 +1453,8 @@ void forward(const LossArgs &a, hipStream_t s) {
     const bool bh = F16 || (!F32 && blocks_h(a)), bw = F16 || (!F32 && blocks_w(a, true));
     const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
-    float *h_unit = reinterpret_cast<float *>(ws + L.unit), *w_unit = h_unit + round64(T);
-    auto halves = [&](const void *x, int64_t rows, uint16_t *out, float *unit) {
+    int32_t *h_unit = reinterpret_cast<int32_t *>(ws + L.unit), *w_unit = h_unit + round64(T);
+    auto halves = [&](const void *x, int64_t rows, uint16_t *out, int32_t *unit) {
         return Halves{static_cast<const float *>(x), rows, round64(rows), reinterpret_cast<_Float16 *>(out), unit};
     };
     g.N = std::min(piece, V);

@@ -634,7 +634,8 @@ ENGRAM_API engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const
  *                e8m0, or both NULL; one of d_y and d_q is wanted
  *   d_rrms       [n_rows] fp32 for the backward, or NULL
  * A row with an infinity or a NaN gives NaN throughout or zeros beside NaN, as
- * the formula has it (and its blocks' scales those of their finite values).
+ * the formula has it (and its blocks' scales those of their finite values); one whose squares' sum
+ * passes fp32's range gives zeros.
  * d_model above 32768: ENGRAM_E_UNSUPPORTED.
  */
 ENGRAM_API engram_status engram_rms_norm(engram_plan p, const void *d_x, const void *d_residual, int64_t n_rows,
@@ -678,11 +679,15 @@ ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s
  *   d_loss, d_lse  [n_tok] fp32 (natural logarithms)
  *   d_workspace  >= engram_cross_entropy_workspace_size(p, n) bytes for an
  *                n >= n_tok, 256-byte aligned
- * Logits and sums are fp32 (an fp32 plan's values are multiplied as three bf16
- * parts each, six products, with fp32 sums; they have to be finite).  A NaN in a
- * token's h, or in a weight, gives NaN losses.  n_tok above 2^27, vocab above
- * 2^22, d_model above 2^20 or 2^22 tiles of 256 x 256 logits and more:
+ * Logits and sums are fp32.  An fp32 plan's values are multiplied by the fp32
+ * matrix instructions where tokens or vocabulary are few, else in two fp16 parts
+ * over a power of two of each row's own (22 bits of what is not 2^-18 and more
+ * below the row's largest value), with fp32 sums.  A NaN in a token's h, or in a
+ * weight, gives NaN losses.  n_tok above 2^26, vocab above 2^22, d_model above
+ * 2^20, or 2^22 tiles of 256 x 256 and more of the logits or of the weights:
  * ENGRAM_E_UNSUPPORTED.
+ * The workspace holds the tiles' maxima and sums, the logits of a few tokens in
+ * parts of K (32 MB at most), copies of h, and 1 GB at most of W's.
  */
 /* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported sizes). */
 ENGRAM_API size_t engram_cross_entropy_workspace_size(engram_plan p, int64_t n_tok);
@@ -697,7 +702,9 @@ ENGRAM_API engram_status engram_cross_entropy(engram_plan p, const void *d_h, co
  *   P[t][v] = g_t * scale * (exp(x[t][v] - lse_t) - [v = target t]),  g_t = dloss_t * dloss_scale
  *   dh = P W,  dW = P^T h, over the tokens that count (the others' dh is 0)
  *   d_lse        as the forward wrote it
- *   d_dloss      [n_tok] fp32 gradient of each token's loss, or NULL: ones
+ *   d_dloss      [n_tok] fp32 gradient of each token's loss, or NULL: ones.  A
+ *                token whose g_t * scale is 0 has no part in either gradient,
+ *                whatever its h holds
  *   dloss_scale  finite factor of it (one over the number of tokens, a loss scale)
  *   flags        ENGRAM_GRAD_ACCUMULATE: add to d_dweight
  *   d_dh         [n_tok][d_model] plan dtype, or NULL
@@ -706,12 +713,16 @@ ENGRAM_API engram_status engram_cross_entropy(engram_plan p, const void *d_h, co
  *                engram_embed_backward's d_dtable; or bf16 (bf16 plans only)
  *   d_workspace  >= engram_cross_entropy_backward_workspace_size(p, n,
  *                dweight_dtype) bytes for an n >= n_tok, 256-byte aligned
- * For bf16 results P is rounded to bf16, as the operand beside it is; for an
- * fp32 d_dweight P is held in two bf16 parts (16 bits), and in an fp32 plan every
- * value in three.
+ * For bf16 results P is rounded to bf16, as the operand beside it is (to two bf16
+ * parts, 16 bits, of 21 tokens and less); for an fp32 d_dweight P is held in three
+ * bf16 parts, 24 bits.  In an fp32 plan every value is held in three, six products
+ * of parts, or multiplied by the fp32 matrix instructions where tokens or
+ * vocabulary are few.
  */
 /* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported
- * sizes; 1.3 GB and some copies of h at most, and 1 GB more in an fp32 plan). */
+ * sizes): P, 1 GB of it at most; dh's sums, 512 MB (or those of one part, where
+ * they are more), and dW's, 64 MB; the logits of a few tokens, 32 MB; copies of h;
+ * of 4096 tokens and more, or in an fp32 plan, copies of W, 1 GB at a time. */
 ENGRAM_API size_t engram_cross_entropy_backward_workspace_size(engram_plan p, int64_t n_tok, engram_dtype dweight_dtype);
 ENGRAM_API engram_status engram_cross_entropy_backward(engram_plan p, const void *d_h, const void *d_weight,
                                                        const int32_t *d_targets, int64_t n_tok, float scale,

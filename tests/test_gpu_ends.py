@@ -54,8 +54,9 @@ class HeadRef:
         self.counts = (self.y >= 0) & (self.y < self.V)
 
     def logits(self, at):
-        """Logits of tokens `at` and how far the kernel's may be off: sums, and the
-        5 u that products of three parts leave out."""
+        """Logits of tokens `at` and how far the kernel's may be off: sums, and what
+        products of parts leave out (5 u of three bf16 parts; 12 u of two fp16 parts,
+        whose sums are chains of three products and not of six)."""
         h = self.h[at]
         x = h @ self.w.t() * self.scale
         mag = h.abs() @ self.w.abs().t() * abs(self.scale)
@@ -218,6 +219,53 @@ def test_tokens_that_do_not_count_may_hold_anything(gpu, dtype, dw_dtype, n_tok,
         results.append((loss, lse, dh, dw))
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+@pytest.mark.parametrize("n_tok,vocab,d", PATHS)
+def test_tokens_whose_loss_has_no_gradient(gpu, dtype, dw_dtype, n_tok, vocab, d):
+    """dloss 0: no part in either gradient, whatever their h and lse hold."""
+    p = make_plan(dtype, d, vocab)
+    h, w, y = head(dtype, n_tok, vocab, d, 1.0, 3, gpu, skip=False)
+    loss, lse = torch.empty(n_tok, device=gpu), torch.empty(n_tok, device=gpu)
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+    out = torch.arange(n_tok, device=gpu) % 3 == 1
+    out[-1] = True
+    dloss = torch.rand(n_tok, generator=gen(8)).to(gpu) + 0.1
+    dloss[out] = 0.0
+    results = []
+    for junk in (None, math.nan, math.inf, -math.inf):
+        hj, lj = h.clone(), lse.clone()
+        if junk is not None:
+            hj[out], lj[out] = junk, junk
+        dh, dw = nan_like(torch.empty_like(h)), nan_like(torch.empty((vocab, d), dtype=dw_dtype, device=gpu))
+        ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+        ws.fill_(255)
+        p.engram_cross_entropy_backward(hj, w, y, lj, dloss, dh, dw, ws)
+        assert not dh[out].count_nonzero() and dh[~out].any(1).all() and torch.isfinite(dw).all()
+        results.append((dh, dw))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("n_tok,vocab,d", [(40, 300, 520), (700, 5003, 520)])
+def test_rows_of_far_apart_sizes(gpu, n_tok, vocab, d):
+    """fp32 rows of 2^100 and 2^-100: their products may be where neither is."""
+    p = make_plan("f32", d, vocab)
+    half = d // 2
+    h = torch.zeros((n_tok, d))
+    h[:, :half] = randn((n_tok, half), "f32", 1) * torch.where(torch.arange(n_tok) % 2 == 0, 2.0 ** 100, 2.0 ** -100)[:, None]
+    w = randn((vocab, d), "f32", 2, 2.0 ** -103)
+    w[:10, :half] = 0.0  # logits 0, from rows whose units are 2^100 and 2^60
+    w[:10, half:] *= 2.0 ** 100
+    w[:10, half:] *= 2.0 ** 63
+    y = (torch.arange(n_tok) * 7 % vocab).to(torch.int32)
+    h, w, y = h.to(gpu), w.to(gpu), y.to(gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+    ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, 1.0, "f32").forward())
+    close(loss, ref, off, "loss")
+    close(lse, ref_lse, off_lse, "lse")
 
 
 @pytest.mark.parametrize("dtype,dw_dtype", GRADS)
