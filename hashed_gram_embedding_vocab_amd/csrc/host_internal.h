@@ -1,7 +1,8 @@
 // host_internal.h -- what the host side of the C ABI shares between its
 // files (api.cpp: plans, retrieval and fusion; api_backward.cpp: the
 // backward; api_offload.cpp: host-resident tables and the prefetcher;
-// api_operators.cpp, api_ends.cpp: the operators beside the layer): the plan, the profiling scope of a launch, argument checks and the row gather.
+// api_operators.cpp, api_ends.cpp: the operators beside the layer): the plan,
+// the profiling scope of a launch, argument checks and the row gather.
 #pragma once
 
 #include <hip/hip_runtime.h>
