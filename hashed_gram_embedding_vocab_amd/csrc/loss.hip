@@ -27,9 +27,9 @@
 //   backward, fp32 plan  h, W and P in three bf16 parts of 8 bits, six products
 //                        (P's values span more than fp16 does)
 //   fp32 dW of bf16 h    P in three bf16 parts, three products
-//   bf16 results         P in one: a rounding of up to 2^-8 of each value, as the operand
-//                        beside it has, which a sum of many averages out; of few
-//                        tokens in two
+//   bf16 results         P in one: a rounding of up to 2^-8 of each value, as the
+//                        operand beside it has, which a sum of many averages out; of
+//                        few tokens in two
 // or, where tokens or vocabulary are few, by the fp32 instructions as they are.
 //
 // 8192 tokens x 129280 x 2560 in bf16: 5.4 TFLOP forward, 16.3 backward; a library's
@@ -495,15 +495,14 @@ struct GradEnd {
                         for (int j = 0; j < FM; ++j) acc[i][j][r] = 0.f;
         }
         if constexpr (PAIRS) {
-            const int64_t all = (stack ? parts : 1) * g.M;
+            const int64_t all = (stack ? parts : 1) * g.M, whole = (all + kBlock - 1) / kBlock * kBlock;
             for (int q = 0; q < parts; ++q) {
                 uint16_t *to = static_cast<uint16_t *>(p) + (stack ? 0 : q * part);
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    // (rows and columns past the last are zeros up to whole blocks:
-                    // of stacked parts, of one block then, behind the last part's)
+                    // (rows and columns past the last are zeros up to whole blocks)
                     const int64_t mine = m0 + 16 * j + (lane & 15), m = mine + q * stack;
-                    if (m >= (all + kBlock - 1) / kBlock * kBlock || (stack && q + 1 < parts && mine >= g.M)) continue;
+                    if (mine >= (stack ? g.M : whole)) continue;
 #pragma unroll
                     for (int i = 0; i < FN; i += 2) {
                         const int64_t n = nl + col(i);
@@ -521,6 +520,18 @@ struct GradEnd {
                         for (int i = 0; i < FN; ++i)
 #pragma unroll
                             for (int r = 0; r < 4; ++r) acc[i][j][r] -= (float)(__bf16)acc[i][j][r];
+            }
+            if (stack) {  // (behind the last part's rows fewer than the first 64 of a tile)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const int64_t m = all + m0 + 16 * j + (lane & 15);
+                    if (m >= whole) continue;
+#pragma unroll
+                    for (int i = 0; i < FN; i += 2) {
+                        const int64_t n = nl + col(i);
+                        if (n < ld) *reinterpret_cast<u32x4_t *>(static_cast<uint16_t *>(p) + block_at(m, n, row64)) = u32x4_t{};
+                    }
+                }
             }
         } else {
 #pragma unroll
@@ -1098,10 +1109,12 @@ __global__ __launch_bounds__(256) void few_grad_kernel(const float *x, int32_t s
         static_cast<float *>(p)[t * ld + v] = y;
         return;
     }
+    __bf16 *const out = static_cast<__bf16 *>(p);
+    const int64_t all = parts * n_tok;
+    if (stack && t < (all + kBlock - 1) / kBlock * kBlock - all) out[block_at(all + t, v, row64)] = (__bf16)0.f;
+    if (stack && t >= n_tok) return;
     for (int32_t q = 0; q < parts; ++q) {
-        const int64_t r = t + q * stack;
-        if (!stack || (r < kBlock && (q + 1 == parts || t < n_tok)))
-            static_cast<__bf16 *>(p)[(stack ? 0 : q * part) + block_at(r, v, row64)] = (__bf16)y;
+        out[(stack ? 0 : q * part) + block_at(t + q * stack, v, row64)] = (__bf16)y;
         y -= (float)(__bf16)y;
     }
 }
@@ -1319,8 +1332,9 @@ int64_t piece_bytes(int64_t vocab, int64_t bytes) {
     return std::max(256 * bytes, std::min(kPieceBytes, padded(vocab) * bytes));
 }
 
-int64_t sum_bytes(int64_t n_tok, int32_t d) {
-    const int64_t one = n_tok * d * 4;
+// (`rows`: twice the tokens where P has two parts below each other)
+int64_t sum_bytes(int64_t rows, int32_t d) {
+    const int64_t one = rows * d * 4;
     return std::max(one, std::min(kSumBytes, kMostSplits * one));
 }
 
@@ -1352,15 +1366,23 @@ bool blocks_h(const LossArgs &a) { return a.bf16 && a.n_tok >= 1024 && a.vocab >
 bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (forward ? 12288 : 4096); }
 
 // A bf16 plan's few tokens: the parts of P are further rows of it, and h's rows
-// stand as often, so that a tile of 64 rows, which these tokens do not fill, holds
-// two parts for dh and dW at no cost (three for an fp32 dW).  One token's gradient
-// is a few products, whose one rounding to bf16 would not average out (up to 2^-8 of
-// its norm, twice what a result's own rounding is).
-bool stacked(const LossArgs &a) { return a.bf16 && a.n_tok <= 21; }
+// stand as often, so that W is still read once for dh, where its bytes are what
+// counts, with two parts of P (for dW two, or three for an fp32 one).  A few tokens'
+// gradients are a few products, whose one rounding to bf16 would not average out
+// (up to 2^-8 of their norm, twice what a result's own rounding is): 33 tokens x 1000
+// x 256 are 1.7e-3 of dh's norm from 64 bits instead of 2.7e-3 (22 -> 26 us), 33 x 129280
+// x 2560 take 705 us instead of 775 (fp32 dW; bf16 541 and 546).  128 tokens would take a fifth longer,
+// and their roundings average out (2.4e-3, where very many end too).
+constexpr int64_t kStack = 64;
+bool stacked(const LossArgs &a) { return a.bf16 && a.n_tok <= kStack; }
 
-// Parts of P, and bytes of P for a token and column.
-int p_parts(const LossArgs &a) { return !a.bf16 || !a.dw_bf16 ? 3 : stacked(a) ? 2 : 1; }
-int64_t p_bytes(const LossArgs &a) { return !a.bf16 && direct32(a, false) ? 4 : stacked(a) ? 2 : 2 * p_parts(a); }
+// Parts of P, rows of it and of the copy of h, and bytes of P for a column.
+int p_parts(const LossArgs &a, bool stack) { return !a.bf16 || !a.dw_bf16 ? 3 : stack ? 2 : 1; }
+int64_t p_rows(const LossArgs &a, int64_t n_tok, bool stack) { return round64(stack ? p_parts(a, true) * n_tok : n_tok); }
+int64_t p_bytes(const LossArgs &a) {
+    const int64_t each = !a.bf16 && direct32(a, false) ? 4 : stacked(a) ? 2 : 2 * p_parts(a, false);
+    return each * p_rows(a, a.n_tok, stacked(a));
+}
 
 int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
 int64_t few_bytes(const LossArgs &a) { return std::min(kFewBytes, kMostSplits * a.n_tok * round8(a.vocab) * 4); }
@@ -1419,9 +1441,11 @@ LossLayout loss_bwd_layout(const LossArgs &a) {
     };
     const bool direct = !a.bf16 && direct32(a, false);
     L.xt = take(a.n_tok * (int64_t)sizeof(Token));
-    L.h = take((a.bf16 ? 2 : direct ? 4 : 6) * round64(a.n_tok) * round64(a.d));
-    L.part = take(piece_bytes(a.vocab, p_bytes(a) * round64(a.n_tok)));
-    L.sum = take(sum_bytes(a.n_tok, a.d));
+    // (a few tokens' rows stand several times: no fewer for more tokens)
+    const int64_t few = a.bf16 ? p_rows(a, std::min(a.n_tok, kStack), true) : 0, rows = std::max(few, round64(a.n_tok));
+    L.h = take((a.bf16 ? 2 : direct ? 4 : 6) * rows * round64(a.d));
+    L.part = take(piece_bytes(a.vocab, std::max(p_bytes(a), 2 * few)));
+    L.sum = take(sum_bytes(std::max(a.n_tok, a.bf16 ? 2 * std::min(a.n_tok, kStack) : 0), a.d));
     L.wsum = take(weight_sum_bytes(a.vocab, a.d));
     L.few = take(few_bytes(a));
     if (a.bf16 ? blocks_w(a, false) : !direct) L.w = take(piece_bytes(a.vocab, round64(a.d) * (a.bf16 ? 2 : 6)));
@@ -1520,25 +1544,26 @@ void backward(const LossArgs &a, hipStream_t s) {
     char *ws = static_cast<char *>(a.ws);
     const int64_t d = a.d, V = a.vocab, T = a.n_tok;
     const bool parts = !F32 && !a.bf16;
-    const int hp = parts ? 3 : 1, pp = F32 ? 1 : p_parts(a);
+    const bool stack = stacked(a);
+    const int hp = parts ? 3 : 1, pp = F32 ? 1 : p_parts(a, stack);
     Token *token = reinterpret_cast<Token *>(ws + L.xt);
     void *h = ws + L.h, *p = ws + L.part;
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.w);
     float *sum = reinterpret_cast<float *>(ws + L.sum), *wsum = reinterpret_cast<float *>(ws + L.wsum);
-    const bool bw = parts || (!F32 && blocks_w(a, false)), stack = stacked(a);
+    const bool bw = parts || (!F32 && blocks_w(a, false));
     if constexpr (F32)
         make_parts<float, float, 1>(a.h, T, a.d, &a, static_cast<float *>(h), token, s);
     else
         make_blocks(a, a.h, T, &a, static_cast<uint16_t *>(h), token, s, stack ? pp : 1);
-    const int64_t p_rows = stack ? pp * T : T;
-    const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, p_rows, d);
-    int64_t piece = piece_for(V, p_bytes(a) * round64(T));
+    const int64_t TP = stack ? pp * T : T;  // rows of P
+    const Operand oh = F32 ? rows_of(h, T, d) : blocks_of(h, TP, d);
+    int64_t piece = piece_for(V, p_bytes(a));
     if (bw) piece = std::min(piece, piece_for(V, round64(d) * (parts ? 6 : 2)));
     const bool one_piece = piece >= V;
     Cut cut_h{};
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
         const int64_t n = std::min(piece, V - v0), ld = round64(n);
-        const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, p_rows, n);
+        const Operand op = F32 ? rows_of(p, T, ld) : blocks_of(p, TP, n);
         const char *rows = static_cast<const char *>(a.w) + v0 * d * (a.bf16 ? 2 : 4);
         if (bw) make_blocks(a, rows, n, nullptr, wp, nullptr, s);
         const Operand ow = bw ? blocks_of(wp, n, d) : rows_of(rows, n, d);
@@ -1566,7 +1591,7 @@ void backward(const LossArgs &a, hipStream_t s) {
             }
         }
         if (a.dh) {
-            const int64_t M = (stack ? 2 : 1) * T;
+            const int64_t M = (stack ? 2 : 1) * T;  // (two parts below each other)
             g.M = M;
             g.N = d;
             g.K = n;
@@ -1575,7 +1600,7 @@ void backward(const LossArgs &a, hipStream_t s) {
             parts_of(g, hp, hp);
             // (the same cut for every piece: its sums go on from one to the next)
             if (v0 == 0)
-                cut_h = cut_for<E>(M, d, n, g.segs, std::min(kMostSplits, sum_bytes(T, a.d) / (M * d * 4)), a.bf16 ? 2 : 4);
+                cut_h = cut_for<E>(M, d, n, g.segs, std::min(kMostSplits, sum_bytes(M, a.d) / (M * d * 4)), a.bf16 ? 2 : 4);
             split_steps(g, ceil_div(n, step_of<E>()), cut_h.splits);
             if (v0 == 0) cut_h.splits = g.splits;
             if (one_piece && cut_h.splits == 1 && !stack)
@@ -1586,16 +1611,16 @@ void backward(const LossArgs &a, hipStream_t s) {
         if (a.dw) {
             g.M = n;
             g.N = d;
-            g.K = p_rows;
+            g.K = TP;
             g.a = op;
             g.b = oh;
             parts_of(g, stack ? 1 : pp, hp);
             const int64_t most = std::min(kMostSplits, weight_sum_bytes(a.vocab, a.d) / (n * d * 4));
-            Cut cut = cut_for<E>(n, d, p_rows, g.segs, most, a.dw_bf16 ? 2 : 4);
-            const Cut walk = cut_for<E>(n, d, p_rows, g.segs, 1, 4, true);
+            Cut cut = cut_for<E>(n, d, TP, g.segs, most, a.dw_bf16 ? 2 : 4);
+            const Cut walk = cut_for<E>(n, d, TP, g.segs, 1, 4, true);
             const bool walks = !a.dw_bf16 && walk.cost < cut.cost;
             if (walks) cut = walk;
-            split_steps(g, ceil_div(p_rows, step_of<E>()), cut.splits);
+            split_steps(g, ceil_div(TP, step_of<E>()), cut.splits);
             char *out = static_cast<char *>(a.dw) + v0 * d * (a.dw_bf16 ? 2 : 4);
             const bool split = g.splits > 1;
             if (walks)

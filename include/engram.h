@@ -714,7 +714,7 @@ ENGRAM_API engram_status engram_cross_entropy(engram_plan p, const void *d_h, co
  *   d_workspace  >= engram_cross_entropy_backward_workspace_size(p, n,
  *                dweight_dtype) bytes for an n >= n_tok, 256-byte aligned
  * For bf16 results P is rounded to bf16, as the operand beside it is (to two bf16
- * parts, 16 bits, of 21 tokens and less); for an fp32 d_dweight P is held in three
+ * parts, 16 bits, of 64 tokens and less); for an fp32 d_dweight P is held in three
  * bf16 parts, 24 bits.  In an fp32 plan every value is held in three, six products
  * of parts, or multiplied by the fp32 matrix instructions where tokens or
  * vocabulary are few.

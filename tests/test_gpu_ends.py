@@ -162,10 +162,10 @@ def test_cross_entropy_backward(gpu, dtype, dw_dtype, n_tok, vocab, d, scale):
 
 
 @pytest.mark.parametrize("dw_dtype", (torch.bfloat16, torch.float32))
-@pytest.mark.parametrize("n_tok", (1, 3, 20, 21, 22))
+@pytest.mark.parametrize("n_tok", (1, 3, 20, 21, 22, 32, 33, 43, 64, 65))
 @pytest.mark.parametrize("vocab,d", [(1, 8), (77, 72), (300, 4104), (9001, 264), (40000, 64)])
 def test_few_tokens_keep_two_parts_of_p(gpu, vocab, d, n_tok, dw_dtype):
-    """Two roundings to bf16 in turn leave 2^-16 of P, up to 21 tokens; one alone 2^-8."""
+    """Two roundings to bf16 in turn leave 2^-16 of P, up to 64 tokens; one alone 2^-8."""
     p = make_plan("bf16", d, vocab)
     h, w, y = head("bf16", n_tok, vocab, d, 1.0, 5, gpu)
     y[n_tok // 2] = -1  # (its h reaches nothing)
@@ -175,7 +175,7 @@ def test_few_tokens_keep_two_parts_of_p(gpu, vocab, d, n_tok, dw_dtype):
     dh, dw = nan_like(torch.empty_like(h)), Guarded((vocab, d), dw_dtype, gpu)
     ws = Guarded((p.engram_cross_entropy_backward_workspace_size(n_tok, dw_dtype),), torch.uint8, gpu)
     p.engram_cross_entropy_backward(h, w, y, lse, g, dh, dw.t, ws.t)
-    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse, g, dw_dtype, p_bits=16 if n_tok <= 21 else 8))
+    rdh, off_h, rdw, off_w = (t.cpu() for t in ref.backward(lse, g, dw_dtype, p_bits=16 if n_tok <= 64 else 8))
     close(dh, rdh, off_h, "dh")
     close(dw.t, rdw, off_w, "dw")
     once = dw.t.clone()
@@ -410,7 +410,7 @@ def test_cross_entropy_past_32_bits(gpu):
 def test_cross_entropy_in_the_largest_batchs_workspace(gpu, dtype, dw_dtype):
     p = make_plan(dtype, 136, 3000)
     big = p.cross_entropy_workspace(5000), p.cross_entropy_backward_workspace(5000, dw_dtype)
-    for n_tok in (1, 21, 22, 65, 700, 2049):
+    for n_tok in (1, 21, 33, 64, 65, 700, 2049):
         h, w, y = head(dtype, n_tok, 3000, 136, 1.0, 3, gpu)
         res = []
         for f, b in (big, (p.cross_entropy_workspace(n_tok), p.cross_entropy_backward_workspace(n_tok, dw_dtype))):
