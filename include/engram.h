@@ -679,7 +679,9 @@ ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s
  *   d_loss, d_lse  [n_tok] fp32 (natural logarithms)
  *   d_workspace  >= engram_cross_entropy_workspace_size(p, n) bytes for an
  *                n >= n_tok, 256-byte aligned
- * Logits and sums are fp32.  An fp32 plan's values are multiplied by the fp32
+ * Logits and sums are fp32; the loss is made as log(1 + what the others' sum is of
+ * the target's exponential), so that one far below lse's own rounding keeps its
+ * digits.  An fp32 plan's values are multiplied by the fp32
  * matrix instructions where tokens or vocabulary are few, else in two fp16 parts
  * over a power of two of each row's own (22 bits of what is not 2^-18 and more
  * below the row's largest value), with fp32 sums.  A NaN in a token's h, or in a

@@ -123,6 +123,47 @@ def test_cross_entropy(gpu, dtype, n_tok, vocab, d, scale):
     close(lse, ref_lse, off_lse, "lse")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d,scale", [(1, 242, 208, 0.5), (40, 300, 64, 1.0), (9, 5000, 136, -1.0), (300, 1, 64, 1.0),
+                                                 (700, 5003, 264, 1.0), (2500, 1000, 512, -0.5), (70, 90, 4104, 1.0)])
+def test_certain_tokens_keep_their_digits(gpu, dtype, n_tok, vocab, d, scale):
+    """A loss is log(1 + exp(a)) with a = log sum of the others' exponentials over the
+    target's: its derivative 1 - exp(-loss) is small where the loss is, and so is what
+    an error of the logits makes of it, down to losses far below lse's own rounding."""
+    p = make_plan(dtype, d, vocab)
+    w = randn((vocab, d), dtype, 3, 1.0 / math.sqrt(d) / abs(scale))
+    y = (torch.arange(n_tok) * 5 % vocab).to(torch.int32)
+    # logits of about 0 to 35 at the target
+    h = torch.randn((n_tok, d), generator=gen(4)) + torch.linspace(0, 35, n_tok).flip(0)[:, None] * scale * w[y.long()].float()
+    h, w, y = h.to(tdt(dtype)).to(gpu), w.to(gpu), y.to(gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok), scale=scale)
+    r = HeadRef(h, w, y, scale, dtype)
+    _, ref_lse, off, off_lse = (t.cpu() for t in r.forward())
+    x = r.logits(torch.arange(n_tok, device=gpu))[0]
+    own = x.gather(1, y.long()[:, None])
+    rest = x.scatter(1, y.long()[:, None], -math.inf).logsumexp(1)
+    ref = torch.log1p((rest - own[:, 0]).exp()).cpu()
+    close(loss, ref, 1.01 * (1 - (-ref).exp()) * off + 8 * U * ref, "loss")
+    close(lse, ref_lse, off_lse, "lse")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n_tok,vocab,d", [(1, 50, 64), (70, 257, 72), (700, 5003, 264), (1100, 17000, 72)])
+def test_logits_scaled_to_nothing(gpu, dtype, n_tok, vocab, d):
+    """scale 0: all logits are 0, loss and lse log(vocab), no gradient."""
+    p = make_plan(dtype, d, vocab)
+    h, w, y = head(dtype, n_tok, vocab, d, 1.0, 3, gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok), scale=0.0)
+    ref = torch.where((y >= 0) & (y < vocab), math.log(vocab), 0.0).double().cpu()
+    close(loss, ref, 300 * U + 4 * U * ref, "loss")
+    close(lse, ref, 300 * U + 4 * U * ref, "lse")
+    dh, dw = nan_like(torch.empty_like(h)), nan_like(torch.empty_like(w))
+    p.engram_cross_entropy_backward(h, w, y, lse, None, dh, dw, p.cross_entropy_backward_workspace(n_tok, w.dtype), scale=0.0)
+    assert not dh.count_nonzero() and not dw.count_nonzero()
+
+
 GRADS = [("bf16", torch.bfloat16), ("bf16", torch.float32), ("f32", torch.float32)]
 
 
