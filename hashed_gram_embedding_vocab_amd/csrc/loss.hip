@@ -725,8 +725,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 #pragma unroll
         for (int i = 0; i < FN; ++i) h.b[i] = rb.template read<H>(stb, wn + i);
     };
-    int rows_left = 0;  // of the tile's rows, those of the result (fp32)
-    auto multiply = [&](const Half &h, auto hc) {
+    auto multiply = [&](const Half &h, int rows_left, auto hc) {
         constexpr int H = decltype(hc)::value;
         if constexpr (sizeof(E) == 2) {
             f32x4_t(&sum)[FN][FM] = acc[SETS > 1 ? H : 0];
@@ -742,8 +741,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
                                                                             __builtin_bit_cast(bf16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
                 }
         } else {
-            // (fragments of rows past the last are left out: a few tokens are bound
-            // by W's bytes then, and not by products with nothing)
+            // (fragments of rows past the last are left out, and stages past K: a few
+            // tokens are bound by W's bytes then, and not by products with nothing)
 #pragma unroll
             for (int j = 0; j < FM; ++j)
                 if (16 * (wm + j) < rows_left)
@@ -779,6 +778,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
     }
     turn();
     Half h0, h1;
+    int tile_rows = 0, past = 0;  // (fp32) of the tile's rows those of the result; stages past K at an item's end
     stage_barrier<NB == 4 ? 6 * kL : NA * kL>();
     read(a0, b0, h0, lo);
     int left = 0;
@@ -788,8 +788,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         // and the multiplications wait for them: P 1.29 PFLOP/s against 1.20)
         constexpr bool SET = T == 256;
         constexpr int kReads = (AX ? 2 : 1) * FM + (BX ? 2 : 1) * FN, kMul = FM * FN;
+        const int rows = sizeof(E) == 4 && left <= past ? 0 : tile_rows;
         read(cur_a, cur_b, h1, hi);
-        multiply(h0, lo);
+        multiply(h0, rows, lo);
         if constexpr (SET) {
             spread<0x100, kReads, kMul - 8>();
             __builtin_amdgcn_sched_barrier(0);
@@ -798,7 +799,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         if constexpr (SET) __builtin_amdgcn_sched_barrier(0);
         fill(cur_b, cur_a);
         read(next_a, next_b, h0, lo);
-        multiply(h1, hi);
+        multiply(h1, rows, hi);
         if constexpr (SET) {
             spread<0x20, 2 * kL, 4 * kL>();
             spread<0x100, kReads, kMul - 4 * kL>();
@@ -810,8 +811,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         int64_t n0, m0;
         int split;
         it.origin(item, n0, m0, split);
-        rows_left = (int)min(g.M - m0, (int64_t)T);
         left = steps_in<E>(g, split) * g.segs;
+        if constexpr (sizeof(E) == 4) {
+            tile_rows = (int)min(g.M - m0, (int64_t)T);
+            past = left - min(g.split_steps, (int)((g.K + 31) / 32) - split * g.split_steps);
+        }
         // (a tile's rows are asked for ahead of its stages, whose waits then cover
         // them: behind them they would wait for the next tile's first stages.  The
         // 256 x 256 tile of P has no registers left for that.)
@@ -1405,11 +1409,11 @@ template <class E>
 Cut few_cut(const LossArgs &a, const GemmArgs &g, int out_bytes) {
     Cut whole = cut_for<E>(g.M, g.N, g.K, g.segs, 1, out_bytes);
     const int64_t one = a.n_tok * round8(a.vocab) * 4;
-    if (one > kFewBytes / 2 || g.N > kFewThreads * kFewEach || ceil_div(g.M, 64) * ceil_div(g.N, 64) > 128) return whole;
+    if (one > kFewBytes / 2 || (out_bytes == 0 && g.N > kFewThreads * kFewEach)) return whole;
     const Cut parts = cut_for<E>(g.M, g.N, g.K, g.segs, few_bytes(a) / one, 4);
     // (the forward's maxima and sums are joined by a launch of their own anyway, which
     // takes less than one of a workgroup for each token)
-    const double more = out_bytes ? 1. : (double)a.n_tok / 200 - 3.;
+    const double more = out_bytes ? 1. : (double)a.n_tok / 100 - 3.;
     return parts.splits > 1 && parts.cost + more < whole.cost ? parts : whole;
 }
 
