@@ -712,8 +712,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
     const int wn = (wave % WN) * FN, wm = (wave / WN) * FM;  // the wave's first row blocks
 
     // (64 x 64 and less: sums of their own for each half of a stage, in fp32 for each
-    // instruction of it, so that long rows round less)
-    constexpr int SETS = T > 64 ? 1 : sizeof(E) == 2 ? 2 : 8;
+    // instruction of it, so that long rows round less.  fp16: of the first parts'
+    // products, and of the lighter ones.)
+    constexpr bool F16 = std::is_same<E, _Float16>::value;
+    constexpr int SETS = F16 ? 2 : T > 64 ? 1 : sizeof(E) == 2 ? 2 : 8;
     f32x4_t acc[SETS][FN][FM] = {};
     struct Half {
         u32x4_t a[FM], b[FN];
@@ -725,7 +727,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 #pragma unroll
         for (int i = 0; i < FN; ++i) h.b[i] = rb.template read<H>(stb, wn + i);
     };
-    auto multiply = [&](const Half &h, int rows_left, auto hc) {
+    auto multiply = [&](const Half &h, const Half &hb, int rows_left, auto hc) {
         constexpr int H = decltype(hc)::value;
         if constexpr (sizeof(E) == 2) {
             f32x4_t(&sum)[FN][FM] = acc[SETS > 1 ? H : 0];
@@ -733,11 +735,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    if constexpr (std::is_same<E, _Float16>::value)
-                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, h.b[i]),
+                    if constexpr (F16)
+                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, hb.b[i]),
                                                                            __builtin_bit_cast(f16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
                     else
-                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, h.b[i]),
+                        sum[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hb.b[i]),
                                                                             __builtin_bit_cast(bf16x8_t, h.a[j]), sum[i][j], 0, 0, 0);
                 }
         } else {
@@ -751,7 +753,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 #pragma unroll
                         for (int i = 0; i < FN; ++i)
                             acc[4 * H + e][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                __uint_as_float(h.b[i][e]), __uint_as_float(h.a[j][e]), acc[4 * H + e][i][j], 0, 0, 0);
+                                __uint_as_float(hb.b[i][e]), __uint_as_float(h.a[j][e]), acc[4 * H + e][i][j], 0, 0, 0);
         }
     };
     // (kAhead loads a wave may be in flight at a step's barrier.  The last fills
@@ -790,7 +792,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         constexpr int kReads = (AX ? 2 : 1) * FM + (BX ? 2 : 1) * FN, kMul = FM * FN;
         const int rows = sizeof(E) == 4 && left <= past ? 0 : tile_rows;
         read(cur_a, cur_b, h1, hi);
-        multiply(h0, rows, lo);
+        multiply(h0, h0, rows, lo);
         if constexpr (SET) {
             spread<0x100, kReads, kMul - 8>();
             __builtin_amdgcn_sched_barrier(0);
@@ -798,8 +800,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
         stage_barrier<kAhead>();
         if constexpr (SET) __builtin_amdgcn_sched_barrier(0);
         fill(cur_b, cur_a);
-        read(next_a, next_b, h0, lo);
-        multiply(h1, rows, hi);
+        if constexpr (F16) {  // (a stage's halves are the two parts of its k)
+            Half h2;
+            read(next_a, next_b, h2, lo);
+            multiply(h0, h1, rows, hi);
+            multiply(h1, h0, rows, hi);
+            h0 = h2;
+        } else {
+            read(next_a, next_b, h0, lo);
+            multiply(h1, h1, rows, hi);
+        }
         if constexpr (SET) {
             spread<0x20, 2 * kL, 4 * kL>();
             spread<0x100, kReads, kMul - 4 * kL>();
@@ -925,10 +935,13 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
     }
 }
 
-// Two fp16 parts of x's rows over their units, in blocks: a row's unit is the power
-// of two over which its largest value lies in [2^14, 2^15), so that the parts hold
-// 22 bits of whatever is not below 2^-18 of that, and 2^-40 of it otherwise.  One
-// wave a row, of one matrix or behind it of a second one (no rows: none).
+// Two fp16 parts of x's rows over their units, in blocks, 32 values' first parts and
+// then their second ones: a stage of 64 brings what three products of parts need, and
+// no part is read twice (517 tokens x 32000 x 1024 181 -> 163 us; tiles of 256 x 256, which
+// have no registers for it, were 3 to 6% faster where all CUs are busy, and 10% slower else).
+// A row's unit is the power of two over which its largest value lies in [2^14, 2^15),
+// so that the parts hold 22 bits of whatever is not below 2^-18 of that, and 2^-40 of it
+// otherwise.  One wave a row, of one matrix or behind it of a second one (no rows: none).
 struct Halves {
     const float *x;
     int64_t rows, all;         // with those up to whole blocks
@@ -937,14 +950,14 @@ struct Halves {
 };
 __global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves second, int32_t d) {
     const int lane = threadIdx.x & 63;
-    const int32_t cols = (d + kBlock - 1) / kBlock * kBlock;
+    const int32_t cols = (d + 31) / 32 * 32;
     typedef _Float16 h8 __attribute__((ext_vector_type(8)));
     for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < first.all + second.all; at += (int64_t)gridDim.x * 4) {
         const bool one = at < first.all;
         const float *const x = one ? first.x : second.x;
         _Float16 *const out = one ? first.out : second.out;
         int32_t *const unit = one ? first.unit : second.unit;
-        const int64_t r = one ? at : at - first.all, rows = one ? first.rows : second.rows, all = one ? first.all : second.all;
+        const int64_t r = one ? at : at - first.all, rows = one ? first.rows : second.rows;
         uint32_t top = 0u;
         if (r < rows)
             for (int32_t c = lane * 8; c < d; c += 512) {
@@ -971,9 +984,9 @@ __global__ __launch_bounds__(256) void half_parts_kernel(Halves first, Halves se
                 p0[i] = (_Float16)y;
                 p1[i] = (_Float16)(y - (float)p0[i]);
             }
-            _Float16 *to = out + block_at(r, c, (int64_t)cols * kBlock);
+            _Float16 *to = out + block_at(r, (c >> 5) * 64 + (c & 31), (int64_t)cols * 2 * kBlock);
             *reinterpret_cast<h8 *>(to) = p0;
-            *reinterpret_cast<h8 *>(to + all * cols) = p1;
+            *reinterpret_cast<h8 *>(to + 32) = p1;
         }
     }
 }
@@ -1219,20 +1232,23 @@ Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_byt
         int tile;
         double one, two, start1, start2, byte1, byte2;
     };
-    constexpr bool F32 = sizeof(E) == 4;
+    constexpr bool F32 = sizeof(E) == 4, PARTS = std::is_same<E, _Float16>::value;
     static constexpr Rate kRates16[3] = {{64, 0.30, 0.44, 3., 4., 0.25, 0.5},
                                          {128, 0.62, 0.92, 5., 6., 0.7, 1.3},
                                          {256, 1.48, 1.48, 5., 5., 2.3, 2.3}};
     // (a stage of fp32: 32 k at a sixteenth of the rate)
     static constexpr Rate kRates32[2] = {{32, 0.36, 0.58, 3., 4., 0.1, 0.2}, {64, 0.55, 0.95, 4., 5., 0.25, 0.5}};
+    // (fp16: three products a stage of 32 k)
+    static constexpr Rate kRatesParts[2] = {{64, 0.35, 0.55, 3., 4., 0.25, 0.5}, {128, 0.75, 1.20, 5., 6., 0.7, 1.3}};
     auto &rates = [&]() -> auto & {
         if constexpr (F32) return kRates32;
+        else if constexpr (PARTS) return kRatesParts;
         else return kRates16;
     }();
     Cut best{64, 1, 1e30};
     const int64_t steps = ceil_div(K, step_of<E>());
     for (const Rate &r : rates) {
-        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile(r.tile, M, N)) continue;
+        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile(r.tile, M, N) && !(PARTS && r.tile == 128)) continue;
         const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
         for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
             const int64_t items = tiles * n, full = items / slots, rest = items % slots;
@@ -1266,7 +1282,7 @@ void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
             }
         launch_kernel((gemm_kernel<E, End, 64, 2, 2, NS, NS, AX, BX>), dim3(grid), dim3(256), s, g, end);
     } else {
-        if constexpr (!SHORT)
+        if constexpr (!SHORT && !std::is_same<E, _Float16>::value)
             if (tile == 256) {
                 launch_kernel((gemm_kernel<E, End, 256, 2, 4, 2, NA, AX, BX>), dim3(grid), dim3(512), s, g, end);
                 return;
@@ -1298,13 +1314,12 @@ void make_blocks(const LossArgs &a, const void *x, int64_t rows, const LossArgs 
         make_parts<float, uint16_t, 3>(x, rows, a.d, mask, out, token, s);
 }
 
-// Products of parts: all pairs (i, j) with i + j up to `most` (2: weights of 2^-16 in
-// bf16; 1: of 2^-11 in fp16, whose two smaller parts' is 2^-22), the lightest first, so
-// that only the last one's sums are rounded at their full size.
-void parts_of(GemmArgs &g, int a_parts, int b_parts, int most = 2) {
+// Products of bf16 parts: all pairs whose weight is 2^-16 and more, the lightest first,
+// so that only the last one's sums are rounded at their full size.
+void parts_of(GemmArgs &g, int a_parts, int b_parts) {
     g.segs = 0;
     g.a_parts = g.b_parts = 0;
-    for (int w = most; w >= 0; --w)
+    for (int w = 2; w >= 0; --w)
         for (int i = 0; i < a_parts; ++i) {
             const int j = w - i;
             if (j < 0 || j >= b_parts) continue;
@@ -1364,12 +1379,13 @@ int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 // reading of W takes (some 100 tokens' products), and where V is small their
 // launches (a time of its own) and, forward, tiles of too few workgroups along
 // all of d.  Measured, us, instructions of fp32 against parts: forward 59 tokens x
-// 61016 x 2832 235 : 520, 517 x 32000 x 1024 377 : 182, 521 x 773 x 5952 72 : 109,
-// 1000 x 773 x 5952 136 : 113, 2500 x 1000 x 256 26 : 25, 6000 x 1000 x 256 46 : 32; backward
+// 61016 x 2832 233 : 484, 517 x 32000 x 1024 377 : 162, 521 x 773 x 5952 72 : 82,
+// 1000 x 773 x 5952 136 : 86, 1000 x 1000 x 256 14 : 16, 6000 x 1000 x 256 46 : 30; backward
 // 59 x 61016 x 2832 857 : 1374, 275 x 22940 x 1496 702 : 567, 521 x 773 x 5952
-// 207 : 174, 1000 x 1000 x 256 46 : 59.  In 49 shapes the rule lost 6% at most.
+// 207 : 174, 1000 x 1000 x 256 46 : 59.  In 49 shapes the rule lost up to 8%, and 19% of two
+// short ones whose second row of tiles was nearly empty (80 x 8962 x 1216, 57 : 47).
 bool direct32(const LossArgs &a, bool forward) {
-    return forward ? (a.n_tok - 100) * a.vocab <= 600000000 / a.d + 400000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
+    return forward ? (a.n_tok - 80) * a.vocab <= 300000000 / a.d + 350000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
 }
 
 // Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
@@ -1433,8 +1449,10 @@ LossLayout loss_layout(const LossArgs &a) {
         return (size_t)o;
     };
     L.xt = take(T * 4);
-    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2), std::min<int64_t>(2 * T * n32, 512 * 32 * 2),
-                                std::min<int64_t>(T * n64, 2048 * 128 * 2)}));
+    // (128 x 128 tiles: an fp32 plan's in any number)
+    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2),
+                                std::min<int64_t>(2 * T * n32, 512 * 32 * 2),
+                                a.bf16 ? std::min<int64_t>(T * n64, 2048 * 128 * 2) : T * n64}));
     L.few = take(few_bytes(a));
     const int64_t each = a.bf16 ? 2 : 4;
     if (a.bf16 ? blocks_h(a) : !direct32(a, true)) {
@@ -1500,8 +1518,8 @@ void forward(const LossArgs &a, hipStream_t s) {
     const int64_t d = a.d, V = a.vocab, T = a.n_tok;
     GemmArgs g{};
     g.M = T;
-    g.K = d;
-    parts_of(g, F16 ? 2 : 1, F16 ? 2 : 1, 1);
+    g.K = F16 ? (d + 31) / 32 * 64 : d;
+    parts_of(g, 1, 1);
     const bool bh = F16 || (!F32 && blocks_h(a)), bw = F16 || (!F32 && blocks_w(a, true));
     const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
@@ -1510,9 +1528,9 @@ void forward(const LossArgs &a, hipStream_t s) {
         return Halves{static_cast<const float *>(x), rows, round64(rows), reinterpret_cast<_Float16 *>(out), unit};
     };
     g.N = std::min(piece, V);
-    const Cut few = F16 ? cut_for<E>(T, g.N, d, g.segs, 1, 0) : few_cut<E>(a, g, 0);
+    const Cut few = F16 ? cut_for<E>(T, g.N, g.K, g.segs, 1, 0) : few_cut<E>(a, g, 0);
     if (bh && !F16) make_blocks(a, a.h, T, nullptr, h, nullptr, s);
-    g.a = bh ? blocks_of(h, T, d) : rows_of(a.h, T, d);
+    g.a = bh ? blocks_of(h, T, g.K) : rows_of(a.h, T, d);
     if constexpr (!F16) {
         if (few.splits > 1) {
             float *x = reinterpret_cast<float *>(ws + L.few);
@@ -1539,7 +1557,7 @@ void forward(const LossArgs &a, hipStream_t s) {
         } else if (bw) {
             make_blocks(a, rows, g.N, nullptr, w, nullptr, s);
         }
-        g.b = bw ? blocks_of(w, g.N, d) : rows_of(rows, g.N, d);
+        g.b = bw ? blocks_of(w, g.N, g.K) : rows_of(rows, g.N, d);
         gemm<E, false, false>(g, end, few.tile, s);
     }
     // (a workgroup a token where its parts are many and tokens are few)
