@@ -42,6 +42,7 @@
 #include <utility>
 
 #include "engram_internal.h"
+#include "loss_cut.h"
 #include "stage.h"
 #include "vec8.h"
 
@@ -49,7 +50,6 @@ namespace engram {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kBlock = 64;  // rows and columns of a block of the workspaces' matrices
 
 // ---------------------------------------------------------------- operands
 // A matrix of rows (of m or n) and columns of k values ("along"), or of rows (one
@@ -67,7 +67,6 @@ struct Operand {
 Operand rows_of(const void *p, int64_t rows, int64_t cols) {
     return Operand{p, cols, kBlock * cols, kBlock, rows * cols, rows * cols};
 }
-int64_t round64(int64_t x) { return (x + kBlock - 1) / kBlock * kBlock; }
 Operand blocks_of(const void *p, int64_t rows, int64_t cols) {
     const int64_t n = round64(rows) * round64(cols);
     return Operand{p, kBlock, round64(cols) * kBlock, kBlock * kBlock, n, n};
@@ -426,13 +425,6 @@ struct LseEnd {
                 part[(v0 + n0) / (16 * FN) * g.M + m] = float2{top == -INFINITY ? top : top * c, sum};
         }
     }
-};
-
-// What the gradient of a token's logits needs: lse, the factor g_t scale (0 for a
-// token that does not count) and the target.
-struct Token {
-    float lse, factor;
-    int32_t target, unused;
 };
 
 // A tile of P, in `parts` parts of bf16 in blocks, or in fp32 rows of ld: zeros
@@ -1068,7 +1060,6 @@ __device__ __forceinline__ float few_logit(const float *x, int64_t at, int32_t s
 }
 
 // One workgroup a token; a thread's logits stay in its registers.
-constexpr int kFewThreads = 1024, kFewEach = 8;
 __global__ __launch_bounds__(kFewThreads) void few_loss_kernel(const float *x, int32_t splits, int64_t split_elems,
                                                                int64_t ld, int32_t vocab, float scale,
                                                                const int32_t *targets, float *loss, float *lse) {
@@ -1197,74 +1188,6 @@ __global__ __launch_bounds__(256) void sum_join_kernel(const float *part, int32_
 }
 
 // ---------------------------------------------------------------- host side
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-template <class E>
-constexpr int64_t step_of() {
-    return 128 / (int64_t)sizeof(E);
-}
-
-// How a product is cut: square tiles, and parts of K.  The tile and the parts are
-// those that should take least, by what a stage takes on a CU (measured, us): 1.48
-// with one workgroup of 256 x 256, 0.92 with two of 128 x 128 (0.62 with one),
-// 0.44 with two of 64 x 64 (0.30), and at its start and end a few us more, which
-// grow with the bytes of a result.  (A 256 x 256 tile's 1.33 PFLOP/s are 1.05 of
-// 128 x 128 and 0.53 of 64 x 64; but 96 tiles of 64 x 64 are six of 256 x 256.)
-// fp32 tiles are 64 x 64 (0.95, 0.55) or 32 x 32 (0.58, 0.36): 33 tokens x 1000 x 256
-// are 16 of the one or 64 of the other, 13.4 us against 10.0.  Parts of K cost a
-// second launch that joins them.  Against the best of each tile forced, and of
-// parts or none, the choice lost less than 5% in 92 shapes but two (5 and 7%).
-struct Cut {
-    int tile;
-    int64_t splits;
-    double cost;
-};
-
-// (the parts of a token's sums, whose number goes with the tile, stay few: loss_layout)
-bool may_tile(int tile, int64_t M, int64_t N) {
-    const int64_t items = ceil_div(M, tile) * ceil_div(N, tile);
-    return tile == 256 || (tile == 128 ? items <= 2048 : tile == 64 ? M <= 64 || items <= 1024 : items <= 512);
-}
-
-template <class E>
-Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_bytes, bool walks = false) {
-    struct Rate {
-        int tile;
-        double one, two, start1, start2, byte1, byte2;
-    };
-    constexpr bool F32 = sizeof(E) == 4, PARTS = std::is_same<E, _Float16>::value;
-    static constexpr Rate kRates16[3] = {{64, 0.30, 0.44, 3., 4., 0.25, 0.5},
-                                         {128, 0.62, 0.92, 5., 6., 0.7, 1.3},
-                                         {256, 1.48, 1.48, 5., 5., 2.3, 2.3}};
-    // (a stage of fp32: 32 k at a sixteenth of the rate)
-    static constexpr Rate kRates32[2] = {{32, 0.36, 0.58, 3., 4., 0.1, 0.2}, {64, 0.55, 0.95, 4., 5., 0.25, 0.5}};
-    // (fp16: three products a stage of 32 k)
-    static constexpr Rate kRatesParts[2] = {{64, 0.35, 0.55, 3., 4., 0.25, 0.5}, {128, 0.75, 1.20, 5., 6., 0.7, 1.3}};
-    auto &rates = [&]() -> auto & {
-        if constexpr (F32) return kRates32;
-        else if constexpr (PARTS) return kRatesParts;
-        else return kRates16;
-    }();
-    Cut best{64, 1, 1e30};
-    const int64_t steps = ceil_div(K, step_of<E>());
-    for (const Rate &r : rates) {
-        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile(r.tile, M, N) && !(PARTS && r.tile == 128)) continue;
-        const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
-        for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
-            const int64_t items = tiles * n, full = items / slots, rest = items % slots;
-            const double each = (double)((walks ? ceil_div(steps, 2) * 2 : ceil_div(steps, n)) * segs);
-            const int bytes = n > 1 ? 4 : out_bytes;
-            const double less = walks ? 0.6 : 1.;  // (the next item's first stages land while one ends)
-            double t = (double)full * (each * r.two + less * (r.start2 + r.byte2 * bytes));
-            if (rest > 0)
-                t += rest <= 256 ? each * r.one + less * (r.start1 + r.byte1 * bytes) : each * r.two + less * (r.start2 + r.byte2 * bytes);
-            if (n > 1) t += 4. + (double)(n * M) * (double)N * 4. / 4.5e6;
-            if (t < best.cost * 0.98) best = Cut{r.tile, n, t};
-        }
-    }
-    return best;
-}
-
 template <class E, bool AX, bool BX, class End>
 void gemm(GemmArgs g, const End &end, int tile, hipStream_t s) {
     g.items = (int32_t)(ceil_div(g.N, tile) * ceil_div(g.M, tile) * g.splits);
@@ -1343,159 +1266,6 @@ void split_steps(GemmArgs &g, int64_t steps, int64_t n) {
     g.splits = (int32_t)ceil_div(steps, per);
 }
 
-constexpr int64_t kPieceBytes = (int64_t)1 << 30;     // of P, and of W's parts, at a time
-constexpr int64_t kSumBytes = (int64_t)512 << 20;     // of dh's sums in several splits
-constexpr int64_t kMostSplits = 64;
-constexpr int64_t kFewBytes = (int64_t)32 << 20;      // of a few tokens' logits in several splits
-
-int64_t padded(int64_t vocab) { return ceil_div(vocab, 256) * 256; }
-
-// Columns of the vocabulary taken at a time: `bytes` for each of them may come
-// to kPieceBytes, but at least 256 columns.
-int64_t piece_for(int64_t vocab, int64_t bytes) {
-    const int64_t most = std::max<int64_t>(256, kPieceBytes / bytes / 256 * 256);
-    const int64_t n = ceil_div(padded(vocab), most);
-    return ceil_div(ceil_div(padded(vocab), n), 256) * 256;
-}
-// What such a piece takes at most; it never falls as `bytes` grows.
-int64_t piece_bytes(int64_t vocab, int64_t bytes) {
-    return std::max(256 * bytes, std::min(kPieceBytes, padded(vocab) * bytes));
-}
-
-// (`rows`: twice the tokens where P has two parts below each other)
-int64_t sum_bytes(int64_t rows, int32_t d) {
-    const int64_t one = rows * d * 4;
-    return std::max(one, std::min(kSumBytes, kMostSplits * one));
-}
-
-// dW's sums in several splits: at most 64 MB.
-int64_t weight_sum_bytes(int64_t vocab, int32_t d) { return std::min<int64_t>((int64_t)64 << 20, kMostSplits * vocab * d * 4); }
-
-int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
-
-// Whether an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
-// of the bf16 ones' rate, or as products of parts (three of fp16 parts forward, six of
-// bf16 parts backward), which need W's parts made first: as long as a second
-// reading of W takes (some 100 tokens' products), and where V is small their
-// launches (a time of its own) and, forward, tiles of too few workgroups along
-// all of d.  Measured, us, instructions of fp32 against parts: forward 59 tokens x
-// 61016 x 2832 233 : 484, 517 x 32000 x 1024 377 : 162, 521 x 773 x 5952 72 : 82,
-// 1000 x 773 x 5952 136 : 86, 1000 x 1000 x 256 14 : 16, 6000 x 1000 x 256 46 : 30; backward
-// 59 x 61016 x 2832 857 : 1374, 275 x 22940 x 1496 702 : 567, 521 x 773 x 5952
-// 207 : 174, 1000 x 1000 x 256 46 : 59.  In 49 shapes the rule lost up to 8%, and 19% of two
-// short ones whose second row of tiles was nearly empty (80 x 8962 x 1216, 57 : 47).
-bool direct32(const LossArgs &a, bool forward) {
-    return forward ? (a.n_tok - 80) * a.vocab <= 300000000 / a.d + 350000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
-}
-
-// Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
-// d = 2560 put a stage's 256 lines on four of an L2's sixteen channels; in blocks
-// the logits of 8192 tokens and 64,640 columns take 2.03 ms (h) and 1.92 ms (h and W)
-// against 2.13 ms, their gradient's product with W 2.08 ms against 2.35 ms.  The
-// copy of W costs 4 bytes a value, 0.14 ms there, so it takes this many tokens.
-bool blocks_h(const LossArgs &a) { return a.bf16 && a.n_tok >= 1024 && a.vocab >= 16384; }
-bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (forward ? 12288 : 4096); }
-
-// A bf16 plan's few tokens: the parts of P are further rows of it, and h's rows
-// stand as often, so that W is still read once for dh, where its bytes are what
-// counts, with two parts of P (for dW two, or three for an fp32 one).  A few tokens'
-// gradients are a few products, whose one rounding to bf16 would not average out
-// (up to 2^-8 of their norm, twice what a result's own rounding is): 33 tokens x 1000
-// x 256 are 1.7e-3 of dh's norm from 64 bits instead of 2.7e-3 (22 -> 26 us), 33 x 129280
-// x 2560 take 705 us instead of 775 (fp32 dW; bf16 541 and 546).  128 tokens would take a fifth longer,
-// and their roundings average out (2.4e-3, where very many end too).
-constexpr int64_t kStack = 64;
-bool stacked(const LossArgs &a) { return a.bf16 && a.n_tok <= kStack; }
-
-// Parts of P, rows of it and of the copy of h, and bytes of P for a column.
-int p_parts(const LossArgs &a, bool stack) { return !a.bf16 || !a.dw_bf16 ? 3 : stack ? 2 : 1; }
-int64_t p_rows(const LossArgs &a, int64_t n_tok, bool stack) { return round64(stack ? p_parts(a, true) * n_tok : n_tok); }
-int64_t p_bytes(const LossArgs &a) {
-    const int64_t each = !a.bf16 && direct32(a, false) ? 4 : stacked(a) ? 2 : 2 * p_parts(a, false);
-    return each * p_rows(a, a.n_tok, stacked(a));
-}
-
-int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
-int64_t few_bytes(const LossArgs &a) { return std::min(kFewBytes, kMostSplits * a.n_tok * round8(a.vocab) * 4); }
-
-// A few tokens of a small vocabulary: the logits in parts of K, where that is
-// faster than whole rows by the tiles there are (122 tokens x 75 x 7680 in fp32: two
-// workgroups would do 240 stages each).  splits 1: not.
-template <class E>
-Cut few_cut(const LossArgs &a, const GemmArgs &g, int out_bytes) {
-    Cut whole = cut_for<E>(g.M, g.N, g.K, g.segs, 1, out_bytes);
-    const int64_t one = a.n_tok * round8(a.vocab) * 4;
-    if (one > kFewBytes / 2 || (out_bytes == 0 && g.N > kFewThreads * kFewEach)) return whole;
-    const Cut parts = cut_for<E>(g.M, g.N, g.K, g.segs, few_bytes(a) / one, 4);
-    // (the forward's maxima and sums are joined by a launch of their own anyway, which
-    // takes less than one of a workgroup for each token)
-    const double more = out_bytes ? 1. : (double)a.n_tok / 100 - 3.;
-    return parts.splits > 1 && parts.cost + more < whole.cost ? parts : whole;
-}
-
-}  // namespace
-
-// The parts of a token's sums: columns of a wave by the tile's size.  One of the
-// largest batch serves the smaller ones (each term grows with the batch, and the
-// tiles of 64 and 128 are only taken up to some number of them).
-LossLayout loss_layout(const LossArgs &a) {
-    LossLayout L{};
-    const int64_t v = padded(a.vocab), T = a.n_tok;
-    const int64_t n128 = v / 128, n64 = v / 64, n32 = v / 32;
-    int64_t off = 0;
-    auto take = [&](int64_t bytes) {
-        const int64_t o = off;
-        off = round256(off + bytes);
-        return (size_t)o;
-    };
-    L.xt = take(T * 4);
-    // (128 x 128 tiles: an fp32 plan's in any number)
-    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2),
-                                std::min<int64_t>(2 * T * n32, 512 * 32 * 2),
-                                a.bf16 ? std::min<int64_t>(T * n64, 2048 * 128 * 2) : T * n64}));
-    L.few = take(few_bytes(a));
-    const int64_t each = a.bf16 ? 2 : 4;
-    if (a.bf16 ? blocks_h(a) : !direct32(a, true)) {
-        L.h = take(each * round64(T) * round64(a.d));
-        L.unit = take(4 * (round64(T) + padded(a.vocab)));
-    }
-    if (a.bf16 ? blocks_w(a, true) : !direct32(a, true)) L.w = take(piece_bytes(a.vocab, round64(a.d) * each));
-    L.total = (size_t)off;
-    return L;
-}
-
-LossLayout loss_bwd_layout(const LossArgs &a) {
-    LossLayout L{};
-    int64_t off = 0;
-    auto take = [&](int64_t bytes) {
-        const int64_t o = off;
-        off = round256(off + bytes);
-        return (size_t)o;
-    };
-    const bool direct = !a.bf16 && direct32(a, false);
-    L.xt = take(a.n_tok * (int64_t)sizeof(Token));
-    // (a few tokens' rows stand several times: no fewer for more tokens)
-    const int64_t few = a.bf16 ? p_rows(a, std::min(a.n_tok, kStack), true) : 0, rows = std::max(few, round64(a.n_tok));
-    L.h = take((a.bf16 ? 2 : direct ? 4 : 6) * rows * round64(a.d));
-    L.part = take(piece_bytes(a.vocab, std::max(p_bytes(a), 2 * few)));
-    L.sum = take(sum_bytes(std::max(a.n_tok, a.bf16 ? 2 * std::min(a.n_tok, kStack) : 0), a.d));
-    L.wsum = take(weight_sum_bytes(a.vocab, a.d));
-    L.few = take(few_bytes(a));
-    if (a.bf16 ? blocks_w(a, false) : !direct) L.w = take(piece_bytes(a.vocab, round64(a.d) * (a.bf16 ? 2 : 6)));
-    L.total = (size_t)off;
-    return L;
-}
-
-bool loss_fits(int64_t n_tok, int32_t vocab, int32_t d) {
-    // items of one launch (fewer than 2^32 threads), and 31-bit offsets in a tile's
-    // rows of d or of a piece of the vocabulary
-    const int64_t t = ceil_div(n_tok, 256), v = ceil_div(vocab, 256), c = ceil_div(d, 256);
-    return t * v < ((int64_t)1 << 22) && v * c < ((int64_t)1 << 22) && t * c < ((int64_t)1 << 18) && d <= (1 << 20) &&
-           vocab <= (1 << 22) && n_tok <= (1 << 26);
-}
-
-namespace {
-
 void join_sums(const float *part, int64_t splits, int64_t split_elems, int64_t rows, int32_t d, const int32_t *targets,
                int32_t vocab, bool bf16, void *out, bool accumulate, hipStream_t s) {
     const int64_t units = rows * d / 8;
@@ -1512,7 +1282,7 @@ void join_sums(const float *part, int64_t splits, int64_t split_elems, int64_t r
 
 template <class E>
 void forward(const LossArgs &a, hipStream_t s) {
-    constexpr bool F32 = sizeof(E) == 4, F16 = std::is_same<E, _Float16>::value;
+    constexpr bool F16 = std::is_same<E, _Float16>::value;
     const LossLayout L = loss_layout(a);
     char *ws = static_cast<char *>(a.ws);
     const int64_t d = a.d, V = a.vocab, T = a.n_tok;
@@ -1520,15 +1290,16 @@ void forward(const LossArgs &a, hipStream_t s) {
     g.M = T;
     g.K = F16 ? (d + 31) / 32 * 64 : d;
     parts_of(g, 1, 1);
-    const bool bh = F16 || (!F32 && blocks_h(a)), bw = F16 || (!F32 && blocks_w(a, true));
-    const int64_t piece = bw ? piece_for(V, round64(d) * (F16 ? 4 : 2)) : padded(V);
+    const ForwardCut f = forward_cut<E>(a);
+    const bool bh = f.blocks_h, bw = f.blocks_w;
+    const int64_t piece = f.piece;
+    const Cut few = f.cut;
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h), *w = reinterpret_cast<uint16_t *>(ws + L.w);
     int32_t *h_unit = reinterpret_cast<int32_t *>(ws + L.unit), *w_unit = h_unit + round64(T);
     auto halves = [&](const void *x, int64_t rows, uint16_t *out, int32_t *unit) {
         return Halves{static_cast<const float *>(x), rows, round64(rows), reinterpret_cast<_Float16 *>(out), unit};
     };
     g.N = std::min(piece, V);
-    const Cut few = F16 ? cut_for<E>(T, g.N, g.K, g.segs, 1, 0) : few_cut<E>(a, g, 0);
     if (bh && !F16) make_blocks(a, a.h, T, nullptr, h, nullptr, s);
     g.a = bh ? blocks_of(h, T, g.K) : rows_of(a.h, T, d);
     if constexpr (!F16) {
@@ -1610,7 +1381,7 @@ void backward(const LossArgs &a, hipStream_t s) {
             parts_of(g, hp, hp);
             // (cut as for one part, so that dh does not change with dW's type)
             const int out = F32 ? 4 : 2;
-            const Cut few = one_piece ? few_cut<E>(a, g, out) : cut_for<E>(T, n, d, g.segs, 1, out);
+            const Cut few = one_piece ? few_cut<E>(a, n, d, g.segs, out) : cut_for<E>(T, n, d, g.segs, 1, out);
             if (few.splits > 1) {
                 float *x = reinterpret_cast<float *>(ws + L.few);
                 const int64_t ldx = round8(V);
