@@ -4,13 +4,10 @@
 
 namespace engram {
 
-// The parts of a token's sums: columns of a wave by the tile's size.  One of the
-// largest batch serves the smaller ones (each term grows with the batch, and the
-// tiles of 64 and 128 are only taken up to some number of them).
+// One of the largest batch serves the smaller ones: each term grows with the batch.
 LossLayout loss_layout(const LossArgs &a) {
     LossLayout L{};
-    const int64_t v = padded(a.vocab), T = a.n_tok;
-    const int64_t n128 = v / 128, n64 = v / 64, n32 = v / 32;
+    const int64_t T = a.n_tok;
     int64_t off = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = off;
@@ -18,10 +15,7 @@ LossLayout loss_layout(const LossArgs &a) {
         return (size_t)o;
     };
     L.xt = take(T * 4);
-    // (128 x 128 tiles: an fp32 plan's in any number)
-    L.part = take(8 * std::max({T * n128, std::min<int64_t>(T, 64) * n32, std::min<int64_t>(T * n32, 1024 * 64 * 2),
-                                std::min<int64_t>(2 * T * n32, 512 * 32 * 2),
-                                a.bf16 ? std::min<int64_t>(T * n64, 2048 * 128 * 2) : T * n64}));
+    L.part = take(8 * lse_pairs(a));
     L.few = take(few_bytes(a));
     const int64_t each = a.bf16 ? 2 : 4;
     if (a.bf16 ? blocks_h(a) : !direct32(a, true)) {

@@ -44,10 +44,12 @@ struct Cut {
     double cost;
 };
 
-// (the parts of a token's sums, whose number goes with the tile, stay few: loss_layout)
+// Tiles of a size that a launch may have where the size is not the largest of its type
+// (any number of 64 x 64 over 64 rows and less): what lse_pairs counts on.
+constexpr int64_t most_items(int tile) { return tile == 128 ? 2048 : tile == 64 ? 1024 : 512; }
+
 inline bool may_tile(int tile, int64_t M, int64_t N) {
-    const int64_t items = ceil_div(M, tile) * ceil_div(N, tile);
-    return tile == 256 || (tile == 128 ? items <= 2048 : tile == 64 ? M <= 64 || items <= 1024 : items <= 512);
+    return tile == 256 || (tile == 64 && M <= 64) || ceil_div(M, tile) * ceil_div(N, tile) <= most_items(tile);
 }
 
 template <class E>
@@ -187,16 +189,33 @@ struct ForwardCut {
     int64_t piece;
     Cut cut;
 };
+// (W's copy has two fp16 parts in an fp32 plan)
+inline int64_t forward_piece(const LossArgs &a, bool copied) {
+    return copied ? piece_for(a.vocab, round64(a.d) * (a.bf16 ? 2 : 4)) : padded(a.vocab);
+}
 template <class E>
 ForwardCut forward_cut(const LossArgs &a) {
     constexpr bool F32 = sizeof(E) == 4, F16 = std::is_same<E, _Float16>::value;
     ForwardCut f;
     f.blocks_h = F16 || (!F32 && blocks_h(a));
     f.blocks_w = F16 || (!F32 && blocks_w(a, true));
-    f.piece = f.blocks_w ? piece_for(a.vocab, round64(a.d) * (F16 ? 4 : 2)) : padded(a.vocab);
+    f.piece = forward_piece(a, f.blocks_w);
     const int64_t n = std::min<int64_t>(f.piece, a.vocab), k = F16 ? (a.d + 31) / 32 * 64 : a.d;
     f.cut = F16 ? cut_for<E>(a.n_tok, n, k, 1, 1, 0) : few_cut<E>(a, n, k, 1, 0);
     return f;
+}
+
+// Pairs of a maximum and a sum that the forward's tiles may write: two of each row of a
+// tile, over the whole vocabulary, of whatever tiles may_tile() allows a launch, which
+// makes one piece of it.  It never falls as tokens are added.
+inline int64_t lse_pairs(const LossArgs &a) {
+    const bool copied = a.bf16 ? blocks_w(a, true) : !direct32(a, true);
+    const int64_t T = a.n_tok, V = a.vocab, pieces = ceil_div(V, forward_piece(a, copied));
+    auto all = [&](int tile, int64_t rows) { return 2 * ceil_div(V, tile) * rows; };
+    auto few = [&](int tile) { return std::min(all(tile, T), pieces * most_items(tile) * 2 * tile); };
+    const int64_t small = std::max({all(64, std::min<int64_t>(T, 64)), few(64), few(32)});
+    // (an fp32 plan's tiles of 128 x 128 are its largest)
+    return std::max(small, a.bf16 ? std::max(all(256, T), few(128)) : all(128, T));
 }
 
 }  // namespace engram
