@@ -44,12 +44,17 @@ struct Cut {
     double cost;
 };
 
-// Tiles of a size that a launch may have where the size is not the largest of its type
-// (any number of 64 x 64 over 64 rows and less): what lse_pairs counts on.
+// A type's largest tile may come in any number, and so may 64 x 64 over 64 rows and less;
+// of the others a launch may have so many (lse_pairs counts on that).
+template <class E>
+constexpr int largest_tile() {
+    return sizeof(E) == 4 ? 64 : std::is_same<E, _Float16>::value ? 128 : 256;
+}
 constexpr int64_t most_items(int tile) { return tile == 128 ? 2048 : tile == 64 ? 1024 : 512; }
 
-inline bool may_tile(int tile, int64_t M, int64_t N) {
-    return tile == 256 || (tile == 64 && M <= 64) || ceil_div(M, tile) * ceil_div(N, tile) <= most_items(tile);
+template <class E>
+bool may_tile(int tile, int64_t M, int64_t N) {
+    return tile == largest_tile<E>() || (tile == 64 && M <= 64) || ceil_div(M, tile) * ceil_div(N, tile) <= most_items(tile);
 }
 
 template <class E>
@@ -71,10 +76,10 @@ Cut cut_for(int64_t M, int64_t N, int64_t K, int segs, int64_t most, int out_byt
         else if constexpr (PARTS) return kRatesParts;
         else return kRates16;
     }();
-    Cut best{64, 1, 1e30};
+    Cut best{0, 1, 1e30};  // (there is a better one: of the largest tile)
     const int64_t steps = ceil_div(K, step_of<E>());
     for (const Rate &r : rates) {
-        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile(r.tile, M, N) && !(PARTS && r.tile == 128)) continue;
+        if (walks ? r.tile == 256 || r.tile == 32 : !may_tile<E>(r.tile, M, N)) continue;
         const int64_t tiles = ceil_div(M, r.tile) * ceil_div(N, r.tile), slots = r.tile == 256 ? 256 : 512;
         for (int64_t n = 1; n == 1 || (n <= most && n * 4 <= steps); n = n < 16 ? n + 1 : n + n / 4) {
             const int64_t items = tiles * n, full = items / slots, rest = items % slots;
@@ -121,7 +126,7 @@ inline int64_t weight_sum_bytes(int64_t vocab, int32_t d) { return std::min<int6
 
 inline int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Whether an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
+// The tokens up to which an fp32 plan's products run on the fp32 matrix instructions, a sixteenth
 // of the bf16 ones' rate, or as products of parts (three of fp16 parts forward, six of
 // bf16 parts backward), which need W's parts made first: as long as a second
 // reading of W takes (some 100 tokens' products), and where V is small their
@@ -132,9 +137,10 @@ inline int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 // 59 x 61016 x 2832 857 : 1374, 275 x 22940 x 1496 702 : 567, 521 x 773 x 5952
 // 207 : 174, 1000 x 1000 x 256 46 : 59.  In 49 shapes the rule lost up to 8%, and 19% of two
 // short ones whose second row of tiles was nearly empty (80 x 8962 x 1216, 57 : 47).
-inline bool direct32(const LossArgs &a, bool forward) {
-    return forward ? (a.n_tok - 80) * a.vocab <= 300000000 / a.d + 350000 : (a.n_tok - 100) * a.vocab <= 800000000 / a.d;
+inline int64_t direct_tokens(const LossArgs &a, bool forward) {
+    return forward ? 80 + (300000000 / a.d + 350000) / a.vocab : 100 + 800000000 / a.d / a.vocab;
 }
+inline bool direct32(const LossArgs &a, bool forward) { return a.n_tok <= direct_tokens(a, forward); }
 
 // Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
 // d = 2560 put a stage's 256 lines on four of an L2's sixteen channels; in blocks
@@ -214,8 +220,8 @@ inline int64_t lse_pairs(const LossArgs &a) {
     auto all = [&](int tile, int64_t rows) { return 2 * ceil_div(V, tile) * rows; };
     auto few = [&](int tile) { return std::min(all(tile, T), pieces * most_items(tile) * 2 * tile); };
     const int64_t small = std::max({all(64, std::min<int64_t>(T, 64)), few(64), few(32)});
-    // (an fp32 plan's tiles of 128 x 128 are its largest)
-    return std::max(small, a.bf16 ? std::max(all(256, T), few(128)) : all(128, T));
+    if (a.bf16) return std::max({small, few(128), all(256, T)});
+    return std::max({small, all(128, T), all(64, std::min(T, direct_tokens(a, true)))});
 }
 
 }  // namespace engram

@@ -2,6 +2,7 @@
 // lays out for them, from its own host code.  Reads lines "dtype n_tok vocab d" (dtype
 // 0: fp32, 1: bf16) and answers each with what loss_cut.h chooses and writes:
 //   tile  splits  cost  pieces  bytes of the tiles' maxima and sums  bytes of their region  bytes of the workspace
+//   and of the gradients' products P, dh, dW as whole rows of the vocabulary: the cost of each
 #include <cstdio>
 
 #include "loss_cut.h"
@@ -30,8 +31,17 @@ int main() {
         for (size_t o : {L.xt, L.few, L.h, L.unit, L.w})
             if (o > L.part) end = std::min(end, o);
         const long long pairs = f.cut.splits > 1 ? 0 : 2 * ceil_div(vocab, f.cut.tile) * n;
-        std::printf("%d %lld %.6g %lld %lld %zu %zu\n", f.cut.tile, (long long)f.cut.splits, f.cut.cost,
+        std::printf("%d %lld %.6g %lld %lld %zu %zu", f.cut.tile, (long long)f.cut.splits, f.cut.cost,
                     (long long)ceil_div(vocab, f.piece), 8 * pairs, end - L.part, L.total);
+        auto costs = [&](auto e) {
+            using E = decltype(e);
+            std::printf(" %.6g %.6g %.6g\n", cut_for<E>(n, vocab, d, 1, 1, 4).cost,
+                        cut_for<E>(n, d, vocab, 1, kMostSplits, 4).cost, cut_for<E>(vocab, d, n, 1, 1, 4).cost);
+        };
+        if (!a.bf16 && direct32(a, false))
+            costs(0.f);
+        else
+            costs((uint16_t)0);
     }
     return 0;
 }

@@ -22,7 +22,8 @@ def _hipcc():
 @pytest.fixture(scope="module")
 def cuts(tmp_path_factory):
     """Of each (dtype, n_tok, vocab, d): tile, splits, cost, pieces, bytes written, bytes
-    of the region, bytes of the workspace; None where the sizes are refused."""
+    of the region, bytes of the workspace, costs of the gradients' products; None where the
+    sizes are refused."""
     if not os.path.exists(_hipcc()):
         pytest.skip("hipcc not available")
     exe = str(tmp_path_factory.mktemp("losscut") / "loss_cut_check")
@@ -65,3 +66,35 @@ def test_sums_of_all_pieces_have_room(cuts):
             seen += 1
             assert a[4] <= a[5], (s, a)
     assert seen > 4000
+
+
+def test_every_cut_is_chosen_and_has_room(cuts):
+    """Also where fp32 instructions run some tokens more than one tile's rows: the tile is
+    one that the costs have, and the sums of it fit their region."""
+    rng = random.Random(2)
+    sizes = [(F32, n, 129280, d) for n in range(60, 90) for d in (8, 1024, 2560)]
+    sizes += [(F32, 80, 1 << 22, 8), (F32, 373, 129280, 8), (BF16, 65, 129280, 2560), (F32, 65, 32833, 64)]
+    sizes += [(rng.choice((F32, BF16)), log_int(rng, 1, 1 << 20), log_int(rng, 1, 1 << 22), 8 * log_int(rng, 1, 1 << 13))
+              for _ in range(20000)]
+    sizes += [(F32, log_int(rng, 60, 400), log_int(rng, 1 << 13, 1 << 22), 8 * log_int(rng, 1, 1 << 10)) for _ in range(5000)]
+    seen = 0
+    for s, a in zip(sizes, cuts(sizes)):
+        if a is not None:
+            seen += 1
+            assert a[4] <= a[5], (s, a)
+            assert max([a[2]] + a[7:]) < 1e20, (s, a)
+    assert seen > 15000
+
+
+def test_workspaces_of_more_tokens_are_no_smaller(cuts):
+    """Across the thresholds of the forward's kinds of products, copies and pieces."""
+    rng = random.Random(3)
+    for _ in range(150):
+        dtype, d = rng.choice((F32, BF16)), 8 * log_int(rng, 1, 1 << 15)
+        vocab = log_int(rng, 1, 1 << 22)
+        ns = sorted({log_int(rng, 1, 1 << 21) for _ in range(150)} | set(range(60, 130)))
+        # (tokens up to which an fp32 plan multiplies by the fp32 instructions)
+        direct = 80 + (300000000 // d + 350000) // vocab
+        ns = sorted(set(ns) | {max(1, direct + j) for j in (-1, 0, 1, 2)})
+        totals = [a[6] for a in cuts([(dtype, n, vocab, d) for n in ns]) if a is not None]
+        assert all(x <= y for x, y in zip(totals, totals[1:])), (dtype, vocab, d)
