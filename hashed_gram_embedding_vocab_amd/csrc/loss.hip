@@ -551,7 +551,7 @@ struct GradEnd {
 // whole rows of 32 FN bytes; the pieces of a row are XOR-swizzled by the row.
 template <int FN, int FM>
 __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[FN][FM], uint8_t *img, uint16_t *c, int64_t ld,
-                                           int64_t rows, int64_t cols, int64_t m0, int64_t n0, int lane, bool accumulate) {
+                                           int64_t rows, int64_t cols, int64_t m0, int64_t n0, int lane) {
     constexpr int kRow = FN * 32, kPieces = FN * 2;
     const int fr = lane & 15;
 #pragma unroll
@@ -570,18 +570,7 @@ __device__ __forceinline__ void store_rows(const f32x4_t (&acc)[FN][FM], uint8_t
         const int r = r0 + lane / kPieces, piece = lane % kPieces;
         const u32x4_t v = *reinterpret_cast<const u32x4_t *>(img + r * kRow + ((piece ^ r) & (kPieces - 1)) * 16);
         const int64_t m = m0 + r, n = n0 + piece * 8;
-        if (m < rows && n < cols) {  // (rows are whole pieces)
-            uint16_t *dst = c + m * ld + n;
-            if (accumulate) {
-                const F8 old = load8(dst);
-                F8 x = Raw8<uint16_t>{v}.get();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x.v[e] += old.v[e];
-                store8(dst, x);
-            } else {
-                *reinterpret_cast<u32x4_t *>(dst) = v;
-            }
-        }
+        if (m < rows && n < cols) *reinterpret_cast<u32x4_t *>(c + m * ld + n) = v;  // (rows are whole pieces)
     }
 }
 
@@ -623,7 +612,23 @@ struct SumEnd {
                 for (int i = 0; i < FN; ++i) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if constexpr (!WALKS) {
             if (bf16) {
-                store_rows<FN, FM>(acc, img, static_cast<uint16_t *>(c), ld, g.M, g.N, m0, n0, lane, accumulate);
+                uint16_t *const out = static_cast<uint16_t *>(c);
+                if (accumulate) {  // (to the fp32 sums: what is there and they are rounded once together)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) {
+                        const int64_t m = m0 + 16 * j + (lane & 15);
+                        if (m >= g.M) continue;
+#pragma unroll
+                        for (int i = 0; i < FN; ++i) {
+                            const int64_t n = n0 + 16 * i + 4 * (lane >> 4);
+                            if (n >= g.N) continue;
+                            const u32x2_t old = *reinterpret_cast<const u32x2_t *>(out + m * ld + n);
+                            acc[i][j] += f32x4_t{__uint_as_float(old[0] << 16), __uint_as_float(old[0] & 0xFFFF0000u),
+                                                 __uint_as_float(old[1] << 16), __uint_as_float(old[1] & 0xFFFF0000u)};
+                        }
+                    }
+                }
+                store_rows<FN, FM>(acc, img, out, ld, g.M, g.N, m0, n0, lane);
                 return;
             }
         }

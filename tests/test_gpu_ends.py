@@ -979,3 +979,28 @@ def test_profiling_counts_the_operators(gpu):
     r = plan.engram_profile_end()
     assert r["aux"]["launches"] == 2 and r["gemm"]["launches"] == 1 and r["bwd_gemm"]["launches"] == 1
     assert r["bwd_fuse"]["launches"] == 1 and r["bwd_gemm"]["total_ms"] > 0
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+@pytest.mark.parametrize("n_tok", (1, 3, 21, 33, 64, 65, 200, 700, 4100))
+@pytest.mark.parametrize("vocab,d", [(5, 8), (300, 72), (1000, 264), (5003, 136), (40000, 64), (2000, 2560)])
+def test_accumulated_weight_gradients_are_rounded_once(gpu, dtype, dw_dtype, n_tok, vocab, d):
+    """What is there plus the increment in fp32, rounded once, however the sums are split.
+    An lse of 1000 beside logits of 0 leaves P = -g at the target and 0 elsewhere; h's and
+    g's few bits make each increment, and its sum with the old value, exact in fp32."""
+    p = make_plan(dtype, d, vocab)
+    h = (torch.randint(-255, 256, (n_tok, d), generator=gen(1)) / 64.0).to(tdt(dtype)).to(gpu)
+    w = torch.zeros((vocab, d), dtype=tdt(dtype), device=gpu)
+    y = (torch.arange(n_tok, device=gpu) % min(vocab, 7) * (vocab // 7 + 1) % vocab).to(torch.int32)
+    g = 2.0 ** torch.randint(-2, 2, (n_tok,), generator=gen(2)).to(gpu)
+    lse = torch.full((n_tok,), 1000.0, device=gpu)
+    # (bf16: 8 bits of 2^-8 and more)
+    old = (torch.randint(-255, 256, (vocab, d), generator=gen(3)) / 256.0).to(dw_dtype).to(gpu)
+    inc = torch.zeros((vocab, d), dtype=torch.float64, device=gpu).index_add_(0, y.long(), -g.double()[:, None] * h.double())
+    want = (old.double() + inc).float()
+    assert torch.equal(want.double(), old.double() + inc)
+    ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+    for dh in (None, torch.empty_like(h)):
+        dw = old.clone()
+        p.engram_cross_entropy_backward(h, w, y, lse, g, dh, dw, ws, flags=8)
+        assert torch.equal(dw, want.to(dw_dtype))
