@@ -142,13 +142,22 @@ inline int64_t direct_tokens(const LossArgs &a, bool forward) {
 }
 inline bool direct32(const LossArgs &a, bool forward) { return a.n_tok <= direct_tokens(a, forward); }
 
-// Whether a bf16 plan's h (forward) and W are copied into blocks first.  Rows of
-// d = 2560 put a stage's 256 lines on four of an L2's sixteen channels; in blocks
-// the logits of 8192 tokens and 64,640 columns take 2.03 ms (h) and 1.92 ms (h and W)
-// against 2.13 ms, their gradient's product with W 2.08 ms against 2.35 ms.  The
-// copy of W costs 4 bytes a value, 0.14 ms there, so it takes this many tokens.
-inline bool blocks_h(const LossArgs &a) { return a.bf16 && a.n_tok >= 1024 && a.vocab >= 16384; }
-inline bool blocks_w(const LossArgs &a, bool forward) { return a.bf16 && a.n_tok >= (forward ? 12288 : 4096); }
+// Whether a bf16 plan's h (forward) and W are copied into blocks first: where their rows
+// are no whole lines of 128 bytes, so that each piece of 128 bytes touches two.  Measured,
+// us, rows as they are : copied (whole calls, the copies' 4 bytes a value among them):
+// h   1024 tokens x 116,816 x 2568 668 : 628, 8192 x 232,912 x 1288 4832 : 4552,
+//     2048 x 24,312 x 2056 181 : 179; 8192 x 3648 x 4104 215 : 229
+// W   forward 16,384 x 38,936 x 2568 2956 : 2607, 12,288 x 15,520 x 1288 461 : 445; 8192 x
+//     24,312 x 2056 682 : 672, 4096 x 12,176 x 4104 329 : 352.  Backward 4096 x 155,272 x
+//     1288 5015 : 4825, 4096 x 30,000 x 1000 723 : 668; 2560 x 97,272 x 2056 2903 : 2903,
+//     1536 x 48,728 x 4104 1715 : 1756
+// Of whole lines the copies cost: forward 0 to 3% in 11 shapes of 8192 tokens and more,
+// backward 0 to 3% in 22 widths of 256 to 8192 (6144 x 106,528 x 2816 9022 : 9143, 8192 x
+// 64,000 x 4096 9477 : 9565) and saved 1 to 3% at d = 2560 alone (8192 x 129,280 13,081 :
+// 12,678), for which no rule on its rows was found.
+inline bool split_lines(const LossArgs &a) { return a.bf16 && a.d % 64 != 0; }
+inline bool blocks_h(const LossArgs &a) { return split_lines(a) && a.n_tok >= 1024 && a.vocab >= 16384; }
+inline bool blocks_w(const LossArgs &a, bool forward) { return split_lines(a) && a.n_tok >= (forward ? 12288 : 4096); }
 
 // A bf16 plan's few tokens: the parts of P are further rows of it, and h's rows
 // stand as often, so that W is still read once for dh, where its bytes are what

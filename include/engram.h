@@ -689,7 +689,9 @@ ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s
  * 2^20, or 2^22 tiles of 256 x 256 and more of the logits or of the weights:
  * ENGRAM_E_UNSUPPORTED.
  * The workspace holds the tiles' maxima and sums, the logits of a few tokens in
- * parts of K (32 MB at most), copies of h, and 1 GB at most of W's.
+ * parts of K (32 MB at most), and in an fp32 plan, or where rows of d_model are no
+ * whole lines of 128 bytes, copies of h and of W, of W 1 GB (or 256 rows, where they
+ * are more) at a time.
  */
 /* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported sizes). */
 ENGRAM_API size_t engram_cross_entropy_workspace_size(engram_plan p, int64_t n_tok);
@@ -722,9 +724,11 @@ ENGRAM_API engram_status engram_cross_entropy(engram_plan p, const void *d_h, co
  * vocabulary are few.
  */
 /* Bytes that serve every call of up to n_tok tokens (0 on invalid or unsupported
- * sizes): P, 1 GB of it at most; dh's sums, 512 MB (or those of one part, where
- * they are more), and dW's, 64 MB; the logits of a few tokens, 32 MB; copies of h;
- * of 4096 tokens and more, or in an fp32 plan, copies of W, 1 GB at a time. */
+ * sizes): P, 1 GB of it at most (or 256 columns, where they are more); dh's sums,
+ * 512 MB (or those of one part, where they are more), and dW's, 64 MB; the logits of
+ * a few tokens, 32 MB; a copy of h; in an fp32 plan, or of 4096 tokens and more where
+ * rows of d_model are no whole lines of 128 bytes, copies of W, 1 GB (or 256 rows, where
+ * they are more) at a time. */
 ENGRAM_API size_t engram_cross_entropy_backward_workspace_size(engram_plan p, int64_t n_tok, engram_dtype dweight_dtype);
 ENGRAM_API engram_status engram_cross_entropy_backward(engram_plan p, const void *d_h, const void *d_weight,
                                                        const int32_t *d_targets, int64_t n_tok, float scale,

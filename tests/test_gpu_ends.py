@@ -1004,3 +1004,17 @@ def test_accumulated_weight_gradients_are_rounded_once(gpu, dtype, dw_dtype, n_t
         dw = old.clone()
         p.engram_cross_entropy_backward(h, w, y, lse, g, dh, dw, ws, flags=8)
         assert torch.equal(dw, want.to(dw_dtype))
+
+
+@pytest.mark.parametrize("n_tok,vocab,d", [(1030, 16500, 128), (4100, 300, 192), (12290, 270, 64), (4100, 1000, 320)])
+def test_rows_of_whole_lines_are_read_where_they_are(gpu, n_tok, vocab, d):
+    """Token counts from which rows that are no whole lines are copied into blocks first."""
+    p = make_plan("bf16", d, vocab)
+    h, w, y = head("bf16", n_tok, vocab, d, 1.0, 3, gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok))
+    ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, 1.0, "bf16").forward())
+    close(loss, ref, off, "loss")
+    close(lse, ref_lse, off_lse, "lse")
+    for dw_dtype in (torch.bfloat16, torch.float32):
+        check_backward(gpu, "bf16", dw_dtype, n_tok, vocab, d, 1.0)
