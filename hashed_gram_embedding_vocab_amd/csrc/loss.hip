@@ -900,7 +900,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void gemm_kernel(GemmArgs g, End e
 template <typename T, typename Out, int PARTS>
 __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, int32_t d, const int32_t *targets,
                                                     int32_t vocab, Out *out, const float *lse, const float *dloss,
-                                                    float factor, Token *token, int32_t copies) {
+                                                    double factor, Token *token, int32_t copies) {
     constexpr bool BLOCKS = sizeof(Out) == 2;
     const int32_t cols = BLOCKS ? (d + kBlock - 1) / kBlock * kBlock : d, units = cols / 8;
     const int64_t all = BLOCKS ? (rows * copies + kBlock - 1) / kBlock * kBlock : rows, n = all * units;
@@ -911,7 +911,8 @@ __global__ __launch_bounds__(256) void parts_kernel(const T *x, int64_t rows, in
         bool counts = r < rows;
         if (targets && counts) {
             const int32_t id = targets[r];
-            const float f = (dloss ? dloss[r] : 1.f) * factor;
+            // (64 bits: the two factors' product may pass fp32's range where the three's does not)
+            const float f = (float)((dloss ? (double)dloss[r] : 1.) * factor);
             counts = id >= 0 && id < vocab && f != 0.f;
             if (c == 0 && copy == 0) token[r] = counts ? Token{lse[r], f, id, 0} : Token{0.f, 0.f, -1, 0};
         }
@@ -1229,7 +1230,8 @@ void make_parts(const void *x, int64_t rows, int32_t d, const LossArgs *a, Out *
     launch_kernel((parts_kernel<T, Out, PARTS>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), s,
                   static_cast<const T *>(x), rows, d, a ? a->targets : static_cast<const int32_t *>(nullptr),
                   a ? a->vocab : 0, out, a ? static_cast<const float *>(a->lse) : static_cast<const float *>(nullptr),
-                  a ? a->dloss : static_cast<const float *>(nullptr), a ? a->dloss_scale * a->scale : 0.f, token, copies);
+                  a ? a->dloss : static_cast<const float *>(nullptr), a ? (double)a->dloss_scale * (double)a->scale : 0., token,
+                  copies);
 }
 
 // A copy in blocks of rows of h or W: a bf16 plan's as they are, an fp32 plan's in

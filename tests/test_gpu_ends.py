@@ -1018,3 +1018,28 @@ def test_rows_of_whole_lines_are_read_where_they_are(gpu, n_tok, vocab, d):
     close(lse, ref_lse, off_lse, "lse")
     for dw_dtype in (torch.bfloat16, torch.float32):
         check_backward(gpu, "bf16", dw_dtype, n_tok, vocab, d, 1.0)
+
+
+@pytest.mark.parametrize("dtype,dw_dtype", GRADS)
+@pytest.mark.parametrize("n_tok,vocab,d", PATHS)
+def test_factors_whose_product_passes_fp32s_range(gpu, dtype, dw_dtype, n_tok, vocab, d):
+    """g_t scale = dloss_t dloss_scale scale counts as a whole: 2^140 and 2^-160 as the last
+    two's product, with the dloss that brings the whole back, give the bits of the same
+    whole made of ordinary factors, and a token whose dloss is 0 has no part."""
+    p = make_plan(dtype, d, vocab)
+    r = torch.rand(n_tok, generator=gen(8)).to(gpu) + 0.1
+    r[::3] = 0.0
+    y = zipf_ids(n_tok, vocab, 3, bad=False).to(gpu)
+    lse = torch.full((n_tok,), math.log(vocab), device=gpu)
+    ws = p.cross_entropy_backward_workspace(n_tok, dw_dtype)
+    for scale, loss_scale, dloss in ((2.0 ** 40, 2.0 ** 100, r * 2.0 ** -120), (2.0 ** -60, 2.0 ** -100, r * 2.0 ** 120)):
+        h, w = randn((n_tok, d), dtype, 1).to(gpu), randn((vocab, d), dtype, 2, 2.0 ** -42 / math.sqrt(d)).to(gpu)
+        results = []
+        for s, g in ((loss_scale, dloss), (1.0, dloss.double() * loss_scale)):
+            dh, dw = nan_like(torch.empty_like(h)), nan_like(torch.empty((vocab, d), dtype=dw_dtype, device=gpu))
+            p.engram_cross_entropy_backward(h, w, y, lse, g.float(), dh, dw, ws, scale=scale, dloss_scale=s)
+            results.append((dh, dw))
+        assert all(torch.equal(a, b) for a, b in zip(*results))
+        dh, dw = results[0]
+        assert torch.isfinite(dh).all() and torch.isfinite(dw).all() and dw.count_nonzero()
+        assert not dh[r == 0].count_nonzero()
