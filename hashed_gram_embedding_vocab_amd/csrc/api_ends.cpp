@@ -36,6 +36,9 @@ size_t rms_bwd_bytes(const engram_plan_s &p, int64_t n_rows) {
     return round_up((size_t)rms_bwd_blocks(n_rows, p.cfg.d_model) * (size_t)p.cfg.d_model * 4, 256);
 }
 
+// (the logits are taken as powers of two: scale / ln 2 has to be finite too)
+bool scale_fits(float scale) { return std::fabs(scale) <= 0x1p127f; }
+
 engram_status check_loss_sizes(const engram_plan_s &p, int64_t n_tok) {
     if (n_tok <= 0) return ENGRAM_E_INVALID_ARG;
     if (!loss_fits(n_tok, p.cfg.vocab, p.cfg.d_model)) return ENGRAM_E_UNSUPPORTED;
@@ -162,7 +165,7 @@ size_t engram_cross_entropy_workspace_size(engram_plan p, int64_t n_tok) {
 engram_status engram_cross_entropy(engram_plan p, const void *d_h, const void *d_weight, const int32_t *d_targets,
                                    int64_t n_tok, float scale, float *d_loss, float *d_lse, void *d_workspace,
                                    size_t workspace_bytes, hipStream_t stream) {
-    if (!p || !d_h || !d_weight || !d_targets || !d_loss || !d_lse || !d_workspace || !std::isfinite(scale))
+    if (!p || !d_h || !d_weight || !d_targets || !d_loss || !d_lse || !d_workspace || !scale_fits(scale))
         return ENGRAM_E_INVALID_ARG;
     const engram_status st = check_loss_sizes(*p, n_tok);
     if (st != ENGRAM_OK) return st;
@@ -208,7 +211,7 @@ engram_status engram_cross_entropy_backward(engram_plan p, const void *d_h, cons
                                             size_t workspace_bytes, hipStream_t stream) {
     if (!p || !d_h || !d_weight || !d_targets || !d_lse || (!d_dh && !d_dweight) || !d_workspace)
         return ENGRAM_E_INVALID_ARG;
-    if (!std::isfinite(scale) || !std::isfinite(dloss_scale) || (flags & ~(uint32_t)ENGRAM_GRAD_ACCUMULATE))
+    if (!scale_fits(scale) || !std::isfinite(dloss_scale) || (flags & ~(uint32_t)ENGRAM_GRAD_ACCUMULATE))
         return ENGRAM_E_INVALID_ARG;
     engram_status st = check_loss_sizes(*p, n_tok);
     if (st == ENGRAM_OK) st = check_dweight(*p, dweight_dtype);

@@ -675,7 +675,7 @@ ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s
  *   d_h          [n_tok][d_model] plan dtype
  *   d_weight     [vocab][d_model] plan dtype (the token embedding's table, where tied)
  *   d_targets    [n_tok] int32
- *   scale        finite factor of the logits
+ *   scale        factor of the logits, at most 2^127 in magnitude
  *   d_loss, d_lse  [n_tok] fp32 (natural logarithms)
  *   d_workspace  >= engram_cross_entropy_workspace_size(p, n) bytes for an
  *                n >= n_tok, 256-byte aligned

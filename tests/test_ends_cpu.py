@@ -259,3 +259,17 @@ def test_a_gradient_list_of_several_shapes(B, monkeypatch):
     assert [(e.n_groups, e.rows, e.row_len, e.dtype) for e in lst.c] == [
         (1, 1, 5, B.F32), (3, 4, 14, B.F32), (1, 1, 0, B.F32), (2, 6, 1, B.BF16)]
     assert all(e.out == e.data for e in lst.c)
+
+
+def test_cross_entropy_refuses_scales_past_its_powers_of_two(B):
+    """2^127 / ln 2 is the largest that fp32 holds: 2^127 passes, and what comes after it
+    is refused; other arguments are bad, so that nothing is launched."""
+    p = plan(B)
+    ws, ws_b = p.engram_cross_entropy_workspace_size(33), p.engram_cross_entropy_backward_workspace_size(33)
+    fwd, bwd = B.lib().engram_cross_entropy, B.lib().engram_cross_entropy_backward
+    for sign in (1, -1):
+        for scale, n, want in ((2.0 ** 127, 1 << 50, B.E_UNSUPPORTED), (2.0 ** 127 * (1 + 2.0 ** -23), 33, B.E_INVALID_ARG),
+                               (3.4e38, 33, B.E_INVALID_ARG)):
+            assert fwd(p._h, at(0), at(1), at(2), n, sign * scale, at(3), at(4), at(5), ws, None) == want
+            assert bwd(p._h, at(0), at(1), at(2), n, sign * scale, at(3), at(4), 1.0, 0, at(5), at(6), B.F32, at(7), ws_b,
+                       None) == want

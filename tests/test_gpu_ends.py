@@ -1043,3 +1043,19 @@ def test_factors_whose_product_passes_fp32s_range(gpu, dtype, dw_dtype, n_tok, v
         dh, dw = results[0]
         assert torch.isfinite(dh).all() and torch.isfinite(dw).all() and dw.count_nonzero()
         assert not dh[r == 0].count_nonzero()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sign", (1, -1))
+def test_the_largest_scale(gpu, dtype, sign):
+    """2^127 over weights of 2^-126: every product and sum is a normal number."""
+    for n_tok, vocab, d in PATHS:
+        p = make_plan(dtype, d, vocab)
+        h = torch.randint(0, 4, (n_tok, d), generator=gen(1)).to(tdt(dtype)).to(gpu)
+        w = (torch.randint(-1, 2, (vocab, d), generator=gen(2)) * 2.0 ** -126).to(tdt(dtype)).to(gpu)
+        y = zipf_ids(n_tok, vocab, 3).to(gpu)
+        loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+        p.engram_cross_entropy(h, w, y, loss, lse, p.cross_entropy_workspace(n_tok), scale=sign * 2.0 ** 127)
+        ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, sign * 2.0 ** 127, dtype).forward())
+        close(loss, ref, off, "loss")
+        close(lse, ref_lse, off_lse, "lse")
