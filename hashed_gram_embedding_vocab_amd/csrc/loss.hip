@@ -33,9 +33,9 @@
 // or, where tokens or vocabulary are few, by the fp32 instructions as they are.
 //
 // 8192 tokens x 129280 x 2560 in bf16: 5.4 TFLOP forward, 16.3 backward; a library's
-// product of 8192^3 runs at 1.40 PFLOP/s here.  Forward 4.1 ms (the product 1.33
-// PFLOP/s), gradients 12.7 ms (P 1.28, dh 1.34, dW 1.36 PFLOP/s, copies and joins
-// 0.3 ms).  The matrix units are busy 62 to 70 % of the cycles, at 1.9 GHz, where
+// product of 8192^3 runs at 1.40 PFLOP/s here.  Forward 4.1 to 4.3 ms on several cards
+// (the product 1.33 PFLOP/s), gradients 13.2 ms (P 1.24, dh 1.26, dW 1.31 PFLOP/s, copy and
+// join 0.1 ms).  The matrix units are busy 60 to 70 % of the cycles, at 1.9 GHz, where
 // their own power holds the clock.  One token: W's 662 MB in 112 us, 5.9 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -1386,7 +1386,8 @@ void backward(const LossArgs &a, hipStream_t s) {
             g.a = oh;
             g.b = ow;
             parts_of(g, hp, hp);
-            // (cut as for one part, so that dh does not change with dW's type)
+            // (cut as for one part of P, so that where the vocabulary is one piece dh does not
+            // go by dW's type; the pieces do, by P's bytes, and with them the order of dh's sums)
             const int out = F32 ? 4 : 2;
             const Cut few = one_piece ? few_cut<E>(a, n, d, g.segs, out) : cut_for<E>(T, n, d, g.segs, 1, out);
             if (few.splits > 1) {

@@ -635,7 +635,8 @@ ENGRAM_API engram_status engram_matmul_fp8(engram_plan p, const void *d_a, const
  *   d_rrms       [n_rows] fp32 for the backward, or NULL
  * A row with an infinity or a NaN gives NaN throughout or zeros beside NaN, as
  * the formula has it (and its blocks' scales those of their finite values); one whose squares' sum
- * passes fp32's range gives zeros.
+ * passes fp32's range gives zeros, and one whose squares' mean falls below it, with an eps of 0,
+ * infinities (NaN where s is 0).
  * d_model above 32768: ENGRAM_E_UNSUPPORTED.
  */
 ENGRAM_API engram_status engram_rms_norm(engram_plan p, const void *d_x, const void *d_residual, int64_t n_rows,
@@ -685,7 +686,7 @@ ENGRAM_API engram_status engram_rms_norm_backward(engram_plan p, const void *d_s
  * matrix instructions where tokens or vocabulary are few, else in two fp16 parts
  * over a power of two of each row's own (22 bits of what is not 2^-18 and more
  * below the row's largest value), with fp32 sums.  A NaN in a token's h, or in a
- * weight, gives NaN losses.  n_tok above 2^26, vocab above 2^22, d_model above
+ * weight, gives NaN losses, and so does a logit past fp32's range.  n_tok above 2^26, vocab above 2^22, d_model above
  * 2^20, or 2^22 tiles of 256 x 256 and more of the logits or of the weights:
  * ENGRAM_E_UNSUPPORTED.
  * The workspace holds the tiles' maxima and sums, the logits of a few tokens in
@@ -757,7 +758,8 @@ typedef struct {
  *   factor = max_norm / norm where norm is finite and above max_norm, else 1
  *   out = factor * x, rounded once
  * A norm that is infinite or NaN (an overflow: the step is to be skipped) scales
- * nothing.  Tensors in place are not written where the factor is 1.
+ * nothing.  One that is finite in 64 bits and past fp32's range scales, and d_norm
+ * holds infinity for it.  Tensors in place are not written where the factor is 1.
  *   grads        HOST array of n_grads tensors, read before the call returns
  *   max_norm     above 0; INFINITY for the norm alone
  *   d_norm       [2] fp32: the norm and the factor (for an optimizer that scales
