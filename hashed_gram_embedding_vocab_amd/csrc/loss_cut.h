@@ -155,7 +155,7 @@ inline bool direct32(const LossArgs &a, bool forward) { return a.n_tok <= direct
 // backward 0 to 3% in 22 widths of 256 to 8192 (6144 x 106,528 x 2816 9022 : 9143, 8192 x
 // 64,000 x 4096 9477 : 9565), and saved 1 to 3% at d = 2560 and 5120 (8192 x 129,280 x 2560
 // 13,081 : 12,678; dh over 160 million weights reads 9.6 GB : 4.6 past the L2s).  No rule was
-// found that names these pitches: 640, 1280, 7680, 10,240 and 12,800 lose, as 2496 and 2624 do.
+// found that names these two: 1280, 7680, 10,240 and 12,800, 2496 and 2624 lose or are even.
 inline bool split_lines(const LossArgs &a) { return a.bf16 && a.d % 64 != 0; }
 inline bool blocks_h(const LossArgs &a) { return split_lines(a) && a.n_tok >= 1024 && a.vocab >= 16384; }
 inline bool blocks_w(const LossArgs &a, bool forward) { return split_lines(a) && a.n_tok >= (forward ? 12288 : 4096); }

@@ -1059,3 +1059,25 @@ def test_the_largest_scale(gpu, dtype, sign):
         ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, sign * 2.0 ** 127, dtype).forward())
         close(loss, ref, off, "loss")
         close(lse, ref_lse, off_lse, "lse")
+
+
+@pytest.mark.parametrize("n_tok,vocab,d", [(80, 129280, 64), (66, 40001, 72), (192, 40130, 6744)])
+def test_the_tiles_sums_stay_in_their_region(gpu, n_tok, vocab, d):
+    """fp32: more tiles of 64 x 64 than a launch of a smaller kind may have, and such tiles in
+    two pieces of the vocabulary.  The logits of a few tokens, which these calls do not
+    make, have the next region: it and what lies behind the workspace stay as they were."""
+    p = make_plan("f32", d, vocab)
+    h, w, y = head("f32", n_tok, vocab, d, 1.0, 3, gpu)
+    loss, lse = nan_like(torch.empty(n_tok, device=gpu)), nan_like(torch.empty(n_tok, device=gpu))
+    size = p.engram_cross_entropy_workspace_size(n_tok)
+    ws = Guarded((size,), torch.uint8, gpu)
+    ws.t.fill_(0x5A)
+    p.engram_cross_entropy(h, w, y, loss, lse, ws.t)
+    ref, ref_lse, off, off_lse = (t.cpu() for t in HeadRef(h, w, y, 1.0, "f32").forward())
+    close(loss, ref, off, "loss")
+    close(lse, ref_lse, off_lse, "lse")
+    assert ws.whole()
+    # targets' logits, then 2 ceil(V / 64) pairs a token at most, then 32 MB at most
+    at = -(-4 * n_tok // 256) * 256 + -(-8 * 2 * -(-vocab // 64) * n_tok // 256) * 256
+    few = min(32 << 20, 64 * n_tok * -(-vocab // 8) * 8 * 4)
+    assert (ws.t[at:at + few] == 0x5A).all()
